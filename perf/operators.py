@@ -366,7 +366,7 @@ def _run_step(s):
             m = s["m"].view(torch.float8_e4m3fn).float().view(-1, BLOCK).mul_(s["m_scale"][:, None]).view(-1)
             v = s["v"].view(torch.float8_e4m3fn).float().view(-1, BLOCK).mul_(s["v_scale"][:, None]).square_().view(-1)
         m.mul_(b1).add_(g * (1.0 - b1))
-        v.mul_(b2).add_(g.square_().mul_(1.0 - b2))
+        v.mul_(b2).add_(g.square().mul_(1.0 - b2))
         r = v.sqrt()
         p = s.get("master", s["weights"])
         p.mul_(decay).sub_(m / (r * root + ADAM_EPS) * rate)
