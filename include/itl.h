@@ -306,6 +306,162 @@ itl_status itl_lmhead_logprob_mxfp4(const uint8_t* Hq, const float* h_scale,
                                     const int32_t* tokens, float* logprob, float* lse,
                                     void* workspace, size_t workspace_bytes, void* stream);
 
+/* The norms around a block, fused with its gate and residual scale: what
+ * makes the head's hidden states from the residual stream. For each row of
+ * x [n_rows, d] (the stream) and y [n_rows, d] (the block's output):
+ *   p = y r_post w_post   r_post = (mean_k y^2 + eps)^-1/2  (w_post NULL: p = y)
+ *   h = x + scale gate p  (gate NULL: 1)
+ *   u = h r_pre w_pre     r_pre = (mean_k h^2 + eps)^-1/2
+ * in fp32 between the loads and the stores; h and u are rounded once each to
+ * dtype (nearest even), and u is taken from the rounded h, so a fused call has
+ * the bits of one that norms the stored h. y NULL: h is x (h is not written
+ * and may be NULL; gate and w_post must be NULL). gate [d] with gate_stride 0
+ * (one gate for all rows) or [n_rows, d] with gate_stride d. All arrays of
+ * `dtype` (ITL_BF16 or ITL_F32), any d in [1, 2^24]; 16-byte aligned where d
+ * is a multiple of 8, else aligned to their elements (ITL_ERR_INVALID_ARG
+ * otherwise). rstd_pre, rstd_post (nullable) fp32 [n_rows]: r_pre, r_post, for
+ * the backward. h may be x. eps in (0, 1).
+ * A row's results depend on the row, d and dtype alone, as everything of this
+ * library's forward [BC]. */
+itl_status itl_residual_norm(const void* x, const void* y, const void* gate, int64_t gate_stride,
+                             const void* w_post, const void* w_pre, itl_dtype dtype,
+                             int64_t n_rows, int64_t d, float scale, float eps,
+                             void* h, void* u, float* rstd_pre, float* rstd_post, void* stream);
+
+/* The same with u as the FP8 head takes it [FP8]: E4M3 codes Uq [n_rows, d]
+ * (8-byte aligned) with u_scale [n_rows] = amax_row / 448 (1 for a zero row),
+ * codes of u / u_scale (fp32 division, to nearest even) straight from the fp32
+ * u: one rounding. d a multiple of 128 (ITL_ERR_UNSUPPORTED otherwise); the
+ * rows must be finite. */
+itl_status itl_residual_norm_fp8(const void* x, const void* y, const void* gate, int64_t gate_stride,
+                                 const void* w_post, const void* w_pre, itl_dtype dtype,
+                                 int64_t n_rows, int64_t d, float scale, float eps,
+                                 void* h, uint8_t* Uq, float* u_scale, float* rstd_pre, float* rstd_post,
+                                 void* stream);
+
+/* Bytes of device workspace itl_residual_norm_backward needs. SIZE_MAX for
+ * invalid sizes. */
+size_t itl_residual_norm_backward_workspace_bytes(int64_t n_rows, int64_t d);
+
+/* Backward of itl_residual_norm. du [n_rows, d] (du_dtype: dtype or ITL_F32,
+ * as the head's backward writes dH) and dh [n_rows, d] of dtype (NULL: 0) are
+ * the gradients with respect to u and h; h, y, the weights, the gate and the
+ * statistics as in the forward. With n = h r_pre, q = y r_post and <.> the
+ * row's mean:
+ *   dx = dh + r_pre (du w_pre - n <du w_pre n>)      dw_pre = sum_t du n
+ *   dp = scale gate dx   dgate = scale p dx           dw_post = sum_t dp q
+ *   dy = r_post (dp w_post - q <dp w_post q>)         (w_post NULL: dy = dp)
+ * dx is the whole gradient of h and so of x. dx, dy of dtype; dw_pre, dw_post
+ * fp32 [d]; dgate fp32 [d] for gate_stride 0, else [n_rows, d] of dtype.
+ * dy, dgate, dw_post only where y, gate, w_post are given. dx may be dh.
+ * n_rows == 0: the sums are zeros. Row results depend on the row alone; the
+ * column sums are run-to-run deterministic. workspace 256-byte aligned. */
+itl_status itl_residual_norm_backward(const void* du, itl_dtype du_dtype, const void* dh, const void* h,
+                                      const void* y, const void* gate, int64_t gate_stride,
+                                      const void* w_post, const void* w_pre,
+                                      const float* rstd_pre, const float* rstd_post, itl_dtype dtype,
+                                      int64_t n_rows, int64_t d, float scale, void* dx, void* dy, void* dgate,
+                                      float* dw_pre, float* dw_post,
+                                      void* workspace, size_t workspace_bytes, void* stream);
+
+/* What itl_cross_entropy's loss is over the counted tokens. */
+enum { ITL_SUM = 0, ITL_MEAN = 1 };
+
+/* Bytes of device workspace itl_cross_entropy (with_grad 0) or
+ * itl_cross_entropy_grad (with_grad 1) needs. With the gradient it holds the
+ * logits and two copies of their gradients for at most 16,384 tokens and a
+ * transposed W, whatever n_tok. SIZE_MAX for invalid sizes or dtypes. */
+size_t itl_cross_entropy_workspace_bytes(int64_t n_tok, int64_t d, int64_t vocab, itl_dtype dtype,
+                                         int32_t with_grad, itl_dtype grad_dtype);
+
+/* Cross entropy over the vocabulary through the head (supervised warm start
+ * of the policy): with z, lse as in itl_lmhead_logprob, e = label_smoothing in
+ * [0, 1) and lam = z_weight >= 0, for every counted token t
+ *   token_loss[t] = (1 - e) (lse - z[t, y_t]) + e (lse - mean_v z[t, v]) + lam lse^2
+ * and loss[0] = their mean (ITL_MEAN) or sum (ITL_SUM). A token counts if
+ * 0 <= targets[t] < vocab; others (prompt and padding tokens, -100 by
+ * convention) get token_loss 0 and lse 0, enter nothing and cost nothing but
+ * the reading of their id. No counted token: loss 0.
+ * H, W, dtype, d, vocab as for itl_lmhead_logprob; targets int32 [n_tok];
+ * loss fp32 [1], token_loss, lse (nullable) fp32 [n_tok]. The losses are summed
+ * in fp64 in a fixed order. A token's loss does not depend on its
+ * batch-mates. */
+itl_status itl_cross_entropy(const void* H, const void* W, itl_dtype dtype,
+                             int64_t n_tok, int64_t d, int64_t vocab, const int32_t* targets,
+                             float label_smoothing, float z_weight, int32_t reduction,
+                             float* loss, float* token_loss, float* lse,
+                             void* workspace, size_t workspace_bytes, void* stream);
+
+/* The same with the gradient of grad_scale * loss: with N the number of
+ * counted tokens (1 for ITL_SUM), for counted t
+ *   G[t, v] = grad_scale / N ((1 + 2 lam lse) p[t, v] - (1 - e) [v = y_t] - e / vocab)
+ *   dH = G W [n_tok, d] (rows of tokens that do not count: 0),  dW = G^T H [vocab, d]
+ * both of grad_dtype (dtype or ITL_F32), overwritten, 16-byte aligned. The
+ * logits are kept for one chunk of at most 16,384 tokens at a time, in the
+ * workspace. G enters its contractions in the head's dtype (bf16: 2^-9 of each
+ * entry; with bf16 gradients the target's entry too, with fp32 ones the
+ * one-hot term is applied exactly in fp32). Sums in fp32; fixed orders, no
+ * atomics: run-to-run deterministic. n_tok == 0: loss 0, dW zeros. vocab above
+ * about 2.1e6 returns ITL_ERR_UNSUPPORTED. */
+itl_status itl_cross_entropy_grad(const void* H, const void* W, itl_dtype dtype,
+                                  int64_t n_tok, int64_t d, int64_t vocab, const int32_t* targets,
+                                  float label_smoothing, float z_weight, int32_t reduction,
+                                  float grad_scale, itl_dtype grad_dtype,
+                                  float* loss, float* token_loss, float* lse, void* dH, void* dW,
+                                  void* workspace, size_t workspace_bytes, void* stream);
+
+/* One tensor of an optimizer step. */
+typedef struct itl_adamw_tensor {
+  void* param;        /* weights, updated in place (device) */
+  const void* grad;   /* their gradients (device) */
+  int64_t n;          /* elements, >= 0 */
+  itl_dtype param_dtype;
+  itl_dtype grad_dtype;
+  float weight_decay; /* decoupled, >= 0 */
+} itl_adamw_tensor;
+
+/* Sizes of a plan over these tensors: the plan's bytes, and the elements of
+ * each flat state (every tensor's state starts at the next multiple of 256). */
+itl_status itl_adamw_plan_sizes(const itl_adamw_tensor* tensors, int32_t n_tensors,
+                                int64_t* plan_bytes, int64_t* state_elements);
+
+/* Writes the plan into HOST memory; the caller copies it to the device (8-byte
+ * aligned) and passes that copy to every step as long as the tensors stay
+ * where they are. The tensors may have any mix of dtypes and any element
+ * alignment (16-byte aligned ones are moved in whole vectors); two of them
+ * that share weights are refused (ITL_ERR_INVALID_ARG). */
+itl_status itl_adamw_plan(const itl_adamw_tensor* tensors, int32_t n_tensors,
+                          void* host_plan, size_t host_plan_bytes);
+
+size_t itl_adamw_step_workspace_bytes(void);
+
+/* One AdamW step over all the plan's tensors, on `stream`:
+ *   t = ++step[0];  g = clip grad
+ *   m = beta1 m + (1 - beta1) g;  v = beta2 v + (1 - beta2) g^2
+ *   w = w (1 - lr weight_decay) - lr / (1 - beta1^t) m / (sqrt(v) / sqrt(1 - beta2^t) + eps)
+ * clip = min(1, max_norm / (norm + 1e-6)), norm = the 2-norm of all gradients
+ * (fp64 sum), written to grad_norm (nullable; without it and with max_norm
+ * infinite it is not computed). A norm that is not finite skips the step:
+ * nothing but grad_norm is written, step[0] included.
+ * state_bits 32: exp_avg, exp_avg_sq fp32 [state_elements]. 8: uint8
+ * [state_elements] holding E4M3 codes of m and of sqrt(v), with
+ * exp_avg_scale, exp_avg_sq_scale fp32 [state_elements / 256], amax / 448 of
+ * each 256 elements (1 for zeros); codes to nearest even, a root that is not
+ * zero at least the smallest code. States start as zeros (codes and scales
+ * too). Elements between the tensors' states are not used (in 32 bits not
+ * touched; in 8 bits written as zeros up to the next multiple of 8).
+ * master (nullable) fp32 [state_elements]: the weights of bf16 tensors, which
+ * then get its rounding (without it a bf16 weight is its own; fp32 weights
+ * never use it). lr fp32 [1] and step int64 [1] are device memory, so that a
+ * captured step replays with the values of the time of the replay. Run-to-run
+ * deterministic. Two steps of one plan, or two that share a workspace, must be
+ * ordered by the caller. */
+itl_status itl_adamw_step(const void* plan, size_t plan_bytes, int32_t state_bits,
+                          void* exp_avg, void* exp_avg_sq, float* exp_avg_scale, float* exp_avg_sq_scale,
+                          float* master, const float* lr, int64_t* step,
+                          double beta1, double beta2, double eps, float max_norm, float* grad_norm,
+                          void* workspace, size_t workspace_bytes, void* stream);
+
 /* Statistics written by itl_mismatch_stats (fp64, indices into `stats`). */
 typedef enum itl_stat {
   ITL_STAT_N_TOK = 0,

@@ -18,6 +18,12 @@ Entry points (same names as the C ABI without the ``itl_`` prefix):
   ``lmhead_logprob_fp8(Hq, h_scale, Wq, w_scale, tokens) -> (logprob, lse)``
 * ``quantize_rows_mxfp4(X) -> (Xq4, scale_codes)``,
   ``lmhead_logprob_mxfp4(Hq, h_scale, Wq4, w_scale_codes, tokens) -> (logprob, lse)``
+* ``residual_norm(x, y, w_pre) -> (h, u, rstd_pre, rstd_post)``,
+  ``residual_norm_fp8(x, y, w_pre) -> (h, Uq, u_scale, rstd_pre, rstd_post)``,
+  ``residual_norm_backward(du, dh, h, y, w_pre, rstd_pre) -> (dx, dy, dw_pre, dw_post, dgate)``
+* ``cross_entropy(H, W, targets) -> (loss, token_loss, lse)``,
+  ``cross_entropy_grad(H, W, targets) -> (loss, token_loss, lse, dH, dW)``
+* ``adamw_plan(params, grads, lr=...) -> plan``, ``adamw_step(plan) -> grad_norm``
 * ``check_inputs(tokens, vocab, resp_offsets=None)``, ``build_info()``
 """
 
@@ -37,6 +43,17 @@ _c_void_p = ctypes.c_void_p
 _i64 = ctypes.c_int64
 _i32 = ctypes.c_int32
 _size = ctypes.c_size_t
+
+
+_f32 = ctypes.c_float
+_f64 = ctypes.c_double
+
+
+class _AdamWTensor(ctypes.Structure):
+    """itl_adamw_tensor."""
+
+    _fields_ = [("param", _c_void_p), ("grad", _c_void_p), ("n", _i64), ("param_dtype", _i32), ("grad_dtype", _i32),
+                ("weight_decay", _f32)]
 
 
 class ItlError(RuntimeError):
@@ -83,6 +100,31 @@ def _load():
                                                    _c_void_p]),
         "itl_lmhead_logprob_mxfp4": (ctypes.c_int, [_c_void_p, _c_void_p, _c_void_p, _c_void_p, _i64, _i64, _i64,
                                                     _c_void_p, _c_void_p, _c_void_p, _c_void_p, _size, _c_void_p]),
+        "itl_residual_norm": (ctypes.c_int, [_c_void_p, _c_void_p, _c_void_p, _i64, _c_void_p, _c_void_p, ctypes.c_int,
+                                             _i64, _i64, _f32, _f32, _c_void_p, _c_void_p, _c_void_p, _c_void_p,
+                                             _c_void_p]),
+        "itl_residual_norm_fp8": (ctypes.c_int, [_c_void_p, _c_void_p, _c_void_p, _i64, _c_void_p, _c_void_p,
+                                                 ctypes.c_int, _i64, _i64, _f32, _f32, _c_void_p, _c_void_p, _c_void_p,
+                                                 _c_void_p, _c_void_p, _c_void_p]),
+        "itl_residual_norm_backward_workspace_bytes": (_size, [_i64, _i64]),
+        "itl_residual_norm_backward": (ctypes.c_int, [_c_void_p, ctypes.c_int, _c_void_p, _c_void_p, _c_void_p,
+                                                      _c_void_p, _i64, _c_void_p, _c_void_p, _c_void_p, _c_void_p,
+                                                      ctypes.c_int, _i64, _i64, _f32, _c_void_p, _c_void_p, _c_void_p,
+                                                      _c_void_p, _c_void_p, _c_void_p, _size, _c_void_p]),
+        "itl_cross_entropy_workspace_bytes": (_size, [_i64, _i64, _i64, ctypes.c_int, _i32, ctypes.c_int]),
+        "itl_cross_entropy": (ctypes.c_int, [_c_void_p, _c_void_p, ctypes.c_int, _i64, _i64, _i64, _c_void_p, _f32,
+                                             _f32, _i32, _c_void_p, _c_void_p, _c_void_p, _c_void_p, _size,
+                                             _c_void_p]),
+        "itl_cross_entropy_grad": (ctypes.c_int, [_c_void_p, _c_void_p, ctypes.c_int, _i64, _i64, _i64, _c_void_p,
+                                                  _f32, _f32, _i32, _f32, ctypes.c_int, _c_void_p, _c_void_p,
+                                                  _c_void_p, _c_void_p, _c_void_p, _c_void_p, _size, _c_void_p]),
+        "itl_adamw_plan_sizes": (ctypes.c_int, [ctypes.POINTER(_AdamWTensor), _i32, ctypes.POINTER(_i64),
+                                                ctypes.POINTER(_i64)]),
+        "itl_adamw_plan": (ctypes.c_int, [ctypes.POINTER(_AdamWTensor), _i32, _c_void_p, _size]),
+        "itl_adamw_step_workspace_bytes": (_size, []),
+        "itl_adamw_step": (ctypes.c_int, [_c_void_p, _size, _i32, _c_void_p, _c_void_p, _c_void_p, _c_void_p,
+                                          _c_void_p, _c_void_p, _c_void_p, _f64, _f64, _f64, _f32, _c_void_p,
+                                          _c_void_p, _size, _c_void_p]),
         "itl_mismatch_stats_workspace_bytes": (_size, [_i64]),
         "itl_mismatch_stats": (ctypes.c_int, [_c_void_p, _c_void_p, _c_void_p, _i64, _c_void_p, _c_void_p, _size,
                                               _c_void_p]),
@@ -115,6 +157,17 @@ EXPORTS = (
     "itl_lmhead_logprob_fp8",
     "itl_quantize_rows_mxfp4",
     "itl_lmhead_logprob_mxfp4",
+    "itl_residual_norm",
+    "itl_residual_norm_fp8",
+    "itl_residual_norm_backward_workspace_bytes",
+    "itl_residual_norm_backward",
+    "itl_cross_entropy_workspace_bytes",
+    "itl_cross_entropy",
+    "itl_cross_entropy_grad",
+    "itl_adamw_plan_sizes",
+    "itl_adamw_plan",
+    "itl_adamw_step_workspace_bytes",
+    "itl_adamw_step",
     "itl_mismatch_stats_workspace_bytes",
     "itl_mismatch_stats",
     "itl_check_inputs",
@@ -453,6 +506,319 @@ def lmhead_logprob_mxfp4(Hq, h_scale, Wq4, w_scale_codes, tokens, *, logprob=Non
                                         _ptr(tokens), _ptr(logprob), _ptr(lse), _ptr(workspace), workspace.numel(),
                                         _stream(dev)))
     return logprob, lse
+
+
+def _new(shape, dtype, like, name, given):
+    """`given`, checked, or a new tensor of that shape and dtype on like's device."""
+    if given is None:
+        return torch.empty(shape, dtype=dtype, device=like.device)
+    _need(given, name, (dtype,), device=like.device, ndim=len(shape))
+    if tuple(given.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(given.shape)}")
+    return given
+
+
+def _workspace(given, need, device):
+    if given is None:  # (sizes the library refuses have no workspace: it says why)
+        return torch.empty(max(need, 1) if need < 1 << 62 else 1, dtype=torch.uint8, device=device)
+    _need(given, "workspace", (torch.uint8,), device=device)
+    return given
+
+
+class _On:
+    """Makes `device` the current one for a launch where it is not."""
+
+    __slots__ = ("device", "before")
+
+    def __init__(self, device):
+        self.device = device
+
+    def __enter__(self):
+        self.before = torch.cuda.current_device()
+        if self.before != self.device.index:
+            torch.cuda.set_device(self.device)
+
+    def __exit__(self, *exc):
+        if self.before != self.device.index:
+            torch.cuda.set_device(self.before)
+
+
+def _norm_operands(x, y, w_pre, w_post, gate, first):
+    """Checks what the norms' forward and backward share; (rows, d, gate stride)."""
+    _need(x, first, tuple(_HEAD_DTYPES), ndim=2)
+    n, d = x.shape
+    if d == 0:
+        raise ValueError(f"{first} must have at least one column")
+    if y is not None:
+        _need(y, "y", (x.dtype,), device=x.device, ndim=2)
+        if y.shape != x.shape:
+            raise ValueError(f"y must have {first}'s shape {tuple(x.shape)}, got {tuple(y.shape)}")
+    elif w_post is not None or gate is not None:
+        raise ValueError("w_post and gate need y")
+    for name, w in (("w_pre", w_pre), ("w_post", w_post)):
+        if w is None and name == "w_post":
+            continue
+        _need(w, name, (x.dtype,), device=x.device, ndim=1)
+        if w.shape[0] != d:
+            raise ValueError(f"{name} must have {d} elements")
+    if gate is None:
+        return n, d, 0
+    _need(gate, "gate", (x.dtype,), device=x.device)
+    if tuple(gate.shape) not in ((d,), (n, d)):
+        raise ValueError(f"gate must have shape ({d},) or ({n}, {d}), got {tuple(gate.shape)}")
+    return n, d, 0 if gate.dim() == 1 else d
+
+
+def residual_norm(x, y, w_pre, *, w_post=None, gate=None, scale=1.0, eps=1e-6, h=None, u=None):
+    """h = x + scale * gate * p and u = rmsnorm(h) * w_pre, where p = y, or
+    rmsnorm(y) * w_post with w_post given.
+
+    x, y [n, d] (bf16 or fp32; y None: h is x), w_pre, w_post [d], gate [d] or
+    [n, d], all of one dtype. Returns (h, u, rstd_pre fp32 [n], rstd_post fp32
+    [n] or None).
+    """
+    n, d, stride = _norm_operands(x, y, w_pre, w_post, gate, "x")
+    h = x if y is None else _new((n, d), x.dtype, x, "h", h)
+    u = _new((n, d), x.dtype, x, "u", u)
+    rstd_pre = torch.empty(n, dtype=torch.float32, device=x.device)
+    rstd_post = None if w_post is None else torch.empty(n, dtype=torch.float32, device=x.device)
+    with _On(x.device):
+        _check(lib.itl_residual_norm(_ptr(x), _ptr(y), _ptr(gate), stride, _ptr(w_post), _ptr(w_pre),
+                                     _HEAD_DTYPES[x.dtype], n, d, scale, eps, _ptr(h), _ptr(u), _ptr(rstd_pre),
+                                     _ptr(rstd_post), _stream(x.device)))
+    return h, u, rstd_pre, rstd_post
+
+
+def residual_norm_fp8(x, y, w_pre, *, w_post=None, gate=None, scale=1.0, eps=1e-6, h=None, Uq=None, u_scale=None):
+    """residual_norm with u as E4M3 codes (uint8 [n, d]) and a scale per row
+    (fp32 [n]), as lmhead_logprob_fp8 takes them; d a multiple of 128. Returns
+    (h, Uq, u_scale, rstd_pre, rstd_post)."""
+    n, d, stride = _norm_operands(x, y, w_pre, w_post, gate, "x")
+    h = x if y is None else _new((n, d), x.dtype, x, "h", h)
+    Uq = _new((n, d), torch.uint8, x, "Uq", Uq)
+    u_scale = _new((n,), torch.float32, x, "u_scale", u_scale)
+    rstd_pre = torch.empty(n, dtype=torch.float32, device=x.device)
+    rstd_post = None if w_post is None else torch.empty(n, dtype=torch.float32, device=x.device)
+    with _On(x.device):
+        _check(lib.itl_residual_norm_fp8(_ptr(x), _ptr(y), _ptr(gate), stride, _ptr(w_post), _ptr(w_pre),
+                                         _HEAD_DTYPES[x.dtype], n, d, scale, eps, _ptr(h), _ptr(Uq), _ptr(u_scale),
+                                         _ptr(rstd_pre), _ptr(rstd_post), _stream(x.device)))
+    return h, Uq, u_scale, rstd_pre, rstd_post
+
+
+def residual_norm_backward_workspace_bytes(n_rows, d):
+    return int(lib.itl_residual_norm_backward_workspace_bytes(n_rows, d))
+
+
+def residual_norm_backward(du, dh, h, y, w_pre, rstd_pre, *, w_post=None, rstd_post=None, gate=None, scale=1.0,
+                           dx=None, dy=None, workspace=None):
+    """Gradients of residual_norm: du [n, d] (h's dtype or fp32) and dh [n, d]
+    (h's dtype, or None) are those of u and h. Returns (dx, dy, dw_pre fp32
+    [d], dw_post fp32 [d], dgate: fp32 [d] for a shared gate, else like gate);
+    dy, dw_post, dgate are None where y, w_post, gate are. dx is the gradient
+    of the residual stream x (all of h's)."""
+    n, d, stride = _norm_operands(h, y, w_pre, w_post, gate, "h")
+    dev = h.device
+    _need(du, "du", (h.dtype, torch.float32), device=dev, ndim=2)
+    if dh is not None:
+        _need(dh, "dh", (h.dtype,), device=dev, ndim=2)
+    for name, t in (("du", du), ("dh", dh)):
+        if t is not None and t.shape != h.shape:
+            raise ValueError(f"{name} must have shape {tuple(h.shape)}, got {tuple(t.shape)}")
+    if w_post is not None and rstd_post is None:
+        raise ValueError("w_post needs rstd_post")
+    for name, t in (("rstd_pre", rstd_pre), ("rstd_post", rstd_post if w_post is not None else rstd_pre)):
+        _need(t, name, (torch.float32,), device=dev, ndim=1)
+        if t.shape[0] != n:
+            raise ValueError(f"{name} must have {n} elements")
+    dx = _new((n, d), h.dtype, h, "dx", dx)
+    dy = None if y is None else _new((n, d), h.dtype, h, "dy", dy)
+    dw_pre = torch.empty(d, dtype=torch.float32, device=dev)
+    dw_post = None if w_post is None else torch.empty(d, dtype=torch.float32, device=dev)
+    dgate = None
+    if gate is not None:
+        dgate = torch.empty(d, dtype=torch.float32, device=dev) if stride == 0 else torch.empty_like(gate)
+    workspace = _workspace(workspace, residual_norm_backward_workspace_bytes(n, d), dev)
+    with _On(dev):
+        _check(lib.itl_residual_norm_backward(_ptr(du), _HEAD_DTYPES[du.dtype], _ptr(dh), _ptr(h), _ptr(y), _ptr(gate),
+                                              stride, _ptr(w_post), _ptr(w_pre), _ptr(rstd_pre),
+                                              _ptr(rstd_post if w_post is not None else None), _HEAD_DTYPES[h.dtype],
+                                              n, d, scale, _ptr(dx), _ptr(dy), _ptr(dgate), _ptr(dw_pre),
+                                              _ptr(dw_post), _ptr(workspace), workspace.numel(), _stream(dev)))
+    return dx, dy, dw_pre, dw_post, dgate
+
+
+_REDUCTIONS = {"sum": 0, "mean": 1}
+
+
+def cross_entropy_workspace_bytes(n_tok, d, vocab, dtype=torch.bfloat16, grad_dtype=None):
+    """Workspace of cross_entropy (grad_dtype None) or cross_entropy_grad."""
+    grad = grad_dtype is not None
+    return int(lib.itl_cross_entropy_workspace_bytes(n_tok, d, vocab, _HEAD_DTYPES[dtype], int(grad),
+                                                     _HEAD_DTYPES[grad_dtype if grad else dtype]))
+
+
+def _cross_entropy_operands(H, W, targets, reduction):
+    _need(H, "H", tuple(_HEAD_DTYPES), ndim=2)
+    _need(W, "W", (H.dtype,), device=H.device, ndim=2)
+    _need(targets, "targets", (torch.int32,), device=H.device, ndim=1)
+    if W.shape[1] != H.shape[1] or targets.shape[0] != H.shape[0]:
+        raise ValueError(f"shape mismatch: H {tuple(H.shape)}, W {tuple(W.shape)}, targets {tuple(targets.shape)}")
+    if reduction not in _REDUCTIONS:
+        raise ValueError(f"reduction must be one of {tuple(_REDUCTIONS)}, got {reduction!r}")
+    return H.shape[0], H.shape[1], W.shape[0]
+
+
+def _loss_outputs(H, n):
+    f = dict(dtype=torch.float32, device=H.device)
+    return torch.empty(1, **f), torch.empty(n, **f), torch.empty(n, **f)
+
+
+def cross_entropy(H, W, targets, *, label_smoothing=0.0, z_weight=0.0, reduction="mean", workspace=None):
+    """Cross entropy of the head's softmax over the tokens that count.
+
+    H [n, d], W [vocab, d] (bf16 or fp32), targets int32 [n]; a target outside
+    [0, vocab), such as -100, does not count. Returns (loss fp32 [1],
+    token_loss fp32 [n], lse fp32 [n]).
+    """
+    n, d, vocab = _cross_entropy_operands(H, W, targets, reduction)
+    loss, token_loss, lse = _loss_outputs(H, n)
+    workspace = _workspace(workspace, cross_entropy_workspace_bytes(n, d, vocab, H.dtype), H.device)
+    with _On(H.device):
+        _check(lib.itl_cross_entropy(_ptr(H), _ptr(W), _HEAD_DTYPES[H.dtype], n, d, vocab, _ptr(targets),
+                                     label_smoothing, z_weight, _REDUCTIONS[reduction], _ptr(loss), _ptr(token_loss),
+                                     _ptr(lse), _ptr(workspace), workspace.numel(), _stream(H.device)))
+    return loss, token_loss, lse
+
+
+def cross_entropy_grad(H, W, targets, *, label_smoothing=0.0, z_weight=0.0, reduction="mean", grad_scale=1.0,
+                       grad_dtype=torch.float32, dH=None, dW=None, workspace=None):
+    """cross_entropy and the gradient of grad_scale * loss in one call.
+    Returns (loss, token_loss, lse, dH [n, d], dW [vocab, d]); the gradients
+    are of grad_dtype (fp32 or H's)."""
+    n, d, vocab = _cross_entropy_operands(H, W, targets, reduction)
+    if grad_dtype not in (H.dtype, torch.float32):
+        raise ValueError(f"grad_dtype must be {H.dtype} or torch.float32, got {grad_dtype}")
+    loss, token_loss, lse = _loss_outputs(H, n)
+    dH = _new((n, d), grad_dtype, H, "dH", dH)
+    dW = _new((vocab, d), grad_dtype, H, "dW", dW)
+    workspace = _workspace(workspace, cross_entropy_workspace_bytes(n, d, vocab, H.dtype, grad_dtype), H.device)
+    with _On(H.device):
+        _check(lib.itl_cross_entropy_grad(_ptr(H), _ptr(W), _HEAD_DTYPES[H.dtype], n, d, vocab, _ptr(targets),
+                                          label_smoothing, z_weight, _REDUCTIONS[reduction], grad_scale,
+                                          _HEAD_DTYPES[grad_dtype], _ptr(loss), _ptr(token_loss), _ptr(lse), _ptr(dH),
+                                          _ptr(dW), _ptr(workspace), workspace.numel(), _stream(H.device)))
+    return loss, token_loss, lse, dH, dW
+
+
+class AdamWPlan:
+    """Weights, gradients and AdamW states of one optimizer, laid out for
+    adamw_step (made by adamw_plan).
+
+    The states are flat: tensor i's begin at offsets[i] (multiples of 256).
+    exp_avg, exp_avg_sq: fp32, or uint8 E4M3 codes of m and sqrt(v) with
+    exp_avg_scale, exp_avg_sq_scale (fp32, one per 256). master: fp32 weights
+    of the bf16 tensors, or None. step (int64 [1]) and lr (fp32 [1]) are device
+    tensors: a captured step sees what they hold when it is replayed.
+    """
+
+    __slots__ = ("params", "grads", "offsets", "state_bits", "exp_avg", "exp_avg_sq", "exp_avg_scale",
+                 "exp_avg_sq_scale", "master", "lr", "step", "device", "_table", "_workspace", "_args")
+
+
+def adamw_plan(params, grads, *, lr, weight_decay=0.0, state_bits=32, step=None, master=None, exp_avg=None,
+               exp_avg_sq=None, exp_avg_scale=None, exp_avg_sq_scale=None):
+    """Lay out an AdamW step over many tensors (any mix of bf16 and fp32).
+
+    params and grads: lists of contiguous tensors of equal sizes, kept by the
+    plan and used where they lie: the gradients of every step are written into
+    them. lr: a float or a device tensor fp32 [1]; weight_decay: a float or one
+    per tensor. States start as zeros (step 0) unless given, as from a
+    checkpoint; master: fp32 flat weights, True (from the params; the default
+    where any is bf16) or False for none.
+    """
+    params, grads = list(params), list(grads)
+    if not params or len(params) != len(grads):
+        raise ValueError(f"params and grads must be equally many and at least one, got {len(params)} and {len(grads)}")
+    decays = list(weight_decay) if isinstance(weight_decay, (list, tuple)) else [weight_decay] * len(params)
+    if len(decays) != len(params):
+        raise ValueError(f"weight_decay must be a number or {len(params)} of them")
+    if state_bits not in (8, 32):
+        raise ValueError(f"state_bits must be 8 or 32, got {state_bits}")
+    table = (_AdamWTensor * len(params))()
+    dev, offsets, total = None, [], 0
+    for i, (p, g, wd) in enumerate(zip(params, grads, decays)):
+        _need(p, f"params[{i}]", tuple(_HEAD_DTYPES), device=dev)
+        dev = p.device
+        _need(g, f"grads[{i}]", tuple(_HEAD_DTYPES), device=dev)
+        if p.numel() != g.numel():
+            raise ValueError(f"grads[{i}] has {g.numel()} elements, params[{i}] {p.numel()}")
+        table[i] = _AdamWTensor(p.data_ptr(), g.data_ptr(), p.numel(), _HEAD_DTYPES[p.dtype], _HEAD_DTYPES[g.dtype], wd)
+        offsets.append(total)
+        total += -(-p.numel() // 256) * 256
+    nbytes, elements = _i64(), _i64()
+    _check(lib.itl_adamw_plan_sizes(table, len(params), ctypes.byref(nbytes), ctypes.byref(elements)))
+    host = torch.empty(max(nbytes.value, 1), dtype=torch.uint8)
+    _check(lib.itl_adamw_plan(table, len(params), _ptr(host), nbytes.value))
+
+    plan = AdamWPlan()
+    plan.params, plan.grads, plan.offsets, plan.state_bits, plan.device = params, grads, offsets, state_bits, dev
+
+    def state(name, given, dtype, n):
+        if given is None:
+            return torch.zeros(n, dtype=dtype, device=dev)
+        _need(given, name, (dtype,), device=dev, ndim=1)
+        if given.shape[0] != n:
+            raise ValueError(f"{name} must have {n} elements, got {given.shape[0]}")
+        return given
+
+    code = torch.float32 if state_bits == 32 else torch.uint8
+    plan.exp_avg = state("exp_avg", exp_avg, code, total)
+    plan.exp_avg_sq = state("exp_avg_sq", exp_avg_sq, code, total)
+    if state_bits == 8:
+        plan.exp_avg_scale = state("exp_avg_scale", exp_avg_scale, torch.float32, total // 256)
+        plan.exp_avg_sq_scale = state("exp_avg_sq_scale", exp_avg_sq_scale, torch.float32, total // 256)
+    elif exp_avg_scale is not None or exp_avg_sq_scale is not None:
+        raise ValueError("scales belong to 8-bit states")
+    else:
+        plan.exp_avg_scale = plan.exp_avg_sq_scale = None
+    if master is None:
+        master = any(p.dtype == torch.bfloat16 for p in params)
+    if master is True:
+        plan.master = torch.zeros(total, dtype=torch.float32, device=dev)
+        for p, o in zip(params, offsets):
+            if p.dtype == torch.bfloat16:
+                plan.master[o:o + p.numel()].copy_(p.detach().reshape(-1))
+    else:
+        plan.master = None if master is False else state("master", master, torch.float32, total)
+    plan.step = state("step", step, torch.int64, 1)
+    plan.lr = torch.full((1,), float(lr), device=dev) if not isinstance(lr, torch.Tensor) else state("lr", lr, torch.float32, 1)
+    plan._table = host[:nbytes.value].to(dev)
+    plan._workspace = torch.empty(int(lib.itl_adamw_step_workspace_bytes()), dtype=torch.uint8, device=dev)
+    plan._args = (_ptr(plan._table), nbytes.value, state_bits, _ptr(plan.exp_avg), _ptr(plan.exp_avg_sq),
+                  _ptr(plan.exp_avg_scale), _ptr(plan.exp_avg_sq_scale), _ptr(plan.master), _ptr(plan.lr),
+                  _ptr(plan.step))
+    return plan
+
+
+def adamw_step(plan, *, betas=(0.9, 0.999), eps=1e-8, max_norm=None, grad_norm=None):
+    """One AdamW step over a plan's tensors, in place. max_norm clips the
+    gradients' norm over all tensors; the norm (fp32 [1]) is returned where it
+    is computed (max_norm or grad_norm, a tensor for it, given), else None. A
+    norm that is not finite skips the step."""
+    if not isinstance(plan, AdamWPlan):
+        raise TypeError("plan must come from adamw_plan")
+    if grad_norm is not None:
+        _need(grad_norm, "grad_norm", (torch.float32,), device=plan.device, ndim=1)
+        if grad_norm.shape[0] != 1:
+            raise ValueError("grad_norm must have 1 element")
+    elif max_norm is not None:
+        grad_norm = torch.empty(1, dtype=torch.float32, device=plan.device)
+    with _On(plan.device):
+        _check(lib.itl_adamw_step(*plan._args, betas[0], betas[1], eps, float("inf") if max_norm is None else max_norm,
+                                  _ptr(grad_norm), _ptr(plan._workspace), plan._workspace.numel(),
+                                  _stream(plan.device)))
+    return grad_norm
 
 
 # Field order of itl_mismatch_stats' output (the itl_stat enum of include/itl.h).

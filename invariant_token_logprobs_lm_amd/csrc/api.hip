@@ -7,9 +7,15 @@
 #include <stdio.h>
 #include <string.h>
 
+#include <algorithm>
+#include <initializer_list>
 #include <mutex>
+#include <new>
 #include <string>
+#include <utility>
+#include <vector>
 
+#include "adamw_plan.h"
 #include "itl.h"
 #include "itl_config.h"
 #include "itl_launch.h"
@@ -357,6 +363,268 @@ itl_status itl_lmhead_logprob_mxfp4(const uint8_t* Hq, const float* h_scale, con
   hipError_t e = itl::launch_lmhead_logprob_mxfp4(Hq, h_scale, Wq4, w_scale_codes, (int)n_tok, (int)d, (int)vocab,
                                                   tokens, logprob, lse, workspace, static_cast<hipStream_t>(stream));
   return e == hipSuccess ? ITL_OK : hip_fail(e, "itl_lmhead_logprob_mxfp4");
+}
+
+namespace {
+
+constexpr int64_t kMaxNormWidth = 1 << 24;
+
+bool known_dtype(itl_dtype dt) { return dt == ITL_BF16 || dt == ITL_F32; }
+
+// Rows the norms move in 16-byte pieces (widths of a multiple of 8) have to
+// start at one; other widths are read value by value.
+bool rows_misaligned(std::initializer_list<const void*> ps, int64_t d, itl_dtype dtype) {
+  const uintptr_t mask = d % 8 == 0 ? 15 : (uintptr_t)elem_size(dtype) - 1;
+  uintptr_t all = 0;
+  for (const void* p : ps) all |= reinterpret_cast<uintptr_t>(p);
+  return (all & mask) != 0;
+}
+
+itl_status check_norm(itl_dtype dtype, int64_t n_rows, int64_t d, int64_t gate_stride, const void* gate, const void* y,
+                      const void* w_post, float scale, float eps) {
+  if (n_rows < 0 || d <= 0) return fail(ITL_ERR_INVALID_ARG, "n_rows must be >= 0 and d > 0");
+  if (!known_dtype(dtype)) return fail(ITL_ERR_UNSUPPORTED, "dtype must be ITL_BF16 or ITL_F32");
+  if (n_rows > INT32_MAX || d > kMaxNormWidth) return fail(ITL_ERR_UNSUPPORTED, "too many rows or columns");
+  if (!(eps > 0.0f) || !(eps < 1.0f)) return fail(ITL_ERR_INVALID_ARG, "eps must be in (0, 1)");
+  if (!(scale - scale == 0.0f)) return fail(ITL_ERR_INVALID_ARG, "scale must be finite");
+  if (gate && gate_stride != 0 && gate_stride != d) return fail(ITL_ERR_INVALID_ARG, "gate_stride must be 0 or d");
+  if (n_rows > 0 && !y && (gate || w_post)) return fail(ITL_ERR_INVALID_ARG, "gate and w_post need y");
+  return ITL_OK;
+}
+
+itl_status residual_norm(const void* x, const void* y, const void* gate, int64_t gate_stride, const void* w_post,
+                         const void* w_pre, itl_dtype dtype, int64_t n_rows, int64_t d, float scale, float eps, void* h,
+                         void* u, uint8_t* codes, float* u_scale, bool fp8, float* rstd_pre, float* rstd_post,
+                         void* stream, const char* name) {
+  itl_status st = check_norm(dtype, n_rows, d, gate_stride, gate, y, w_post, scale, eps);
+  if (st != ITL_OK) return st;
+  if (fp8 && d % kFp8DMultiple != 0) return fail(ITL_ERR_UNSUPPORTED, "d must be a multiple of 128");
+  if (n_rows == 0) return ITL_OK;
+  if (!x || !w_pre || (y && !h) || (fp8 ? !codes || !u_scale : !u))
+    return fail(ITL_ERR_INVALID_ARG, "null x, w_pre, h (with y) or output");
+  if (rows_misaligned({x, y, gate, w_post, w_pre, y ? h : nullptr, u}, d, dtype))
+    return fail(ITL_ERR_INVALID_ARG, "arrays must be 16-byte aligned where d is a multiple of 8, else by element");
+  if (fp8 && (reinterpret_cast<uintptr_t>(codes) & 7) != 0) return fail(ITL_ERR_INVALID_ARG, "Uq must be 8-byte aligned");
+  hipError_t e = itl::launch_residual_norm(x, y, gate, gate_stride, w_post, w_pre, (int)dtype, n_rows, (int)d, scale, eps,
+                                           h, u, codes, u_scale, rstd_pre, rstd_post, static_cast<hipStream_t>(stream));
+  return e == hipSuccess ? ITL_OK : hip_fail(e, name);
+}
+
+}  // namespace
+
+itl_status itl_residual_norm(const void* x, const void* y, const void* gate, int64_t gate_stride, const void* w_post,
+                             const void* w_pre, itl_dtype dtype, int64_t n_rows, int64_t d, float scale, float eps,
+                             void* h, void* u, float* rstd_pre, float* rstd_post, void* stream) {
+  g_last_error.clear();
+  return residual_norm(x, y, gate, gate_stride, w_post, w_pre, dtype, n_rows, d, scale, eps, h, u, nullptr, nullptr, false,
+                       rstd_pre, rstd_post, stream, "itl_residual_norm");
+}
+
+itl_status itl_residual_norm_fp8(const void* x, const void* y, const void* gate, int64_t gate_stride, const void* w_post,
+                                 const void* w_pre, itl_dtype dtype, int64_t n_rows, int64_t d, float scale, float eps,
+                                 void* h, uint8_t* Uq, float* u_scale, float* rstd_pre, float* rstd_post, void* stream) {
+  g_last_error.clear();
+  return residual_norm(x, y, gate, gate_stride, w_post, w_pre, dtype, n_rows, d, scale, eps, h, nullptr, Uq, u_scale, true,
+                       rstd_pre, rstd_post, stream, "itl_residual_norm_fp8");
+}
+
+size_t itl_residual_norm_backward_workspace_bytes(int64_t n_rows, int64_t d) {
+  if (n_rows < 0 || d <= 0 || n_rows > INT32_MAX || d > kMaxNormWidth) return SIZE_MAX;
+  return itl::norm_backward_workspace_bytes(n_rows, d);
+}
+
+itl_status itl_residual_norm_backward(const void* du, itl_dtype du_dtype, const void* dh, const void* h, const void* y,
+                                      const void* gate, int64_t gate_stride, const void* w_post, const void* w_pre,
+                                      const float* rstd_pre, const float* rstd_post, itl_dtype dtype, int64_t n_rows,
+                                      int64_t d, float scale, void* dx, void* dy, void* dgate, float* dw_pre,
+                                      float* dw_post, void* workspace, size_t workspace_bytes, void* stream) {
+  g_last_error.clear();
+  itl_status st = check_norm(dtype, n_rows, d, gate_stride, gate, y, w_post, scale, 0.5f);
+  if (st != ITL_OK) return st;
+  if (du_dtype != dtype && du_dtype != ITL_F32) return fail(ITL_ERR_UNSUPPORTED, "du_dtype must be dtype or ITL_F32");
+  if (!w_pre || !dw_pre || (gate && !dgate) || (w_post && !dw_post))
+    return fail(ITL_ERR_INVALID_ARG, "null w_pre, dw_pre, dgate (with gate) or dw_post (with w_post)");
+  if (n_rows > 0 && (!du || !h || !dx || !rstd_pre || (y && !dy) || (w_post && !rstd_post)))
+    return fail(ITL_ERR_INVALID_ARG, "null du, h, dx, rstd_pre, dy (with y) or rstd_post (with w_post)");
+  if (n_rows > 0 && (rows_misaligned({dh, h, y, gate, w_post, w_pre, dx, y ? dy : nullptr,
+                                      gate && gate_stride ? dgate : nullptr}, d, dtype) ||
+                     rows_misaligned({du}, d, du_dtype)))
+    return fail(ITL_ERR_INVALID_ARG, "arrays must be 16-byte aligned where d is a multiple of 8, else by element");
+  if (!workspace || workspace_bytes < itl::norm_backward_workspace_bytes(n_rows, d))
+    return fail(ITL_ERR_WORKSPACE, "workspace missing or smaller than itl_residual_norm_backward_workspace_bytes()");
+  if (misaligned(workspace)) return fail(ITL_ERR_WORKSPACE, "workspace must be 256-byte aligned");
+  hipError_t e = itl::launch_residual_norm_backward(du, (int)du_dtype, dh, h, y, gate, gate_stride, w_post, w_pre,
+                                                    rstd_pre, rstd_post, (int)dtype, n_rows, (int)d, scale, dx, dy, dgate,
+                                                    dw_pre, dw_post, workspace, static_cast<hipStream_t>(stream));
+  return e == hipSuccess ? ITL_OK : hip_fail(e, "itl_residual_norm_backward");
+}
+
+namespace {
+
+itl_status cross_entropy(const itl::CeCall& c, bool grad, size_t workspace_bytes, void* stream, const char* name) {
+  itl_status st = check_head(c.dtype, c.n_tok, c.d, c.vocab);
+  if (st != ITL_OK) return st;
+  if (!(c.smoothing >= 0.0f && c.smoothing < 1.0f)) return fail(ITL_ERR_INVALID_ARG, "label_smoothing must be in [0, 1)");
+  if (!(c.z_weight >= 0.0f && c.z_weight - c.z_weight == 0.0f))
+    return fail(ITL_ERR_INVALID_ARG, "z_weight must be finite and >= 0");
+  if (c.mean != 0 && c.mean != 1) return fail(ITL_ERR_INVALID_ARG, "reduction must be ITL_SUM or ITL_MEAN");
+  if (grad && !(c.grad_scale - c.grad_scale == 0.0f)) return fail(ITL_ERR_INVALID_ARG, "grad_scale must be finite");
+  if (grad && c.grad_dtype != c.dtype && c.grad_dtype != ITL_F32)
+    return fail(ITL_ERR_UNSUPPORTED, "grad_dtype must be dtype or ITL_F32");
+  if (grad && c.vocab > itl::kBwdMaxVocab) return fail(ITL_ERR_UNSUPPORTED, "vocab too large for the gradient");
+  if (!c.W || !c.loss || (grad && !c.dW)) return fail(ITL_ERR_INVALID_ARG, "null W, loss or dW");
+  if (c.n_tok > 0 && (!c.H || !c.targets || !c.token_loss || (grad && !c.dH)))
+    return fail(ITL_ERR_INVALID_ARG, "null H, targets, token_loss or dH");
+  if (misaligned16(c.H, c.W) || misaligned16(c.dH, c.dW))
+    return fail(ITL_ERR_INVALID_ARG, "H, W, dH and dW must be 16-byte aligned");
+  const size_t need = itl::cross_entropy_workspace_bytes(c.n_tok, c.d, c.vocab, c.dtype, grad, c.grad_dtype);
+  if (need > 0 && (!c.workspace || workspace_bytes < need))
+    return fail(ITL_ERR_WORKSPACE, "workspace missing or smaller than itl_cross_entropy_workspace_bytes()");
+  if (need > 0 && misaligned(c.workspace)) return fail(ITL_ERR_WORKSPACE, "workspace must be 256-byte aligned");
+  hipError_t e = itl::launch_cross_entropy(c, static_cast<hipStream_t>(stream));
+  return e == hipSuccess ? ITL_OK : hip_fail(e, name);
+}
+
+}  // namespace
+
+size_t itl_cross_entropy_workspace_bytes(int64_t n_tok, int64_t d, int64_t vocab, itl_dtype dtype, int32_t with_grad,
+                                         itl_dtype grad_dtype) {
+  if (n_tok < 0 || d <= 0 || vocab <= 0 || n_tok > kMaxTok || vocab > kMaxVocab || !known_dtype(dtype)) return SIZE_MAX;
+  if (d % itl::kDMultiple != 0 || d >= ((int64_t)1 << 31) / (elem_size(dtype) * (int64_t)itl::kBT)) return SIZE_MAX;
+  if (with_grad && (vocab > itl::kBwdMaxVocab || (grad_dtype != dtype && grad_dtype != ITL_F32))) return SIZE_MAX;
+  return itl::cross_entropy_workspace_bytes(n_tok, d, vocab, (int)dtype, with_grad != 0, (int)grad_dtype);
+}
+
+itl_status itl_cross_entropy(const void* H, const void* W, itl_dtype dtype, int64_t n_tok, int64_t d, int64_t vocab,
+                             const int32_t* targets, float label_smoothing, float z_weight, int32_t reduction, float* loss,
+                             float* token_loss, float* lse, void* workspace, size_t workspace_bytes, void* stream) {
+  g_last_error.clear();
+  const itl::CeCall c{H, W, (int)dtype, n_tok, d, vocab, targets, label_smoothing, z_weight, reduction, 0.0f, (int)dtype,
+                      loss, token_loss, lse, nullptr, nullptr, workspace};
+  return cross_entropy(c, false, workspace_bytes, stream, "itl_cross_entropy");
+}
+
+itl_status itl_cross_entropy_grad(const void* H, const void* W, itl_dtype dtype, int64_t n_tok, int64_t d, int64_t vocab,
+                                  const int32_t* targets, float label_smoothing, float z_weight, int32_t reduction,
+                                  float grad_scale, itl_dtype grad_dtype, float* loss, float* token_loss, float* lse,
+                                  void* dH, void* dW, void* workspace, size_t workspace_bytes, void* stream) {
+  g_last_error.clear();
+  const itl::CeCall c{H, W, (int)dtype, n_tok, d, vocab, targets, label_smoothing, z_weight, reduction, grad_scale,
+                      (int)grad_dtype, loss, token_loss, lse, dH, dW, workspace};
+  return cross_entropy(c, true, workspace_bytes, stream, "itl_cross_entropy_grad");
+}
+
+namespace {
+
+// Checks the tensors and counts the plan's pieces and the flat states' elements.
+itl_status adamw_layout(const itl_adamw_tensor* tensors, int32_t n_tensors, int64_t* n_pieces, int64_t* n_state) {
+  if (n_tensors < 0 || (n_tensors > 0 && !tensors)) return fail(ITL_ERR_INVALID_ARG, "null tensors or n_tensors < 0");
+  int64_t pieces = 0, state = 0;
+  for (int32_t i = 0; i < n_tensors; ++i) {
+    const itl_adamw_tensor& t = tensors[i];
+    if (t.n < 0 || t.n > ((int64_t)1 << 40)) return fail(ITL_ERR_INVALID_ARG, "a tensor's n must be in [0, 2^40]");
+    if (!known_dtype(t.param_dtype) || !known_dtype(t.grad_dtype))
+      return fail(ITL_ERR_UNSUPPORTED, "param_dtype and grad_dtype must be ITL_BF16 or ITL_F32");
+    if (t.n > 0 && (!t.param || !t.grad)) return fail(ITL_ERR_INVALID_ARG, "null param or grad");
+    if (!(t.weight_decay >= 0.0f && t.weight_decay - t.weight_decay == 0.0f))
+      return fail(ITL_ERR_INVALID_ARG, "weight_decay must be finite and >= 0");
+    if ((reinterpret_cast<uintptr_t>(t.param) & (elem_size(t.param_dtype) - 1)) != 0 ||
+        (reinterpret_cast<uintptr_t>(t.grad) & (elem_size(t.grad_dtype) - 1)) != 0)
+      return fail(ITL_ERR_INVALID_ARG, "param and grad must be aligned to their elements");
+    pieces += itl::ceil_div(t.n, itl::kAdamPiece);
+    state += itl::ceil_div(t.n, itl::kAdamBlock) * itl::kAdamBlock;
+    if (pieces > INT32_MAX) return fail(ITL_ERR_UNSUPPORTED, "too many elements for one plan");
+  }
+  *n_pieces = pieces;
+  *n_state = state;
+  return ITL_OK;
+}
+
+}  // namespace
+
+itl_status itl_adamw_plan_sizes(const itl_adamw_tensor* tensors, int32_t n_tensors, int64_t* plan_bytes,
+                                int64_t* state_elements) {
+  g_last_error.clear();
+  if (!plan_bytes || !state_elements) return fail(ITL_ERR_INVALID_ARG, "null plan_bytes or state_elements");
+  int64_t pieces = 0;
+  itl_status st = adamw_layout(tensors, n_tensors, &pieces, state_elements);
+  if (st == ITL_OK) *plan_bytes = pieces * (int64_t)sizeof(itl::AdamPiece);
+  return st;
+}
+
+itl_status itl_adamw_plan(const itl_adamw_tensor* tensors, int32_t n_tensors, void* host_plan, size_t host_plan_bytes) {
+  g_last_error.clear();
+  int64_t pieces = 0, state = 0;
+  itl_status st = adamw_layout(tensors, n_tensors, &pieces, &state);
+  if (st != ITL_OK) return st;
+  if (pieces == 0) return ITL_OK;
+  if (!host_plan || host_plan_bytes < (size_t)pieces * sizeof(itl::AdamPiece))
+    return fail(ITL_ERR_WORKSPACE, "host_plan missing or smaller than itl_adamw_plan_sizes() says");
+  // two entries that share weights would be written by two workgroups at once
+  try {
+    std::vector<std::pair<uintptr_t, uintptr_t>> spans;
+    for (int32_t i = 0; i < n_tensors; ++i)
+      if (tensors[i].n > 0) {
+        const uintptr_t at = reinterpret_cast<uintptr_t>(tensors[i].param);
+        spans.emplace_back(at, at + (uintptr_t)tensors[i].n * elem_size(tensors[i].param_dtype));
+      }
+    std::sort(spans.begin(), spans.end());
+    for (size_t i = 1; i < spans.size(); ++i)
+      if (spans[i].first < spans[i - 1].second) return fail(ITL_ERR_INVALID_ARG, "two tensors share weights");
+  } catch (const std::bad_alloc&) {
+    return fail(ITL_ERR_INVALID_ARG, "out of host memory");
+  }
+  char* out = static_cast<char*>(host_plan);
+  int64_t at = 0;
+  for (int32_t i = 0; i < n_tensors; ++i) {
+    const itl_adamw_tensor& t = tensors[i];
+    const int ep = elem_size(t.param_dtype), eg = elem_size(t.grad_dtype);
+    const bool vec = !misaligned16(t.param, t.grad);
+    for (int64_t o = 0; o < t.n; o += itl::kAdamPiece) {
+      itl::AdamPiece p{};
+      p.param = static_cast<char*>(t.param) + o * ep;
+      p.grad = static_cast<const char*>(t.grad) + o * eg;
+      p.state = at + o;
+      p.count = (int32_t)std::min<int64_t>(itl::kAdamPiece, t.n - o);
+      p.flags = (t.param_dtype == ITL_F32 ? itl::kAdamParamF32 : 0) | (t.grad_dtype == ITL_F32 ? itl::kAdamGradF32 : 0) |
+                (vec ? itl::kAdamVectors : 0);
+      p.weight_decay = t.weight_decay;
+      memcpy(out, &p, sizeof p);
+      out += sizeof p;
+    }
+    at += itl::ceil_div(t.n, itl::kAdamBlock) * itl::kAdamBlock;
+  }
+  return ITL_OK;
+}
+
+size_t itl_adamw_step_workspace_bytes(void) { return itl::adamw_workspace_bytes(); }
+
+itl_status itl_adamw_step(const void* plan, size_t plan_bytes, int32_t state_bits, void* exp_avg, void* exp_avg_sq,
+                          float* exp_avg_scale, float* exp_avg_sq_scale, float* master, const float* lr, int64_t* step,
+                          double beta1, double beta2, double eps, float max_norm, float* grad_norm, void* workspace,
+                          size_t workspace_bytes, void* stream) {
+  g_last_error.clear();
+  if (plan_bytes % sizeof(itl::AdamPiece) != 0) return fail(ITL_ERR_INVALID_ARG, "plan_bytes is not a plan's");
+  if (state_bits != 8 && state_bits != 32) return fail(ITL_ERR_UNSUPPORTED, "state_bits must be 8 or 32");
+  if (!(beta1 >= 0.0 && beta1 < 1.0) || !(beta2 >= 0.0 && beta2 < 1.0))
+    return fail(ITL_ERR_INVALID_ARG, "beta1 and beta2 must be in [0, 1)");
+  if (!(eps > 0.0 && eps < 1.0)) return fail(ITL_ERR_INVALID_ARG, "eps must be in (0, 1)");
+  if (!(max_norm > 0.0f)) return fail(ITL_ERR_INVALID_ARG, "max_norm must be > 0 (infinity: no clipping)");
+  const int64_t pieces = (int64_t)(plan_bytes / sizeof(itl::AdamPiece));
+  if (pieces > INT32_MAX) return fail(ITL_ERR_UNSUPPORTED, "too many elements for one plan");
+  if (!lr || !step) return fail(ITL_ERR_INVALID_ARG, "null lr or step");
+  if (pieces > 0 && (!plan || !exp_avg || !exp_avg_sq || (state_bits == 8 && (!exp_avg_scale || !exp_avg_sq_scale))))
+    return fail(ITL_ERR_INVALID_ARG, "null plan or state");
+  if (misaligned16(exp_avg, exp_avg_sq) || misaligned16(master, nullptr) || (reinterpret_cast<uintptr_t>(plan) & 7) != 0)
+    return fail(ITL_ERR_INVALID_ARG, "states must be 16-byte aligned, the plan 8-byte aligned");
+  if (!workspace || workspace_bytes < itl::adamw_workspace_bytes())
+    return fail(ITL_ERR_WORKSPACE, "workspace missing or smaller than itl_adamw_step_workspace_bytes()");
+  if (misaligned(workspace)) return fail(ITL_ERR_WORKSPACE, "workspace must be 256-byte aligned");
+  const bool with_norm = grad_norm || max_norm < __builtin_inff();
+  hipError_t e = itl::launch_adamw_step(plan, pieces, state_bits, exp_avg, exp_avg_sq, exp_avg_scale, exp_avg_sq_scale,
+                                        master, lr, step, beta1, beta2, eps, with_norm, max_norm, grad_norm, workspace,
+                                        static_cast<hipStream_t>(stream));
+  return e == hipSuccess ? ITL_OK : hip_fail(e, "itl_adamw_step");
 }
 
 size_t itl_mismatch_stats_workspace_bytes(int64_t n_tok) {

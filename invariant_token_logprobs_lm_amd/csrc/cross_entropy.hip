@@ -1,0 +1,813 @@
+// Cross entropy over the vocabulary and its gradient, through the LM head,
+// for the tokens that count.
+//
+//   z[t, v] = sum_k H[t, k] W[v, k]            fp32 accumulate
+//   lse[t]  = log sum_v exp(z[t, v])
+//   l[t]    = (1 - e) (lse - z[t, y_t]) + e (lse - mean_v z[t, v]) + lam lse^2
+//   loss    = (1 / N) sum_t l[t]               over the N tokens with 0 <= y_t < V
+//   G[t, v] = s / N ((1 + 2 lam lse) p[t, v] - (1 - e) [v = y_t] - e / V),  p = exp(z - lse)
+//   dH = G W,  dW = G^T H
+//
+// The logits exist for one chunk of kCeChunk tokens at a time, in the
+// workspace. A token whose id is outside [0, V) costs nothing beyond the
+// loads of its id: the counted tokens' rows of H are gathered first (their
+// number stays on the device; workgroups past it leave at once), and every
+// contraction runs over them alone.
+//
+// With the gradient, for each chunk:
+//   1. z = H W^T by the forward's contraction (eight-wavefront engine), kept
+//      in fp32, with the online log-sum-exp folds of the logprob's forward;
+//   2. G in the head's type, token-major (for dH) and vocabulary-major (dW);
+//   3. dH = G (W^T)^T, K = the vocabulary, split over several workgroups
+//      when the chunk has few row blocks (fp32 partials added in order);
+//   4. dW += G^T (H^T)^T, K = the chunk's tokens.
+// That is three contractions, the least there is (keeping the logits saves
+// the fourth: a chunk's 12 bytes of traffic per logit cost less than a
+// contraction of 2 d operations each for d > about 1000, the widths here).
+//
+// Every sum has a fixed order and there are no atomics: token losses depend
+// on the token alone, the loss and the gradients are run-to-run
+// deterministic.
+
+#include <algorithm>
+
+#include "itl_launch.h"
+#include "learner_common.h"
+#include "logit_store.h"
+#include "lse_fold.h"
+#include "tile_engine.h"
+#include "tile_engine8.h"
+
+namespace itl {
+
+namespace {
+
+constexpr int kCeChunk = 16384;  // tokens per chunk (a multiple of kBT)
+static_assert(kCeChunk % kBT == 0, "chunks hold whole token blocks");
+
+long long round_up(long long x, long long m) { return (x + m - 1) / m * m; }
+
+// ---- which tokens count
+
+// One workgroup: rows[j] = the j-th counted token, ids[j] its target,
+// slot[t] = token t's place j or -1; *count = N.
+constexpr int kSelectThreads = 1024;
+__global__ __launch_bounds__(kSelectThreads) void ce_select_kernel(const int32_t* __restrict__ targets, int n, int vocab,
+                                                                   int32_t* __restrict__ rows, int32_t* __restrict__ ids,
+                                                                   int32_t* __restrict__ slot, int32_t* __restrict__ count) {
+  __shared__ int wave_n[kSelectThreads / 64];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  int base = 0;
+  for (int t0 = 0; t0 < n; t0 += kSelectThreads) {
+    const int t = t0 + threadIdx.x;
+    const int y = t < n ? targets[t] : -1;
+    const bool in = (unsigned)y < (unsigned)vocab;
+    const uint64_t mask = __ballot(in);
+    if (lane == 0) wave_n[wave] = __popcll(mask);
+    __syncthreads();
+    int before = base;
+    for (int w = 0; w < kSelectThreads / 64; ++w) {
+      if (w < wave) before += wave_n[w];
+      base += wave_n[w];
+    }
+    const int j = before + __popcll(mask & ((1ull << lane) - 1ull));
+    if (in) {
+      rows[j] = t;
+      ids[j] = y;
+    }
+    if (t < n) slot[t] = in ? j : -1;
+    __syncthreads();
+  }
+  if (threadIdx.x == 0) *count = base;
+}
+
+// A chunk's share of the count.
+__device__ __forceinline__ int chunk_live(const int32_t* count, int c0, int cap) {
+  return max(0, min(*count - c0, cap));
+}
+
+// Hc[j] = H[rows[c0 + j]], 16 bytes per thread.
+__global__ __launch_bounds__(256) void ce_gather_kernel(const uint4* __restrict__ H, const int32_t* __restrict__ rows,
+                                                        const int32_t* __restrict__ count, int c0, int cap,
+                                                        int row_chunks, uint4* __restrict__ Hc) {
+  const int live = chunk_live(count, c0, cap);
+  const int j = blockIdx.x;
+  if (j >= live) return;
+  const uint4* src = H + (size_t)rows[c0 + j] * row_chunks;
+  uint4* dst = Hc + (size_t)j * row_chunks;
+  for (int i = threadIdx.x; i < row_chunks; i += 256) dst[i] = src[i];
+}
+
+// ---- the forward's contraction over the gathered rows
+
+// lmhead_lse_partial8_kernel's walk with the number of rows on the device;
+// the partials' row stride is `stride`.
+template <int kDtype, bool kKeep, bool kBFar>
+__global__ __launch_bounds__(kThreads8, 1) void ce_partial_kernel(
+    const char* __restrict__ H, const char* __restrict__ W, const int32_t* __restrict__ ids,
+    const int32_t* __restrict__ count, int c0, int cap, int stride, int row_bytes, int vocab, int n_tb, int n_slices,
+    int group, float2* __restrict__ part, float* __restrict__ zy_out, float* __restrict__ logits, long long ld) {
+  __shared__ uint4 smem[kEngineSmemChunks];
+  const Lanes8 L = lanes8();
+  const int wv = L.wv, tq = L.tq, quad = L.quad, c16 = L.c16;
+
+  const int S = n_slices;
+  const WideWork work = wide_work(blockIdx.x, n_tb, S, group);
+  const int t0 = work.tb * kBT;
+  const int n_tok = __builtin_amdgcn_readfirstlane(chunk_live(count, c0, cap));
+  if (t0 >= n_tok) return;
+  const int n_vt = (vocab + kBV - 1) / kBV;
+  const int tile_begin = slice_tile(work.slice_first, n_vt, S);
+  const int tile_end = slice_tile(work.slice_end, n_vt, S);
+  const int nks = row_bytes / kStepBytes;
+
+  Col16 c[4];
+#pragma unroll
+  for (int bn = 0; bn < 4; ++bn) {
+    const int tok = t0 + tq * 64 + bn * 16 + c16;
+    c[bn] = Col16{tok < n_tok ? ids[tok] : -1, -INFINITY, 0.0f};
+  }
+  auto w_rsrc = [&](int tile) {
+    const int v0 = tile * kBV;
+    return rsrc_words(W + (size_t)v0 * row_bytes, (uint32_t)min(kBV, vocab - v0) * row_bytes);
+  };
+  const int4v hr = rsrc_words(H + (size_t)t0 * row_bytes, (uint32_t)min(kBT, n_tok - t0) * row_bytes);
+
+  int slice = work.slice_first;
+  int slice_last_tile = slice_tile(slice + 1, n_vt, S) - 1;
+  auto epilogue = [&](int tile, floatx4 (&acc)[8][4]) {
+    const int vw = tile * kBV + wv * 128;
+    int lt = L.lane;  // made opaque: formed here, not kept live across the K loop
+    asm volatile("" : "+v"(lt));
+    lt = tq * 64 + (lt & 15);
+    auto fold_tile = [&](auto partial, auto pick) {
+#pragma unroll
+      for (int bn = 0; bn < 4; ++bn) {
+        if constexpr (kKeep) {
+          const LogitRows rows = logit_rows(logits, ld, t0 + tq * 64, 64, n_tok, c16, quad);
+#pragma unroll
+          for (int bm = 0; bm < 8; ++bm) store_logits(rows, bn, vw + bm * 16, quad, vocab, acc[bm][bn], partial);
+        }
+        floatx4 z[8];
+#pragma unroll
+        for (int bm = 0; bm < 8; ++bm) z[bm] = acc[bm][bn];
+        if constexpr (decltype(pick)::value) pick_sampled(c[bn], z, vw, quad, zy_out + (t0 + lt + bn * 16));
+        fold_column16(c[bn], z, vw, quad, vocab, partial);
+        __builtin_amdgcn_sched_barrier(0);  // one token column at a time (register pressure)
+      }
+    };
+    bool mine = false;
+#pragma unroll
+    for (int bn = 0; bn < 4; ++bn) {
+      int y = c[bn].y;
+      asm volatile("" : "+v"(y));
+      mine = mine || (unsigned)(y - vw) < 128u;
+    }
+    if (tile * kBV + kBV > vocab) fold_tile(std::true_type{}, std::true_type{});
+    else if (__builtin_amdgcn_ballot_w64(mine) != 0) fold_tile(std::false_type{}, std::true_type{});
+    else fold_tile(std::false_type{}, std::false_type{});
+    if (tile == slice_last_tile) {
+#pragma unroll
+      for (int bn = 0; bn < 4; ++bn) {
+        const int tok = t0 + lt + bn * 16;
+        flush_slice16(c[bn], tok, n_tok, quad, ((size_t)slice * 2 + wv) * stride + tok, part);
+      }
+      ++slice;
+      int Sx = S;
+      asm volatile("" : "+s"(Sx));
+      slice_last_tile = slice_tile(slice + 1, n_vt, Sx) - 1;
+    }
+  };
+  run_tiles8<kDtype, kBFar>(smem, L, row_bytes, tile_begin, tile_end, nks, w_rsrc, hr, epilogue);
+}
+
+// ---- mean of the logits (label smoothing): z's mean over v is H . mean_v W[v]
+
+constexpr int kMeanRows = 512;  // rows of W per partial sum
+
+// part[b, k] = sum of W[v, k] over kMeanRows rows v; 256 columns per workgroup.
+template <int kDtype>
+__global__ __launch_bounds__(256) void ce_colsum_kernel(const typename Elem<kDtype>::T* __restrict__ W, int vocab, int d,
+                                                        float* __restrict__ part) {
+  using E = Elem<kDtype>;
+  const int k = blockIdx.y * 256 + threadIdx.x;
+  if (k >= d) return;
+  const int v0 = blockIdx.x * kMeanRows, v1 = min(vocab, v0 + kMeanRows);
+  float s = 0.0f;
+  for (int v = v0; v < v1; ++v) s += E::to_f(W[(size_t)v * d + k]);
+  part[(size_t)blockIdx.x * d + k] = s;
+}
+
+__global__ __launch_bounds__(256) void ce_colmean_kernel(const float* __restrict__ part, int n_part, int d, int vocab,
+                                                         float* __restrict__ wmean) {
+  const int k = blockIdx.x * 256 + threadIdx.x;
+  if (k >= d) return;
+  double s = 0.0;
+  for (int b = 0; b < n_part; ++b) s += (double)part[(size_t)b * d + k];
+  wmean[k] = (float)(s / (double)vocab);
+}
+
+// ---- the tokens' losses
+
+// One wavefront per token of the call: its loss (0 where it does not count)
+// and its lse, and per workgroup the fp64 sum of four losses.
+template <int kDtype>
+__global__ __launch_bounds__(256) void ce_token_loss_kernel(const typename Elem<kDtype>::T* __restrict__ H, int n, int d,
+                                                            const int32_t* __restrict__ slot,
+                                                            const float* __restrict__ logprob, const float* __restrict__ lse,
+                                                            const float* __restrict__ wmean, float smoothing, float z_weight,
+                                                            float* __restrict__ token_loss, float* __restrict__ lse_out,
+                                                            double* __restrict__ part) {
+  using E = Elem<kDtype>;
+  __shared__ double lds[4];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int t = blockIdx.x * 4 + wave;
+  const int j = t < n ? slot[t] : -1;
+  float l = 0.0f, s = 0.0f;
+  if (j >= 0) {
+    s = lse[j];
+    l = -(1.0f - smoothing) * logprob[j];
+    if (wmean) {
+      float zm = 0.0f;
+      for (int k = lane; k < d; k += 64) zm += E::to_f(H[(size_t)t * d + k]) * wmean[k];
+      l += smoothing * (s - wave_sum(zm));
+    }
+    l += z_weight * s * s;
+  }
+  if (lane == 0) {
+    if (t < n) {
+      token_loss[t] = l;
+      if (lse_out) lse_out[t] = s;
+    }
+    lds[wave] = (double)l;
+  }
+  __syncthreads();
+  if (threadIdx.x == 0) part[blockIdx.x] = ((lds[0] + lds[1]) + lds[2]) + lds[3];
+}
+
+// The fp64 sums in a fixed order, over N (0 when no token counts).
+__global__ __launch_bounds__(1024) void ce_loss_kernel(const double* __restrict__ part, int n_part,
+                                                       const int32_t* __restrict__ count, int mean,
+                                                       float* __restrict__ loss) {
+  __shared__ double lds[16];
+  double s = 0.0;
+  for (int i = threadIdx.x; i < n_part; i += 1024) s += part[i];
+  s = wave_sum_d(s);
+  if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = s;
+  __syncthreads();
+  if (threadIdx.x != 0) return;
+  for (int w = 1; w < 16; ++w) s += lds[w];
+  *loss = (float)(mean ? s / (double)max(1, *count) : s);
+}
+
+// ---- G
+
+// out[c, r] = in[r, c] for r < rows (0 to out_cols), 64 x 64 tiles through
+// LDS; rows is the chunk's live count where `count` is given.
+template <typename T>
+__global__ __launch_bounds__(256) void ce_transpose_kernel(const T* __restrict__ in, int rows, int cols,
+                                                           T* __restrict__ out, int out_cols,
+                                                           const int32_t* __restrict__ count, int c0) {
+  __shared__ T tile[64][65];
+  const int r0 = blockIdx.x * 64, k0 = blockIdx.y * 64;
+  if (count) {
+    rows = chunk_live(count, c0, rows);
+    if (r0 >= max(rows, 1)) return;
+  }
+  const int tx = threadIdx.x & 63, ty = threadIdx.x >> 6;
+  for (int i = ty; i < 64; i += 4) {
+    const int r = r0 + i, c = k0 + tx;
+    tile[i][tx] = (r < rows && c < cols) ? in[(size_t)r * cols + c] : T(0);
+  }
+  __syncthreads();
+  for (int i = ty; i < 64; i += 4) {
+    const int c = k0 + i, r = r0 + tx;
+    if (c < cols && r < out_cols) out[(size_t)c * out_cols + r] = tile[tx][i];
+  }
+}
+
+// G is held in units of u = (1 - e) s / N, which the contractions' epilogues
+// apply in fp32: a p - [v = y] - c with a = (1 + 2 lam lse) / (1 - e) and
+// c = e / (V (1 - e)). The target's entry is then near -1, which bf16 holds
+// to 2^-10 or better; with u folded in, every target's entry would carry the
+// same rounding error of u, up to 2^-9 of the whole gradient (measured:
+// dH and dW 0.0027 off at d = 2560, V = 151936 with 16-bit results; 0.0020 so).
+struct GradScale {
+  float smoothing, z_weight, scale, inv_vocab;
+  int mean;
+};
+
+__device__ __forceinline__ float grad_unit(const GradScale& g, const int32_t* count) {
+  const double u = (double)g.scale * (1.0 - (double)g.smoothing);
+  return (float)(g.mean ? u / (double)max(1, *count) : u);
+}
+
+// G from the kept logits, a tile of 128 tokens x 128 vocabulary rows: Gd
+// [token, vpad] and GT [vpad, ld_t]. With kExact the target's entry is
+// stored without its -1, which dH and dW then take in fp32.
+constexpr int kGTile = 128;
+
+template <int kDtype, bool kExact>
+__global__ __launch_bounds__(256) void ce_grad_logits_kernel(
+    const float* __restrict__ logits, long long ld, const int32_t* __restrict__ ids, const int32_t* __restrict__ count,
+    int c0, int cap, int vocab, int vpad, int ld_t, const float* __restrict__ lse, GradScale gs,
+    typename Elem<kDtype>::T* __restrict__ Gd, typename Elem<kDtype>::T* __restrict__ GT) {
+  using E = Elem<kDtype>;
+  using T = typename E::T;
+  constexpr int kPack = 4 / (int)sizeof(T);  // tokens per 32-bit word
+  constexpr int kRowWords = kGTile / kPack + 1;
+  __shared__ uint32_t tile[kGTile * kRowWords];
+  const int live = chunk_live(count, c0, cap);
+  const int v0 = blockIdx.x * kGTile;
+  const int t0 = blockIdx.y * kGTile;
+  if (t0 >= max(live, 1)) return;  // (the first tile is always written: dW's contraction reads it)
+  const float rest = 1.0f / (1.0f - gs.smoothing);
+  const float cc = gs.smoothing * gs.inv_vocab * rest;
+  const int vq = threadIdx.x & 31;  // vocabulary rows v0 + 4 vq .. + 3
+  const int tr = threadIdx.x >> 5;  // 0..7
+  const int v = v0 + 4 * vq;
+  for (int p = 0; p < kGTile / (8 * kPack); ++p) {
+    T g[kPack][4];
+#pragma unroll
+    for (int k = 0; k < kPack; ++k) {
+      const int t = t0 + (tr + 8 * p) * kPack + k;
+      if (t < live) {
+        const float s = lse[t];
+        const float l2e_lse = s * kLog2e;
+        const float a = rest * (1.0f + 2.0f * gs.z_weight * s);
+        const int y = ids[t];
+        const float* row = logits + (size_t)t * (size_t)ld;
+        floatx4 z;
+        if (v + 3 < vocab) {
+          z = __builtin_nontemporal_load(reinterpret_cast<const floatx4*>(row + v));
+        } else {
+#pragma unroll
+          for (int r = 0; r < 4; ++r) z[r] = v + r < vocab ? row[v + r] : 0.0f;
+        }
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          float x = a * fast_exp2(z[r] * kLog2e - l2e_lse) - cc;
+          if (!kExact && v + r == y) x -= 1.0f;
+          g[k][r] = E::from_f(v + r < vocab ? x : 0.0f);
+        }
+      } else {
+#pragma unroll
+        for (int r = 0; r < 4; ++r) g[k][r] = E::from_f(0.0f);
+      }
+      if constexpr (kDtype == 0) {
+        uint2 pk;
+        pk.x = (uint32_t)g[k][0] | ((uint32_t)g[k][1] << 16);
+        pk.y = (uint32_t)g[k][2] | ((uint32_t)g[k][3] << 16);
+        *reinterpret_cast<uint2*>(Gd + (size_t)t * vpad + v) = pk;
+      } else {
+        *reinterpret_cast<float4*>(Gd + (size_t)t * vpad + v) = make_float4(g[k][0], g[k][1], g[k][2], g[k][3]);
+      }
+    }
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      uint32_t w;
+      if constexpr (kDtype == 0) w = (uint32_t)g[0][r] | ((uint32_t)g[1][r] << 16);
+      else w = __float_as_uint(g[0][r]);
+      tile[(4 * vq + r) * kRowWords + tr + 8 * p] = w;
+    }
+  }
+  __syncthreads();
+  constexpr int kLanesPerRow = kGTile / kPack / 4;
+  constexpr int kRowsPerPass = 256 / kLanesPerRow;
+  const int j = threadIdx.x % kLanesPerRow;
+  for (int vr = threadIdx.x / kLanesPerRow; vr < kGTile; vr += kRowsPerPass) {
+    const uint32_t* src = tile + vr * kRowWords + 4 * j;
+    *reinterpret_cast<uint4*>(reinterpret_cast<char*>(GT + (size_t)(v0 + vr) * ld_t + t0) + 16 * j) =
+        make_uint4(src[0], src[1], src[2], src[3]);
+  }
+}
+
+// coef[j] = -u for the chunk's live tokens, 0 (and id -1) past them: the
+// exact one-hot term of the fp32 gradients.
+__global__ __launch_bounds__(256) void ce_onehot_kernel(const int32_t* __restrict__ ids, const int32_t* __restrict__ count,
+                                                        int c0, int cap, GradScale gs, float* __restrict__ coef,
+                                                        int32_t* __restrict__ chunk_ids) {
+  const int j = blockIdx.x * 256 + threadIdx.x;
+  if (j >= cap) return;
+  const bool in = j < chunk_live(count, c0, cap);
+  coef[j] = in ? -grad_unit(gs, count) : 0.0f;
+  chunk_ids[j] = in ? ids[j] : -1;
+}
+
+// ---- dH
+
+__device__ __forceinline__ void store_grad4(void* out, int grad_f32, size_t at, const float (&o)[4]) {
+  if (grad_f32) {
+    *reinterpret_cast<float4*>(static_cast<float*>(out) + at) = make_float4(o[0], o[1], o[2], o[3]);
+  } else {
+    uint2 pk;
+    pk.x = (uint32_t)Elem<0>::from_f(o[0]) | ((uint32_t)Elem<0>::from_f(o[1]) << 16);
+    pk.y = (uint32_t)Elem<0>::from_f(o[2]) | ((uint32_t)Elem<0>::from_f(o[3]) << 16);
+    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(out) + at) = pk;
+  }
+}
+
+// Partial s of dH for the chunk: A = W^T tile (d rows), B = Gd token block,
+// K = the vocabulary steps [nks s / splits, nks (s + 1) / splits). Writes
+// fp32 rows part[s, j, :].
+template <int kDtype, bool kBFar>
+__global__ __launch_bounds__(kThreads8, 1) void ce_dh_kernel(const char* __restrict__ WT, const char* __restrict__ Gd,
+                                                             int vpad, int d, const int32_t* __restrict__ count, int c0,
+                                                             int cap, int n_tb, int n_dt, int splits,
+                                                             float* __restrict__ part) {
+  __shared__ uint4 smem[kEngineSmemChunks];
+  const Lanes8 L = lanes8();
+  const int live = __builtin_amdgcn_readfirstlane(chunk_live(count, c0, cap));
+  // token blocks fastest: workgroups that run together share W^T's rows
+  const int tb = blockIdx.x % n_tb, rest = blockIdx.x / n_tb;
+  const int dt = rest % n_dt, sp = rest / n_dt;
+  const int t0 = tb * kBT;
+  if (t0 >= live) return;
+  const int row_bytes = vpad * Elem<kDtype>::kSize;
+  const int nks_all = row_bytes / kStepBytes;
+  const int ks0 = (int)((long long)nks_all * sp / splits), ks1 = (int)((long long)nks_all * (sp + 1) / splits);
+  const uint32_t skip = (uint32_t)ks0 * kStepBytes;
+  auto a_rsrc = [&](int tile) {
+    const int k0 = tile * kBV;
+    return rsrc_words(WT + (size_t)k0 * row_bytes + skip, (uint32_t)min(kBV, d - k0) * row_bytes - skip);
+  };
+  const int4v br = rsrc_words(Gd + (size_t)t0 * row_bytes + skip, (uint32_t)min(kBT, live - t0) * row_bytes - skip);
+  auto epilogue = [&](int tile, floatx4 (&acc)[8][4]) {
+    const int kw = tile * kBV + L.wv * 128 + 4 * L.quad;
+#pragma unroll
+    for (int bn = 0; bn < 4; ++bn) {
+      const int t = t0 + L.tq * 64 + bn * 16 + L.c16;
+#pragma unroll
+      for (int bm = 0; bm < 8; ++bm) {
+        const int k = kw + bm * 16;
+        if (t < live && k < d) {
+          const floatx4& o = acc[bm][bn];
+          *reinterpret_cast<float4*>(part + ((size_t)sp * cap + t) * d + k) = make_float4(o[0], o[1], o[2], o[3]);
+        }
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  };
+  run_tiles8<kDtype, kBFar>(smem, L, row_bytes, dt, dt + 1, ks1 - ks0, a_rsrc, br, epilogue);
+}
+
+// dH rows: the splits added in order (plus, with coef, the exact one-hot
+// term coef[j] W[y]), four values per thread, to the token's own row.
+template <int kDtype>
+__global__ __launch_bounds__(256) void ce_dh_finish_kernel(const float* __restrict__ part, int splits, int cap, int d,
+                                                           const int32_t* __restrict__ rows, const int32_t* __restrict__ ids,
+                                                           const int32_t* __restrict__ count, int c0, GradScale gs,
+                                                           const float* __restrict__ coef,
+                                                           const typename Elem<kDtype>::T* __restrict__ W, int grad_f32,
+                                                           void* __restrict__ dH) {
+  using E = Elem<kDtype>;
+  const int j = blockIdx.x;
+  if (j >= chunk_live(count, c0, cap)) return;
+  const float unit = grad_unit(gs, count);
+  for (int k = threadIdx.x * 4; k < d; k += 1024) {
+    float o[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    for (int s = 0; s < splits; ++s) {
+      const float4 v = *reinterpret_cast<const float4*>(part + ((size_t)s * cap + j) * d + k);
+      o[0] += v.x, o[1] += v.y, o[2] += v.z, o[3] += v.w;
+    }
+#pragma unroll
+    for (int r = 0; r < 4; ++r) o[r] *= unit;
+    if (coef) {
+      const float c = coef[j];
+      const typename E::T* w = W + (size_t)ids[j] * d + k;
+#pragma unroll
+      for (int r = 0; r < 4; ++r) o[r] += c * E::to_f(w[r]);
+    }
+    store_grad4(dH, grad_f32, (size_t)rows[c0 + j] * d + k, o);
+  }
+}
+
+// Zero rows of dH where the token does not count.
+__global__ __launch_bounds__(256) void ce_zero_rows_kernel(const int32_t* __restrict__ slot, int row_chunks,
+                                                           uint4* __restrict__ dH) {
+  const int t = blockIdx.x;
+  if (slot[t] >= 0) return;
+  for (int i = threadIdx.x; i < row_chunks; i += 256) dH[(size_t)t * row_chunks + i] = make_uint4(0u, 0u, 0u, 0u);
+}
+
+// ---- dW
+
+// The chunk's part of dW: A = GT vocabulary tile (K = the chunk's tokens),
+// B = H^T block of d. add: dW already holds earlier parts (fp32).
+template <int kDtype>
+__global__ __launch_bounds__(kThreads8, 1) void ce_dw_kernel(const char* __restrict__ GT, const char* __restrict__ HT,
+                                                             int ld_t, const int32_t* __restrict__ count, int c0, int cap,
+                                                             int vocab, int d, int n_vt, int n_dt, GradScale gs, int add,
+                                                             int out_f32,
+                                                             void* __restrict__ dW) {
+  using E = Elem<kDtype>;
+  __shared__ uint4 smem[kEngineSmemChunks];
+  const Lanes8 L = lanes8();
+  const int live = __builtin_amdgcn_readfirstlane(chunk_live(count, c0, cap));
+  if (live == 0 && c0 > 0) return;  // (the first chunk writes its zeros)
+  const int band = blockIdx.x / (kBwdSuperBand * n_dt);
+  const int first = band * kBwdSuperBand;
+  const int nb = min(kBwdSuperBand, n_vt - first);
+  const int rem = blockIdx.x - band * kBwdSuperBand * n_dt;
+  const int vt = first + rem % nb, dt = rem / nb;
+  const int row_bytes = ld_t * E::kSize;
+  const int k0 = dt * kBT;
+  constexpr int kStep = kStepBytes / E::kSize;
+  const int nks = max(1, (live + kStep - 1) / kStep);
+  const float unit = grad_unit(gs, count);
+  auto a_rsrc = [&](int tile) {
+    const int v0 = tile * kBV;
+    return rsrc_words(GT + (size_t)v0 * row_bytes, (uint32_t)kBV * row_bytes);
+  };
+  const int4v br = rsrc_words(HT + (size_t)k0 * row_bytes, (uint32_t)min(kBT, d - k0) * row_bytes);
+  auto epilogue = [&](int tile, floatx4 (&acc)[8][4]) {
+    const int vw = tile * kBV + L.wv * 128 + 4 * L.quad;
+#pragma unroll
+    for (int bn = 0; bn < 4; ++bn) {
+      const int k = k0 + L.tq * 64 + bn * 16 + L.c16;
+#pragma unroll
+      for (int bm = 0; bm < 8; ++bm)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const int v = vw + bm * 16 + r;
+          if (v < vocab && k < d) {
+            const size_t at = (size_t)v * d + k;
+            float x = acc[bm][bn][r] * unit;
+            if (add) x += static_cast<float*>(dW)[at];
+            if (out_f32) static_cast<float*>(dW)[at] = x;
+            else static_cast<uint16_t*>(dW)[at] = Elem<0>::from_f(x);
+          }
+        }
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  };
+  run_tiles8<kDtype, false>(smem, L, row_bytes, vt, vt + 1, nks, a_rsrc, br, epilogue);
+}
+
+// The accumulated fp32 dW rounded to bf16.
+__global__ __launch_bounds__(256) void ce_round_kernel(const float4* __restrict__ in, long long n4, uint2* __restrict__ out) {
+  const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
+  if (i >= n4) return;
+  const float4 v = in[i];
+  out[i] = make_uint2((uint32_t)Elem<0>::from_f(v.x) | ((uint32_t)Elem<0>::from_f(v.y) << 16),
+                      (uint32_t)Elem<0>::from_f(v.z) | ((uint32_t)Elem<0>::from_f(v.w) << 16));
+}
+
+__global__ __launch_bounds__(256) void ce_add_kernel(const float4* __restrict__ in, long long n4, float4* __restrict__ out) {
+  const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
+  if (i >= n4) return;
+  const float4 v = in[i];
+  float4 o = out[i];
+  o.x += v.x, o.y += v.y, o.z += v.z, o.w += v.w;
+  out[i] = o;
+}
+
+// out = 0 in 16-byte pieces; *one = 0 where given.
+__global__ __launch_bounds__(256) void ce_clear_kernel(uint4* __restrict__ out, long long n16, float* __restrict__ one) {
+  const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
+  if (i < n16) out[i] = make_uint4(0u, 0u, 0u, 0u);
+  if (one && i == 0) *one = 0.0f;
+}
+
+// ---- workspace
+
+// Workgroups of dH's contraction without a split cover n_tb x n_dt tiles:
+// the split count (up to 16, each with at least 16 K steps) that leaves the
+// fewest rounds of 256 workgroups per unit of work, the smallest such.
+int dh_splits(long long n_tb, long long n_dt, long long nks) {
+  int best = 1;
+  double best_cost = 1e30;
+  for (int s = 1; s <= 16 && nks / s >= 16; ++s) {
+    const double cost = (double)ceil_div(n_tb * n_dt * s, 256) / s * (1.0 + 0.01 * s);
+    if (cost < best_cost * 0.999) best = s, best_cost = cost;
+  }
+  return best;
+}
+
+struct CeLayout {
+  int cap, ld_t, vpad;
+  size_t rows, ids, slot, count, lp, lse, zy, part, loss, wmean, wpart, hc, z, gd, gt, wt, ht, dhp, coef, cids, dwacc,
+      sampled, total;
+};
+
+CeLayout ce_layout(long long n_tok, long long d, long long vocab, int dtype, bool grad, int grad_dtype) {
+  CeLayout L{};
+  const int es = dtype == 0 ? 2 : 4;
+  L.vpad = (int)round_up(vocab, kBV);
+  L.cap = (int)(grad ? std::min<long long>(kCeChunk, round_up(n_tok, kBT)) : n_tok);
+  L.ld_t = (int)round_up(L.cap, kBT);
+  size_t off = 0;
+  auto take = [&](size_t bytes) {
+    const size_t at = off;
+    off += align256(bytes);
+    return at;
+  };
+  L.rows = take((size_t)n_tok * 4);
+  L.ids = take((size_t)n_tok * 4);
+  L.slot = take((size_t)n_tok * 4);
+  L.count = take(4);
+  L.lp = take((size_t)round_up(n_tok, kBT) * 4);
+  L.lse = take((size_t)round_up(n_tok, kBT) * 4);
+  L.zy = take((size_t)L.cap * 4);
+  L.part = take((size_t)2 * n_slices(vocab) * L.cap * sizeof(float2));
+  L.loss = take((size_t)ceil_div(n_tok, 4) * 8);
+  L.wmean = take((size_t)d * 4);
+  L.wpart = take((size_t)ceil_div(vocab, kMeanRows) * d * 4);
+  L.hc = take((size_t)L.cap * d * es);
+  if (grad) {
+    const long long n_tb = L.cap / kBT, n_dt = ceil_div(d, kBT);
+    const long long nks = (long long)L.vpad * es / kStepBytes, last = n_tok - (n_tok - 1) / L.cap * L.cap;
+    L.z = take((size_t)L.cap * L.vpad * 4);
+    L.gd = take((size_t)L.cap * L.vpad * es);
+    L.gt = take((size_t)L.vpad * L.ld_t * es);
+    L.wt = take((size_t)d * L.vpad * es);
+    L.ht = take((size_t)d * L.ld_t * es);
+    // the partials of a whole chunk, or of the (smaller) last one
+    const size_t whole = (size_t)dh_splits(n_tb, n_dt, nks) * L.cap, rest = (size_t)dh_splits(ceil_div(last, kBT), n_dt, nks) * last;
+    L.dhp = take(std::max(whole, rest) * d * 4);
+    if (dtype == 0 && grad_dtype == 1) {
+      L.coef = take((size_t)L.cap * 4);
+      L.cids = take((size_t)L.cap * 4);
+      L.sampled = take(sampled_dw_workspace_bytes(L.cap, d, vocab));
+    }
+    if (dtype == 0 && n_tok > L.cap)
+      L.dwacc = take((size_t)vocab * d * 4);
+  }
+  L.total = off;
+  return L;
+}
+
+#define ITL_CHECK_LAUNCH()         \
+  do {                             \
+    e = hipGetLastError();         \
+    if (e != hipSuccess) return e; \
+  } while (0)
+
+template <int kDtype, bool kKeep>
+void launch_ce_partial(const char* Hc, const char* W, const int32_t* ids, const int32_t* count, int c0, int cap, int d,
+                       int vocab, float2* part, float* zy, float* logits, long long ld, hipStream_t stream) {
+  const int row_bytes = d * Elem<kDtype>::kSize;
+  const int S = n_slices(vocab), G = slices_per_group(cap, vocab), ntb = (int)ceil_div(cap, kBT);
+  const dim3 grid((unsigned)ntb * (unsigned)n_slice_groups(cap, vocab));
+  // the load schedule's rule, and its exception for fp32 kept logits, as in the logprob's forward
+  constexpr bool kFarOnly = kDtype == 1 && kKeep;
+  if (kFarOnly || row_bytes / kStepBytes > kNearBMaxSteps)
+    hipLaunchKernelGGL((ce_partial_kernel<kDtype, kKeep, true>), grid, dim3(kThreads8), 0, stream, Hc, W, ids, count, c0,
+                       cap, cap, row_bytes, vocab, ntb, S, G, part, zy, logits, ld);
+  else if constexpr (!kFarOnly)
+    hipLaunchKernelGGL((ce_partial_kernel<kDtype, kKeep, false>), grid, dim3(kThreads8), 0, stream, Hc, W, ids, count, c0,
+                       cap, cap, row_bytes, vocab, ntb, S, G, part, zy, logits, ld);
+}
+
+template <int kDtype>
+hipError_t run_cross_entropy(const CeCall& c, hipStream_t stream) {
+  using E = Elem<kDtype>;
+  using T = typename E::T;
+  const bool grad = c.dW != nullptr;
+  if (c.n_tok == 0) {  // no token: loss 0, dW zeros
+    hipLaunchKernelGGL(ce_clear_kernel, dim3(1), dim3(256), 0, stream, reinterpret_cast<uint4*>(c.loss), 0LL, c.loss);
+    if (grad) {
+      const long long n16 = c.vocab * c.d * (c.grad_dtype == 0 ? 2 : 4) / 16;
+      hipLaunchKernelGGL(ce_clear_kernel, dim3((unsigned)ceil_div(n16, 256)), dim3(256), 0, stream,
+                         static_cast<uint4*>(c.dW), n16, nullptr);
+    }
+    return hipGetLastError();
+  }
+  const CeLayout L = ce_layout(c.n_tok, c.d, c.vocab, kDtype, grad, c.grad_dtype);
+  char* ws = static_cast<char*>(c.workspace);
+  auto at = [&](size_t off) { return ws + off; };
+  int32_t* rows = reinterpret_cast<int32_t*>(at(L.rows));
+  int32_t* ids = reinterpret_cast<int32_t*>(at(L.ids));
+  int32_t* slot = reinterpret_cast<int32_t*>(at(L.slot));
+  int32_t* count = reinterpret_cast<int32_t*>(at(L.count));
+  float* lp = reinterpret_cast<float*>(at(L.lp));
+  float* lse = reinterpret_cast<float*>(at(L.lse));
+  float* zy = reinterpret_cast<float*>(at(L.zy));
+  float2* part = reinterpret_cast<float2*>(at(L.part));
+  double* loss_part = reinterpret_cast<double*>(at(L.loss));
+  float* wmean = c.smoothing > 0.0f ? reinterpret_cast<float*>(at(L.wmean)) : nullptr;
+  float* wpart = reinterpret_cast<float*>(at(L.wpart));
+  char* Hc = at(L.hc);
+  const T* H = static_cast<const T*>(c.H);
+  const T* W = static_cast<const T*>(c.W);
+  const int n = (int)c.n_tok, d = (int)c.d, vocab = (int)c.vocab, S = n_slices(vocab);
+  const int row_chunks = d * E::kSize / 16;
+  hipError_t e;
+
+  hipLaunchKernelGGL(ce_select_kernel, dim3(1), dim3(kSelectThreads), 0, stream, c.targets, n, vocab, rows, ids, slot,
+                     count);
+  ITL_CHECK_LAUNCH();
+  if (wmean) {
+    const int nb = (int)ceil_div(vocab, kMeanRows);
+    hipLaunchKernelGGL(ce_colsum_kernel<kDtype>, dim3((unsigned)nb, (unsigned)ceil_div(d, 256)), dim3(256), 0, stream, W,
+                       vocab, d, wpart);
+    hipLaunchKernelGGL(ce_colmean_kernel, dim3((unsigned)ceil_div(d, 256)), dim3(256), 0, stream, wpart, nb, d, vocab,
+                       wmean);
+    ITL_CHECK_LAUNCH();
+  }
+  GradScale gs{c.smoothing, c.z_weight, c.grad_scale, 1.0f / (float)vocab, c.mean};
+  const bool exact = grad && kDtype == 0 && c.grad_dtype == 1;
+  if (grad) {
+    hipLaunchKernelGGL(ce_transpose_kernel<T>, dim3((unsigned)(L.vpad / 64), (unsigned)ceil_div(d, 64)), dim3(256), 0,
+                       stream, W, vocab, d, reinterpret_cast<T*>(at(L.wt)), L.vpad, nullptr, 0);
+    hipLaunchKernelGGL(ce_zero_rows_kernel, dim3((unsigned)n), dim3(256), 0, stream, slot,
+                       d * (c.grad_dtype == 0 ? 2 : 4) / 16, static_cast<uint4*>(c.dH));
+    ITL_CHECK_LAUNCH();
+  }
+  for (int c0 = 0; c0 < n; c0 += L.cap) {
+    const int cap = std::min(L.cap, n - c0);
+    hipLaunchKernelGGL(ce_gather_kernel, dim3((unsigned)cap), dim3(256), 0, stream, reinterpret_cast<const uint4*>(H),
+                       rows, count, c0, cap, row_chunks, reinterpret_cast<uint4*>(Hc));
+    float* z = grad ? reinterpret_cast<float*>(at(L.z)) : nullptr;
+    if (grad)
+      launch_ce_partial<kDtype, true>(Hc, reinterpret_cast<const char*>(W), ids + c0, count, c0, cap, d, vocab, part, zy,
+                                      z, L.vpad, stream);
+    else
+      launch_ce_partial<kDtype, false>(Hc, reinterpret_cast<const char*>(W), ids + c0, count, c0, cap, d, vocab, part, zy,
+                                       nullptr, 0, stream);
+    ITL_CHECK_LAUNCH();
+    e = launch_lse_combine(part, zy, cap, 2 * S, lp + c0, lse + c0, stream);
+    if (e != hipSuccess) return e;
+    if (!grad) continue;
+
+    T* Gd = reinterpret_cast<T*>(at(L.gd));
+    T* GT = reinterpret_cast<T*>(at(L.gt));
+    T* HT = reinterpret_cast<T*>(at(L.ht));
+    const dim3 g_grid((unsigned)(L.vpad / kGTile), (unsigned)ceil_div(cap, kGTile));
+    if (exact)
+      hipLaunchKernelGGL((ce_grad_logits_kernel<kDtype, true>), g_grid, dim3(256), 0, stream, z, (long long)L.vpad,
+                         ids + c0, count, c0, cap, vocab, L.vpad, L.ld_t, lse + c0, gs, Gd, GT);
+    else
+      hipLaunchKernelGGL((ce_grad_logits_kernel<kDtype, false>), g_grid, dim3(256), 0, stream, z, (long long)L.vpad,
+                         ids + c0, count, c0, cap, vocab, L.vpad, L.ld_t, lse + c0, gs, Gd, GT);
+    ITL_CHECK_LAUNCH();
+    float* coef = nullptr;
+    int32_t* cids = reinterpret_cast<int32_t*>(at(L.cids));
+    if (exact) {
+      coef = reinterpret_cast<float*>(at(L.coef));
+      hipLaunchKernelGGL(ce_onehot_kernel, dim3((unsigned)ceil_div(cap, 256)), dim3(256), 0, stream, ids + c0, count, c0,
+                         cap, gs, coef, cids);
+      ITL_CHECK_LAUNCH();
+    }
+    // dH
+    float* dhp = reinterpret_cast<float*>(at(L.dhp));
+    const int n_tb = (int)ceil_div(cap, kBT), n_dt = (int)ceil_div(d, kBT), n_vt = L.vpad / kBV;
+    const int splits = dh_splits(n_tb, n_dt, (long long)L.vpad * E::kSize / kStepBytes);
+    const bool far = L.vpad * E::kSize / kStepBytes / splits > kNearBMaxSteps;
+    hipLaunchKernelGGL((far ? ce_dh_kernel<kDtype, true> : ce_dh_kernel<kDtype, false>),
+                       dim3((unsigned)(n_tb * n_dt * splits)), dim3(kThreads8), 0, stream, at(L.wt),
+                       reinterpret_cast<const char*>(Gd), L.vpad, d, count, c0, cap, n_tb, n_dt, splits, dhp);
+    ITL_CHECK_LAUNCH();
+    hipLaunchKernelGGL(ce_dh_finish_kernel<kDtype>, dim3((unsigned)cap), dim3(256), 0, stream, dhp, splits, cap, d, rows,
+                       ids + c0, count, c0, gs, coef, W, c.grad_dtype, c.dH);
+    ITL_CHECK_LAUNCH();
+    // dW
+    hipLaunchKernelGGL(ce_transpose_kernel<T>, dim3((unsigned)ceil_div(cap, 64), (unsigned)ceil_div(d, 64)), dim3(256), 0,
+                       stream, reinterpret_cast<const T*>(Hc), cap, d, HT, L.ld_t, count, c0);
+    ITL_CHECK_LAUNCH();
+    const bool single = n <= L.cap;
+    float* acc = single ? nullptr : c.grad_dtype == 1 && !exact ? static_cast<float*>(c.dW) : reinterpret_cast<float*>(at(L.dwacc));
+    void* out = c.dW;
+    int add = 0, out_f32 = c.grad_dtype;
+    if (exact) {
+      // the chunk's one-hot rows first (every row of the target is written), then the contraction on top
+      float* target = single ? static_cast<float*>(c.dW) : c0 == 0 ? static_cast<float*>(c.dW) : acc;
+      e = launch_sampled_dw(Hc, kDtype, cap, d, vocab, cids, coef, target, at(L.sampled), stream);
+      if (e != hipSuccess) return e;
+      out = target, add = 1;
+    } else if (!single) {
+      out = acc, out_f32 = 1, add = c0 > 0;
+    }
+    hipLaunchKernelGGL(ce_dw_kernel<kDtype>, dim3((unsigned)(n_vt * n_dt)), dim3(kThreads8), 0, stream,
+                       reinterpret_cast<const char*>(GT), reinterpret_cast<const char*>(HT), L.ld_t, count, c0, cap,
+                       vocab, d, n_vt, n_dt, gs, add, out_f32, out);
+    ITL_CHECK_LAUNCH();
+    if (exact && !single && c0 > 0) {
+      hipLaunchKernelGGL(ce_add_kernel, dim3((unsigned)ceil_div((long long)vocab * d / 4, 256)), dim3(256), 0, stream,
+                         reinterpret_cast<const float4*>(acc), (long long)vocab * d / 4, static_cast<float4*>(c.dW));
+      ITL_CHECK_LAUNCH();
+    }
+    if (!exact && !single && c0 + L.cap >= n && c.grad_dtype == 0) {
+      hipLaunchKernelGGL(ce_round_kernel, dim3((unsigned)ceil_div((long long)vocab * d / 4, 256)), dim3(256), 0, stream,
+                         reinterpret_cast<const float4*>(acc), (long long)vocab * d / 4, static_cast<uint2*>(c.dW));
+      ITL_CHECK_LAUNCH();
+    }
+  }
+  hipLaunchKernelGGL(ce_token_loss_kernel<kDtype>, dim3((unsigned)ceil_div(n, 4)), dim3(256), 0, stream, H, n, d, slot, lp,
+                     lse, wmean, c.smoothing, c.z_weight, c.token_loss, c.lse, loss_part);
+  hipLaunchKernelGGL(ce_loss_kernel, dim3(1), dim3(1024), 0, stream, loss_part, (int)ceil_div(n, 4), count, c.mean, c.loss);
+  ITL_CHECK_LAUNCH();
+  return hipSuccess;
+}
+
+}  // namespace
+
+size_t cross_entropy_workspace_bytes(long long n_tok, long long d, long long vocab, int dtype, bool grad, int grad_dtype) {
+  return n_tok <= 0 ? 0 : ce_layout(n_tok, d, vocab, dtype, grad, grad_dtype).total;
+}
+
+hipError_t launch_cross_entropy(const CeCall& c, hipStream_t stream) {
+  return c.dtype == 0 ? run_cross_entropy<0>(c, stream) : run_cross_entropy<1>(c, stream);
+}
+
+}  // namespace itl

@@ -82,6 +82,46 @@ hipError_t launch_mismatch_stats(const float* lp, const float* lpr, const float*
 hipError_t launch_check_inputs(const int32_t* tokens, long long n_tok, int vocab, const int64_t* resp_offsets,
                                int n_resp, int* flag, hipStream_t stream);
 
+// The norms around a block (norm.hip). codes (nullable): u as E4M3 codes with
+// u_scale instead of u. gate_stride: 0 (one gate for all rows) or d.
+hipError_t launch_residual_norm(const void* x, const void* y, const void* gate, long long gate_stride,
+                                const void* w_post, const void* w_pre, int dtype, long long n_rows, int d, float scale,
+                                float eps, void* h, void* u, uint8_t* codes, float* u_scale, float* rstd_pre,
+                                float* rstd_post, hipStream_t stream);
+
+size_t norm_backward_workspace_bytes(long long n_rows, long long d);
+
+// dgate: fp32 [d] for one shared gate, else rows of the norm's type.
+hipError_t launch_residual_norm_backward(const void* du, int grad_dtype, const void* dh, const void* h, const void* y,
+                                         const void* gate, long long gate_stride, const void* w_post,
+                                         const void* w_pre, const float* rstd_pre, const float* rstd_post, int dtype,
+                                         long long n_rows, int d, float scale, void* dx, void* dy, void* dgate,
+                                         float* dw_pre, float* dw_post, void* workspace, hipStream_t stream);
+
+// The vocabulary cross entropy (cross_entropy.hip), with the gradient where dH is given.
+struct CeCall {
+  const void *H, *W;
+  int dtype;
+  long long n_tok, d, vocab;
+  const int32_t* targets;
+  float smoothing, z_weight;
+  int mean;  // the loss is the mean over the counted tokens (else their sum)
+  float grad_scale;
+  int grad_dtype;
+  float *loss, *token_loss, *lse;  // lse nullable
+  void *dH, *dW;
+  void* workspace;
+};
+size_t cross_entropy_workspace_bytes(long long n_tok, long long d, long long vocab, int dtype, bool grad, int grad_dtype);
+hipError_t launch_cross_entropy(const CeCall& c, hipStream_t stream);
+
+// One AdamW step over a plan's pieces (adamw.hip).
+size_t adamw_workspace_bytes();
+hipError_t launch_adamw_step(const void* plan, long long n_pieces, int state_bits, void* m, void* v, float* m_scale,
+                             float* v_scale, float* master, const float* lr, int64_t* step, double beta1, double beta2,
+                             double eps, bool with_norm, float max_norm, float* norm, void* workspace,
+                             hipStream_t stream);
+
 inline size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 
 }  // namespace itl

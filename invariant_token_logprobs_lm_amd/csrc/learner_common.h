@@ -1,0 +1,50 @@
+// Element access and roundings shared by the learner's kernels (norms, cross
+// entropy, optimizer step).
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "device_common.h"
+#include "itl_config.h"
+
+namespace itl {
+
+template <int kDtype>
+struct Elem;
+
+template <>
+struct Elem<0> {
+  using T = uint16_t;  // bf16 bits
+  static constexpr int kSize = 2;
+  __device__ static __forceinline__ float to_f(T x) { return __uint_as_float((uint32_t)x << 16); }
+  // Round to nearest even; a NaN stays a (quiet) NaN, an overflow is infinite.
+  __device__ static __forceinline__ T from_f(float f) { return __builtin_bit_cast(T, (__bf16)f); }
+};
+
+template <>
+struct Elem<1> {
+  using T = float;
+  static constexpr int kSize = 4;
+  __device__ static __forceinline__ float to_f(T x) { return x; }
+  __device__ static __forceinline__ T from_f(float f) { return f; }
+};
+
+// E4M3 code of |x| <= 448 (up to the rounding of a quotient by amax / 448),
+// to nearest even, subnormals included, by the conversion instruction
+// (gfx950 converts to the OCP format: the codes of all roundings are tested
+// against the format's definition).
+__device__ __forceinline__ uint32_t e4m3_code(float x) {
+  return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(x, x, 0, false) & 0xffu;
+}
+
+// Four codes, the first in the low byte.
+__device__ __forceinline__ uint32_t e4m3_code4(float a, float b, float c, float d) {
+  int w = __builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false);
+  w = __builtin_amdgcn_cvt_pk_fp8_f32(c, d, w, true);
+  return (uint32_t)w;
+}
+
+__device__ __forceinline__ float e4m3_value(uint32_t code) { return __builtin_amdgcn_cvt_f32_fp8((int)code, 0); }
+
+}  // namespace itl
