@@ -17,12 +17,21 @@
 //   dp = scale gate dx,  dgate = scale p dx (summed over rows for one shared gate)
 //   dw_post = sum_t dp q,  dq = dp w_post,  dy = r_post (dq - q <dq q>)
 //
-// Rows: one workgroup of 256 threads per row; a thread takes columns
-// tid, tid + 256, ...; sums go up a fixed tree (thread, wavefront butterfly,
-// wavefronts in order), so a row's results depend on the row and its width
-// alone. Column sums (dw_pre, dw_post, a shared dgate) are taken over fixed
-// runs of rows, then over the runs in order: run-to-run deterministic, no
-// atomics.
+// Rows of up to kNormMaxWidth values are held in registers: read once,
+// written once. A row belongs to one wavefront (up to kWaveWidth values) or
+// to a workgroup of four; a thread holds groups of 8 values, consecutive ones
+// (16-byte loads) where the width is a multiple of 8, else ones a row of
+// threads apart (whole lines per wavefront still). Wider rows are walked by
+// norm_rows_kernel, which reads them again for each pass. Sums go up a fixed
+// tree (thread, wavefront butterfly, wavefronts in order) chosen by the width
+// alone, so a row's results depend on the row and its width alone.
+//
+// The backward needs two means per row, the second of values that hold the
+// first; written out, <dq q> = <s (dh + r_pre dn)> - <dn n> <s r_pre n> with
+// s = scale gate w_post q, so three sums in one go give both. A thread keeps
+// the column sums (dw_pre, dw_post, a shared dgate) of its columns over all
+// rows of its workgroup in registers; the workgroups' sums are then added in
+// order: run-to-run deterministic, no atomics.
 
 #include <algorithm>
 
@@ -72,6 +81,162 @@ struct NormArgs {
   int d;
   float scale, eps;
 };
+
+// ---- rows in registers
+
+// Eight columns of a thread: group c of a row of T threads. Whole vectors:
+// columns 8 (c T + lane) .. + 7; else c 8 T + j T + lane.
+template <bool kVec>
+struct Columns {
+  int d, T, lane;
+  __device__ __forceinline__ int at(int c, int j) const { return kVec ? 8 * (c * T + lane) + j : (8 * c + j) * T + lane; }
+};
+
+// Values of group c (zeros past the row).
+template <int kDtype, bool kVec>
+__device__ __forceinline__ void load_group(const void* row, const Columns<kVec>& k, int c, float (&v)[8]) {
+  using E = Elem<kDtype>;
+  using T = typename E::T;
+  if constexpr (kVec) {
+    const int at = k.at(c, 0);
+    uint4 w[E::kSize / 2];
+#pragma unroll
+    for (int i = 0; i < E::kSize / 2; ++i)
+      w[i] = at < k.d ? reinterpret_cast<const uint4*>(static_cast<const T*>(row) + at)[i] : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const uint32_t x = (&w[0].x)[kDtype == 0 ? j >> 1 : j];
+      v[j] = kDtype == 1 ? __uint_as_float(x) : __uint_as_float((j & 1) ? (x & 0xffff0000u) : (x << 16));
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int at = k.at(c, j);
+      v[j] = at < k.d ? E::to_f(static_cast<const T*>(row)[at]) : 0.0f;
+    }
+  }
+}
+
+// Stores group c rounded to the type; v becomes the stored values.
+template <int kDtype, bool kVec>
+__device__ __forceinline__ void store_group(void* row, const Columns<kVec>& k, int c, float (&v)[8]) {
+  using E = Elem<kDtype>;
+  using T = typename E::T;
+  if constexpr (kDtype == 0 && kVec) {
+    uint32_t w[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      w[j] = (uint32_t)E::from_f(v[2 * j]) | ((uint32_t)E::from_f(v[2 * j + 1]) << 16);
+      v[2 * j] = __uint_as_float(w[j] << 16);
+      v[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
+    }
+    const int at = k.at(c, 0);
+    if (at < k.d) *reinterpret_cast<uint4*>(static_cast<T*>(row) + at) = make_uint4(w[0], w[1], w[2], w[3]);
+  } else if constexpr (kVec) {
+    const int at = k.at(c, 0);
+    if (at < k.d) {
+      float4* o = reinterpret_cast<float4*>(static_cast<float*>(row) + at);
+      o[0] = make_float4(v[0], v[1], v[2], v[3]);
+      o[1] = make_float4(v[4], v[5], v[6], v[7]);
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const T s = E::from_f(v[j]);
+      v[j] = E::to_f(s);
+      const int at = k.at(c, j);
+      if (at < k.d) static_cast<T*>(row)[at] = s;
+    }
+  }
+}
+
+// One row per kWaves wavefronts, kGroups groups of 8 values per thread.
+template <int kDtype, bool kFp8, bool kVec, int kWaves, int kGroups>
+__global__ __launch_bounds__(kNormThreads) void norm_held_kernel(NormArgs a) {
+  using T = typename Elem<kDtype>::T;
+  __shared__ float lds[kWaves];
+  const long long row = kWaves == 1 ? (long long)blockIdx.x * (kNormThreads / 64) + (threadIdx.x >> 6) : blockIdx.x;
+  if (row >= a.n_rows) return;  // (whole wavefronts, and only where a wavefront is alone)
+  const Columns<kVec> k{a.d, 64 * kWaves, kWaves == 1 ? (int)(threadIdx.x & 63) : (int)threadIdx.x};
+  const size_t base = (size_t)row * a.d;
+  const float inv_d = (float)a.d;
+  float x[kGroups][8], y[kGroups][8];
+#pragma unroll
+  for (int c = 0; c < kGroups; ++c) {
+    load_group<kDtype>(static_cast<const T*>(a.x) + base, k, c, x[c]);
+    if (a.y) load_group<kDtype>(static_cast<const T*>(a.y) + base, k, c, y[c]);
+  }
+  if (a.y) {
+    if (a.w_post) {
+      float ss = 0.0f;
+#pragma unroll
+      for (int c = 0; c < kGroups; ++c)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) ss += y[c][j] * y[c][j];
+      const float r_post = 1.0f / sqrtf(block_sum<kWaves>(ss, lds) / inv_d + a.eps);
+      if (k.lane == 0 && a.rstd_post) a.rstd_post[row] = r_post;
+#pragma unroll
+      for (int c = 0; c < kGroups; ++c) {
+        float w[8];
+        load_group<kDtype>(a.w_post, k, c, w);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) y[c][j] = y[c][j] * r_post * w[j];
+      }
+    }
+    if (a.gate) {
+#pragma unroll
+      for (int c = 0; c < kGroups; ++c) {
+        float w[8];
+        load_group<kDtype>(static_cast<const T*>(a.gate) + (size_t)row * a.gate_stride, k, c, w);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) y[c][j] *= w[j];
+      }
+    }
+#pragma unroll
+    for (int c = 0; c < kGroups; ++c) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) x[c][j] += a.scale * y[c][j];
+      store_group<kDtype>(static_cast<T*>(a.h) + base, k, c, x[c]);
+    }
+  }
+  float ss = 0.0f;
+#pragma unroll
+  for (int c = 0; c < kGroups; ++c)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) ss += x[c][j] * x[c][j];
+  const float r_pre = 1.0f / sqrtf(block_sum<kWaves>(ss, lds) / inv_d + a.eps);
+  if (k.lane == 0 && a.rstd_pre) a.rstd_pre[row] = r_pre;
+#pragma unroll
+  for (int c = 0; c < kGroups; ++c) {
+    float w[8];
+    load_group<kDtype>(a.w_pre, k, c, w);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) x[c][j] = x[c][j] * r_pre * w[j];
+    if constexpr (!kFp8) store_group<kDtype>(static_cast<T*>(a.u) + base, k, c, x[c]);
+  }
+  if constexpr (kFp8) {
+    float amax = 0.0f;
+#pragma unroll
+    for (int c = 0; c < kGroups; ++c)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) amax = fmaxf(amax, fabsf(x[c][j]));
+    amax = block_max<kWaves>(amax, lds);
+    const float s = amax > 0.0f ? __fdiv_rn(amax, 448.0f) : 1.0f;
+    if (k.lane == 0) a.u_scale[row] = s;
+#pragma unroll
+    for (int c = 0; c < kGroups; ++c) {
+      const int at = k.at(c, 0);
+      float q[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) q[j] = __fdiv_rn(x[c][j], s);
+      if (at < k.d)
+        *reinterpret_cast<uint2*>(a.codes + base + at) =
+            make_uint2(e4m3_code4(q[0], q[1], q[2], q[3]), e4m3_code4(q[4], q[5], q[6], q[7]));
+    }
+  }
+}
+
+// ---- rows of any width
 
 // Any width: columns one by one, a row's later passes read it again (from
 // the caches; h by the thread that wrote it).
@@ -140,6 +305,113 @@ struct NormBwdArgs {
   int d, runs;
   float scale;
 };
+
+// The whole backward of rows blockIdx.x, + gridDim.x, ... (kGroups groups of 8
+// columns per thread, blockDim.x threads per row), its column sums to
+// part[blockIdx.x].
+constexpr int kBwdMaxWaves = 8;
+
+template <int kDtype, int kGrad, bool kVec, int kGroups>
+__global__ __launch_bounds__(64 * kBwdMaxWaves) void norm_backward_held_kernel(NormBwdArgs a) {
+  using T = typename Elem<kDtype>::T;
+  using TG = typename Elem<kGrad>::T;
+  __shared__ float lds[2][kBwdMaxWaves][3];
+  const Columns<kVec> k{a.d, (int)blockDim.x, (int)threadIdx.x};
+  const int wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
+  const float inv_d = (float)a.d;
+  const bool shared_gate = a.gate && a.gate_stride == 0;
+  float s_pre[kGroups][8], s_post[kGroups][8], s_gate[kGroups][8];
+#pragma unroll
+  for (int c = 0; c < kGroups; ++c)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) s_pre[c][j] = s_post[c][j] = s_gate[c][j] = 0.0f;
+  int flip = 0;
+  for (long long row = blockIdx.x; row < a.n_rows; row += gridDim.x, flip ^= 1) {
+    const size_t base = (size_t)row * a.d;
+    const float r_pre = a.rstd_pre[row], r_post = a.w_post ? a.rstd_post[row] : 1.0f;
+    // dx without the mean's part, n and q; b = gate scale (w_post)
+    float g[kGroups][8], n[kGroups][8], q[kGroups][8], dn[kGroups][8];
+    float A = 0.0f, B = 0.0f, C = 0.0f;
+#pragma unroll
+    for (int c = 0; c < kGroups; ++c) {
+      float w[8];
+      load_group<kGrad>(static_cast<const TG*>(a.du) + base, k, c, dn[c]);
+      load_group<kDtype>(static_cast<const T*>(a.h) + base, k, c, n[c]);
+      if (a.dh) load_group<kDtype>(static_cast<const T*>(a.dh) + base, k, c, g[c]);
+      if (a.y) load_group<kDtype>(static_cast<const T*>(a.y) + base, k, c, q[c]);
+      load_group<kDtype>(a.w_pre, k, c, w);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        n[c][j] *= r_pre;
+        s_pre[c][j] += dn[c][j] * n[c][j];
+        dn[c][j] *= w[j];
+        A += dn[c][j] * n[c][j];
+        const float v = r_pre * dn[c][j];
+        g[c][j] = a.dh ? g[c][j] + v : v;
+      }
+      if (a.w_post) {
+        float wp[8], gt[8];
+        load_group<kDtype>(a.w_post, k, c, wp);
+        if (a.gate) load_group<kDtype>(static_cast<const T*>(a.gate) + (size_t)row * a.gate_stride, k, c, gt);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          q[c][j] *= r_post;
+          const float s = a.scale * (a.gate ? gt[j] : 1.0f) * wp[j] * q[c][j];
+          B += s * g[c][j];
+          C += s * (r_pre * n[c][j]);
+        }
+      }
+    }
+    A = wave_sum(A);
+    if (a.w_post) B = wave_sum(B), C = wave_sum(C);
+    // (two buffers: a row's sums are read while the next row's are written)
+    if ((threadIdx.x & 63) == 0) {
+      lds[flip][wave][0] = A;
+      lds[flip][wave][1] = B;
+      lds[flip][wave][2] = C;
+    }
+    __syncthreads();
+    A = lds[flip][0][0], B = lds[flip][0][1], C = lds[flip][0][2];
+    for (int w = 1; w < waves; ++w) A += lds[flip][w][0], B += lds[flip][w][1], C += lds[flip][w][2];
+    const float c1 = A / inv_d;
+    const float c2 = (B - c1 * C) / inv_d;
+#pragma unroll
+    for (int c = 0; c < kGroups; ++c) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) g[c][j] -= r_pre * (n[c][j] * c1);
+      if (a.y) {
+        float wp[8], gt[8], dy[8], dg[8];
+        if (a.w_post) load_group<kDtype>(a.w_post, k, c, wp);
+        if (a.gate) load_group<kDtype>(static_cast<const T*>(a.gate) + (size_t)row * a.gate_stride, k, c, gt);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const float sdx = a.scale * g[c][j];
+          const float dp = a.gate ? sdx * gt[j] : sdx;
+          if (a.gate) {
+            dg[j] = sdx * (a.w_post ? q[c][j] * wp[j] : q[c][j]);
+            s_gate[c][j] += dg[j];
+          }
+          if (a.w_post) {
+            s_post[c][j] += dp * q[c][j];
+            dy[j] = r_post * (dp * wp[j] - q[c][j] * c2);
+          } else {
+            dy[j] = dp;
+          }
+        }
+        store_group<kDtype>(static_cast<T*>(a.dy) + base, k, c, dy);
+        if (a.dgate_rows) store_group<kDtype>(static_cast<T*>(a.dgate_rows) + base, k, c, dg);
+      }
+      store_group<kDtype>(static_cast<T*>(a.dx) + base, k, c, g[c]);
+    }
+  }
+  float* part = a.part + (size_t)blockIdx.x * 3 * a.d;
+#pragma unroll
+  for (int c = 0; c < kGroups; ++c) {
+    store_group<1>(part, k, c, s_pre[c]);
+    if (a.w_post) store_group<1>(part + a.d, k, c, s_post[c]);
+    if (shared_gate) store_group<1>(part + 2 * (size_t)a.d, k, c, s_gate[c]);
+  }
+}
 
 // The rows' part of the backward, any width. means_only: just the rows'
 // means, for column sums that are taken before dx is written over dh.
@@ -246,26 +518,68 @@ __global__ __launch_bounds__(kNormThreads) void norm_backward_columns_kernel(Nor
   }
 }
 
-// The runs' sums in order: thread (column, which of the three).
-__global__ __launch_bounds__(256) void norm_backward_finish_kernel(const float* __restrict__ part, int runs, int d,
-                                                                   float* __restrict__ dw_pre,
-                                                                   float* __restrict__ dw_post,
-                                                                   float* __restrict__ dgate) {
-  const int k = blockIdx.x * 256 + threadIdx.x;
+// The runs' sums: 64 columns of one of the three sums per workgroup, its 16
+// wavefronts over runs w, w + 16, ... in order, then the wavefronts in order.
+constexpr int kFinishWaves = 16;
+__global__ __launch_bounds__(64 * kFinishWaves) void norm_backward_finish_kernel(const float* __restrict__ part, int runs,
+                                                                                 int d, float* __restrict__ dw_pre,
+                                                                                 float* __restrict__ dw_post,
+                                                                                 float* __restrict__ dgate) {
+  __shared__ float lds[kFinishWaves][64];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int k = blockIdx.x * 64 + lane;
   float* out = blockIdx.y == 0 ? dw_pre : blockIdx.y == 1 ? dw_post : dgate;
-  if (k >= d || !out) return;
+  if (!out) return;
   float s = 0.0f;
-  for (int r = 0; r < runs; ++r) s += part[((size_t)r * 3 + blockIdx.y) * d + k];
+  if (k < d) {
+#pragma unroll 8
+    for (int r = wave; r < runs; r += kFinishWaves) s += part[((size_t)r * 3 + blockIdx.y) * d + k];
+  }
+  lds[wave][lane] = s;
+  __syncthreads();
+  if (wave != 0 || k >= d) return;
+  for (int w = 1; w < kFinishWaves; ++w) s += lds[w][lane];
   out[k] = s;
 }
 
-// Runs of rows of the column sums: about 64 rows each, at most 256.
-int norm_runs(long long n_rows) { return (int)std::min<long long>(256, ceil_div(n_rows, 64)); }
+constexpr int kWaveWidth = 4096;      // widest row of one wavefront
+constexpr int kNormMaxWidth = 16384;  // widest row held in registers
+constexpr int kBwdMaxWidth = 8192;    // the same of the backward
+
+// Runs of rows of the column sums. Held rows: a workgroup's, about 4 rows
+// or more each and at most 1024 (four workgroups per CU at the narrower
+// widths). Wider rows: about 64 rows each, at most 256.
+int norm_runs(long long n_rows, long long d) {
+  return d <= kBwdMaxWidth ? (int)std::min<long long>(1024, ceil_div(n_rows, 4))
+                            : (int)std::min<long long>(256, ceil_div(n_rows, 64));
+}
+
+template <int kDtype, bool kFp8, bool kVec>
+void run_norm(const NormArgs& a, hipStream_t stream) {
+  const dim3 block(kNormThreads), one((unsigned)ceil_div(a.n_rows, kNormThreads / 64)), four((unsigned)a.n_rows);
+  const int groups = (int)ceil_div(a.d, 8);
+#define ITL_NORM(waves, n, grid) \
+  hipLaunchKernelGGL((norm_held_kernel<kDtype, kFp8, kVec, waves, n>), grid, block, 0, stream, a)
+  if (a.d <= kWaveWidth) {
+    if (groups <= 64) ITL_NORM(1, 1, one);
+    else if (groups <= 128) ITL_NORM(1, 2, one);
+    else if (groups <= 256) ITL_NORM(1, 4, one);
+    else if (groups <= 320) ITL_NORM(1, 5, one);
+    else ITL_NORM(1, 8, one);
+  } else if (a.d <= kNormMaxWidth) {
+    if (groups <= 768) ITL_NORM(4, 3, four);
+    else if (groups <= 1024) ITL_NORM(4, 4, four);
+    else ITL_NORM(4, 8, four);
+  } else {
+    hipLaunchKernelGGL((norm_rows_kernel<kDtype, kFp8>), four, block, 0, stream, a);
+  }
+#undef ITL_NORM
+}
 
 }  // namespace
 
 size_t norm_backward_workspace_bytes(long long n_rows, long long d) {
-  return align256((size_t)n_rows * 4) + align256((size_t)norm_runs(n_rows) * 3 * (size_t)d * 4);
+  return align256((size_t)n_rows * 4) + align256((size_t)norm_runs(n_rows, d) * 3 * (size_t)d * 4);
 }
 
 hipError_t launch_residual_norm(const void* x, const void* y, const void* gate, long long gate_stride,
@@ -273,21 +587,40 @@ hipError_t launch_residual_norm(const void* x, const void* y, const void* gate, 
                                 float eps, void* h, void* u, uint8_t* codes, float* u_scale, float* rstd_pre,
                                 float* rstd_post, hipStream_t stream) {
   const NormArgs a{x, y, gate, w_post, w_pre, h, u, codes, u_scale, rstd_pre, rstd_post, n_rows, gate_stride, d, scale, eps};
-  const dim3 grid((unsigned)n_rows), block(kNormThreads);
   if (codes) {
-    if (dtype == 0) hipLaunchKernelGGL((norm_rows_kernel<0, true>), grid, block, 0, stream, a);
-    else hipLaunchKernelGGL((norm_rows_kernel<1, true>), grid, block, 0, stream, a);
+    if (dtype == 0) run_norm<0, true, true>(a, stream);
+    else run_norm<1, true, true>(a, stream);
+  } else if (d % 8 == 0) {
+    if (dtype == 0) run_norm<0, false, true>(a, stream);
+    else run_norm<1, false, true>(a, stream);
   } else {
-    if (dtype == 0) hipLaunchKernelGGL((norm_rows_kernel<0, false>), grid, block, 0, stream, a);
-    else hipLaunchKernelGGL((norm_rows_kernel<1, false>), grid, block, 0, stream, a);
+    if (dtype == 0) run_norm<0, false, false>(a, stream);
+    else run_norm<1, false, false>(a, stream);
   }
   return hipGetLastError();
 }
 
 namespace {
 
+template <int kDtype, int kGrad, bool kVec>
+void run_held_backward(const NormBwdArgs& a, hipStream_t stream) {
+  const int groups = (int)ceil_div(a.d, 8);
+  const dim3 grid((unsigned)a.runs);
+  if (groups <= 64 * kBwdMaxWaves)
+    hipLaunchKernelGGL((norm_backward_held_kernel<kDtype, kGrad, kVec, 1>), grid, dim3((unsigned)(ceil_div(groups, 64) * 64)),
+                       0, stream, a);
+  else
+    hipLaunchKernelGGL((norm_backward_held_kernel<kDtype, kGrad, kVec, 2>), grid,
+                       dim3((unsigned)(ceil_div(groups, 128) * 64)), 0, stream, a);
+}
+
 template <int kDtype, int kGrad>
 void run_norm_backward(const NormBwdArgs& a, hipStream_t stream) {
+  if (a.d <= kBwdMaxWidth) {
+    if (a.d % 8 == 0) run_held_backward<kDtype, kGrad, true>(a, stream);
+    else run_held_backward<kDtype, kGrad, false>(a, stream);
+    return;
+  }
   const dim3 rows((unsigned)a.n_rows), columns((unsigned)ceil_div(a.d, 64), (unsigned)a.runs), block(kNormThreads);
   const bool over = a.dx == a.dh;
   hipLaunchKernelGGL((norm_backward_rows_kernel<kDtype, kGrad>), rows, block, 0, stream, a, over);
@@ -306,7 +639,7 @@ hipError_t launch_residual_norm_backward(const void* du, int grad_dtype, const v
   const bool shared_gate = gate && gate_stride == 0;
   NormBwdArgs a{du, dh, h, y, gate, w_post, w_pre, rstd_pre, rstd_post, dx, dy, gate && !shared_gate ? dgate : nullptr,
                 reinterpret_cast<float*>(ws), reinterpret_cast<float*>(ws + align256((size_t)n_rows * 4)), n_rows,
-                gate_stride, d, norm_runs(n_rows), scale};
+                gate_stride, d, norm_runs(n_rows, d), scale};
   if (n_rows > 0) {
     if (dtype == 0) {
       if (grad_dtype == 0) run_norm_backward<0, 0>(a, stream);
@@ -315,7 +648,7 @@ hipError_t launch_residual_norm_backward(const void* du, int grad_dtype, const v
       run_norm_backward<1, 1>(a, stream);
     }
   }
-  hipLaunchKernelGGL(norm_backward_finish_kernel, dim3((unsigned)ceil_div(d, 256), 3), dim3(256), 0, stream, a.part,
+  hipLaunchKernelGGL(norm_backward_finish_kernel, dim3((unsigned)ceil_div(d, 64), 3), dim3(64 * kFinishWaves), 0, stream, a.part,
                      a.runs, d, dw_pre, w_post ? dw_post : nullptr, shared_gate ? static_cast<float*>(dgate) : nullptr);
   return hipGetLastError();
 }
