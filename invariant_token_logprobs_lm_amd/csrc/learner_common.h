@@ -47,4 +47,22 @@ __device__ __forceinline__ uint32_t e4m3_code4(float a, float b, float c, float 
 
 __device__ __forceinline__ float e4m3_value(uint32_t code) { return __builtin_amdgcn_cvt_f32_fp8((int)code, 0); }
 
+// wave_sum's butterfly (the same additions, so the same bits) with its steps
+// within 16 lanes as register moves between lanes instead of LDS permutes:
+// after the steps over lanes 1 and 2 apart a quad's lanes hold one value, so
+// mirroring 8 lanes is the step 4 apart; then mirroring 16 the step 8 apart.
+template <int kControl>
+__device__ __forceinline__ float lane_move(float x) {
+  return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(x), kControl, 0xf, 0xf, true));
+}
+__device__ __forceinline__ float wave_sum_moves(float x) {
+  x += lane_move<0xB1>(x);   // lanes 1, 0, 3, 2 of each quad
+  x += lane_move<0x4E>(x);   // lanes 2, 3, 0, 1
+  x += lane_move<0x141>(x);  // 8 lanes mirrored
+  x += lane_move<0x140>(x);  // 16 lanes mirrored
+  x += __shfl_xor(x, 16, 64);
+  x += __shfl_xor(x, 32, 64);
+  return x;
+}
+
 }  // namespace itl

@@ -47,7 +47,7 @@ constexpr int kNormThreads = 256;
 // Sum over a workgroup of kWaves wavefronts, the same bits in every thread.
 template <int kWaves>
 __device__ __forceinline__ float block_sum(float x, float* lds) {
-  x = wave_sum(x);
+  x = wave_sum_moves(x);
   if constexpr (kWaves == 1) return x;
   __syncthreads();  // the previous sum's readers are done
   if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = x;
@@ -92,29 +92,45 @@ struct Columns {
   __device__ __forceinline__ int at(int c, int j) const { return kVec ? 8 * (c * T + lane) + j : (8 * c + j) * T + lane; }
 };
 
-// Values of group c (zeros past the row).
+// Group c as it lies in memory (zeros past the row), and its values.
 template <int kDtype, bool kVec>
-__device__ __forceinline__ void load_group(const void* row, const Columns<kVec>& k, int c, float (&v)[8]) {
+struct Group {
   using E = Elem<kDtype>;
   using T = typename E::T;
-  if constexpr (kVec) {
-    const int at = k.at(c, 0);
-    uint4 w[E::kSize / 2];
+  uint32_t w[kVec ? 2 * E::kSize : 8];
+
+  __device__ __forceinline__ void load(const void* row, const Columns<kVec>& k, int c) {
+    if constexpr (kVec) {
+      const int at = k.at(c, 0);
 #pragma unroll
-    for (int i = 0; i < E::kSize / 2; ++i)
-      w[i] = at < k.d ? reinterpret_cast<const uint4*>(static_cast<const T*>(row) + at)[i] : make_uint4(0u, 0u, 0u, 0u);
+      for (int i = 0; i < E::kSize / 2; ++i) {
+        const uint4 v = at < k.d ? reinterpret_cast<const uint4*>(static_cast<const T*>(row) + at)[i]
+                                 : make_uint4(0u, 0u, 0u, 0u);
+        w[4 * i] = v.x, w[4 * i + 1] = v.y, w[4 * i + 2] = v.z, w[4 * i + 3] = v.w;
+      }
+    } else {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const uint32_t x = (&w[0].x)[kDtype == 0 ? j >> 1 : j];
-      v[j] = kDtype == 1 ? __uint_as_float(x) : __uint_as_float((j & 1) ? (x & 0xffff0000u) : (x << 16));
-    }
-  } else {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const int at = k.at(c, j);
-      v[j] = at < k.d ? E::to_f(static_cast<const T*>(row)[at]) : 0.0f;
+      for (int j = 0; j < 8; ++j) {
+        const int at = k.at(c, j);
+        const T v = at < k.d ? static_cast<const T*>(row)[at] : T(0);
+        if constexpr (kDtype == 0) w[j] = v;
+        else w[j] = __float_as_uint(v);
+      }
     }
   }
+  __device__ __forceinline__ float operator[](int j) const {
+    if constexpr (kDtype == 1) return __uint_as_float(w[j]);
+    else if constexpr (kVec) return __uint_as_float((j & 1) ? (w[j >> 1] & 0xffff0000u) : (w[j >> 1] << 16));
+    else return __uint_as_float(w[j] << 16);
+  }
+};
+
+template <int kDtype, bool kVec>
+__device__ __forceinline__ void load_group(const void* row, const Columns<kVec>& k, int c, float (&v)[8]) {
+  Group<kDtype, kVec> g;
+  g.load(row, k, c);
+#pragma unroll
+  for (int j = 0; j < 8; ++j) v[j] = g[j];
 }
 
 // Stores group c rounded to the type; v becomes the stored values.
@@ -312,7 +328,7 @@ struct NormBwdArgs {
 constexpr int kBwdMaxWaves = 8;
 
 template <int kDtype, int kGrad, bool kVec, int kGroups>
-__global__ __launch_bounds__(64 * kBwdMaxWaves) void norm_backward_held_kernel(NormBwdArgs a) {
+__global__ __launch_bounds__(64 * kBwdMaxWaves, kGroups == 1 ? 3 : 2) void norm_backward_held_kernel(NormBwdArgs a) {
   using T = typename Elem<kDtype>::T;
   using TG = typename Elem<kGrad>::T;
   __shared__ float lds[2][kBwdMaxWaves][3];
@@ -325,45 +341,68 @@ __global__ __launch_bounds__(64 * kBwdMaxWaves) void norm_backward_held_kernel(N
   for (int c = 0; c < kGroups; ++c)
 #pragma unroll
     for (int j = 0; j < 8; ++j) s_pre[c][j] = s_post[c][j] = s_gate[c][j] = 0.0f;
+  using G = Group<kDtype, kVec>;
+  G w_pre[kGroups], w_post[kGroups], gate[kGroups];
+#pragma unroll
+  for (int c = 0; c < kGroups; ++c) {
+    w_pre[c].load(a.w_pre, k, c);
+    if (a.w_post) w_post[c].load(a.w_post, k, c);
+    if (shared_gate) gate[c].load(a.gate, k, c);
+  }
+  // A row's values as loaded: the next row's are on their way while a row is
+  // summed and written.
+  Group<kGrad, kVec> r_du[kGroups];
+  G r_h[kGroups], r_dh[kGroups], r_y[kGroups], r_gate[kGroups];
+  float n_pre, n_post;
+  auto fetch = [&](long long row) {
+    const size_t base = (size_t)row * a.d;
+    n_pre = a.rstd_pre[row];
+    n_post = a.w_post ? a.rstd_post[row] : 1.0f;
+#pragma unroll
+    for (int c = 0; c < kGroups; ++c) {
+      r_du[c].load(static_cast<const TG*>(a.du) + base, k, c);
+      r_h[c].load(static_cast<const T*>(a.h) + base, k, c);
+      if (a.dh) r_dh[c].load(static_cast<const T*>(a.dh) + base, k, c);
+      if (a.y) r_y[c].load(static_cast<const T*>(a.y) + base, k, c);
+      if (a.gate && !shared_gate) r_gate[c].load(static_cast<const T*>(a.gate) + base, k, c);
+    }
+  };
+  constexpr bool kAhead = kGroups == 1;  // (two groups have no registers left for it)
+  if (kAhead && blockIdx.x < a.n_rows) fetch(blockIdx.x);
   int flip = 0;
   for (long long row = blockIdx.x; row < a.n_rows; row += gridDim.x, flip ^= 1) {
     const size_t base = (size_t)row * a.d;
-    const float r_pre = a.rstd_pre[row], r_post = a.w_post ? a.rstd_post[row] : 1.0f;
-    // dx without the mean's part, n and q; b = gate scale (w_post)
-    float g[kGroups][8], n[kGroups][8], q[kGroups][8], dn[kGroups][8];
+    if constexpr (!kAhead) fetch(row);
+    const float r_pre = n_pre, r_post = n_post;
+    // g = dx without the mean's part, n, q
+    float g[kGroups][8], n[kGroups][8], q[kGroups][8];
     float A = 0.0f, B = 0.0f, C = 0.0f;
 #pragma unroll
     for (int c = 0; c < kGroups; ++c) {
-      float w[8];
-      load_group<kGrad>(static_cast<const TG*>(a.du) + base, k, c, dn[c]);
-      load_group<kDtype>(static_cast<const T*>(a.h) + base, k, c, n[c]);
-      if (a.dh) load_group<kDtype>(static_cast<const T*>(a.dh) + base, k, c, g[c]);
-      if (a.y) load_group<kDtype>(static_cast<const T*>(a.y) + base, k, c, q[c]);
-      load_group<kDtype>(a.w_pre, k, c, w);
+      if (!shared_gate) gate[c] = r_gate[c];
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        n[c][j] *= r_pre;
-        s_pre[c][j] += dn[c][j] * n[c][j];
-        dn[c][j] *= w[j];
-        A += dn[c][j] * n[c][j];
-        const float v = r_pre * dn[c][j];
-        g[c][j] = a.dh ? g[c][j] + v : v;
+        const float u = r_du[c][j];
+        n[c][j] = r_h[c][j] * r_pre;
+        s_pre[c][j] += u * n[c][j];
+        const float dn = u * w_pre[c][j];
+        A += dn * n[c][j];
+        const float v = r_pre * dn;
+        g[c][j] = a.dh ? r_dh[c][j] + v : v;
+        q[c][j] = a.y ? r_y[c][j] * r_post : 0.0f;
       }
       if (a.w_post) {
-        float wp[8], gt[8];
-        load_group<kDtype>(a.w_post, k, c, wp);
-        if (a.gate) load_group<kDtype>(static_cast<const T*>(a.gate) + (size_t)row * a.gate_stride, k, c, gt);
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-          q[c][j] *= r_post;
-          const float s = a.scale * (a.gate ? gt[j] : 1.0f) * wp[j] * q[c][j];
+          const float s = a.scale * (a.gate ? gate[c][j] : 1.0f) * w_post[c][j] * q[c][j];
           B += s * g[c][j];
           C += s * (r_pre * n[c][j]);
         }
       }
     }
-    A = wave_sum(A);
-    if (a.w_post) B = wave_sum(B), C = wave_sum(C);
+    if (kAhead && row + gridDim.x < a.n_rows) fetch(row + gridDim.x);
+    A = wave_sum_moves(A);
+    if (a.w_post) B = wave_sum_moves(B), C = wave_sum_moves(C);
     // (two buffers: a row's sums are read while the next row's are written)
     if ((threadIdx.x & 63) == 0) {
       lds[flip][wave][0] = A;
@@ -380,20 +419,18 @@ __global__ __launch_bounds__(64 * kBwdMaxWaves) void norm_backward_held_kernel(N
 #pragma unroll
       for (int j = 0; j < 8; ++j) g[c][j] -= r_pre * (n[c][j] * c1);
       if (a.y) {
-        float wp[8], gt[8], dy[8], dg[8];
-        if (a.w_post) load_group<kDtype>(a.w_post, k, c, wp);
-        if (a.gate) load_group<kDtype>(static_cast<const T*>(a.gate) + (size_t)row * a.gate_stride, k, c, gt);
+        float dy[8], dg[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
           const float sdx = a.scale * g[c][j];
-          const float dp = a.gate ? sdx * gt[j] : sdx;
+          const float dp = a.gate ? sdx * gate[c][j] : sdx;
           if (a.gate) {
-            dg[j] = sdx * (a.w_post ? q[c][j] * wp[j] : q[c][j]);
+            dg[j] = sdx * (a.w_post ? q[c][j] * w_post[c][j] : q[c][j]);
             s_gate[c][j] += dg[j];
           }
           if (a.w_post) {
             s_post[c][j] += dp * q[c][j];
-            dy[j] = r_post * (dp * wp[j] - q[c][j] * c2);
+            dy[j] = r_post * (dp * w_post[c][j] - q[c][j] * c2);
           } else {
             dy[j] = dp;
           }
@@ -546,12 +583,22 @@ constexpr int kWaveWidth = 4096;      // widest row of one wavefront
 constexpr int kNormMaxWidth = 16384;  // widest row held in registers
 constexpr int kBwdMaxWidth = 8192;    // the same of the backward
 
-// Runs of rows of the column sums. Held rows: a workgroup's, about 4 rows
-// or more each and at most 1024 (four workgroups per CU at the narrower
-// widths). Wider rows: about 64 rows each, at most 256.
+// Whether the backward holds the rows (two groups of scattered columns would
+// not fit the registers), and its wavefronts per row then.
+bool held_backward(long long d) { return d <= (d % 8 == 0 ? kBwdMaxWidth : kBwdMaxWidth / 2); }
+int held_waves(long long d) {
+  const long long groups = ceil_div(d, 8);
+  return (int)(groups <= 64 * kBwdMaxWaves ? ceil_div(groups, 64) : ceil_div(groups, 128));
+}
+
+// Runs of rows of the column sums. Held rows: a workgroup's, as many
+// workgroups as run at once (12 wavefronts per CU with one group, 8 with two:
+// their registers), so that few sums are left to add, and 4 rows each where
+// there are fewer. Other rows: about 64 rows each, at most 256.
 int norm_runs(long long n_rows, long long d) {
-  return d <= kBwdMaxWidth ? (int)std::min<long long>(1024, ceil_div(n_rows, 4))
-                            : (int)std::min<long long>(256, ceil_div(n_rows, 64));
+  if (!held_backward(d)) return (int)std::min<long long>(256, ceil_div(n_rows, 64));
+  const int per_cu = std::max(1, (ceil_div(d, 8) <= 64 * kBwdMaxWaves ? 12 : 8) / held_waves(d));
+  return (int)std::min<long long>(256 * std::min(per_cu, 8), ceil_div(n_rows, 4));
 }
 
 template <int kDtype, bool kFp8, bool kVec>
@@ -604,19 +651,16 @@ namespace {
 
 template <int kDtype, int kGrad, bool kVec>
 void run_held_backward(const NormBwdArgs& a, hipStream_t stream) {
-  const int groups = (int)ceil_div(a.d, 8);
-  const dim3 grid((unsigned)a.runs);
-  if (groups <= 64 * kBwdMaxWaves)
-    hipLaunchKernelGGL((norm_backward_held_kernel<kDtype, kGrad, kVec, 1>), grid, dim3((unsigned)(ceil_div(groups, 64) * 64)),
-                       0, stream, a);
-  else
-    hipLaunchKernelGGL((norm_backward_held_kernel<kDtype, kGrad, kVec, 2>), grid,
-                       dim3((unsigned)(ceil_div(groups, 128) * 64)), 0, stream, a);
+  const dim3 grid((unsigned)a.runs), block((unsigned)held_waves(a.d) * 64);
+  if (ceil_div(a.d, 8) <= 64 * kBwdMaxWaves)
+    hipLaunchKernelGGL((norm_backward_held_kernel<kDtype, kGrad, kVec, 1>), grid, block, 0, stream, a);
+  else if constexpr (kVec)
+    hipLaunchKernelGGL((norm_backward_held_kernel<kDtype, kGrad, kVec, 2>), grid, block, 0, stream, a);
 }
 
 template <int kDtype, int kGrad>
 void run_norm_backward(const NormBwdArgs& a, hipStream_t stream) {
-  if (a.d <= kBwdMaxWidth) {
+  if (held_backward(a.d)) {
     if (a.d % 8 == 0) run_held_backward<kDtype, kGrad, true>(a, stream);
     else run_held_backward<kDtype, kGrad, false>(a, stream);
     return;
