@@ -17,10 +17,11 @@
 // With the gradient, for each chunk:
 //   1. z = H W^T by the forward's contraction (eight-wavefront engine), kept
 //      in fp32, with the online log-sum-exp folds of the logprob's forward;
-//   2. G in the head's type, token-major (for dH) and vocabulary-major (dW);
-//   3. dH = G (W^T)^T, K = the vocabulary, split over several workgroups
-//      when the chunk has few row blocks (fp32 partials added in order);
-//   4. dW += G^T (H^T)^T, K = the chunk's tokens.
+//   2. G [chunk, Vpad] in the head's type;
+//   3. dH = G W, K = the vocabulary, split over several workgroups when the
+//      chunk has few tiles (fp32 partials added in order);
+//   4. dW += G^T H, K = the chunk's tokens.
+// 3 and 4 read W, G and H as they lie (tile_engine_km.h): no transposed copy.
 // That is three contractions, the least there is (keeping the logits saves
 // the fourth: a chunk's 12 bytes of traffic per logit cost less than a
 // contraction of 2 d operations each for d > about 1000, the widths here).
@@ -37,6 +38,7 @@
 #include "lse_fold.h"
 #include "tile_engine.h"
 #include "tile_engine8.h"
+#include "tile_engine_km.h"
 
 namespace itl {
 
@@ -47,14 +49,39 @@ static_assert(kCeChunk % kBT == 0, "chunks hold whole token blocks");
 
 long long round_up(long long x, long long m) { return (x + m - 1) / m * m; }
 
+// Tiles of the gradient's contractions: 256 x 256 (bf16), 64 x 64 (fp32); K
+// steps of 128 bytes.
+template <int kDtype>
+struct GradTile {
+  static constexpr int kRows = kDtype == 0 ? 256 : kF32Tile;
+  static constexpr int kStepK = kStepBytes / Elem<kDtype>::kSize;
+  static constexpr int kSlots = kDtype == 0 ? 256 : 768;  // workgroups at a time
+};
+
+// Workgroups that share the K steps of a dH tile (each at least 16 steps):
+// the count that takes the fewest K steps of time, rounds x steps per
+// workgroup, with 12 steps' worth of start and end per round and the fp32
+// partials' traffic (a step's time moves those of about 4 tiles).
+__host__ __device__ inline int dh_splits(long long tiles, long long nks, long long slots) {
+  long long best = 1, best_cost = -1;
+  for (long long s = 1; s <= 16 && (s == 1 || nks / s >= 16); ++s) {
+    const long long rounds = (tiles * s + slots - 1) / slots;
+    const long long cost = rounds * ((nks + s - 1) / s + 12) + s * tiles / 4;
+    if (best_cost < 0 || cost < best_cost) best = s, best_cost = cost;
+  }
+  return (int)best;
+}
+
 // ---- which tokens count
 
 // One workgroup: rows[j] = the j-th counted token, ids[j] its target,
-// slot[t] = token t's place j or -1; *count = N.
+// slot[t] = token t's place j or -1; *count = N; and each chunk's dH splits.
 constexpr int kSelectThreads = 1024;
 __global__ __launch_bounds__(kSelectThreads) void ce_select_kernel(const int32_t* __restrict__ targets, int n, int vocab,
                                                                    int32_t* __restrict__ rows, int32_t* __restrict__ ids,
-                                                                   int32_t* __restrict__ slot, int32_t* __restrict__ count) {
+                                                                   int32_t* __restrict__ slot, int32_t* __restrict__ count,
+                                                                   int32_t* __restrict__ splits, int chunk, int rows_per_tile,
+                                                                   int n_dt, int nks, int slots) {
   __shared__ int wave_n[kSelectThreads / 64];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   int base = 0;
@@ -79,6 +106,12 @@ __global__ __launch_bounds__(kSelectThreads) void ce_select_kernel(const int32_t
     __syncthreads();
   }
   if (threadIdx.x == 0) *count = base;
+  // dH's splits of every chunk
+  if (splits)
+    for (int c = threadIdx.x; (long long)c * chunk < n; c += kSelectThreads) {
+      const int live = max(0, min(base - c * chunk, chunk));
+      splits[c] = dh_splits((long long)((live + rows_per_tile - 1) / rows_per_tile) * n_dt, nks, slots);
+    }
 }
 
 // A chunk's share of the count.
@@ -181,6 +214,69 @@ __global__ __launch_bounds__(kThreads8, 1) void ce_partial_kernel(
   run_tiles8<kDtype, kBFar>(smem, L, row_bytes, tile_begin, tile_end, nks, w_rsrc, hr, epilogue);
 }
 
+// The same for few tokens or small vocabularies: blocks of kBRows tokens, one
+// workgroup per (token block, slice), the arithmetic and bits as above
+// (lmhead_lse_partial_narrow_kernel's walk).
+template <int kDtype, bool kKeep, int kBRows>
+__global__ __launch_bounds__(kThreads, 1) void ce_partial_narrow_kernel(
+    const char* __restrict__ H, const char* __restrict__ W, const int32_t* __restrict__ ids,
+    const int32_t* __restrict__ count, int c0, int cap, int stride, int row_bytes, int vocab, int n_slices,
+    float2* __restrict__ part, float* __restrict__ zy_out, float* __restrict__ logits, long long ld) {
+  __shared__ uint4 smem[kEngineSmemChunks];
+  const Lanes L = lanes();
+  const int wv = L.wv, wt = L.wt, quad = L.lane >> 4, c16 = L.lane & 15;
+  const int S = n_slices;
+  const int slice = blockIdx.x % S;
+  constexpr int kBN = kBRows / 32;
+  constexpr int kWaveToks = kBRows / 2;
+  const int t0 = (blockIdx.x / S) * kBRows;
+  const int n_tok = __builtin_amdgcn_readfirstlane(chunk_live(count, c0, cap));
+  if (t0 >= n_tok) return;
+  const int n_vt = (vocab + kBV - 1) / kBV;
+  const int tile_begin = slice_tile(slice, n_vt, S);
+  const int tile_end = slice_tile(slice + 1, n_vt, S);
+  const int nks = row_bytes / kStepBytes;
+  Col16 c[kBN];
+#pragma unroll
+  for (int bn = 0; bn < kBN; ++bn) {
+    const int tok = t0 + wt * kWaveToks + bn * 16 + c16;
+    c[bn] = Col16{tok < n_tok ? ids[tok] : -1, -INFINITY, 0.0f};
+  }
+  auto w_rsrc = [&](int tile) {
+    const int v0 = tile * kBV;
+    return rsrc_words(W + (size_t)v0 * row_bytes, (uint32_t)min(kBV, vocab - v0) * row_bytes);
+  };
+  const int4v hr = rsrc_words(H + (size_t)t0 * row_bytes, (uint32_t)min(kBRows, n_tok - t0) * row_bytes);
+  const LogitRows rows = logit_rows(logits, ld, t0 + wt * kWaveToks, kWaveToks, n_tok, c16, quad);
+  auto epilogue = [&](int tile, floatx4 (&acc)[8][kBN]) {
+    const int vw = tile * kBV + wv * 128;
+    auto fold_tile = [&](auto partial) {
+      if constexpr (kKeep) {
+#pragma unroll
+        for (int bn = 0; bn < kBN; ++bn)
+#pragma unroll
+          for (int bm = 0; bm < 8; ++bm) store_logits(rows, bn, vw + bm * 16, quad, vocab, acc[bm][bn], partial);
+      }
+#pragma unroll
+      for (int bn = 0; bn < kBN; ++bn) {
+        floatx4 z[8];
+#pragma unroll
+        for (int bm = 0; bm < 8; ++bm) z[bm] = acc[bm][bn];
+        pick_sampled(c[bn], z, vw, quad, zy_out + (t0 + wt * kWaveToks + bn * 16 + c16));
+        fold_column16(c[bn], z, vw, quad, vocab, partial);
+      }
+    };
+    if (tile * kBV + kBV > vocab) fold_tile(std::true_type{});
+    else fold_tile(std::false_type{});
+  };
+  run_tiles_narrow<kDtype, kBRows>(smem, L, row_bytes, tile_begin, tile_end, nks, w_rsrc, hr, epilogue);
+#pragma unroll
+  for (int bn = 0; bn < kBN; ++bn) {
+    const int tok = t0 + wt * kWaveToks + bn * 16 + c16;
+    flush_slice16(c[bn], tok, n_tok, quad, ((size_t)slice * 2 + wv) * stride + tok, part);
+  }
+}
+
 // ---- mean of the logits (label smoothing): z's mean over v is H . mean_v W[v]
 
 constexpr int kMeanRows = 512;  // rows of W per partial sum
@@ -262,30 +358,6 @@ __global__ __launch_bounds__(1024) void ce_loss_kernel(const double* __restrict_
 
 // ---- G
 
-// out[c, r] = in[r, c] for r < rows (0 to out_cols), 64 x 64 tiles through
-// LDS; rows is the chunk's live count where `count` is given.
-template <typename T>
-__global__ __launch_bounds__(256) void ce_transpose_kernel(const T* __restrict__ in, int rows, int cols,
-                                                           T* __restrict__ out, int out_cols,
-                                                           const int32_t* __restrict__ count, int c0) {
-  __shared__ T tile[64][65];
-  const int r0 = blockIdx.x * 64, k0 = blockIdx.y * 64;
-  if (count) {
-    rows = chunk_live(count, c0, rows);
-    if (r0 >= max(rows, 1)) return;
-  }
-  const int tx = threadIdx.x & 63, ty = threadIdx.x >> 6;
-  for (int i = ty; i < 64; i += 4) {
-    const int r = r0 + i, c = k0 + tx;
-    tile[i][tx] = (r < rows && c < cols) ? in[(size_t)r * cols + c] : T(0);
-  }
-  __syncthreads();
-  for (int i = ty; i < 64; i += 4) {
-    const int c = k0 + i, r = r0 + tx;
-    if (c < cols && r < out_cols) out[(size_t)c * out_cols + r] = tile[tx][i];
-  }
-}
-
 // G is held in units of u = (1 - e) s / N, which the contractions' epilogues
 // apply in fp32: a p - [v = y] - c with a = (1 + 2 lam lse) / (1 - e) and
 // c = e / (V (1 - e)). The target's entry is then near -1, which bf16 holds
@@ -302,83 +374,52 @@ __device__ __forceinline__ float grad_unit(const GradScale& g, const int32_t* co
   return (float)(g.mean ? u / (double)max(1, *count) : u);
 }
 
-// G from the kept logits, a tile of 128 tokens x 128 vocabulary rows: Gd
-// [token, vpad] and GT [vpad, ld_t]. With kExact the target's entry is
-// stored without its -1, which dH and dW then take in fp32.
-constexpr int kGTile = 128;
+// G from the kept logits: 8 vocabulary entries of one token per thread; past
+// the vocabulary zeros. With kExact the target's entry is stored without its
+// -1, which dH and dW then take in fp32.
+constexpr int kGradVec = 8;
 
 template <int kDtype, bool kExact>
 __global__ __launch_bounds__(256) void ce_grad_logits_kernel(
     const float* __restrict__ logits, long long ld, const int32_t* __restrict__ ids, const int32_t* __restrict__ count,
-    int c0, int cap, int vocab, int vpad, int ld_t, const float* __restrict__ lse, GradScale gs,
-    typename Elem<kDtype>::T* __restrict__ Gd, typename Elem<kDtype>::T* __restrict__ GT) {
+    int c0, int cap, int vocab, int vpad, const float* __restrict__ lse, GradScale gs,
+    typename Elem<kDtype>::T* __restrict__ Gd) {
   using E = Elem<kDtype>;
-  using T = typename E::T;
-  constexpr int kPack = 4 / (int)sizeof(T);  // tokens per 32-bit word
-  constexpr int kRowWords = kGTile / kPack + 1;
-  __shared__ uint32_t tile[kGTile * kRowWords];
-  const int live = chunk_live(count, c0, cap);
-  const int v0 = blockIdx.x * kGTile;
-  const int t0 = blockIdx.y * kGTile;
-  if (t0 >= max(live, 1)) return;  // (the first tile is always written: dW's contraction reads it)
+  const int t = blockIdx.y;
+  const int v = (blockIdx.x * 256 + threadIdx.x) * kGradVec;
+  if (t >= chunk_live(count, c0, cap) || v >= vpad) return;
   const float rest = 1.0f / (1.0f - gs.smoothing);
   const float cc = gs.smoothing * gs.inv_vocab * rest;
-  const int vq = threadIdx.x & 31;  // vocabulary rows v0 + 4 vq .. + 3
-  const int tr = threadIdx.x >> 5;  // 0..7
-  const int v = v0 + 4 * vq;
-  for (int p = 0; p < kGTile / (8 * kPack); ++p) {
-    T g[kPack][4];
+  const float s = lse[t];
+  const float l2e_lse = s * kLog2e;
+  const float a = rest * (1.0f + 2.0f * gs.z_weight * s);
+  const int y = ids[t];
+  const float* row = logits + (size_t)t * (size_t)ld;
+  float z[kGradVec];
+  if (v + kGradVec <= vocab) {
+    const floatx4 lo = __builtin_nontemporal_load(reinterpret_cast<const floatx4*>(row + v));
+    const floatx4 hi = __builtin_nontemporal_load(reinterpret_cast<const floatx4*>(row + v + 4));
 #pragma unroll
-    for (int k = 0; k < kPack; ++k) {
-      const int t = t0 + (tr + 8 * p) * kPack + k;
-      if (t < live) {
-        const float s = lse[t];
-        const float l2e_lse = s * kLog2e;
-        const float a = rest * (1.0f + 2.0f * gs.z_weight * s);
-        const int y = ids[t];
-        const float* row = logits + (size_t)t * (size_t)ld;
-        floatx4 z;
-        if (v + 3 < vocab) {
-          z = __builtin_nontemporal_load(reinterpret_cast<const floatx4*>(row + v));
-        } else {
+    for (int r = 0; r < 4; ++r) z[r] = lo[r], z[4 + r] = hi[r];
+  } else {
 #pragma unroll
-          for (int r = 0; r < 4; ++r) z[r] = v + r < vocab ? row[v + r] : 0.0f;
-        }
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          float x = a * fast_exp2(z[r] * kLog2e - l2e_lse) - cc;
-          if (!kExact && v + r == y) x -= 1.0f;
-          g[k][r] = E::from_f(v + r < vocab ? x : 0.0f);
-        }
-      } else {
-#pragma unroll
-        for (int r = 0; r < 4; ++r) g[k][r] = E::from_f(0.0f);
-      }
-      if constexpr (kDtype == 0) {
-        uint2 pk;
-        pk.x = (uint32_t)g[k][0] | ((uint32_t)g[k][1] << 16);
-        pk.y = (uint32_t)g[k][2] | ((uint32_t)g[k][3] << 16);
-        *reinterpret_cast<uint2*>(Gd + (size_t)t * vpad + v) = pk;
-      } else {
-        *reinterpret_cast<float4*>(Gd + (size_t)t * vpad + v) = make_float4(g[k][0], g[k][1], g[k][2], g[k][3]);
-      }
-    }
-#pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      uint32_t w;
-      if constexpr (kDtype == 0) w = (uint32_t)g[0][r] | ((uint32_t)g[1][r] << 16);
-      else w = __float_as_uint(g[0][r]);
-      tile[(4 * vq + r) * kRowWords + tr + 8 * p] = w;
-    }
+    for (int r = 0; r < kGradVec; ++r) z[r] = v + r < vocab ? row[v + r] : 0.0f;
   }
-  __syncthreads();
-  constexpr int kLanesPerRow = kGTile / kPack / 4;
-  constexpr int kRowsPerPass = 256 / kLanesPerRow;
-  const int j = threadIdx.x % kLanesPerRow;
-  for (int vr = threadIdx.x / kLanesPerRow; vr < kGTile; vr += kRowsPerPass) {
-    const uint32_t* src = tile + vr * kRowWords + 4 * j;
-    *reinterpret_cast<uint4*>(reinterpret_cast<char*>(GT + (size_t)(v0 + vr) * ld_t + t0) + 16 * j) =
-        make_uint4(src[0], src[1], src[2], src[3]);
+#pragma unroll
+  for (int r = 0; r < kGradVec; ++r) {
+    float x = a * fast_exp2(z[r] * kLog2e - l2e_lse) - cc;
+    if (!kExact && v + r == y) x -= 1.0f;
+    z[r] = v + r < vocab ? x : 0.0f;
+  }
+  typename E::T* out = Gd + (size_t)t * vpad + v;
+  if constexpr (kDtype == 0) {
+    uint32_t w[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) w[j] = (uint32_t)E::from_f(z[2 * j]) | ((uint32_t)E::from_f(z[2 * j + 1]) << 16);
+    *reinterpret_cast<uint4*>(out) = make_uint4(w[0], w[1], w[2], w[3]);
+  } else {
+    reinterpret_cast<float4*>(out)[0] = make_float4(z[0], z[1], z[2], z[3]);
+    reinterpret_cast<float4*>(out)[1] = make_float4(z[4], z[5], z[6], z[7]);
   }
 }
 
@@ -407,54 +448,58 @@ __device__ __forceinline__ void store_grad4(void* out, int grad_f32, size_t at, 
   }
 }
 
-// Partial s of dH for the chunk: A = W^T tile (d rows), B = Gd token block,
-// K = the vocabulary steps [nks s / splits, nks (s + 1) / splits). Writes
-// fp32 rows part[s, j, :].
-template <int kDtype, bool kBFar>
-__global__ __launch_bounds__(kThreads8, 1) void ce_dh_kernel(const char* __restrict__ WT, const char* __restrict__ Gd,
-                                                             int vpad, int d, const int32_t* __restrict__ count, int c0,
-                                                             int cap, int n_tb, int n_dt, int splits,
-                                                             float* __restrict__ part) {
-  __shared__ uint4 smem[kEngineSmemChunks];
-  const Lanes8 L = lanes8();
+// Partial sp of dH for the chunk: A = W (columns d0 .. of rows v), B = rows of
+// Gd, K = the vocabulary steps [nks sp / splits, nks (sp + 1) / splits). Writes
+// fp32 rows part[sp, t, :] (tile rows of the live tokens per split). Token
+// blocks fastest: workgroups that run together share W's rows.
+template <int kDtype>
+__global__ __launch_bounds__(kDtype == 0 ? kThreads8 : kF32Threads, 1) void ce_dh_kernel(
+    const char* __restrict__ W, const char* __restrict__ Gd, int vocab, int vpad, int d, const int32_t* __restrict__ count,
+    int c0, int cap, int n_dt, const int32_t* __restrict__ splits_of, float* __restrict__ part) {
+  constexpr int kT = GradTile<kDtype>::kRows, kStepK = GradTile<kDtype>::kStepK, es = Elem<kDtype>::kSize;
+  __shared__ uint4 smem[kDtype == 0 ? kEngineSmemChunks : kF32SmemChunks];
   const int live = __builtin_amdgcn_readfirstlane(chunk_live(count, c0, cap));
-  // token blocks fastest: workgroups that run together share W^T's rows
+  const int splits = __builtin_amdgcn_readfirstlane(*splits_of);
+  const int n_tb = (live + kT - 1) / kT;
+  if ((long long)blockIdx.x >= (long long)n_tb * n_dt * splits) return;
   const int tb = blockIdx.x % n_tb, rest = blockIdx.x / n_tb;
   const int dt = rest % n_dt, sp = rest / n_dt;
-  const int t0 = tb * kBT;
-  if (t0 >= live) return;
-  const int row_bytes = vpad * Elem<kDtype>::kSize;
-  const int nks_all = row_bytes / kStepBytes;
+  const int t0 = tb * kT;
+  const int nks_all = vpad / kStepK;
   const int ks0 = (int)((long long)nks_all * sp / splits), ks1 = (int)((long long)nks_all * (sp + 1) / splits);
-  const uint32_t skip = (uint32_t)ks0 * kStepBytes;
-  auto a_rsrc = [&](int tile) {
-    const int k0 = tile * kBV;
-    return rsrc_words(WT + (size_t)k0 * row_bytes + skip, (uint32_t)min(kBV, d - k0) * row_bytes - skip);
+  const uint32_t w_row = (uint32_t)d * es, g_row = (uint32_t)vpad * es, d_off = (uint32_t)dt * kT * es;
+  const KmOperand A{W + (size_t)ks0 * kStepK * w_row + d_off, w_row, vocab - ks0 * kStepK, d_off};
+  const KmOperand B{Gd + (size_t)t0 * g_row + (size_t)ks0 * kStepBytes, g_row, min(kT, live - t0),
+                    (uint32_t)ks0 * kStepBytes};
+  float* out = part + (size_t)sp * n_tb * kT * d;
+  auto store = [&](int t, int k, const floatx4& o) {
+    if (t < live && k < d) *reinterpret_cast<float4*>(out + (size_t)t * d + k) = make_float4(o[0], o[1], o[2], o[3]);
   };
-  const int4v br = rsrc_words(Gd + (size_t)t0 * row_bytes + skip, (uint32_t)min(kBT, live - t0) * row_bytes - skip);
-  auto epilogue = [&](int tile, floatx4 (&acc)[8][4]) {
-    const int kw = tile * kBV + L.wv * 128 + 4 * L.quad;
+  if constexpr (kDtype == 0) {
+    const Lanes8 L = lanes8();
+    run_tile_km<false>(smem, L, A, B, ks1 - ks0, [&](floatx4 (&acc)[8][4]) {
 #pragma unroll
-    for (int bn = 0; bn < 4; ++bn) {
-      const int t = t0 + L.tq * 64 + bn * 16 + L.c16;
+      for (int bn = 0; bn < 4; ++bn)
 #pragma unroll
-      for (int bm = 0; bm < 8; ++bm) {
-        const int k = kw + bm * 16;
-        if (t < live && k < d) {
-          const floatx4& o = acc[bm][bn];
-          *reinterpret_cast<float4*>(part + ((size_t)sp * cap + t) * d + k) = make_float4(o[0], o[1], o[2], o[3]);
-        }
-      }
-      __builtin_amdgcn_sched_barrier(0);
-    }
-  };
-  run_tiles8<kDtype, kBFar>(smem, L, row_bytes, dt, dt + 1, ks1 - ks0, a_rsrc, br, epilogue);
+        for (int bm = 0; bm < 8; ++bm)
+          store(t0 + L.tq * 64 + bn * 16 + L.c16, dt * kT + L.wv * 128 + bm * 16 + 4 * L.quad, acc[bm][bn]);
+    });
+  } else {
+    run_tile_f32<false>(smem, A, B, ks1 - ks0, [&](floatx4 (&acc)[2][2], int wave, int quad, int c16) {
+#pragma unroll
+      for (int bn = 0; bn < 2; ++bn)
+#pragma unroll
+        for (int bm = 0; bm < 2; ++bm)
+          store(t0 + 32 * (wave >> 1) + 16 * bn + c16, dt * kT + 32 * (wave & 1) + 16 * bm + 4 * quad, acc[bm][bn]);
+    });
+  }
 }
 
 // dH rows: the splits added in order (plus, with coef, the exact one-hot
 // term coef[j] W[y]), four values per thread, to the token's own row.
 template <int kDtype>
-__global__ __launch_bounds__(256) void ce_dh_finish_kernel(const float* __restrict__ part, int splits, int cap, int d,
+__global__ __launch_bounds__(256) void ce_dh_finish_kernel(const float* __restrict__ part,
+                                                           const int32_t* __restrict__ splits_of, int cap, int d,
                                                            const int32_t* __restrict__ rows, const int32_t* __restrict__ ids,
                                                            const int32_t* __restrict__ count, int c0, GradScale gs,
                                                            const float* __restrict__ coef,
@@ -462,12 +507,16 @@ __global__ __launch_bounds__(256) void ce_dh_finish_kernel(const float* __restri
                                                            void* __restrict__ dH) {
   using E = Elem<kDtype>;
   const int j = blockIdx.x;
-  if (j >= chunk_live(count, c0, cap)) return;
+  const int live = chunk_live(count, c0, cap);
+  if (j >= live) return;
+  constexpr int kT = GradTile<kDtype>::kRows;
+  const int splits = *splits_of;
+  const size_t per_split = (size_t)((live + kT - 1) / kT * kT) * d;
   const float unit = grad_unit(gs, count);
   for (int k = threadIdx.x * 4; k < d; k += 1024) {
     float o[4] = {0.0f, 0.0f, 0.0f, 0.0f};
     for (int s = 0; s < splits; ++s) {
-      const float4 v = *reinterpret_cast<const float4*>(part + ((size_t)s * cap + j) * d + k);
+      const float4 v = *reinterpret_cast<const float4*>(part + s * per_split + (size_t)j * d + k);
       o[0] += v.x, o[1] += v.y, o[2] += v.z, o[3] += v.w;
     }
 #pragma unroll
@@ -492,17 +541,16 @@ __global__ __launch_bounds__(256) void ce_zero_rows_kernel(const int32_t* __rest
 
 // ---- dW
 
-// The chunk's part of dW: A = GT vocabulary tile (K = the chunk's tokens),
-// B = H^T block of d. add: dW already holds earlier parts (fp32).
+// The chunk's part of dW: A = Hc (columns d0 ..), B = Gd (columns v0 ..), K =
+// the chunk's live tokens. add: dW already holds earlier parts (fp32).
+// Vocabulary tiles fastest within bands: workgroups that run together share
+// operands.
 template <int kDtype>
-__global__ __launch_bounds__(kThreads8, 1) void ce_dw_kernel(const char* __restrict__ GT, const char* __restrict__ HT,
-                                                             int ld_t, const int32_t* __restrict__ count, int c0, int cap,
-                                                             int vocab, int d, int n_vt, int n_dt, GradScale gs, int add,
-                                                             int out_f32,
-                                                             void* __restrict__ dW) {
-  using E = Elem<kDtype>;
-  __shared__ uint4 smem[kEngineSmemChunks];
-  const Lanes8 L = lanes8();
+__global__ __launch_bounds__(kDtype == 0 ? kThreads8 : kF32Threads, 1) void ce_dw_kernel(
+    const char* __restrict__ Gd, const char* __restrict__ Hc, int vpad, const int32_t* __restrict__ count, int c0, int cap,
+    int vocab, int d, int n_vt, int n_dt, GradScale gs, int add, int out_f32, void* __restrict__ dW) {
+  constexpr int kT = GradTile<kDtype>::kRows, kStepK = GradTile<kDtype>::kStepK, es = Elem<kDtype>::kSize;
+  __shared__ uint4 smem[kDtype == 0 ? kEngineSmemChunks : kF32SmemChunks];
   const int live = __builtin_amdgcn_readfirstlane(chunk_live(count, c0, cap));
   if (live == 0 && c0 > 0) return;  // (the first chunk writes its zeros)
   const int band = blockIdx.x / (kBwdSuperBand * n_dt);
@@ -510,38 +558,39 @@ __global__ __launch_bounds__(kThreads8, 1) void ce_dw_kernel(const char* __restr
   const int nb = min(kBwdSuperBand, n_vt - first);
   const int rem = blockIdx.x - band * kBwdSuperBand * n_dt;
   const int vt = first + rem % nb, dt = rem / nb;
-  const int row_bytes = ld_t * E::kSize;
-  const int k0 = dt * kBT;
-  constexpr int kStep = kStepBytes / E::kSize;
-  const int nks = max(1, (live + kStep - 1) / kStep);
+  const int nks = max(1, (live + kStepK - 1) / kStepK);
+  const uint32_t h_row = (uint32_t)d * es, g_row = (uint32_t)vpad * es;
+  const uint32_t d_off = (uint32_t)dt * kT * es, v_off = (uint32_t)vt * kT * es;
+  const KmOperand A{Hc + d_off, h_row, live, d_off}, B{Gd + v_off, g_row, live, v_off};
   const float unit = grad_unit(gs, count);
-  auto a_rsrc = [&](int tile) {
-    const int v0 = tile * kBV;
-    return rsrc_words(GT + (size_t)v0 * row_bytes, (uint32_t)kBV * row_bytes);
-  };
-  const int4v br = rsrc_words(HT + (size_t)k0 * row_bytes, (uint32_t)min(kBT, d - k0) * row_bytes);
-  auto epilogue = [&](int tile, floatx4 (&acc)[8][4]) {
-    const int vw = tile * kBV + L.wv * 128 + 4 * L.quad;
-#pragma unroll
-    for (int bn = 0; bn < 4; ++bn) {
-      const int k = k0 + L.tq * 64 + bn * 16 + L.c16;
-#pragma unroll
-      for (int bm = 0; bm < 8; ++bm)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const int v = vw + bm * 16 + r;
-          if (v < vocab && k < d) {
-            const size_t at = (size_t)v * d + k;
-            float x = acc[bm][bn][r] * unit;
-            if (add) x += static_cast<float*>(dW)[at];
-            if (out_f32) static_cast<float*>(dW)[at] = x;
-            else static_cast<uint16_t*>(dW)[at] = Elem<0>::from_f(x);
-          }
-        }
-      __builtin_amdgcn_sched_barrier(0);
+  auto store = [&](int v, int k, const floatx4& o) {
+    if (v >= vocab || k >= d) return;
+    const size_t at = (size_t)v * d + k;
+    float x[4] = {o[0] * unit, o[1] * unit, o[2] * unit, o[3] * unit};
+    if (add) {
+      const float4 old = *reinterpret_cast<const float4*>(static_cast<const float*>(dW) + at);
+      x[0] += old.x, x[1] += old.y, x[2] += old.z, x[3] += old.w;
     }
+    store_grad4(dW, out_f32, at, x);
   };
-  run_tiles8<kDtype, false>(smem, L, row_bytes, vt, vt + 1, nks, a_rsrc, br, epilogue);
+  if constexpr (kDtype == 0) {
+    const Lanes8 L = lanes8();
+    run_tile_km<true>(smem, L, A, B, nks, [&](floatx4 (&acc)[8][4]) {
+#pragma unroll
+      for (int bn = 0; bn < 4; ++bn)
+#pragma unroll
+        for (int bm = 0; bm < 8; ++bm)
+          store(vt * kT + L.tq * 64 + bn * 16 + L.c16, dt * kT + L.wv * 128 + bm * 16 + 4 * L.quad, acc[bm][bn]);
+    });
+  } else {
+    run_tile_f32<true>(smem, A, B, nks, [&](floatx4 (&acc)[2][2], int wave, int quad, int c16) {
+#pragma unroll
+      for (int bn = 0; bn < 2; ++bn)
+#pragma unroll
+        for (int bm = 0; bm < 2; ++bm)
+          store(vt * kT + 32 * (wave >> 1) + 16 * bn + c16, dt * kT + 32 * (wave & 1) + 16 * bm + 4 * quad, acc[bm][bn]);
+    });
+  }
 }
 
 // The accumulated fp32 dW rounded to bf16.
@@ -571,31 +620,32 @@ __global__ __launch_bounds__(256) void ce_clear_kernel(uint4* __restrict__ out, 
 
 // ---- workspace
 
-// Workgroups of dH's contraction without a split cover n_tb x n_dt tiles:
-// the split count (up to 16, each with at least 16 K steps) that leaves the
-// fewest rounds of 256 workgroups per unit of work, the smallest such.
-int dh_splits(long long n_tb, long long n_dt, long long nks) {
-  int best = 1;
-  double best_cost = 1e30;
-  for (int s = 1; s <= 16 && nks / s >= 16; ++s) {
-    const double cost = (double)ceil_div(n_tb * n_dt * s, 256) / s * (1.0 + 0.01 * s);
-    if (cost < best_cost * 0.999) best = s, best_cost = cost;
+// The most workgroups, and fp32 partial rows, that a chunk of up to cap tokens
+// can take in dH's contraction, over all live counts.
+void dh_most(long long cap, long long d, long long vpad, int dtype, long long* groups, long long* rows) {
+  const long long tile = dtype == 0 ? GradTile<0>::kRows : GradTile<1>::kRows;
+  const long long slots = dtype == 0 ? GradTile<0>::kSlots : GradTile<1>::kSlots;
+  const long long nks = vpad / (dtype == 0 ? GradTile<0>::kStepK : GradTile<1>::kStepK), n_dt = ceil_div(d, tile);
+  *groups = *rows = 0;
+  for (long long n_tb = 1; n_tb <= ceil_div(cap, tile); ++n_tb) {
+    const long long s = dh_splits(n_tb * n_dt, nks, slots);
+    *groups = std::max(*groups, n_tb * n_dt * s);
+    *rows = std::max(*rows, n_tb * tile * s);
   }
-  return best;
 }
 
 struct CeLayout {
-  int cap, ld_t, vpad;
-  size_t rows, ids, slot, count, lp, lse, zy, part, loss, wmean, wpart, hc, z, gd, gt, wt, ht, dhp, coef, cids, dwacc,
-      sampled, total;
+  int cap, vpad;
+  long long dh_groups;
+  size_t rows, ids, slot, count, splits, lp, lse, zy, part, loss, wmean, wpart, hc, z, gd, dhp, coef, cids, dwacc, sampled,
+      total;
 };
 
 CeLayout ce_layout(long long n_tok, long long d, long long vocab, int dtype, bool grad, int grad_dtype) {
   CeLayout L{};
   const int es = dtype == 0 ? 2 : 4;
   L.vpad = (int)round_up(vocab, kBV);
-  L.cap = (int)(grad ? std::min<long long>(kCeChunk, round_up(n_tok, kBT)) : n_tok);
-  L.ld_t = (int)round_up(L.cap, kBT);
+  L.cap = (int)(grad ? std::min<long long>(kCeChunk, n_tok) : n_tok);
   size_t off = 0;
   auto take = [&](size_t bytes) {
     const size_t at = off;
@@ -606,8 +656,8 @@ CeLayout ce_layout(long long n_tok, long long d, long long vocab, int dtype, boo
   L.ids = take((size_t)n_tok * 4);
   L.slot = take((size_t)n_tok * 4);
   L.count = take(4);
-  L.lp = take((size_t)round_up(n_tok, kBT) * 4);
-  L.lse = take((size_t)round_up(n_tok, kBT) * 4);
+  L.lp = take((size_t)n_tok * 4);
+  L.lse = take((size_t)n_tok * 4);
   L.zy = take((size_t)L.cap * 4);
   L.part = take((size_t)2 * n_slices(vocab) * L.cap * sizeof(float2));
   L.loss = take((size_t)ceil_div(n_tok, 4) * 8);
@@ -615,23 +665,18 @@ CeLayout ce_layout(long long n_tok, long long d, long long vocab, int dtype, boo
   L.wpart = take((size_t)ceil_div(vocab, kMeanRows) * d * 4);
   L.hc = take((size_t)L.cap * d * es);
   if (grad) {
-    const long long n_tb = L.cap / kBT, n_dt = ceil_div(d, kBT);
-    const long long nks = (long long)L.vpad * es / kStepBytes, last = n_tok - (n_tok - 1) / L.cap * L.cap;
+    long long rows;
+    dh_most(L.cap, d, L.vpad, dtype, &L.dh_groups, &rows);
+    L.splits = take((size_t)ceil_div(n_tok, L.cap) * 4);
     L.z = take((size_t)L.cap * L.vpad * 4);
     L.gd = take((size_t)L.cap * L.vpad * es);
-    L.gt = take((size_t)L.vpad * L.ld_t * es);
-    L.wt = take((size_t)d * L.vpad * es);
-    L.ht = take((size_t)d * L.ld_t * es);
-    // the partials of a whole chunk, or of the (smaller) last one
-    const size_t whole = (size_t)dh_splits(n_tb, n_dt, nks) * L.cap, rest = (size_t)dh_splits(ceil_div(last, kBT), n_dt, nks) * last;
-    L.dhp = take(std::max(whole, rest) * d * 4);
+    L.dhp = take((size_t)rows * d * 4);
     if (dtype == 0 && grad_dtype == 1) {
       L.coef = take((size_t)L.cap * 4);
       L.cids = take((size_t)L.cap * 4);
       L.sampled = take(sampled_dw_workspace_bytes(L.cap, d, vocab));
     }
-    if (dtype == 0 && n_tok > L.cap)
-      L.dwacc = take((size_t)vocab * d * 4);
+    if (dtype == 0 && n_tok > L.cap) L.dwacc = take((size_t)vocab * d * 4);
   }
   L.total = off;
   return L;
@@ -648,6 +693,20 @@ void launch_ce_partial(const char* Hc, const char* W, const int32_t* ids, const 
                        int vocab, float2* part, float* zy, float* logits, long long ld, hipStream_t stream) {
   const int row_bytes = d * Elem<kDtype>::kSize;
   const int S = n_slices(vocab), G = slices_per_group(cap, vocab), ntb = (int)ceil_div(cap, kBT);
+  // Few workgroups: the narrow walk's blocks are a quarter of the wide one's
+  // (two rounds of them over the CUs still half its time), of 128 tokens a
+  // half. The bits are the same.
+  const long long narrow = ceil_div(cap, kNarrowBRows) * S;
+  if (cap <= kNarrowMaxTokens || narrow <= 512) {
+    hipLaunchKernelGGL((ce_partial_narrow_kernel<kDtype, kKeep, kNarrowBRows>), dim3((unsigned)narrow), dim3(kThreads), 0,
+                       stream, Hc, W, ids, count, c0, cap, cap, row_bytes, vocab, S, part, zy, logits, ld);
+    return;
+  }
+  if (cap <= kNarrow128MaxTokens) {
+    hipLaunchKernelGGL((ce_partial_narrow_kernel<kDtype, kKeep, kNarrow128MaxTokens>), dim3((unsigned)S), dim3(kThreads), 0,
+                       stream, Hc, W, ids, count, c0, cap, cap, row_bytes, vocab, S, part, zy, logits, ld);
+    return;
+  }
   const dim3 grid((unsigned)ntb * (unsigned)n_slice_groups(cap, vocab));
   // the load schedule's rule, and its exception for fp32 kept logits, as in the logprob's forward
   constexpr bool kFarOnly = kDtype == 1 && kKeep;
@@ -695,7 +754,9 @@ hipError_t run_cross_entropy(const CeCall& c, hipStream_t stream) {
   hipError_t e;
 
   hipLaunchKernelGGL(ce_select_kernel, dim3(1), dim3(kSelectThreads), 0, stream, c.targets, n, vocab, rows, ids, slot,
-                     count);
+                     count, grad ? reinterpret_cast<int32_t*>(at(L.splits)) : nullptr, L.cap, GradTile<kDtype>::kRows,
+                     (int)ceil_div(d, GradTile<kDtype>::kRows), L.vpad / GradTile<kDtype>::kStepK,
+                     GradTile<kDtype>::kSlots);
   ITL_CHECK_LAUNCH();
   if (wmean) {
     const int nb = (int)ceil_div(vocab, kMeanRows);
@@ -708,8 +769,6 @@ hipError_t run_cross_entropy(const CeCall& c, hipStream_t stream) {
   GradScale gs{c.smoothing, c.z_weight, c.grad_scale, 1.0f / (float)vocab, c.mean};
   const bool exact = grad && kDtype == 0 && c.grad_dtype == 1;
   if (grad) {
-    hipLaunchKernelGGL(ce_transpose_kernel<T>, dim3((unsigned)(L.vpad / 64), (unsigned)ceil_div(d, 64)), dim3(256), 0,
-                       stream, W, vocab, d, reinterpret_cast<T*>(at(L.wt)), L.vpad, nullptr, 0);
     hipLaunchKernelGGL(ce_zero_rows_kernel, dim3((unsigned)n), dim3(256), 0, stream, slot,
                        d * (c.grad_dtype == 0 ? 2 : 4) / 16, static_cast<uint4*>(c.dH));
     ITL_CHECK_LAUNCH();
@@ -731,15 +790,13 @@ hipError_t run_cross_entropy(const CeCall& c, hipStream_t stream) {
     if (!grad) continue;
 
     T* Gd = reinterpret_cast<T*>(at(L.gd));
-    T* GT = reinterpret_cast<T*>(at(L.gt));
-    T* HT = reinterpret_cast<T*>(at(L.ht));
-    const dim3 g_grid((unsigned)(L.vpad / kGTile), (unsigned)ceil_div(cap, kGTile));
+    const dim3 g_grid((unsigned)ceil_div(L.vpad, 256 * kGradVec), (unsigned)cap);
     if (exact)
       hipLaunchKernelGGL((ce_grad_logits_kernel<kDtype, true>), g_grid, dim3(256), 0, stream, z, (long long)L.vpad,
-                         ids + c0, count, c0, cap, vocab, L.vpad, L.ld_t, lse + c0, gs, Gd, GT);
+                         ids + c0, count, c0, cap, vocab, L.vpad, lse + c0, gs, Gd);
     else
       hipLaunchKernelGGL((ce_grad_logits_kernel<kDtype, false>), g_grid, dim3(256), 0, stream, z, (long long)L.vpad,
-                         ids + c0, count, c0, cap, vocab, L.vpad, L.ld_t, lse + c0, gs, Gd, GT);
+                         ids + c0, count, c0, cap, vocab, L.vpad, lse + c0, gs, Gd);
     ITL_CHECK_LAUNCH();
     float* coef = nullptr;
     int32_t* cids = reinterpret_cast<int32_t*>(at(L.cids));
@@ -751,20 +808,18 @@ hipError_t run_cross_entropy(const CeCall& c, hipStream_t stream) {
     }
     // dH
     float* dhp = reinterpret_cast<float*>(at(L.dhp));
-    const int n_tb = (int)ceil_div(cap, kBT), n_dt = (int)ceil_div(d, kBT), n_vt = L.vpad / kBV;
-    const int splits = dh_splits(n_tb, n_dt, (long long)L.vpad * E::kSize / kStepBytes);
-    const bool far = L.vpad * E::kSize / kStepBytes / splits > kNearBMaxSteps;
-    hipLaunchKernelGGL((far ? ce_dh_kernel<kDtype, true> : ce_dh_kernel<kDtype, false>),
-                       dim3((unsigned)(n_tb * n_dt * splits)), dim3(kThreads8), 0, stream, at(L.wt),
-                       reinterpret_cast<const char*>(Gd), L.vpad, d, count, c0, cap, n_tb, n_dt, splits, dhp);
+    constexpr int kT = GradTile<kDtype>::kRows;
+    const dim3 g_block(kDtype == 0 ? kThreads8 : kF32Threads);
+    const int n_dt = (int)ceil_div(d, kT), n_vt = (int)ceil_div(vocab, kT);
+    const int32_t* splits = reinterpret_cast<const int32_t*>(at(L.splits)) + c0 / L.cap;
+    hipLaunchKernelGGL(ce_dh_kernel<kDtype>, dim3((unsigned)L.dh_groups), g_block, 0, stream,
+                       reinterpret_cast<const char*>(W), reinterpret_cast<const char*>(Gd), vocab, L.vpad, d, count, c0, cap,
+                       n_dt, splits, dhp);
     ITL_CHECK_LAUNCH();
     hipLaunchKernelGGL(ce_dh_finish_kernel<kDtype>, dim3((unsigned)cap), dim3(256), 0, stream, dhp, splits, cap, d, rows,
                        ids + c0, count, c0, gs, coef, W, c.grad_dtype, c.dH);
     ITL_CHECK_LAUNCH();
     // dW
-    hipLaunchKernelGGL(ce_transpose_kernel<T>, dim3((unsigned)ceil_div(cap, 64), (unsigned)ceil_div(d, 64)), dim3(256), 0,
-                       stream, reinterpret_cast<const T*>(Hc), cap, d, HT, L.ld_t, count, c0);
-    ITL_CHECK_LAUNCH();
     const bool single = n <= L.cap;
     float* acc = single ? nullptr : c.grad_dtype == 1 && !exact ? static_cast<float*>(c.dW) : reinterpret_cast<float*>(at(L.dwacc));
     void* out = c.dW;
@@ -778,9 +833,9 @@ hipError_t run_cross_entropy(const CeCall& c, hipStream_t stream) {
     } else if (!single) {
       out = acc, out_f32 = 1, add = c0 > 0;
     }
-    hipLaunchKernelGGL(ce_dw_kernel<kDtype>, dim3((unsigned)(n_vt * n_dt)), dim3(kThreads8), 0, stream,
-                       reinterpret_cast<const char*>(GT), reinterpret_cast<const char*>(HT), L.ld_t, count, c0, cap,
-                       vocab, d, n_vt, n_dt, gs, add, out_f32, out);
+    hipLaunchKernelGGL(ce_dw_kernel<kDtype>, dim3((unsigned)(n_vt * n_dt)), g_block, 0, stream,
+                       reinterpret_cast<const char*>(Gd), Hc, L.vpad, count, c0, cap, vocab, d, n_vt, n_dt, gs, add, out_f32,
+                       out);
     ITL_CHECK_LAUNCH();
     if (exact && !single && c0 > 0) {
       hipLaunchKernelGGL(ce_add_kernel, dim3((unsigned)ceil_div((long long)vocab * d / 4, 256)), dim3(256), 0, stream,

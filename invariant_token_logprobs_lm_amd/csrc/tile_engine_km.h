@@ -1,0 +1,296 @@
+// Tile products whose operands lie with the contracted index outermost
+// (K-major: row k holds the tile's 256 columns), as a gradient's do: dH = G W
+// contracts W's rows, dW = G^T H the rows of both. Transposed copies of W, G
+// and H are not made: the operand comes into LDS as it lies, and the fragments
+// are read through the transposing LDS read.
+//
+// bf16 (run_tile_km): 256 x 256 tiles on the eight-wavefront schedule of
+// tile_engine8.h (same wavefront tiles, slots, barriers and load places). A
+// K step of a K-major operand is 64 rows of 512 bytes, 32 KiB, one slot. The
+// read (ds_read_b64_tr_b16, measured layout): in each group of 16 lanes, lane
+// a addresses 8 bytes, row k0 + a / 4, columns 4 (a mod 4) .. + 3, and lane i
+// receives column i of rows k0 .. k0 + 3. Two reads give a lane the 8 values
+// of k that the K-contiguous operand's 16-byte chunk holds, so both kinds
+// meet in one instruction. The 32-byte piece (16 columns) P of row k sits at
+// piece P ^ f(k), f(k) = (k mod 4) + 4 ((k / 8) mod 4): a group's 4 rows fall
+// on 128 consecutive bytes, a read's 16 rows on 16 different pieces.
+//
+// fp32 (run_tile_f32): 64 x 64 tiles, four wavefronts of 32 x 32. The fp32
+// matrix rate is a sixteenth of bf16's, so such a tile is bound by it all the
+// same and small problems fill the chip; lanes read single values, row by
+// row, which needs no transposing.
+#pragma once
+
+#include "tile_engine.h"
+#include "tile_engine8.h"
+
+namespace itl {
+
+typedef short shortx4 __attribute__((ext_vector_type(4)));
+
+// An operand of a tile: `base` its first row k (K-major: at the tile's first
+// column; K-contiguous: row 0 of the tile at the first k), rows or columns
+// past it never read.
+struct KmOperand {
+  const char* base;
+  uint32_t row_bytes;  // between rows
+  int rows;            // K-major: rows k in all; K-contiguous: the tile's rows
+  uint32_t skip;       // bytes before base in its row (the range ends with the last row)
+};
+
+// K-major rows 64 s .. of a K step as a buffer range: rows past the end load
+// zeros.
+__device__ __forceinline__ int4v km_step_rsrc(const KmOperand& o, int s, int step_rows) {
+  const int left = o.rows - s * step_rows;
+  const uint32_t n = left <= 0 ? 0u : (uint32_t)(left < step_rows ? left : step_rows) * o.row_bytes - o.skip;
+  return rsrc_words(o.base + (size_t)s * step_rows * o.row_bytes, n);
+}
+
+__device__ __forceinline__ int km_swz(int k) { return (k & 3) | (((k >> 3) & 3) << 2); }
+
+// acc = A B^T over nks steps of 64 k: A K-major, B K-major or K-contiguous
+// (kBMajor). epi(acc) as in run_tiles8: acc[bm][bn][i] is A column 128 wv + 16
+// bm + 4 quad + i against B 64 tq + 16 bn + c16. All 512 threads call this.
+template <bool kBMajor, class Epi>
+__device__ __forceinline__ void run_tile_km(uint4* smem, const Lanes8& L, const KmOperand& A, const KmOperand& B, int nks,
+                                            Epi&& epi) {
+  constexpr int kAS = kWSlots, kBS = kHSlots;
+  const int lane = L.lane, wave = L.wave, quad = L.quad, c16 = L.c16;
+  const uint32_t lds0 = (uint32_t)(size_t)((__attribute__((address_space(3))) uint4*)smem);
+  const uint32_t my_rows = (uint32_t)wave * 32 * kStepBytes;  // a wavefront's 4 KiB of a slot, either kind
+
+  // Loads. K-major: load j of wavefront w fetches rows 8 w + 2 j + (lane / 32)
+  // at the chunk that belongs at position lane mod 32. K-contiguous: as in
+  // run_tiles8. Offsets less 1024 j for dma16x4, which underflow only for
+  // rows of less than 512 bytes: those are loaded one by one.
+  auto offsets = [&](uint32_t (&voff)[4], bool major, uint32_t row_bytes) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if (major) {
+        const int k = 8 * wave + 2 * j + (lane >> 5);
+        voff[j] = (uint32_t)k * row_bytes + (uint32_t)(((lane & 31) ^ (2 * km_swz(k))) * 16);
+      } else {
+        const int lr = lane >> 3;
+        voff[j] = (uint32_t)(wave * 32 + j * kDmaRows + lr) * row_bytes + (((lane & 7) ^ lr ^ (j & 1)) * 16);
+      }
+    }
+  };
+  uint32_t avoff[4], bvoff[4];
+  offsets(avoff, true, A.row_bytes);
+  offsets(bvoff, kBMajor, B.row_bytes);
+  const bool a_four = A.row_bytes >= 512, b_four = !kBMajor || B.row_bytes >= 512;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    if (a_four) avoff[j] -= 1024u * j;
+    if (b_four) bvoff[j] -= 1024u * j;
+  }
+  auto load = [&](const int4v& r, const uint32_t (&voff)[4], uint32_t soff, uint32_t lds, bool four) {
+    if (four) {
+      dma16x4(r, voff, soff, lds);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) dma16(r, voff[j], soff, lds + 1024u * j);
+    }
+  };
+  // a step past the end loads the last one again into a slot nothing reads
+  auto a_load = [&](int s) {
+    load(km_step_rsrc(A, s < nks ? s : nks - 1, 64), avoff, 0u, lds0 + (uint32_t)(s % kAS) * kSlotBytes + my_rows, a_four);
+  };
+  const int4v b_rows = rsrc_words(B.base, kBMajor ? 0u : (uint32_t)B.rows * B.row_bytes - B.skip);
+  auto b_load = [&](int s) {
+    const int st = s < nks ? s : nks - 1;
+    const uint32_t lds = lds0 + (uint32_t)(kAS + s % kBS) * kSlotBytes + my_rows;
+    if constexpr (kBMajor) load(km_step_rsrc(B, st, 64), bvoff, 0u, lds, b_four);
+    else load(b_rows, bvoff, (uint32_t)st * kStepBytes, lds, true);
+  };
+
+  // Fragment addresses within a slot (bytes). K-major block b, half kk, part
+  // p: row 32 kk + 8 lane_chunk(quad) + 4 p + c16 / 4, piece b ^ f.
+  const int krow = 8 * lane_chunk(quad) + (c16 >> 2);
+  const int f = km_swz(krow);  // (bits 2 and 5 of the row do not enter)
+  uint32_t a_off[8], b_off[4];
+#pragma unroll
+  for (int bm = 0; bm < 8; ++bm) a_off[bm] = (uint32_t)(krow * 512 + ((L.wv * 8 + bm) ^ f) * 32 + (c16 & 3) * 8);
+#pragma unroll
+  for (int bn = 0; bn < 4; ++bn) {
+    if constexpr (kBMajor) b_off[bn] = (uint32_t)(krow * 512 + ((L.tq * 4 + bn) ^ f) * 32 + (c16 & 3) * 8);
+    else b_off[bn] = 0;
+  }
+  int bc_off[2];
+#pragma unroll
+  for (int kk = 0; kk < 2; ++kk) bc_off[kk] = (L.tq * 64 + c16) * kRowChunks + ((4 * kk + lane_chunk(quad)) ^ swz(c16));
+
+  typedef __attribute__((address_space(3))) shortx4 lds_s4;
+  auto tr8 = [&](uint32_t at) {
+    const shortx4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4*)(size_t)at);
+    const shortx4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4*)(size_t)(at + 4 * 512));
+    const uint2 a = __builtin_bit_cast(uint2, lo), b = __builtin_bit_cast(uint2, hi);
+    return make_uint4(a.x, a.y, b.x, b.y);
+  };
+
+  b_load(0);
+  a_load(0);
+  b_load(1);
+  a_load(1);
+  wait_and_barrier<2 * kDma8PerWave>();
+  __builtin_amdgcn_sched_barrier(0);
+
+  uint4 FA[2][2], FB[2][4];
+  auto read_a = [&](int s, int kk, int bm) {
+    FA[(bm >> 1) & 1][bm & 1] = tr8(lds0 + (uint32_t)(s % kAS) * kSlotBytes + a_off[bm] + (uint32_t)kk * (32 * 512));
+  };
+  auto read_b = [&](int s, int kk, int bn) {
+    if constexpr (kBMajor)
+      FB[kk][bn] = tr8(lds0 + (uint32_t)(kAS + s % kBS) * kSlotBytes + b_off[bn] + (uint32_t)kk * (32 * 512));
+    else
+      FB[kk][bn] = smem[(kAS + s % kBS) * kSlotChunks + bc_off[kk] + bn * 16 * kRowChunks];
+  };
+  floatx4 acc[8][4];
+#pragma unroll
+  for (int bm = 0; bm < 8; ++bm)
+#pragma unroll
+    for (int bn = 0; bn < 4; ++bn) acc[bm][bn] = floatx4{};
+  // the sub-steps of run_tiles8, the far operand A, the near one B
+  auto sub = [&](auto J, auto next, int s) {
+    constexpr int j = decltype(J)::value;
+    constexpr int kk = j >> 2, p = j & 3;
+#pragma unroll
+    for (int q = 0; q < 8; ++q) {
+      const int b = q >> 2, bn = q & 3;
+      Mma16<0>::step(acc[2 * p + b][bn], FA[p & 1][b], FB[kk][bn]);
+      if constexpr (j < 6) {
+        if (q < 2) read_a(s, (j + 1) >> 2, 2 * ((j + 1) & 3) + q);
+        if (j < 4 && q == 2) read_b(s, 1, j);
+      } else if constexpr (j == 6) {
+        if (q < 2) read_a(s, 1, 6 + q);
+        if (q == 5) {
+          wait_and_barrier<kDma8PerWave>();
+          b_load(s + 2);
+        }
+        if (decltype(next)::value && q >= 6) read_b(s + 1, 0, q - 6);
+      } else {
+        if (decltype(next)::value && q < 2) read_a(s + 1, 0, q);
+        if (decltype(next)::value && (q == 2 || q == 3)) read_b(s + 1, 0, q);
+      }
+      if constexpr (j == 0) {
+        if (q == 3) a_load(s + 2);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  };
+  auto k_step = [&](int s, auto next) {
+    sub(std::integral_constant<int, 0>{}, next, s);
+    sub(std::integral_constant<int, 1>{}, next, s);
+    sub(std::integral_constant<int, 2>{}, next, s);
+    sub(std::integral_constant<int, 3>{}, next, s);
+    sub(std::integral_constant<int, 4>{}, next, s);
+    sub(std::integral_constant<int, 5>{}, next, s);
+    sub(std::integral_constant<int, 6>{}, next, s);
+    sub(std::integral_constant<int, 7>{}, next, s);
+  };
+  read_a(0, 0, 0);
+  read_a(0, 0, 1);
+#pragma unroll
+  for (int bn = 0; bn < 4; ++bn) read_b(0, 0, bn);
+  for (int s = 0; s + 1 < nks; ++s) k_step(s, std::true_type{});
+  k_step(nks - 1, std::false_type{});
+  // loads of the steps past the end may still be writing LDS
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+  epi(acc);
+}
+
+// ---- fp32
+
+constexpr int kF32Tile = 64;
+constexpr int kF32StepK = 32;                                            // 128 bytes of a K-contiguous row
+constexpr int kF32SlotBytes = kF32Tile * kF32StepK * 4;                  // 8 KiB, either kind
+constexpr int kF32Slots = 3;                                             // per operand, loaded two steps ahead
+constexpr int kF32SmemChunks = 2 * kF32Slots * kF32SlotBytes / 16;       // 48 KiB: three workgroups per CU
+constexpr int kF32Threads = 256;
+
+// acc = A B^T over nks steps of 32 k, 64 x 64: wavefront w holds A columns
+// 32 (w mod 2) .. against B 32 (w / 2) .., as 2 x 2 blocks; acc[bm][bn][i] is
+// A 32 (w & 1) + 16 bm + 4 quad + i, B 32 (w >> 1) + 16 bn + c16. A is
+// K-major, B K-major or K-contiguous. K-major rows are 256 bytes; their
+// 64-byte piece (16 columns) P of row k sits at P ^ ((k / 4) mod 4).
+template <bool kBMajor, class Epi>
+__device__ __forceinline__ void run_tile_f32(uint4* smem, const KmOperand& A, const KmOperand& B, int nks, Epi&& epi) {
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int quad = lane >> 4, c16 = lane & 15;
+  const uint32_t lds0 = (uint32_t)(size_t)((__attribute__((address_space(3))) uint4*)smem);
+  // two loads per operand, step and wavefront: 2 KiB of the 8 KiB slot
+  auto offset = [&](int j, bool major, uint32_t row_bytes) -> uint32_t {
+    if (major) {  // rows 8 w + 4 j + lane / 16
+      const int k = 8 * wave + 4 * j + (lane >> 4);
+      return (uint32_t)k * row_bytes + (uint32_t)(((lane & 15) ^ (4 * ((k >> 2) & 3))) * 16);
+    }
+    const int lr = lane >> 3;  // rows 16 w + 8 j + lane / 8
+    return (uint32_t)(16 * wave + 8 * j + lr) * row_bytes + (((lane & 7) ^ lr ^ (j & 1)) * 16);
+  };
+  const uint32_t ao[2] = {offset(0, true, A.row_bytes), offset(1, true, A.row_bytes)};
+  const uint32_t bo[2] = {offset(0, kBMajor, B.row_bytes), offset(1, kBMajor, B.row_bytes)};
+  const int4v b_rows = rsrc_words(B.base, kBMajor ? 0u : (uint32_t)B.rows * B.row_bytes - B.skip);
+  auto load = [&](int s) {
+    const int st = s < nks ? s : nks - 1;
+    const uint32_t slot = (uint32_t)(s % kF32Slots) * kF32SlotBytes + (uint32_t)wave * 2048u;
+    const int4v ar = km_step_rsrc(A, st, kF32StepK);
+    const int4v br = kBMajor ? km_step_rsrc(B, st, kF32StepK) : b_rows;
+    const uint32_t soff = kBMajor ? 0u : (uint32_t)st * kStepBytes;
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      dma16(ar, ao[j], 0u, lds0 + slot + 1024u * j);
+      dma16(br, bo[j], soff, lds0 + kF32Slots * kF32SlotBytes + slot + 1024u * j);
+    }
+  };
+  const float* lds_f = reinterpret_cast<const float*>(smem);
+  floatx4 acc[2][2];
+#pragma unroll
+  for (int bm = 0; bm < 2; ++bm)
+#pragma unroll
+    for (int bn = 0; bn < 2; ++bn) acc[bm][bn] = floatx4{};
+  load(0);
+  load(1);
+  for (int s = 0; s < nks; ++s) {
+    // step s landed (step s + 1 may be in flight); every wavefront is done
+    // with step s - 1, whose slot takes step s + 2
+    wait_and_barrier<4>();
+    load(s + 2);
+    const int slot = (s % kF32Slots) * (kF32SlotBytes / 4);
+    const float* sa = lds_f + slot;
+    const float* sb = lds_f + kF32Slots * (kF32SlotBytes / 4) + slot;
+    // value j of half kk: k = 16 kk + 4 lane_chunk(quad) + j
+    auto major = [&](const float* t, int block, int kk, int j) {
+      const int k = 16 * kk + 4 * lane_chunk(quad) + j;
+      return t[k * 64 + ((block ^ ((k >> 2) & 3)) * 16) + c16];
+    };
+#pragma unroll
+    for (int kk = 0; kk < 2; ++kk) {
+      float a[2][4], b[2][4];
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) a[t][j] = major(sa, 2 * (wave & 1) + t, kk, j);
+        if constexpr (kBMajor) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) b[t][j] = major(sb, 2 * (wave >> 1) + t, kk, j);
+        } else {
+          const int row = 32 * (wave >> 1) + 16 * t + c16;
+          const float4 v = reinterpret_cast<const float4*>(sb)[row * kRowChunks + ((4 * kk + lane_chunk(quad)) ^ swz(c16))];
+          b[t][0] = v.x, b[t][1] = v.y, b[t][2] = v.z, b[t][3] = v.w;
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int bm = 0; bm < 2; ++bm)
+#pragma unroll
+          for (int bn = 0; bn < 2; ++bn)
+            acc[bm][bn] = __builtin_amdgcn_mfma_f32_16x16x4f32(a[bm][j], b[bn][j], acc[bm][bn], 0, 0, 0);
+    }
+  }
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+  epi(acc, wave, quad, c16);
+}
+
+}  // namespace itl
