@@ -279,27 +279,61 @@ __global__ __launch_bounds__(kThreads, 1) void ce_partial_narrow_kernel(
 
 // ---- mean of the logits (label smoothing): z's mean over v is H . mean_v W[v]
 
-constexpr int kMeanRows = 512;  // rows of W per partial sum
+constexpr int kMeanRows = 256;  // rows of W per partial sum
 
-// part[b, k] = sum of W[v, k] over kMeanRows rows v; 256 columns per workgroup.
+// part[b, k] = sum of W[v, k] over kMeanRows rows v: 512 columns per workgroup,
+// 8 per thread, four wavefronts on rows v, v + 4, ... each, then added in
+// order. One pass over W at the memory's rate.
 template <int kDtype>
 __global__ __launch_bounds__(256) void ce_colsum_kernel(const typename Elem<kDtype>::T* __restrict__ W, int vocab, int d,
                                                         float* __restrict__ part) {
   using E = Elem<kDtype>;
-  const int k = blockIdx.y * 256 + threadIdx.x;
-  if (k >= d) return;
+  __shared__ float lds[3][512];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int k = blockIdx.y * 512 + 8 * lane;  // (d is a multiple of 8)
   const int v0 = blockIdx.x * kMeanRows, v1 = min(vocab, v0 + kMeanRows);
-  float s = 0.0f;
-  for (int v = v0; v < v1; ++v) s += E::to_f(W[(size_t)v * d + k]);
-  part[(size_t)blockIdx.x * d + k] = s;
+  float s[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+  if (k < d) {
+#pragma unroll 8
+    for (int v = v0 + wave; v < v1; v += 4) {
+      const uint4* row = reinterpret_cast<const uint4*>(W + (size_t)v * d + k);
+      uint4 w[E::kSize / 2];
+#pragma unroll
+      for (int i = 0; i < E::kSize / 2; ++i) w[i] = row[i];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const uint32_t x = (&w[0].x)[kDtype == 0 ? j >> 1 : j];
+        s[j] += kDtype == 1 ? __uint_as_float(x) : __uint_as_float((j & 1) ? (x & 0xffff0000u) : (x << 16));
+      }
+    }
+  }
+  if (wave > 0) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) lds[wave - 1][j * 64 + lane] = s[j];
+  }
+  __syncthreads();
+  if (wave > 0 || k >= d) return;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) s[j] = ((s[j] + lds[0][j * 64 + lane]) + lds[1][j * 64 + lane]) + lds[2][j * 64 + lane];
+  float4* out = reinterpret_cast<float4*>(part + (size_t)blockIdx.x * d + k);
+  out[0] = make_float4(s[0], s[1], s[2], s[3]);
+  out[1] = make_float4(s[4], s[5], s[6], s[7]);
 }
 
-__global__ __launch_bounds__(256) void ce_colmean_kernel(const float* __restrict__ part, int n_part, int d, int vocab,
-                                                         float* __restrict__ wmean) {
-  const int k = blockIdx.x * 256 + threadIdx.x;
-  if (k >= d) return;
+// The partial sums in a fixed order (16 wavefronts on every 16th, then the
+// wavefronts), over V.
+__global__ __launch_bounds__(1024) void ce_colmean_kernel(const float* __restrict__ part, int n_part, int d, int vocab,
+                                                          float* __restrict__ wmean) {
+  __shared__ double lds[16][64];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int k = blockIdx.x * 64 + lane;  // (d is a multiple of 64)
   double s = 0.0;
-  for (int b = 0; b < n_part; ++b) s += (double)part[(size_t)b * d + k];
+#pragma unroll 8
+  for (int b = wave; b < n_part; b += 16) s += (double)part[(size_t)b * d + k];
+  lds[wave][lane] = s;
+  __syncthreads();
+  if (wave > 0) return;
+  for (int w = 1; w < 16; ++w) s += lds[w][lane];
   wmean[k] = (float)(s / (double)vocab);
 }
 
@@ -760,9 +794,9 @@ hipError_t run_cross_entropy(const CeCall& c, hipStream_t stream) {
   ITL_CHECK_LAUNCH();
   if (wmean) {
     const int nb = (int)ceil_div(vocab, kMeanRows);
-    hipLaunchKernelGGL(ce_colsum_kernel<kDtype>, dim3((unsigned)nb, (unsigned)ceil_div(d, 256)), dim3(256), 0, stream, W,
+    hipLaunchKernelGGL(ce_colsum_kernel<kDtype>, dim3((unsigned)nb, (unsigned)ceil_div(d, 512)), dim3(256), 0, stream, W,
                        vocab, d, wpart);
-    hipLaunchKernelGGL(ce_colmean_kernel, dim3((unsigned)ceil_div(d, 256)), dim3(256), 0, stream, wpart, nb, d, vocab,
+    hipLaunchKernelGGL(ce_colmean_kernel, dim3((unsigned)(d / 64)), dim3(1024), 0, stream, wpart, nb, d, vocab,
                        wmean);
     ITL_CHECK_LAUNCH();
   }
