@@ -491,7 +491,7 @@ __global__ __launch_bounds__(kDtype == 0 ? kThreads8 : kF32Threads, 1) void ce_d
     const char* __restrict__ W, const char* __restrict__ Gd, int vocab, int vpad, int d, const int32_t* __restrict__ count,
     int c0, int cap, int n_dt, const int32_t* __restrict__ splits_of, float* __restrict__ part) {
   constexpr int kT = GradTile<kDtype>::kRows, kStepK = GradTile<kDtype>::kStepK, es = Elem<kDtype>::kSize;
-  __shared__ uint4 smem[kDtype == 0 ? kEngineSmemChunks : kF32SmemChunks];
+  __shared__ __align__(1024) uint4 smem[kDtype == 0 ? kEngineSmemChunks : kF32SmemChunks];
   const int live = __builtin_amdgcn_readfirstlane(chunk_live(count, c0, cap));
   const int splits = __builtin_amdgcn_readfirstlane(*splits_of);
   const int n_tb = (live + kT - 1) / kT;
@@ -502,7 +502,8 @@ __global__ __launch_bounds__(kDtype == 0 ? kThreads8 : kF32Threads, 1) void ce_d
   const int nks_all = vpad / kStepK;
   const int ks0 = (int)((long long)nks_all * sp / splits), ks1 = (int)((long long)nks_all * (sp + 1) / splits);
   const uint32_t w_row = (uint32_t)d * es, g_row = (uint32_t)vpad * es, d_off = (uint32_t)dt * kT * es;
-  const KmOperand A{W + (size_t)ks0 * kStepK * w_row + d_off, w_row, vocab - ks0 * kStepK, d_off};
+  const char* w_rows = W + (size_t)ks0 * kStepK * w_row;
+  const int w_left = vocab - ks0 * kStepK;
   const KmOperand B{Gd + (size_t)t0 * g_row + (size_t)ks0 * kStepBytes, g_row, min(kT, live - t0),
                     (uint32_t)ks0 * kStepBytes};
   float* out = part + (size_t)sp * n_tb * kT * d;
@@ -511,7 +512,8 @@ __global__ __launch_bounds__(kDtype == 0 ? kThreads8 : kF32Threads, 1) void ce_d
   };
   if constexpr (kDtype == 0) {
     const Lanes8 L = lanes8();
-    run_tile_km<false>(smem, L, A, B, ks1 - ks0, [&](floatx4 (&acc)[8][4]) {
+    run_tiles_km<false, false>(smem, L, KmOperand{w_rows, w_row, w_left, 0u}, B, dt, dt + 1, ks1 - ks0,
+                        [&](int, floatx4 (&acc)[8][4]) {
 #pragma unroll
       for (int bn = 0; bn < 4; ++bn)
 #pragma unroll
@@ -519,7 +521,7 @@ __global__ __launch_bounds__(kDtype == 0 ? kThreads8 : kF32Threads, 1) void ce_d
           store(t0 + L.tq * 64 + bn * 16 + L.c16, dt * kT + L.wv * 128 + bm * 16 + 4 * L.quad, acc[bm][bn]);
     });
   } else {
-    run_tile_f32<false>(smem, A, B, ks1 - ks0, [&](floatx4 (&acc)[2][2], int wave, int quad, int c16) {
+    run_tile_f32<false>(smem, KmOperand{w_rows + d_off, w_row, w_left, d_off}, B, ks1 - ks0, [&](floatx4 (&acc)[2][2], int wave, int quad, int c16) {
 #pragma unroll
       for (int bn = 0; bn < 2; ++bn)
 #pragma unroll
@@ -576,48 +578,56 @@ __global__ __launch_bounds__(256) void ce_zero_rows_kernel(const int32_t* __rest
 // ---- dW
 
 // The chunk's part of dW: A = Hc (columns d0 ..), B = Gd (columns v0 ..), K =
-// the chunk's live tokens. add: dW already holds earlier parts (fp32).
+// the chunk's live tokens.
 // Vocabulary tiles fastest within bands: workgroups that run together share
-// operands.
-template <int kDtype>
+// operands. A workgroup walks up to `walk` tiles of d (fp32: one), so that a
+// tile's first loads and last stores run under its neighbours' products.
+enum { kDwRound = 0, kDwWrite = 1, kDwAdd = 2 };  // bf16 results; fp32 ones; fp32 ones on top of dW
+
+template <int kDtype, int kMode>
 __global__ __launch_bounds__(kDtype == 0 ? kThreads8 : kF32Threads, 1) void ce_dw_kernel(
     const char* __restrict__ Gd, const char* __restrict__ Hc, int vpad, const int32_t* __restrict__ count, int c0, int cap,
-    int vocab, int d, int n_vt, int n_dt, GradScale gs, int add, int out_f32, void* __restrict__ dW) {
+    int vocab, int d, int n_vt, int n_dt, int walk, GradScale gs, void* __restrict__ dW) {
   constexpr int kT = GradTile<kDtype>::kRows, kStepK = GradTile<kDtype>::kStepK, es = Elem<kDtype>::kSize;
-  __shared__ uint4 smem[kDtype == 0 ? kEngineSmemChunks : kF32SmemChunks];
+  __shared__ __align__(1024) uint4 smem[kDtype == 0 ? kEngineSmemChunks : kF32SmemChunks];
   const int live = __builtin_amdgcn_readfirstlane(chunk_live(count, c0, cap));
   if (live == 0 && c0 > 0) return;  // (the first chunk writes its zeros)
-  const int band = blockIdx.x / (kBwdSuperBand * n_dt);
+  const int n_walk = (n_dt + walk - 1) / walk;  // walks of up to `walk` tiles of d
+  const int band = blockIdx.x / (kBwdSuperBand * n_walk);
   const int first = band * kBwdSuperBand;
   const int nb = min(kBwdSuperBand, n_vt - first);
-  const int rem = blockIdx.x - band * kBwdSuperBand * n_dt;
-  const int vt = first + rem % nb, dt = rem / nb;
+  const int rem = blockIdx.x - band * kBwdSuperBand * n_walk;
+  const int vt = first + rem % nb, dt = rem / nb * walk, dt_end = min(dt + walk, n_dt);
   const int nks = max(1, (live + kStepK - 1) / kStepK);
   const uint32_t h_row = (uint32_t)d * es, g_row = (uint32_t)vpad * es;
   const uint32_t d_off = (uint32_t)dt * kT * es, v_off = (uint32_t)vt * kT * es;
-  const KmOperand A{Hc + d_off, h_row, live, d_off}, B{Gd + v_off, g_row, live, v_off};
+  const KmOperand B{Gd + v_off, g_row, live, v_off};
   const float unit = grad_unit(gs, count);
   auto store = [&](int v, int k, const floatx4& o) {
     if (v >= vocab || k >= d) return;
     const size_t at = (size_t)v * d + k;
     float x[4] = {o[0] * unit, o[1] * unit, o[2] * unit, o[3] * unit};
-    if (add) {
+    if constexpr (kMode == kDwAdd) {
       const float4 old = *reinterpret_cast<const float4*>(static_cast<const float*>(dW) + at);
       x[0] += old.x, x[1] += old.y, x[2] += old.z, x[3] += old.w;
     }
-    store_grad4(dW, out_f32, at, x);
+    store_grad4(dW, kMode != kDwRound, at, x);
   };
   if constexpr (kDtype == 0) {
     const Lanes8 L = lanes8();
-    run_tile_km<true>(smem, L, A, B, nks, [&](floatx4 (&acc)[8][4]) {
+    run_tiles_km<true, true>(smem, L, KmOperand{Hc, h_row, live, 0u}, B, dt, dt_end, nks, [&](int tile, floatx4 (&acc)[8][4]) {
+      int lane = L.lane;  // made opaque: addresses formed here, not kept live across the K loop
+      asm volatile("" : "+v"(lane));
+      const int v0 = vt * kT + L.tq * 64 + (lane & 15), k0 = tile * kT + L.wv * 128 + 4 * (lane >> 4);
 #pragma unroll
-      for (int bn = 0; bn < 4; ++bn)
+      for (int bn = 0; bn < 4; ++bn) {
 #pragma unroll
-        for (int bm = 0; bm < 8; ++bm)
-          store(vt * kT + L.tq * 64 + bn * 16 + L.c16, dt * kT + L.wv * 128 + bm * 16 + 4 * L.quad, acc[bm][bn]);
+        for (int bm = 0; bm < 8; ++bm) store(v0 + bn * 16, k0 + bm * 16, acc[bm][bn]);
+        __builtin_amdgcn_sched_barrier(0);
+      }
     });
   } else {
-    run_tile_f32<true>(smem, A, B, nks, [&](floatx4 (&acc)[2][2], int wave, int quad, int c16) {
+    run_tile_f32<true>(smem, KmOperand{Hc + d_off, h_row, live, d_off}, B, nks, [&](floatx4 (&acc)[2][2], int wave, int quad, int c16) {
 #pragma unroll
       for (int bn = 0; bn < 2; ++bn)
 #pragma unroll
@@ -666,6 +676,18 @@ void dh_most(long long cap, long long d, long long vpad, int dtype, long long* g
     *groups = std::max(*groups, n_tb * n_dt * s);
     *rows = std::max(*rows, n_tb * tile * s);
   }
+}
+
+// Tiles of d a dW workgroup walks: the count that takes the fewest K steps of
+// time over the rounds of 256 workgroups, with 12 steps' worth (the first
+// loads and the last stores) for each workgroup's start and end.
+int dw_walk(long long n_vt, long long n_dt, long long nks) {
+  long long best = 1, best_cost = -1;
+  for (long long w = 1; w <= n_dt; ++w) {
+    const long long cost = ceil_div(n_vt * ceil_div(n_dt, w), 256) * (w * nks + 12);
+    if (best_cost < 0 || cost < best_cost) best = w, best_cost = cost;
+  }
+  return (int)best;
 }
 
 struct CeLayout {
@@ -845,6 +867,7 @@ hipError_t run_cross_entropy(const CeCall& c, hipStream_t stream) {
     constexpr int kT = GradTile<kDtype>::kRows;
     const dim3 g_block(kDtype == 0 ? kThreads8 : kF32Threads);
     const int n_dt = (int)ceil_div(d, kT), n_vt = (int)ceil_div(vocab, kT);
+    const int walk = kDtype == 0 ? dw_walk(n_vt, n_dt, ceil_div(cap, GradTile<kDtype>::kStepK)) : 1;
     const int32_t* splits = reinterpret_cast<const int32_t*>(at(L.splits)) + c0 / L.cap;
     hipLaunchKernelGGL(ce_dh_kernel<kDtype>, dim3((unsigned)L.dh_groups), g_block, 0, stream,
                        reinterpret_cast<const char*>(W), reinterpret_cast<const char*>(Gd), vocab, L.vpad, d, count, c0, cap,
@@ -867,9 +890,14 @@ hipError_t run_cross_entropy(const CeCall& c, hipStream_t stream) {
     } else if (!single) {
       out = acc, out_f32 = 1, add = c0 > 0;
     }
-    hipLaunchKernelGGL(ce_dw_kernel<kDtype>, dim3((unsigned)(n_vt * n_dt)), g_block, 0, stream,
-                       reinterpret_cast<const char*>(Gd), Hc, L.vpad, count, c0, cap, vocab, d, n_vt, n_dt, gs, add, out_f32,
-                       out);
+    auto dw = [&](auto mode) {
+      hipLaunchKernelGGL((ce_dw_kernel<kDtype, decltype(mode)::value>), dim3((unsigned)(n_vt * ceil_div(n_dt, walk))),
+                         g_block, 0, stream, reinterpret_cast<const char*>(Gd), Hc, L.vpad, count, c0, cap, vocab, d, n_vt,
+                         n_dt, walk, gs, out);
+    };
+    if (add) dw(std::integral_constant<int, kDwAdd>{});
+    else if (out_f32) dw(std::integral_constant<int, kDwWrite>{});
+    else dw(std::integral_constant<int, kDwRound>{});
     ITL_CHECK_LAUNCH();
     if (exact && !single && c0 > 0) {
       hipLaunchKernelGGL(ce_add_kernel, dim3((unsigned)ceil_div((long long)vocab * d / 4, 256)), dim3(256), 0, stream,

@@ -4,7 +4,7 @@
 // and H are not made: the operand comes into LDS as it lies, and the fragments
 // are read through the transposing LDS read.
 //
-// bf16 (run_tile_km): 256 x 256 tiles on the eight-wavefront schedule of
+// bf16 (run_tiles_km): 256 x 256 tiles on the eight-wavefront schedule of
 // tile_engine8.h (same wavefront tiles, slots, barriers and load places). A
 // K step of a K-major operand is 64 rows of 512 bytes, 32 KiB, one slot. The
 // read (ds_read_b64_tr_b16, measured layout): in each group of 16 lanes, lane
@@ -12,8 +12,9 @@
 // receives column i of rows k0 .. k0 + 3. Two reads give a lane the 8 values
 // of k that the K-contiguous operand's 16-byte chunk holds, so both kinds
 // meet in one instruction. The 32-byte piece (16 columns) P of row k sits at
-// piece P ^ f(k), f(k) = (k mod 4) + 4 ((k / 8) mod 4): a group's 4 rows fall
-// on 128 consecutive bytes, a read's 16 rows on 16 different pieces.
+// piece P ^ f(k), f(k) = (k mod 4) + 4 (bit 4 of k) + 8 (bit 3 of k): the 8
+// rows that lanes 0-31 (or 32-63) read, whose k differ in bits 0, 1 and 4 (see
+// lane_chunk), fall on 8 pieces that cover all 64 banks.
 //
 // fp32 (run_tile_f32): 64 x 64 tiles, four wavefronts of 32 x 32. The fp32
 // matrix rate is a sixteenth of bf16's, so such a tile is bound by it all the
@@ -46,15 +47,19 @@ __device__ __forceinline__ int4v km_step_rsrc(const KmOperand& o, int s, int ste
   return rsrc_words(o.base + (size_t)s * step_rows * o.row_bytes, n);
 }
 
-__device__ __forceinline__ int km_swz(int k) { return (k & 3) | (((k >> 3) & 3) << 2); }
+__device__ __forceinline__ int km_swz(int k) { return (k & 3) | (((k >> 4) & 1) << 2) | (((k >> 3) & 1) << 3); }
 
-// acc = A B^T over nks steps of 64 k: A K-major, B K-major or K-contiguous
-// (kBMajor). epi(acc) as in run_tiles8: acc[bm][bn][i] is A column 128 wv + 16
-// bm + 4 quad + i against B 64 tq + 16 bn + c16. All 512 threads call this.
-template <bool kBMajor, class Epi>
-__device__ __forceinline__ void run_tile_km(uint4* smem, const Lanes8& L, const KmOperand& A, const KmOperand& B, int nks,
-                                            Epi&& epi) {
-  constexpr int kAS = kWSlots, kBS = kHSlots;
+// For tiles tile_begin .. tile_end - 1 of A (a tile's columns 512 bytes behind
+// the last one's; A is given at column 0, skip 0): acc = A_tile B^T over nks
+// steps of 64 k, A K-major, B K-major or K-contiguous (kBMajor). epi(tile, acc)
+// as in run_tiles8 (smem 1 KiB aligned): acc[bm][bn][i] is A column 128 wv + 16 bm + 4 quad + i
+// against B 64 tq + 16 bn + c16. The next tile's first steps are loaded while
+// a tile ends and is stored. All 512 threads call this.
+// The far operand (three slots, loaded two steps ahead) is A, with kBFar B.
+template <bool kBMajor, bool kBFar, class Epi>
+__device__ __forceinline__ void run_tiles_km(uint4* smem, const Lanes8& L, const KmOperand& A, const KmOperand& B,
+                                             int tile_begin, int tile_end, int nks, Epi&& epi) {
+  constexpr int kAS = kBFar ? kHSlots : kWSlots, kBS = kBFar ? kWSlots : kHSlots;
   const int lane = L.lane, wave = L.wave, quad = L.quad, c16 = L.c16;
   const uint32_t lds0 = (uint32_t)(size_t)((__attribute__((address_space(3))) uint4*)smem);
   const uint32_t my_rows = (uint32_t)wave * 32 * kStepBytes;  // a wavefront's 4 KiB of a slot, either kind
@@ -92,30 +97,36 @@ __device__ __forceinline__ void run_tile_km(uint4* smem, const Lanes8& L, const 
       for (int j = 0; j < 4; ++j) dma16(r, voff[j], soff, lds + 1024u * j);
     }
   };
-  // a step past the end loads the last one again into a slot nothing reads
+  // Each operand's loads come in step order: running counts of the step
+  // within the tile. A step past the end loads the last one again into a slot
+  // nothing reads.
+  int a_tile = tile_begin, a_ks = 0, b_ks = 0, b_left = (tile_end - tile_begin) * nks;
   auto a_load = [&](int s) {
-    load(km_step_rsrc(A, s < nks ? s : nks - 1, 64), avoff, 0u, lds0 + (uint32_t)(s % kAS) * kSlotBytes + my_rows, a_four);
+    const uint32_t at = (uint32_t)a_tile * 512u;
+    load(km_step_rsrc(KmOperand{A.base + at, A.row_bytes, A.rows, at}, a_ks, 64), avoff, 0u,
+         lds0 + (uint32_t)(s % kAS) * kSlotBytes + my_rows, a_four);
+    if (a_ks + 1 < nks) ++a_ks;
+    else if (a_tile + 1 < tile_end) a_ks = 0, ++a_tile;
+    a_ks = __builtin_amdgcn_readfirstlane(a_ks);
+    a_tile = __builtin_amdgcn_readfirstlane(a_tile);
   };
   const int4v b_rows = rsrc_words(B.base, kBMajor ? 0u : (uint32_t)B.rows * B.row_bytes - B.skip);
   auto b_load = [&](int s) {
-    const int st = s < nks ? s : nks - 1;
     const uint32_t lds = lds0 + (uint32_t)(kAS + s % kBS) * kSlotBytes + my_rows;
-    if constexpr (kBMajor) load(km_step_rsrc(B, st, 64), bvoff, 0u, lds, b_four);
-    else load(b_rows, bvoff, (uint32_t)st * kStepBytes, lds, true);
+    if constexpr (kBMajor) load(km_step_rsrc(B, b_ks, 64), bvoff, 0u, lds, b_four);
+    else load(b_rows, bvoff, (uint32_t)b_ks * kStepBytes, lds, true);
+    if (--b_left > 0) b_ks = b_ks + 1 < nks ? b_ks + 1 : 0;
+    b_ks = __builtin_amdgcn_readfirstlane(b_ks);
   };
 
   // Fragment addresses within a slot (bytes). K-major block b, half kk, part
-  // p: row 32 kk + 8 lane_chunk(quad) + 4 p + c16 / 4, piece b ^ f.
+  // p: row 32 kk + 8 lane_chunk(quad) + 4 p + c16 / 4, piece b ^ f. A block's
+  // number enters bits 5 and up by an exclusive or alone, so one register
+  // serves all blocks.
   const int krow = 8 * lane_chunk(quad) + (c16 >> 2);
   const int f = km_swz(krow);  // (bits 2 and 5 of the row do not enter)
-  uint32_t a_off[8], b_off[4];
-#pragma unroll
-  for (int bm = 0; bm < 8; ++bm) a_off[bm] = (uint32_t)(krow * 512 + ((L.wv * 8 + bm) ^ f) * 32 + (c16 & 3) * 8);
-#pragma unroll
-  for (int bn = 0; bn < 4; ++bn) {
-    if constexpr (kBMajor) b_off[bn] = (uint32_t)(krow * 512 + ((L.tq * 4 + bn) ^ f) * 32 + (c16 & 3) * 8);
-    else b_off[bn] = 0;
-  }
+  const uint32_t a_off = (uint32_t)(krow * 512 + ((L.wv * 8) ^ f) * 32 + (c16 & 3) * 8);
+  const uint32_t b_off = (uint32_t)(krow * 512 + ((L.tq * 4) ^ f) * 32 + (c16 & 3) * 8);
   int bc_off[2];
 #pragma unroll
   for (int kk = 0; kk < 2; ++kk) bc_off[kk] = (L.tq * 64 + c16) * kRowChunks + ((4 * kk + lane_chunk(quad)) ^ swz(c16));
@@ -128,29 +139,39 @@ __device__ __forceinline__ void run_tile_km(uint4* smem, const Lanes8& L, const 
     return make_uint4(a.x, a.y, b.x, b.y);
   };
 
-  b_load(0);
-  a_load(0);
-  b_load(1);
-  a_load(1);
+  auto near_load = [&](int s) {
+    if constexpr (kBFar) a_load(s);
+    else b_load(s);
+  };
+  auto far_load = [&](int s) {
+    if constexpr (kBFar) b_load(s);
+    else a_load(s);
+  };
+  near_load(0);
+  far_load(0);
+  near_load(1);
+  far_load(1);
   wait_and_barrier<2 * kDma8PerWave>();
   __builtin_amdgcn_sched_barrier(0);
 
   uint4 FA[2][2], FB[2][4];
   auto read_a = [&](int s, int kk, int bm) {
-    FA[(bm >> 1) & 1][bm & 1] = tr8(lds0 + (uint32_t)(s % kAS) * kSlotBytes + a_off[bm] + (uint32_t)kk * (32 * 512));
+    FA[(bm >> 1) & 1][bm & 1] = tr8(((lds0 + (uint32_t)(s % kAS) * kSlotBytes + a_off) ^ (uint32_t)(bm * 32)) + (uint32_t)kk * (32 * 512));
   };
   auto read_b = [&](int s, int kk, int bn) {
     if constexpr (kBMajor)
-      FB[kk][bn] = tr8(lds0 + (uint32_t)(kAS + s % kBS) * kSlotBytes + b_off[bn] + (uint32_t)kk * (32 * 512));
+      FB[kk][bn] = tr8(((lds0 + (uint32_t)(kAS + s % kBS) * kSlotBytes + b_off) ^ (uint32_t)(bn * 32)) + (uint32_t)kk * (32 * 512));
     else
       FB[kk][bn] = smem[(kAS + s % kBS) * kSlotChunks + bc_off[kk] + bn * 16 * kRowChunks];
   };
   floatx4 acc[8][4];
+  auto zero_acc = [&]() {
 #pragma unroll
-  for (int bm = 0; bm < 8; ++bm)
+    for (int bm = 0; bm < 8; ++bm)
 #pragma unroll
-    for (int bn = 0; bn < 4; ++bn) acc[bm][bn] = floatx4{};
-  // the sub-steps of run_tiles8, the far operand A, the near one B
+      for (int bn = 0; bn < 4; ++bn) acc[bm][bn] = floatx4{};
+  };
+  // the sub-steps of run_tiles8
   auto sub = [&](auto J, auto next, int s) {
     constexpr int j = decltype(J)::value;
     constexpr int kk = j >> 2, p = j & 3;
@@ -165,7 +186,7 @@ __device__ __forceinline__ void run_tile_km(uint4* smem, const Lanes8& L, const 
         if (q < 2) read_a(s, 1, 6 + q);
         if (q == 5) {
           wait_and_barrier<kDma8PerWave>();
-          b_load(s + 2);
+          near_load(s + 2);
         }
         if (decltype(next)::value && q >= 6) read_b(s + 1, 0, q - 6);
       } else {
@@ -173,7 +194,7 @@ __device__ __forceinline__ void run_tile_km(uint4* smem, const Lanes8& L, const 
         if (decltype(next)::value && (q == 2 || q == 3)) read_b(s + 1, 0, q);
       }
       if constexpr (j == 0) {
-        if (q == 3) a_load(s + 2);
+        if (q == 3) far_load(s + 2);
       }
       __builtin_amdgcn_sched_barrier(0);
     }
@@ -188,15 +209,27 @@ __device__ __forceinline__ void run_tile_km(uint4* smem, const Lanes8& L, const 
     sub(std::integral_constant<int, 6>{}, next, s);
     sub(std::integral_constant<int, 7>{}, next, s);
   };
-  read_a(0, 0, 0);
-  read_a(0, 0, 1);
+  auto read_first = [&](int s) {
+    read_a(s, 0, 0);
+    read_a(s, 0, 1);
 #pragma unroll
-  for (int bn = 0; bn < 4; ++bn) read_b(0, 0, bn);
-  for (int s = 0; s + 1 < nks; ++s) k_step(s, std::true_type{});
-  k_step(nks - 1, std::false_type{});
+    for (int bn = 0; bn < 4; ++bn) read_b(s, 0, bn);
+  };
+  zero_acc();
+  read_first(0);
+  int s = 0;
+  for (int tile = tile_begin; tile < tile_end; ++tile) {
+    for (int ks = 0; ks + 1 < nks; ++ks, ++s) k_step(s, std::true_type{});
+    k_step(s, std::false_type{});
+    ++s;
+    epi(tile, acc);
+    __builtin_amdgcn_sched_barrier(0);
+    asm volatile("" ::: "memory");
+    zero_acc();
+    if (tile + 1 < tile_end) read_first(s);
+  }
   // loads of the steps past the end may still be writing LDS
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-  epi(acc);
 }
 
 // ---- fp32
