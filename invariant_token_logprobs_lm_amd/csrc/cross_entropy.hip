@@ -577,10 +577,34 @@ __global__ __launch_bounds__(256) void ce_zero_rows_kernel(const int32_t* __rest
 
 // ---- dW
 
+// Tile of workgroup b of dW's contraction. Workgroups go to the 8 XCDs in
+// turn; XCD x takes the vocabulary tiles x, x + 8, ..., in blocks of 5 of them
+// by 6 tiles of d, so that the 30 or so workgroups it runs together share 5
+// columns of G and 6 of H through its L2, and G comes from memory once for
+// every 6 tiles of d. (With 32 vocabulary tiles side by side, each XCD read G
+// once per tile of d: 16 GB in 3.9 ms at d = 7168, the memory's limit.)
+constexpr int kDwWalk = 1;
+constexpr int kDwVocabTiles = 5, kDwWidthTiles = 6;
+
+__host__ __device__ inline bool dw_work(int b, int n_vt, int n_dt, int& vt, int& dt) {
+  const int x = b & 7, i = b >> 3;
+  const int rows = kDwVocabTiles * n_dt;
+  const int rem = i % rows, g = rem / (kDwVocabTiles * kDwWidthTiles);
+  const int left = n_dt - g * kDwWidthTiles, w = left < kDwWidthTiles ? left : kDwWidthTiles;
+  const int r = rem - g * kDwVocabTiles * kDwWidthTiles;
+  dt = g * kDwWidthTiles + r % w;
+  vt = x + 8 * (i / rows * kDwVocabTiles + r / w);
+  return vt < n_vt;
+}
+
+// Workgroups that cover every tile (a few of them past the last).
+inline long long dw_groups(long long n_vt, long long n_dt) {
+  return 8 * ceil_div(ceil_div(n_vt, 8), kDwVocabTiles) * kDwVocabTiles * n_dt;
+}
+
 // The chunk's part of dW: A = Hc (columns d0 ..), B = Gd (columns v0 ..), K =
 // the chunk's live tokens.
-// Vocabulary tiles fastest within bands: workgroups that run together share
-// operands. A workgroup walks up to `walk` tiles of d (fp32: one), so that a
+// A workgroup walks up to `walk` tiles of d (fp32: one), so that a
 // tile's first loads and last stores run under its neighbours' products.
 enum { kDwRound = 0, kDwWrite = 1, kDwAdd = 2 };  // bf16 results; fp32 ones; fp32 ones on top of dW
 
@@ -592,12 +616,10 @@ __global__ __launch_bounds__(kDtype == 0 ? kThreads8 : kF32Threads, 1) void ce_d
   __shared__ __align__(1024) uint4 smem[kDtype == 0 ? kEngineSmemChunks : kF32SmemChunks];
   const int live = __builtin_amdgcn_readfirstlane(chunk_live(count, c0, cap));
   if (live == 0 && c0 > 0) return;  // (the first chunk writes its zeros)
-  const int n_walk = (n_dt + walk - 1) / walk;  // walks of up to `walk` tiles of d
-  const int band = blockIdx.x / (kBwdSuperBand * n_walk);
-  const int first = band * kBwdSuperBand;
-  const int nb = min(kBwdSuperBand, n_vt - first);
-  const int rem = blockIdx.x - band * kBwdSuperBand * n_walk;
-  const int vt = first + rem % nb, dt = rem / nb * walk, dt_end = min(dt + walk, n_dt);
+  int vt, dt;
+  if (!dw_work(blockIdx.x, n_vt, (n_dt + walk - 1) / walk, vt, dt)) return;
+  dt *= walk;
+  const int dt_end = min(dt + walk, n_dt);
   const int nks = max(1, (live + kStepK - 1) / kStepK);
   const uint32_t h_row = (uint32_t)d * es, g_row = (uint32_t)vpad * es;
   const uint32_t d_off = (uint32_t)dt * kT * es, v_off = (uint32_t)vt * kT * es;
@@ -676,18 +698,6 @@ void dh_most(long long cap, long long d, long long vpad, int dtype, long long* g
     *groups = std::max(*groups, n_tb * n_dt * s);
     *rows = std::max(*rows, n_tb * tile * s);
   }
-}
-
-// Tiles of d a dW workgroup walks: the count that takes the fewest K steps of
-// time over the rounds of 256 workgroups, with 12 steps' worth (the first
-// loads and the last stores) for each workgroup's start and end.
-int dw_walk(long long n_vt, long long n_dt, long long nks) {
-  long long best = 1, best_cost = -1;
-  for (long long w = 1; w <= n_dt; ++w) {
-    const long long cost = ceil_div(n_vt * ceil_div(n_dt, w), 256) * (w * nks + 12);
-    if (best_cost < 0 || cost < best_cost) best = w, best_cost = cost;
-  }
-  return (int)best;
 }
 
 struct CeLayout {
@@ -867,7 +877,7 @@ hipError_t run_cross_entropy(const CeCall& c, hipStream_t stream) {
     constexpr int kT = GradTile<kDtype>::kRows;
     const dim3 g_block(kDtype == 0 ? kThreads8 : kF32Threads);
     const int n_dt = (int)ceil_div(d, kT), n_vt = (int)ceil_div(vocab, kT);
-    const int walk = kDtype == 0 ? dw_walk(n_vt, n_dt, ceil_div(cap, GradTile<kDtype>::kStepK)) : 1;
+    const int walk = kDwWalk;
     const int32_t* splits = reinterpret_cast<const int32_t*>(at(L.splits)) + c0 / L.cap;
     hipLaunchKernelGGL(ce_dh_kernel<kDtype>, dim3((unsigned)L.dh_groups), g_block, 0, stream,
                        reinterpret_cast<const char*>(W), reinterpret_cast<const char*>(Gd), vocab, L.vpad, d, count, c0, cap,
@@ -891,7 +901,7 @@ hipError_t run_cross_entropy(const CeCall& c, hipStream_t stream) {
       out = acc, out_f32 = 1, add = c0 > 0;
     }
     auto dw = [&](auto mode) {
-      hipLaunchKernelGGL((ce_dw_kernel<kDtype, decltype(mode)::value>), dim3((unsigned)(n_vt * ceil_div(n_dt, walk))),
+      hipLaunchKernelGGL((ce_dw_kernel<kDtype, decltype(mode)::value>), dim3((unsigned)dw_groups(n_vt, ceil_div(n_dt, walk))),
                          g_block, 0, stream, reinterpret_cast<const char*>(Gd), Hc, L.vpad, count, c0, cap, vocab, d, n_vt,
                          n_dt, walk, gs, out);
     };
