@@ -138,17 +138,21 @@ __global__ __launch_bounds__(256) void ce_gather_kernel(const uint4* __restrict_
 template <int kDtype, bool kKeep, bool kBFar>
 __global__ __launch_bounds__(kThreads8, 1) void ce_partial_kernel(
     const char* __restrict__ H, const char* __restrict__ W, const int32_t* __restrict__ ids,
-    const int32_t* __restrict__ count, int c0, int cap, int stride, int row_bytes, int vocab, int n_tb, int n_slices,
-    int group, float2* __restrict__ part, float* __restrict__ zy_out, float* __restrict__ logits, long long ld) {
+    const int32_t* __restrict__ count, int c0, int cap, int stride, int row_bytes, int vocab, int n_slices, int group,
+    float2* __restrict__ part, float* __restrict__ zy_out, float* __restrict__ logits, long long ld) {
   __shared__ uint4 smem[kEngineSmemChunks];
   const Lanes8 L = lanes8();
   const int wv = L.wv, tq = L.tq, quad = L.quad, c16 = L.c16;
 
   const int S = n_slices;
+  const int n_tok = __builtin_amdgcn_readfirstlane(chunk_live(count, c0, cap));
+  // The walk is that of the live token blocks, workgroups past it leave: dead
+  // blocks in between would leave some XCDs idle (3072 of 4096 tokens: 2.32 ms
+  // so, 2.0 ms without).
+  const int n_tb = (n_tok + kBT - 1) / kBT;
+  if ((long long)blockIdx.x >= (long long)n_tb * ((S + group - 1) / group)) return;
   const WideWork work = wide_work(blockIdx.x, n_tb, S, group);
   const int t0 = work.tb * kBT;
-  const int n_tok = __builtin_amdgcn_readfirstlane(chunk_live(count, c0, cap));
-  if (t0 >= n_tok) return;
   const int n_vt = (vocab + kBV - 1) / kBV;
   const int tile_begin = slice_tile(work.slice_first, n_vt, S);
   const int tile_end = slice_tile(work.slice_end, n_vt, S);
@@ -579,12 +583,14 @@ __global__ __launch_bounds__(256) void ce_zero_rows_kernel(const int32_t* __rest
 
 // Tile of workgroup b of dW's contraction. Workgroups go to the 8 XCDs in
 // turn; XCD x takes the vocabulary tiles x, x + 8, ..., in blocks of 5 of them
-// by 6 tiles of d, so that the 30 or so workgroups it runs together share 5
-// columns of G and 6 of H through its L2, and G comes from memory once for
-// every 6 tiles of d. (With 32 vocabulary tiles side by side, each XCD read G
-// once per tile of d: 16 GB in 3.9 ms at d = 7168, the memory's limit.)
-constexpr int kDwWalk = 1;
-constexpr int kDwVocabTiles = 5, kDwWidthTiles = 6;
+// by 3 walks of two tiles of d, so that the 30 or so workgroups it runs
+// together (two blocks) share few columns of G and H through its L2, and G
+// comes from memory once for every 6 tiles of d or so. (With 32 vocabulary
+// tiles side by side, each XCD read G once per tile of d: 16 GB in 3.9 ms at d
+// = 7168, the memory's limit. Blocks of 4 x 4, 8 x 4 and walks of one measured
+// within 1.5 %.)
+constexpr int kDwWalk = 2;  // tiles of d a workgroup walks (fp32: one)
+constexpr int kDwVocabTiles = 5, kDwWidthTiles = 3;  // of walks
 
 __host__ __device__ inline bool dw_work(int b, int n_vt, int n_dt, int& vt, int& dt) {
   const int x = b & 7, i = b >> 3;
@@ -778,10 +784,10 @@ void launch_ce_partial(const char* Hc, const char* W, const int32_t* ids, const 
   constexpr bool kFarOnly = kDtype == 1 && kKeep;
   if (kFarOnly || row_bytes / kStepBytes > kNearBMaxSteps)
     hipLaunchKernelGGL((ce_partial_kernel<kDtype, kKeep, true>), grid, dim3(kThreads8), 0, stream, Hc, W, ids, count, c0,
-                       cap, cap, row_bytes, vocab, ntb, S, G, part, zy, logits, ld);
+                       cap, cap, row_bytes, vocab, S, G, part, zy, logits, ld);
   else if constexpr (!kFarOnly)
     hipLaunchKernelGGL((ce_partial_kernel<kDtype, kKeep, false>), grid, dim3(kThreads8), 0, stream, Hc, W, ids, count, c0,
-                       cap, cap, row_bytes, vocab, ntb, S, G, part, zy, logits, ld);
+                       cap, cap, row_bytes, vocab, S, G, part, zy, logits, ld);
 }
 
 template <int kDtype>
@@ -877,7 +883,7 @@ hipError_t run_cross_entropy(const CeCall& c, hipStream_t stream) {
     constexpr int kT = GradTile<kDtype>::kRows;
     const dim3 g_block(kDtype == 0 ? kThreads8 : kF32Threads);
     const int n_dt = (int)ceil_div(d, kT), n_vt = (int)ceil_div(vocab, kT);
-    const int walk = kDwWalk;
+    const int walk = kDtype == 0 ? kDwWalk : 1;
     const int32_t* splits = reinterpret_cast<const int32_t*>(at(L.splits)) + c0 / L.cap;
     hipLaunchKernelGGL(ce_dh_kernel<kDtype>, dim3((unsigned)L.dh_groups), g_block, 0, stream,
                        reinterpret_cast<const char*>(W), reinterpret_cast<const char*>(Gd), vocab, L.vpad, d, count, c0, cap,
