@@ -58,13 +58,13 @@ struct GradTile {
   static constexpr int kSlots = kDtype == 0 ? 256 : 768;  // workgroups at a time
 };
 
-// Workgroups that share the K steps of a dH tile (each at least 16 steps):
+// Workgroups that share the K steps of a dH tile (each at least 4 steps):
 // the count that takes the fewest K steps of time, rounds x steps per
 // workgroup, with 12 steps' worth of start and end per round and the fp32
 // partials' traffic (a step's time moves those of about 4 tiles).
 __host__ __device__ inline int dh_splits(long long tiles, long long nks, long long slots) {
   long long best = 1, best_cost = -1;
-  for (long long s = 1; s <= 16 && (s == 1 || nks / s >= 16); ++s) {
+  for (long long s = 1; s <= 16 && (s == 1 || nks / s >= 4); ++s) {
     const long long rounds = (tiles * s + slots - 1) / slots;
     const long long cost = rounds * ((nks + s - 1) / s + 12) + s * tiles / 4;
     if (best_cost < 0 || cost < best_cost) best = s, best_cost = cost;
@@ -114,18 +114,22 @@ __global__ __launch_bounds__(kSelectThreads) void ce_select_kernel(const int32_t
     }
 }
 
-// A chunk's share of the count.
+// A chunk's share of the count (no count: every token).
 __device__ __forceinline__ int chunk_live(const int32_t* count, int c0, int cap) {
-  return max(0, min(*count - c0, cap));
+  return count ? max(0, min(*count - c0, cap)) : cap;
 }
 
-// Hc[j] = H[rows[c0 + j]], 16 bytes per thread.
+// Hc[j] = H[rows[c0 + j]], 16 bytes per thread; with the first chunk also dH's
+// zero rows (nullable), where a token does not count. One workgroup per token
+// of the call (chunks past the first: per row of the chunk).
 __global__ __launch_bounds__(256) void ce_gather_kernel(const uint4* __restrict__ H, const int32_t* __restrict__ rows,
-                                                        const int32_t* __restrict__ count, int c0, int cap,
-                                                        int row_chunks, uint4* __restrict__ Hc) {
-  const int live = chunk_live(count, c0, cap);
+                                                        const int32_t* __restrict__ slot, const int32_t* __restrict__ count,
+                                                        int c0, int cap, int row_chunks, uint4* __restrict__ Hc,
+                                                        uint4* __restrict__ dH, int grad_chunks) {
   const int j = blockIdx.x;
-  if (j >= live) return;
+  if (dH && slot[j] < 0)
+    for (int i = threadIdx.x; i < grad_chunks; i += 256) dH[(size_t)j * grad_chunks + i] = make_uint4(0u, 0u, 0u, 0u);
+  if (j >= chunk_live(count, c0, cap)) return;
   const uint4* src = H + (size_t)rows[c0 + j] * row_chunks;
   uint4* dst = Hc + (size_t)j * row_chunks;
   for (int i = threadIdx.x; i < row_chunks; i += 256) dst[i] = src[i];
@@ -394,6 +398,50 @@ __global__ __launch_bounds__(1024) void ce_loss_kernel(const double* __restrict_
   *loss = (float)(mean ? s / (double)max(1, *count) : s);
 }
 
+// Both of the above for at most kSmallTokens tokens without smoothing, in one
+// launch: a thread takes four consecutive tokens (the additions are the same,
+// so the loss's bits are). slot == nullptr: the tokens were not gathered, a
+// token's place is its own and N is counted here.
+constexpr int kSmallTokens = 4096;
+__global__ __launch_bounds__(1024) void ce_small_loss_kernel(const int32_t* __restrict__ targets, int n, int vocab,
+                                                             const int32_t* __restrict__ slot,
+                                                             const int32_t* __restrict__ count,
+                                                             const float* __restrict__ logprob, const float* __restrict__ lse,
+                                                             float z_weight, int mean, float* __restrict__ token_loss,
+                                                             float* __restrict__ lse_out, float* __restrict__ loss) {
+  __shared__ double lds[16];
+  __shared__ int lds_n[16];
+  float l[4];
+  int live = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int t = 4 * threadIdx.x + i;
+    l[i] = 0.0f;
+    float s = 0.0f;
+    if (t < n) {
+      const int j = slot ? slot[t] : (unsigned)targets[t] < (unsigned)vocab ? t : -1;
+      if (j >= 0) {
+        ++live;
+        s = lse[j];
+        l[i] = -logprob[j];
+        l[i] += z_weight * s * s;
+      }
+      token_loss[t] = l[i];
+      if (lse_out) lse_out[t] = s;
+    }
+  }
+  double sum = (((double)l[0] + (double)l[1]) + (double)l[2]) + (double)l[3];
+  sum = wave_sum_d(sum);
+#pragma unroll
+  for (int off = 32; off >= 1; off >>= 1) live += __shfl_xor(live, off, 64);
+  if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = sum, lds_n[threadIdx.x >> 6] = live;
+  __syncthreads();
+  if (threadIdx.x != 0) return;
+  for (int w = 1; w < 16; ++w) sum += lds[w], live += lds_n[w];
+  if (count) live = *count;
+  *loss = (float)(mean ? sum / (double)max(1, live) : sum);
+}
+
 // ---- G
 
 // G is held in units of u = (1 - e) s / N, which the contractions' epilogues
@@ -569,14 +617,6 @@ __global__ __launch_bounds__(256) void ce_dh_finish_kernel(const float* __restri
     }
     store_grad4(dH, grad_f32, (size_t)rows[c0 + j] * d + k, o);
   }
-}
-
-// Zero rows of dH where the token does not count.
-__global__ __launch_bounds__(256) void ce_zero_rows_kernel(const int32_t* __restrict__ slot, int row_chunks,
-                                                           uint4* __restrict__ dH) {
-  const int t = blockIdx.x;
-  if (slot[t] >= 0) return;
-  for (int i = threadIdx.x; i < row_chunks; i += 256) dH[(size_t)t * row_chunks + i] = make_uint4(0u, 0u, 0u, 0u);
 }
 
 // ---- dW
@@ -825,11 +865,16 @@ hipError_t run_cross_entropy(const CeCall& c, hipStream_t stream) {
   const int row_chunks = d * E::kSize / 16;
   hipError_t e;
 
-  hipLaunchKernelGGL(ce_select_kernel, dim3(1), dim3(kSelectThreads), 0, stream, c.targets, n, vocab, rows, ids, slot,
-                     count, grad ? reinterpret_cast<int32_t*>(at(L.splits)) : nullptr, L.cap, GradTile<kDtype>::kRows,
-                     (int)ceil_div(d, GradTile<kDtype>::kRows), L.vpad / GradTile<kDtype>::kStepK,
-                     GradTile<kDtype>::kSlots);
-  ITL_CHECK_LAUNCH();
+  // A few tokens without their gradient: one block holds them all, counted or
+  // not, so nothing is gathered.
+  const bool direct = !grad && !wmean && n <= kNarrow128MaxTokens;
+  if (!direct) {
+      hipLaunchKernelGGL(ce_select_kernel, dim3(1), dim3(kSelectThreads), 0, stream, c.targets, n, vocab, rows, ids, slot,
+                         count, grad ? reinterpret_cast<int32_t*>(at(L.splits)) : nullptr, L.cap, GradTile<kDtype>::kRows,
+                         (int)ceil_div(d, GradTile<kDtype>::kRows), L.vpad / GradTile<kDtype>::kStepK,
+                         GradTile<kDtype>::kSlots);
+      ITL_CHECK_LAUNCH();
+  }
   if (wmean) {
     const int nb = (int)ceil_div(vocab, kMeanRows);
     hipLaunchKernelGGL(ce_colsum_kernel<kDtype>, dim3((unsigned)nb, (unsigned)ceil_div(d, 512)), dim3(256), 0, stream, W,
@@ -840,21 +885,20 @@ hipError_t run_cross_entropy(const CeCall& c, hipStream_t stream) {
   }
   GradScale gs{c.smoothing, c.z_weight, c.grad_scale, 1.0f / (float)vocab, c.mean};
   const bool exact = grad && kDtype == 0 && c.grad_dtype == 1;
-  if (grad) {
-    hipLaunchKernelGGL(ce_zero_rows_kernel, dim3((unsigned)n), dim3(256), 0, stream, slot,
-                       d * (c.grad_dtype == 0 ? 2 : 4) / 16, static_cast<uint4*>(c.dH));
-    ITL_CHECK_LAUNCH();
-  }
   for (int c0 = 0; c0 < n; c0 += L.cap) {
     const int cap = std::min(L.cap, n - c0);
-    hipLaunchKernelGGL(ce_gather_kernel, dim3((unsigned)cap), dim3(256), 0, stream, reinterpret_cast<const uint4*>(H),
-                       rows, count, c0, cap, row_chunks, reinterpret_cast<uint4*>(Hc));
+    if (!direct)
+      hipLaunchKernelGGL(ce_gather_kernel, dim3((unsigned)(c0 == 0 ? n : cap)), dim3(256), 0, stream,
+                         reinterpret_cast<const uint4*>(H), rows, slot, count, c0, cap, row_chunks,
+                         reinterpret_cast<uint4*>(Hc), c0 == 0 ? static_cast<uint4*>(c.dH) : nullptr,
+                         d * (c.grad_dtype == 0 ? 2 : 4) / 16);
     float* z = grad ? reinterpret_cast<float*>(at(L.z)) : nullptr;
     if (grad)
       launch_ce_partial<kDtype, true>(Hc, reinterpret_cast<const char*>(W), ids + c0, count, c0, cap, d, vocab, part, zy,
                                       z, L.vpad, stream);
     else
-      launch_ce_partial<kDtype, false>(Hc, reinterpret_cast<const char*>(W), ids + c0, count, c0, cap, d, vocab, part, zy,
+      launch_ce_partial<kDtype, false>(direct ? reinterpret_cast<const char*>(H) : Hc, reinterpret_cast<const char*>(W),
+                                       direct ? c.targets : ids + c0, direct ? nullptr : count, c0, cap, d, vocab, part, zy,
                                        nullptr, 0, stream);
     ITL_CHECK_LAUNCH();
     e = launch_lse_combine(part, zy, cap, 2 * S, lp + c0, lse + c0, stream);
@@ -926,9 +970,15 @@ hipError_t run_cross_entropy(const CeCall& c, hipStream_t stream) {
       ITL_CHECK_LAUNCH();
     }
   }
-  hipLaunchKernelGGL(ce_token_loss_kernel<kDtype>, dim3((unsigned)ceil_div(n, 4)), dim3(256), 0, stream, H, n, d, slot, lp,
-                     lse, wmean, c.smoothing, c.z_weight, c.token_loss, c.lse, loss_part);
-  hipLaunchKernelGGL(ce_loss_kernel, dim3(1), dim3(1024), 0, stream, loss_part, (int)ceil_div(n, 4), count, c.mean, c.loss);
+  if (!wmean && n <= kSmallTokens) {
+    hipLaunchKernelGGL(ce_small_loss_kernel, dim3(1), dim3(1024), 0, stream, c.targets, n, vocab, direct ? nullptr : slot,
+                       direct ? nullptr : count, lp, lse, c.z_weight, c.mean, c.token_loss, c.lse, c.loss);
+  } else {
+    hipLaunchKernelGGL(ce_token_loss_kernel<kDtype>, dim3((unsigned)ceil_div(n, 4)), dim3(256), 0, stream, H, n, d, slot, lp,
+                       lse, wmean, c.smoothing, c.z_weight, c.token_loss, c.lse, loss_part);
+    hipLaunchKernelGGL(ce_loss_kernel, dim3(1), dim3(1024), 0, stream, loss_part, (int)ceil_div(n, 4), count, c.mean,
+                       c.loss);
+  }
   ITL_CHECK_LAUNCH();
   return hipSuccess;
 }
