@@ -55,19 +55,22 @@ template <int kDtype>
 struct GradTile {
   static constexpr int kRows = kDtype == 0 ? 256 : kF32Tile;
   static constexpr int kStepK = kStepBytes / Elem<kDtype>::kSize;
-  static constexpr int kSlots = kDtype == 0 ? 256 : 768;  // workgroups at a time
 };
 
-// Workgroups that share the K steps of a dH tile (each at least 4 steps):
-// the count that takes the fewest K steps of time, rounds x steps per
-// workgroup, with 12 steps' worth of start and end per round and the fp32
-// partials' traffic (a step's time moves those of about 4 tiles).
-__host__ __device__ inline int dh_splits(long long tiles, long long nks, long long slots) {
-  long long best = 1, best_cost = -1;
-  for (long long s = 1; s <= 16 && (s == 1 || nks / s >= 4); ++s) {
-    const long long rounds = (tiles * s + slots - 1) / slots;
-    const long long cost = rounds * ((nks + s - 1) / s + 12) + s * tiles / 4;
-    if (best_cost < 0 || cost < best_cost) best = s, best_cost = cost;
+// Workgroups that share the K steps of a dH tile (each at least 4 steps): the
+// count that takes the fewest K steps of time, rounds over the CUs x steps per
+// workgroup, beside each round's start and end (12 steps' worth) and the fp32
+// partials' traffic (a step's time moves those of about 4 tiles). fp32: three
+// workgroups fit a CU and share its matrix cores; one alone waits for its loads
+// (a step takes 1.6 times as long), starts and ends overlap, and the partials
+// are a sixteenth.
+__host__ __device__ inline int dh_splits(uint32_t tiles, uint32_t nks, bool f32) {
+  uint32_t best = 1, best_cost = 0xffffffffu;
+  for (uint32_t s = 1; s <= 16 && (s == 1 || nks / s >= 4); ++s) {
+    const uint32_t rounds = (tiles * s + 255) / 256, steps = (nks + s - 1) / s;
+    const uint32_t cost = f32 ? rounds * (steps + 4) + (rounds == 1 ? steps * 3 / 5 : 0) + s * tiles / 64
+                              : rounds * (steps + 12) + s * tiles / 4;
+    if (cost < best_cost) best = s, best_cost = cost;
   }
   return (int)best;
 }
@@ -81,7 +84,7 @@ __global__ __launch_bounds__(kSelectThreads) void ce_select_kernel(const int32_t
                                                                    int32_t* __restrict__ rows, int32_t* __restrict__ ids,
                                                                    int32_t* __restrict__ slot, int32_t* __restrict__ count,
                                                                    int32_t* __restrict__ splits, int chunk, int rows_per_tile,
-                                                                   int n_dt, int nks, int slots) {
+                                                                   int n_dt, int nks, int f32) {
   __shared__ int wave_n[kSelectThreads / 64];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   int base = 0;
@@ -110,7 +113,7 @@ __global__ __launch_bounds__(kSelectThreads) void ce_select_kernel(const int32_t
   if (splits)
     for (int c = threadIdx.x; (long long)c * chunk < n; c += kSelectThreads) {
       const int live = max(0, min(base - c * chunk, chunk));
-      splits[c] = dh_splits((long long)((live + rows_per_tile - 1) / rows_per_tile) * n_dt, nks, slots);
+      splits[c] = dh_splits((uint32_t)((live + rows_per_tile - 1) / rows_per_tile * n_dt), (uint32_t)nks, f32 != 0);
     }
 }
 
@@ -287,7 +290,7 @@ __global__ __launch_bounds__(kThreads, 1) void ce_partial_narrow_kernel(
 
 // ---- mean of the logits (label smoothing): z's mean over v is H . mean_v W[v]
 
-constexpr int kMeanRows = 256;  // rows of W per partial sum
+constexpr int kMeanRows = 128;  // rows of W per partial sum
 
 // part[b, k] = sum of W[v, k] over kMeanRows rows v: 512 columns per workgroup,
 // 8 per thread, four wavefronts on rows v, v + 4, ... each, then added in
@@ -302,7 +305,7 @@ __global__ __launch_bounds__(256) void ce_colsum_kernel(const typename Elem<kDty
   const int v0 = blockIdx.x * kMeanRows, v1 = min(vocab, v0 + kMeanRows);
   float s[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
   if (k < d) {
-#pragma unroll 8
+#pragma unroll 16
     for (int v = v0 + wave; v < v1; v += 4) {
       const uint4* row = reinterpret_cast<const uint4*>(W + (size_t)v * d + k);
       uint4 w[E::kSize / 2];
@@ -367,7 +370,23 @@ __global__ __launch_bounds__(256) void ce_token_loss_kernel(const typename Elem<
     l = -(1.0f - smoothing) * logprob[j];
     if (wmean) {
       float zm = 0.0f;
-      for (int k = lane; k < d; k += 64) zm += E::to_f(H[(size_t)t * d + k]) * wmean[k];
+      // (d is a multiple of 64: 8 values per lane while whole groups of 512 last, then one)
+      int k = 8 * lane;
+#pragma unroll 2
+      for (; k - 8 * lane + 512 <= d; k += 512) {
+        const uint4* hr = reinterpret_cast<const uint4*>(H + (size_t)t * d + k);
+        uint4 w[E::kSize / 2];
+#pragma unroll
+        for (int i = 0; i < E::kSize / 2; ++i) w[i] = hr[i];
+        const float4 m0 = *reinterpret_cast<const float4*>(wmean + k), m1 = *reinterpret_cast<const float4*>(wmean + k + 4);
+        const float m[8] = {m0.x, m0.y, m0.z, m0.w, m1.x, m1.y, m1.z, m1.w};
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const uint32_t x = (&w[0].x)[kDtype == 0 ? j >> 1 : j];
+          zm += (kDtype == 1 ? __uint_as_float(x) : __uint_as_float((j & 1) ? (x & 0xffff0000u) : (x << 16))) * m[j];
+        }
+      }
+      for (k = k - 8 * lane + lane; k < d; k += 64) zm += E::to_f(H[(size_t)t * d + k]) * wmean[k];
       l += smoothing * (s - wave_sum(zm));
     }
     l += z_weight * s * s;
@@ -705,6 +724,42 @@ __global__ __launch_bounds__(kDtype == 0 ? kThreads8 : kF32Threads, 1) void ce_d
   }
 }
 
+// dW of a chunk of few tokens (bf16): 128 x 128 tiles, the tiles of d fastest.
+constexpr int kFewTokens = 256;
+template <int kMode>
+__global__ __launch_bounds__(kFewThreads, 4) void ce_dw_few_kernel(const char* __restrict__ Gd, const char* __restrict__ Hc,
+                                                                   int vpad, const int32_t* __restrict__ count, int c0,
+                                                                   int cap, int vocab, int d, int n_dt, GradScale gs,
+                                                                   void* __restrict__ dW) {
+  __shared__ __align__(1024) uint4 smem[kFewSmemChunks];
+  const int live = __builtin_amdgcn_readfirstlane(chunk_live(count, c0, cap));
+  const int dt = blockIdx.x % n_dt, vt = blockIdx.x / n_dt;
+  const uint32_t d_off = (uint32_t)dt * kFewTile * 2, v_off = (uint32_t)vt * kFewTile * 2;
+  const float unit = grad_unit(gs, count);
+  run_tile_few(smem, KmOperand{Hc + d_off, (uint32_t)d * 2, live, d_off},
+               KmOperand{Gd + v_off, (uint32_t)vpad * 2, live, v_off},
+               [&](floatx4 (&acc)[4][4], int wave, int quad, int c16) {
+#pragma unroll
+    for (int bn = 0; bn < 4; ++bn) {
+      const int v = vt * kFewTile + 64 * (wave >> 1) + 16 * bn + c16;
+      if (v >= vocab) continue;
+#pragma unroll
+      for (int bm = 0; bm < 4; ++bm) {
+        const int k = dt * kFewTile + 64 * (wave & 1) + 16 * bm + 4 * quad;
+        if (k >= d) continue;
+        const size_t at = (size_t)v * d + k;
+        const floatx4& o = acc[bm][bn];
+        float x[4] = {o[0] * unit, o[1] * unit, o[2] * unit, o[3] * unit};
+        if constexpr (kMode == kDwAdd) {
+          const float4 old = *reinterpret_cast<const float4*>(static_cast<const float*>(dW) + at);
+          x[0] += old.x, x[1] += old.y, x[2] += old.z, x[3] += old.w;
+        }
+        store_grad4(dW, kMode != kDwRound, at, x);
+      }
+    }
+  });
+}
+
 // The accumulated fp32 dW rounded to bf16.
 __global__ __launch_bounds__(256) void ce_round_kernel(const float4* __restrict__ in, long long n4, uint2* __restrict__ out) {
   const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
@@ -736,11 +791,10 @@ __global__ __launch_bounds__(256) void ce_clear_kernel(uint4* __restrict__ out, 
 // can take in dH's contraction, over all live counts.
 void dh_most(long long cap, long long d, long long vpad, int dtype, long long* groups, long long* rows) {
   const long long tile = dtype == 0 ? GradTile<0>::kRows : GradTile<1>::kRows;
-  const long long slots = dtype == 0 ? GradTile<0>::kSlots : GradTile<1>::kSlots;
   const long long nks = vpad / (dtype == 0 ? GradTile<0>::kStepK : GradTile<1>::kStepK), n_dt = ceil_div(d, tile);
   *groups = *rows = 0;
   for (long long n_tb = 1; n_tb <= ceil_div(cap, tile); ++n_tb) {
-    const long long s = dh_splits(n_tb * n_dt, nks, slots);
+    const long long s = dh_splits((uint32_t)(n_tb * n_dt), (uint32_t)nks, dtype == 1);
     *groups = std::max(*groups, n_tb * n_dt * s);
     *rows = std::max(*rows, n_tb * tile * s);
   }
@@ -872,7 +926,7 @@ hipError_t run_cross_entropy(const CeCall& c, hipStream_t stream) {
       hipLaunchKernelGGL(ce_select_kernel, dim3(1), dim3(kSelectThreads), 0, stream, c.targets, n, vocab, rows, ids, slot,
                          count, grad ? reinterpret_cast<int32_t*>(at(L.splits)) : nullptr, L.cap, GradTile<kDtype>::kRows,
                          (int)ceil_div(d, GradTile<kDtype>::kRows), L.vpad / GradTile<kDtype>::kStepK,
-                         GradTile<kDtype>::kSlots);
+                         kDtype);
       ITL_CHECK_LAUNCH();
   }
   if (wmean) {
@@ -951,6 +1005,14 @@ hipError_t run_cross_entropy(const CeCall& c, hipStream_t stream) {
       out = acc, out_f32 = 1, add = c0 > 0;
     }
     auto dw = [&](auto mode) {
+      if constexpr (kDtype == 0) {
+        if (n <= kFewTokens) {
+          const int n_dt2 = (int)ceil_div(d, kFewTile), n_vt2 = (int)ceil_div(vocab, kFewTile);
+          hipLaunchKernelGGL((ce_dw_few_kernel<decltype(mode)::value>), dim3((unsigned)(n_vt2 * n_dt2)), dim3(kFewThreads), 0,
+                             stream, reinterpret_cast<const char*>(Gd), Hc, L.vpad, count, c0, cap, vocab, d, n_dt2, gs, out);
+          return;
+        }
+      }
       hipLaunchKernelGGL((ce_dw_kernel<kDtype, decltype(mode)::value>), dim3((unsigned)dw_groups(n_vt, ceil_div(n_dt, walk))),
                          g_block, 0, stream, reinterpret_cast<const char*>(Gd), Hc, L.vpad, count, c0, cap, vocab, d, n_vt,
                          n_dt, walk, gs, out);

@@ -232,6 +232,80 @@ __device__ __forceinline__ void run_tiles_km(uint4* smem, const Lanes8& L, const
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
 }
 
+// ---- bf16, few k
+
+// A product over few k is bound by its results' stores, not its contraction:
+// 128 x 128 tiles (four wavefronts of 64 x 64), 32 KiB of LDS and at most 128
+// registers, so that four workgroups per CU have stores and loads in flight
+// at once where the 256 x 256 tile has one. Both operands K-major, rows of 256
+// bytes in LDS; the 32-byte piece P of row k sits at P ^ g(k), g(k) = (k mod 4)
+// + 4 (bit 4 of k).
+constexpr int kFewTile = 128;
+constexpr int kFewThreads = 256;
+constexpr int kFewSmemChunks = 2 * 64 * 256 / 16;
+
+__device__ __forceinline__ int few_swz(int k) { return (k & 3) | (((k >> 4) & 1) << 2); }
+
+// acc = A B^T over the operands' rows, 64 at a time: wavefront w holds A
+// columns 64 (w mod 2) .. against B 64 (w / 2) ..; acc[bm][bn][i] is A 64 (w &
+// 1) + 16 bm + 4 quad + i, B 64 (w >> 1) + 16 bn + c16.
+template <class Epi>
+__device__ __forceinline__ void run_tile_few(uint4* smem, const KmOperand& A, const KmOperand& B, Epi&& epi) {
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int quad = lane >> 4, c16 = lane & 15;
+  const uint32_t lds0 = (uint32_t)(size_t)((__attribute__((address_space(3))) uint4*)smem);
+  // load j of wavefront w: rows 16 w + 4 j + lane / 16 of either operand
+  uint32_t ao[4], bo[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const int k = 16 * wave + 4 * j + (lane >> 4);
+    const uint32_t chunk = (uint32_t)(((lane & 15) ^ (2 * few_swz(k))) * 16);
+    ao[j] = (uint32_t)k * A.row_bytes + chunk;
+    bo[j] = (uint32_t)k * B.row_bytes + chunk;
+  }
+  const int krow = 8 * lane_chunk(quad) + (c16 >> 2);
+  const int f = few_swz(krow);
+  typedef __attribute__((address_space(3))) shortx4 lds_s4;
+  auto tr8 = [&](uint32_t at) {
+    const shortx4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4*)(size_t)at);
+    const shortx4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4*)(size_t)(at + 4 * 256));
+    const uint2 a = __builtin_bit_cast(uint2, lo), b = __builtin_bit_cast(uint2, hi);
+    return make_uint4(a.x, a.y, b.x, b.y);
+  };
+  const uint32_t at0 = lds0 + (uint32_t)(krow * 256 + (c16 & 3) * 8);
+  floatx4 acc[4][4];
+#pragma unroll
+  for (int bm = 0; bm < 4; ++bm)
+#pragma unroll
+    for (int bn = 0; bn < 4; ++bn) acc[bm][bn] = floatx4{};
+  const int steps = (A.rows + 63) / 64;
+  for (int s = 0; s < steps; ++s) {
+    const int4v ar = km_step_rsrc(A, s, 64), br = km_step_rsrc(B, s, 64);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      dma16(ar, ao[j], 0u, lds0 + (uint32_t)(wave * 4096 + j * 1024));
+      dma16(br, bo[j], 0u, lds0 + 16384u + (uint32_t)(wave * 4096 + j * 1024));
+    }
+    wait_and_barrier<0>();
+    const int halves = A.rows - 64 * s > 32 ? 2 : 1;
+    for (int kk = 0; kk < halves; ++kk) {
+      uint4 a[4], b[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        a[i] = tr8(at0 + (uint32_t)(kk * 32 * 256 + ((4 * (wave & 1) + i) ^ f) * 32));
+        b[i] = tr8(at0 + 16384u + (uint32_t)(kk * 32 * 256 + ((4 * (wave >> 1) + i) ^ f) * 32));
+      }
+#pragma unroll
+      for (int bm = 0; bm < 4; ++bm)
+#pragma unroll
+        for (int bn = 0; bn < 4; ++bn) Mma16<0>::step(acc[bm][bn], a[bm], b[bn]);
+    }
+    __syncthreads();  // every wavefront is done with the step's rows
+  }
+  epi(acc, wave, quad, c16);
+}
+
 // ---- fp32
 
 constexpr int kF32Tile = 64;
