@@ -369,8 +369,10 @@ enum { ITL_SUM = 0, ITL_MEAN = 1 };
 
 /* Bytes of device workspace itl_cross_entropy (with_grad 0) or
  * itl_cross_entropy_grad (with_grad 1) needs. With the gradient it holds the
- * logits and two copies of their gradients for at most 16,384 tokens and a
- * transposed W, whatever n_tok. SIZE_MAX for invalid sizes or dtypes. */
+ * logits (fp32) and their gradients (dtype) of at most 16,384 tokens, whatever
+ * n_tok, and one fp32 copy of dW where a bf16 head has more tokens than that;
+ * without it the logits of at most 4,096 tokens of an fp32 head, none of a
+ * bf16 one. SIZE_MAX for invalid sizes or dtypes. */
 size_t itl_cross_entropy_workspace_bytes(int64_t n_tok, int64_t d, int64_t vocab, itl_dtype dtype,
                                          int32_t with_grad, itl_dtype grad_dtype);
 
@@ -384,8 +386,9 @@ size_t itl_cross_entropy_workspace_bytes(int64_t n_tok, int64_t d, int64_t vocab
  * the reading of their id. No counted token: loss 0.
  * H, W, dtype, d, vocab as for itl_lmhead_logprob; targets int32 [n_tok];
  * loss fp32 [1], token_loss, lse (nullable) fp32 [n_tok]. The losses are summed
- * in fp64 in a fixed order. A token's loss does not depend on its
- * batch-mates. */
+ * in fp64 in a fixed order. A token's loss does not depend on its batch-mates
+ * (bf16 heads: its z and lse have itl_lmhead_logprob's bits). fp32 heads with a
+ * vocab above about 2.1e6 return ITL_ERR_UNSUPPORTED. */
 itl_status itl_cross_entropy(const void* H, const void* W, itl_dtype dtype,
                              int64_t n_tok, int64_t d, int64_t vocab, const int32_t* targets,
                              float label_smoothing, float z_weight, int32_t reduction,
@@ -398,9 +401,9 @@ itl_status itl_cross_entropy(const void* H, const void* W, itl_dtype dtype,
  *   dH = G W [n_tok, d] (rows of tokens that do not count: 0),  dW = G^T H [vocab, d]
  * both of grad_dtype (dtype or ITL_F32), overwritten, 16-byte aligned. The
  * logits are kept for one chunk of at most 16,384 tokens at a time, in the
- * workspace. G enters its contractions in the head's dtype (bf16: 2^-9 of each
- * entry; with bf16 gradients the target's entry too, with fp32 ones the
- * one-hot term is applied exactly in fp32). Sums in fp32; fixed orders, no
+ * workspace. G enters its contractions in the head's dtype (bf16: each entry
+ * within 2^-8 of itself, calls of at most 128 tokens 2^-16; with fp32 gradients
+ * the one-hot term is applied exactly in fp32). Sums in fp32; fixed orders, no
  * atomics: run-to-run deterministic. n_tok == 0: loss 0, dW zeros. vocab above
  * about 2.1e6 returns ITL_ERR_UNSUPPORTED. */
 itl_status itl_cross_entropy_grad(const void* H, const void* W, itl_dtype dtype,

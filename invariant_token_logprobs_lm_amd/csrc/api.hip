@@ -471,7 +471,8 @@ itl_status cross_entropy(const itl::CeCall& c, bool grad, size_t workspace_bytes
   if (grad && !(c.grad_scale - c.grad_scale == 0.0f)) return fail(ITL_ERR_INVALID_ARG, "grad_scale must be finite");
   if (grad && c.grad_dtype != c.dtype && c.grad_dtype != ITL_F32)
     return fail(ITL_ERR_UNSUPPORTED, "grad_dtype must be dtype or ITL_F32");
-  if (grad && c.vocab > itl::kBwdMaxVocab) return fail(ITL_ERR_UNSUPPORTED, "vocab too large for the gradient");
+  if ((grad || c.dtype == ITL_F32) && c.vocab > itl::kBwdMaxVocab)
+    return fail(ITL_ERR_UNSUPPORTED, "vocab too large for the gradient or an fp32 head");
   if (!c.W || !c.loss || (grad && !c.dW)) return fail(ITL_ERR_INVALID_ARG, "null W, loss or dW");
   if (c.n_tok > 0 && (!c.H || !c.targets || !c.token_loss || (grad && !c.dH)))
     return fail(ITL_ERR_INVALID_ARG, "null H, targets, token_loss or dH");
@@ -491,7 +492,8 @@ size_t itl_cross_entropy_workspace_bytes(int64_t n_tok, int64_t d, int64_t vocab
                                          itl_dtype grad_dtype) {
   if (n_tok < 0 || d <= 0 || vocab <= 0 || n_tok > kMaxTok || vocab > kMaxVocab || !known_dtype(dtype)) return SIZE_MAX;
   if (d % itl::kDMultiple != 0 || d >= ((int64_t)1 << 31) / (elem_size(dtype) * (int64_t)itl::kBT)) return SIZE_MAX;
-  if (with_grad && (vocab > itl::kBwdMaxVocab || (grad_dtype != dtype && grad_dtype != ITL_F32))) return SIZE_MAX;
+  if ((with_grad || dtype == ITL_F32) && vocab > itl::kBwdMaxVocab) return SIZE_MAX;
+  if (with_grad && grad_dtype != dtype && grad_dtype != ITL_F32) return SIZE_MAX;
   return itl::cross_entropy_workspace_bytes(n_tok, d, vocab, (int)dtype, with_grad != 0, (int)grad_dtype);
 }
 

@@ -15,8 +15,10 @@
 // contraction runs over them alone.
 //
 // With the gradient, for each chunk:
-//   1. z = H W^T by the forward's contraction (eight-wavefront engine), kept
-//      in fp32, with the online log-sum-exp folds of the logprob's forward;
+//   1. z = H W^T, kept in fp32: bf16 heads by the logprob forward's
+//      contraction and online log-sum-exp folds (the same bits; without the
+//      gradient nothing is kept), fp32 heads by 64 x 64 tiles and a pass over
+//      z for the log-sum-exp;
 //   2. G [chunk, Vpad] in the head's type;
 //   3. dH = G W, K = the vocabulary, split over several workgroups when the
 //      chunk has few tiles (fp32 partials added in order);
@@ -44,7 +46,8 @@ namespace itl {
 
 namespace {
 
-constexpr int kCeChunk = 16384;  // tokens per chunk (a multiple of kBT)
+constexpr int kCeChunk = 16384;    // tokens per chunk with the gradient (a multiple of kBT)
+constexpr int kCeF32Chunk = 4096;  // the same of fp32 heads without it (their logits are kept too)
 static_assert(kCeChunk % kBT == 0, "chunks hold whole token blocks");
 
 long long round_up(long long x, long long m) { return (x + m - 1) / m * m; }
@@ -84,12 +87,12 @@ __global__ __launch_bounds__(kSelectThreads) void ce_select_kernel(const int32_t
                                                                    int32_t* __restrict__ rows, int32_t* __restrict__ ids,
                                                                    int32_t* __restrict__ slot, int32_t* __restrict__ count,
                                                                    int32_t* __restrict__ splits, int chunk, int rows_per_tile,
-                                                                   int n_dt, int nks, int f32) {
+                                                                   int parts, int n_dt, int nks, int f32) {
   __shared__ int wave_n[kSelectThreads / 64];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   int base = 0;
-  for (int t0 = 0; t0 < n; t0 += kSelectThreads) {
-    const int t = t0 + threadIdx.x;
+  for (long long t0 = 0; t0 < n; t0 += kSelectThreads) {
+    const long long t = t0 + threadIdx.x;
     const int y = t < n ? targets[t] : -1;
     const bool in = (unsigned)y < (unsigned)vocab;
     const uint64_t mask = __ballot(in);
@@ -102,7 +105,7 @@ __global__ __launch_bounds__(kSelectThreads) void ce_select_kernel(const int32_t
     }
     const int j = before + __popcll(mask & ((1ull << lane) - 1ull));
     if (in) {
-      rows[j] = t;
+      rows[j] = (int)t;
       ids[j] = y;
     }
     if (t < n) slot[t] = in ? j : -1;
@@ -112,7 +115,7 @@ __global__ __launch_bounds__(kSelectThreads) void ce_select_kernel(const int32_t
   // dH's splits of every chunk
   if (splits)
     for (int c = threadIdx.x; (long long)c * chunk < n; c += kSelectThreads) {
-      const int live = max(0, min(base - c * chunk, chunk));
+      const int live = parts * max(0, min(base - c * chunk, chunk));
       splits[c] = dh_splits((uint32_t)((live + rows_per_tile - 1) / rows_per_tile * n_dt), (uint32_t)nks, f32 != 0);
     }
 }
@@ -124,18 +127,24 @@ __device__ __forceinline__ int chunk_live(const int32_t* count, int c0, int cap)
 
 // Hc[j] = H[rows[c0 + j]], 16 bytes per thread; with the first chunk also dH's
 // zero rows (nullable), where a token does not count. One workgroup per token
-// of the call (chunks past the first: per row of the chunk).
+// of the call (chunks past the first: per row of the chunk). parts == 2: the
+// rows once more behind themselves (see kPairTokens).
 __global__ __launch_bounds__(256) void ce_gather_kernel(const uint4* __restrict__ H, const int32_t* __restrict__ rows,
                                                         const int32_t* __restrict__ slot, const int32_t* __restrict__ count,
-                                                        int c0, int cap, int row_chunks, uint4* __restrict__ Hc,
+                                                        int c0, int cap, int parts, int row_chunks, uint4* __restrict__ Hc,
                                                         uint4* __restrict__ dH, int grad_chunks) {
   const int j = blockIdx.x;
   if (dH && slot[j] < 0)
     for (int i = threadIdx.x; i < grad_chunks; i += 256) dH[(size_t)j * grad_chunks + i] = make_uint4(0u, 0u, 0u, 0u);
-  if (j >= chunk_live(count, c0, cap)) return;
+  const int live = chunk_live(count, c0, cap);
+  if (j >= live) return;
   const uint4* src = H + (size_t)rows[c0 + j] * row_chunks;
   uint4* dst = Hc + (size_t)j * row_chunks;
-  for (int i = threadIdx.x; i < row_chunks; i += 256) dst[i] = src[i];
+  for (int i = threadIdx.x; i < row_chunks; i += 256) {
+    const uint4 v = src[i];
+    dst[i] = v;
+    if (parts == 2) dst[(size_t)live * row_chunks + i] = v;
+  }
 }
 
 // ---- the forward's contraction over the gathered rows
@@ -286,6 +295,75 @@ __global__ __launch_bounds__(kThreads, 1) void ce_partial_narrow_kernel(
     const int tok = t0 + wt * kWaveToks + bn * 16 + c16;
     flush_slice16(c[bn], tok, n_tok, quad, ((size_t)slice * 2 + wv) * stride + tok, part);
   }
+}
+
+// fp32 heads: z in 64 x 64 tiles (vocabulary tiles fastest), columns past the
+// vocabulary zero up to ld.
+__global__ __launch_bounds__(kF32Threads, 1) void ce_logits_f32_kernel(const char* __restrict__ Hc,
+                                                                       const char* __restrict__ W,
+                                                                       const int32_t* __restrict__ count, int c0, int cap,
+                                                                       int row_bytes, int vocab, int n_vt,
+                                                                       float* __restrict__ z, long long ld) {
+  __shared__ __align__(1024) uint4 smem[kF32SmemChunks];
+  const int live = __builtin_amdgcn_readfirstlane(chunk_live(count, c0, cap));
+  const int vt = blockIdx.x % n_vt, t0 = blockIdx.x / n_vt * kF32Tile, v0 = vt * kF32Tile;
+  if (t0 >= live) return;
+  const KmOperand A{W + (size_t)v0 * row_bytes, (uint32_t)row_bytes, min(kF32Tile, vocab - v0), 0u};
+  const KmOperand B{Hc + (size_t)t0 * row_bytes, (uint32_t)row_bytes, min(kF32Tile, live - t0), 0u};
+  run_tile_f32<false, false>(smem, A, B, row_bytes / kStepBytes, [&](floatx4 (&acc)[2][2], int wave, int quad, int c16) {
+#pragma unroll
+    for (int bn = 0; bn < 2; ++bn) {
+      const int t = t0 + 32 * (wave >> 1) + 16 * bn + c16;
+      if (t >= live) continue;
+#pragma unroll
+      for (int bm = 0; bm < 2; ++bm) {
+        const floatx4& o = acc[bm][bn];
+        *reinterpret_cast<float4*>(z + (size_t)t * ld + v0 + 32 * (wave & 1) + 16 * bm + 4 * quad) =
+            make_float4(o[0], o[1], o[2], o[3]);
+      }
+    }
+  });
+}
+
+// lse and logprob of a row of z: each thread folds entries 4 (tid + 256 i) .. +
+// 3 into its (max, sum), then a fixed tree.
+__global__ __launch_bounds__(256) void ce_lse_f32_kernel(const float* __restrict__ z, long long ld,
+                                                         const int32_t* __restrict__ ids, const int32_t* __restrict__ count,
+                                                         int c0, int cap, int vocab, float* __restrict__ logprob,
+                                                         float* __restrict__ lse) {
+  __shared__ float2 lds[4];
+  const int t = blockIdx.x;
+  if (t >= chunk_live(count, c0, cap)) return;
+  const float* row = z + (size_t)t * ld;
+  float m = -INFINITY, s = 0.0f;
+  for (int v = 4 * threadIdx.x; v < vocab; v += 1024) {
+    const float4 q = *reinterpret_cast<const float4*>(row + v);  // (ld is a multiple of 256)
+    float x[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[i] = v + i < vocab ? x[i] : -INFINITY;
+    const float top = fmaxf(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])), m);
+    const float ref = top == -INFINITY ? 0.0f : top;
+    float e = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) e += fast_exp2((x[i] - ref) * kLog2e);
+    s = __builtin_fmaf(s, fast_exp2((m - ref) * kLog2e), e);
+    m = top;
+  }
+#pragma unroll
+  for (int off = 32; off >= 1; off >>= 1) {
+    const float m2 = __shfl_xor(m, off, 64), s2 = __shfl_xor(s, off, 64);
+    lse_merge(m, s, m2, s2);
+  }
+  if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = make_float2(m, s);
+  __syncthreads();
+  if (threadIdx.x != 0) return;
+  for (int w = 1; w < 4; ++w) lse_merge(m, s, lds[w].x, lds[w].y);
+  // (z_y - m) - ln s: lse itself is rounded to a step of its size, which may be
+  // many times the loss. s >= 1, the maximum's own term is 1.
+  const float ln_s = fast_log2(s) * kLn2;
+  const int y = ids[t];  // (not gathered: it may not count)
+  logprob[t] = ((unsigned)y < (unsigned)vocab ? row[y] - m : 0.0f) - ln_s;
+  lse[t] = m + ln_s;
 }
 
 // ---- mean of the logits (label smoothing): z's mean over v is H . mean_v W[v]
@@ -484,15 +562,24 @@ __device__ __forceinline__ float grad_unit(const GradScale& g, const int32_t* co
 // -1, which dH and dW then take in fp32.
 constexpr int kGradVec = 8;
 
+// Up to this many tokens (bf16), G is held as two bf16 rows per token, its
+// rounding and the rounding of what that leaves, the second one's rows behind
+// all of the first's: both contractions are bound by W and dW then, so the
+// second row costs nothing and G's error falls from 2^-8 to 2^-16 of an entry.
+// (With few tokens one entry's rounding can be all of a gradient's error;
+// with many they average out.)
+constexpr int kPairTokens = 128;
+
 template <int kDtype, bool kExact>
 __global__ __launch_bounds__(256) void ce_grad_logits_kernel(
     const float* __restrict__ logits, long long ld, const int32_t* __restrict__ ids, const int32_t* __restrict__ count,
-    int c0, int cap, int vocab, int vpad, const float* __restrict__ lse, GradScale gs,
+    int c0, int cap, int parts, int vocab, int vpad, const float* __restrict__ lse, GradScale gs,
     typename Elem<kDtype>::T* __restrict__ Gd) {
   using E = Elem<kDtype>;
   const int t = blockIdx.y;
   const int v = (blockIdx.x * 256 + threadIdx.x) * kGradVec;
-  if (t >= chunk_live(count, c0, cap) || v >= vpad) return;
+  const int live = chunk_live(count, c0, cap);
+  if (t >= live || v >= vpad) return;
   const float rest = 1.0f / (1.0f - gs.smoothing);
   const float cc = gs.smoothing * gs.inv_vocab * rest;
   const float s = lse[t];
@@ -518,10 +605,17 @@ __global__ __launch_bounds__(256) void ce_grad_logits_kernel(
   }
   typename E::T* out = Gd + (size_t)t * vpad + v;
   if constexpr (kDtype == 0) {
-    uint32_t w[4];
+    for (int part = 0; part < parts; ++part) {
+      uint32_t w[4];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) w[j] = (uint32_t)E::from_f(z[2 * j]) | ((uint32_t)E::from_f(z[2 * j + 1]) << 16);
-    *reinterpret_cast<uint4*>(out) = make_uint4(w[0], w[1], w[2], w[3]);
+      for (int j = 0; j < 4; ++j) {
+        w[j] = (uint32_t)E::from_f(z[2 * j]) | ((uint32_t)E::from_f(z[2 * j + 1]) << 16);
+        z[2 * j] -= __uint_as_float(w[j] << 16);
+        z[2 * j + 1] -= __uint_as_float(w[j] & 0xffff0000u);
+      }
+      *reinterpret_cast<uint4*>(out) = make_uint4(w[0], w[1], w[2], w[3]);
+      out += (size_t)live * vpad;
+    }
   } else {
     reinterpret_cast<float4*>(out)[0] = make_float4(z[0], z[1], z[2], z[3]);
     reinterpret_cast<float4*>(out)[1] = make_float4(z[4], z[5], z[6], z[7]);
@@ -560,10 +654,10 @@ __device__ __forceinline__ void store_grad4(void* out, int grad_f32, size_t at, 
 template <int kDtype>
 __global__ __launch_bounds__(kDtype == 0 ? kThreads8 : kF32Threads, 1) void ce_dh_kernel(
     const char* __restrict__ W, const char* __restrict__ Gd, int vocab, int vpad, int d, const int32_t* __restrict__ count,
-    int c0, int cap, int n_dt, const int32_t* __restrict__ splits_of, float* __restrict__ part) {
+    int c0, int cap, int parts, int n_dt, const int32_t* __restrict__ splits_of, float* __restrict__ part) {
   constexpr int kT = GradTile<kDtype>::kRows, kStepK = GradTile<kDtype>::kStepK, es = Elem<kDtype>::kSize;
   __shared__ __align__(1024) uint4 smem[kDtype == 0 ? kEngineSmemChunks : kF32SmemChunks];
-  const int live = __builtin_amdgcn_readfirstlane(chunk_live(count, c0, cap));
+  const int live = __builtin_amdgcn_readfirstlane(parts * chunk_live(count, c0, cap));
   const int splits = __builtin_amdgcn_readfirstlane(*splits_of);
   const int n_tb = (live + kT - 1) / kT;
   if ((long long)blockIdx.x >= (long long)n_tb * n_dt * splits) return;
@@ -592,7 +686,7 @@ __global__ __launch_bounds__(kDtype == 0 ? kThreads8 : kF32Threads, 1) void ce_d
           store(t0 + L.tq * 64 + bn * 16 + L.c16, dt * kT + L.wv * 128 + bm * 16 + 4 * L.quad, acc[bm][bn]);
     });
   } else {
-    run_tile_f32<false>(smem, KmOperand{w_rows + d_off, w_row, w_left, d_off}, B, ks1 - ks0, [&](floatx4 (&acc)[2][2], int wave, int quad, int c16) {
+    run_tile_f32<true, false>(smem, KmOperand{w_rows + d_off, w_row, w_left, d_off}, B, ks1 - ks0, [&](floatx4 (&acc)[2][2], int wave, int quad, int c16) {
 #pragma unroll
       for (int bn = 0; bn < 2; ++bn)
 #pragma unroll
@@ -606,7 +700,7 @@ __global__ __launch_bounds__(kDtype == 0 ? kThreads8 : kF32Threads, 1) void ce_d
 // term coef[j] W[y]), four values per thread, to the token's own row.
 template <int kDtype>
 __global__ __launch_bounds__(256) void ce_dh_finish_kernel(const float* __restrict__ part,
-                                                           const int32_t* __restrict__ splits_of, int cap, int d,
+                                                           const int32_t* __restrict__ splits_of, int cap, int parts, int d,
                                                            const int32_t* __restrict__ rows, const int32_t* __restrict__ ids,
                                                            const int32_t* __restrict__ count, int c0, GradScale gs,
                                                            const float* __restrict__ coef,
@@ -618,13 +712,18 @@ __global__ __launch_bounds__(256) void ce_dh_finish_kernel(const float* __restri
   if (j >= live) return;
   constexpr int kT = GradTile<kDtype>::kRows;
   const int splits = *splits_of;
-  const size_t per_split = (size_t)((live + kT - 1) / kT * kT) * d;
+  const size_t per_split = (size_t)((parts * live + kT - 1) / kT * kT) * d;
   const float unit = grad_unit(gs, count);
   for (int k = threadIdx.x * 4; k < d; k += 1024) {
     float o[4] = {0.0f, 0.0f, 0.0f, 0.0f};
     for (int s = 0; s < splits; ++s) {
-      const float4 v = *reinterpret_cast<const float4*>(part + s * per_split + (size_t)j * d + k);
+      const float* at = part + s * per_split + (size_t)j * d + k;
+      float4 v = *reinterpret_cast<const float4*>(at);
       o[0] += v.x, o[1] += v.y, o[2] += v.z, o[3] += v.w;
+      if (parts == 2) {
+        v = *reinterpret_cast<const float4*>(at + (size_t)live * d);
+        o[0] += v.x, o[1] += v.y, o[2] += v.z, o[3] += v.w;
+      }
     }
 #pragma unroll
     for (int r = 0; r < 4; ++r) o[r] *= unit;
@@ -714,7 +813,7 @@ __global__ __launch_bounds__(kDtype == 0 ? kThreads8 : kF32Threads, 1) void ce_d
       }
     });
   } else {
-    run_tile_f32<true>(smem, KmOperand{Hc + d_off, h_row, live, d_off}, B, nks, [&](floatx4 (&acc)[2][2], int wave, int quad, int c16) {
+    run_tile_f32<true, true>(smem, KmOperand{Hc + d_off, h_row, live, d_off}, B, nks, [&](floatx4 (&acc)[2][2], int wave, int quad, int c16) {
 #pragma unroll
       for (int bn = 0; bn < 2; ++bn)
 #pragma unroll
@@ -729,10 +828,10 @@ constexpr int kFewTokens = 256;
 template <int kMode>
 __global__ __launch_bounds__(kFewThreads, 4) void ce_dw_few_kernel(const char* __restrict__ Gd, const char* __restrict__ Hc,
                                                                    int vpad, const int32_t* __restrict__ count, int c0,
-                                                                   int cap, int vocab, int d, int n_dt, GradScale gs,
-                                                                   void* __restrict__ dW) {
+                                                                   int cap, int parts, int vocab, int d, int n_dt,
+                                                                   GradScale gs, void* __restrict__ dW) {
   __shared__ __align__(1024) uint4 smem[kFewSmemChunks];
-  const int live = __builtin_amdgcn_readfirstlane(chunk_live(count, c0, cap));
+  const int live = __builtin_amdgcn_readfirstlane(parts * chunk_live(count, c0, cap));
   const int dt = blockIdx.x % n_dt, vt = blockIdx.x / n_dt;
   const uint32_t d_off = (uint32_t)dt * kFewTile * 2, v_off = (uint32_t)vt * kFewTile * 2;
   const float unit = grad_unit(gs, count);
@@ -801,7 +900,7 @@ void dh_most(long long cap, long long d, long long vpad, int dtype, long long* g
 }
 
 struct CeLayout {
-  int cap, vpad;
+  int cap, vpad, parts;
   long long dh_groups;
   size_t rows, ids, slot, count, splits, lp, lse, zy, part, loss, wmean, wpart, hc, z, gd, dhp, coef, cids, dwacc, sampled,
       total;
@@ -811,7 +910,9 @@ CeLayout ce_layout(long long n_tok, long long d, long long vocab, int dtype, boo
   CeLayout L{};
   const int es = dtype == 0 ? 2 : 4;
   L.vpad = (int)round_up(vocab, kBV);
-  L.cap = (int)(grad ? std::min<long long>(kCeChunk, n_tok) : n_tok);
+  // bf16 without the gradient keeps no logits: one chunk
+  L.cap = (int)(grad ? std::min<long long>(kCeChunk, n_tok) : dtype == 1 ? std::min<long long>(kCeF32Chunk, n_tok) : n_tok);
+  L.parts = dtype == 0 && grad && n_tok <= kPairTokens ? 2 : 1;
   size_t off = 0;
   auto take = [&](size_t bytes) {
     const size_t at = off;
@@ -824,18 +925,20 @@ CeLayout ce_layout(long long n_tok, long long d, long long vocab, int dtype, boo
   L.count = take(4);
   L.lp = take((size_t)n_tok * 4);
   L.lse = take((size_t)n_tok * 4);
-  L.zy = take((size_t)L.cap * 4);
-  L.part = take((size_t)2 * n_slices(vocab) * L.cap * sizeof(float2));
+  if (dtype == 0) {
+    L.zy = take((size_t)L.cap * 4);
+    L.part = take((size_t)2 * n_slices(vocab) * L.cap * sizeof(float2));
+  }
   L.loss = take((size_t)ceil_div(n_tok, 4) * 8);
   L.wmean = take((size_t)d * 4);
   L.wpart = take((size_t)ceil_div(vocab, kMeanRows) * d * 4);
-  L.hc = take((size_t)L.cap * d * es);
+  L.hc = take((size_t)L.parts * L.cap * d * es);
+  if (grad || dtype == 1) L.z = take((size_t)L.cap * L.vpad * 4);
   if (grad) {
     long long rows;
-    dh_most(L.cap, d, L.vpad, dtype, &L.dh_groups, &rows);
+    dh_most(L.parts * L.cap, d, L.vpad, dtype, &L.dh_groups, &rows);
     L.splits = take((size_t)ceil_div(n_tok, L.cap) * 4);
-    L.z = take((size_t)L.cap * L.vpad * 4);
-    L.gd = take((size_t)L.cap * L.vpad * es);
+    L.gd = take((size_t)L.parts * L.cap * L.vpad * es);
     L.dhp = take((size_t)rows * d * 4);
     if (dtype == 0 && grad_dtype == 1) {
       L.coef = take((size_t)L.cap * 4);
@@ -854,33 +957,32 @@ CeLayout ce_layout(long long n_tok, long long d, long long vocab, int dtype, boo
     if (e != hipSuccess) return e; \
   } while (0)
 
-template <int kDtype, bool kKeep>
+template <bool kKeep>
 void launch_ce_partial(const char* Hc, const char* W, const int32_t* ids, const int32_t* count, int c0, int cap, int d,
                        int vocab, float2* part, float* zy, float* logits, long long ld, hipStream_t stream) {
-  const int row_bytes = d * Elem<kDtype>::kSize;
+  const int row_bytes = d * 2;
   const int S = n_slices(vocab), G = slices_per_group(cap, vocab), ntb = (int)ceil_div(cap, kBT);
   // Few workgroups: the narrow walk's blocks are a quarter of the wide one's
   // (two rounds of them over the CUs still half its time), of 128 tokens a
   // half. The bits are the same.
   const long long narrow = ceil_div(cap, kNarrowBRows) * S;
   if (cap <= kNarrowMaxTokens || narrow <= 512) {
-    hipLaunchKernelGGL((ce_partial_narrow_kernel<kDtype, kKeep, kNarrowBRows>), dim3((unsigned)narrow), dim3(kThreads), 0,
+    hipLaunchKernelGGL((ce_partial_narrow_kernel<0, kKeep, kNarrowBRows>), dim3((unsigned)narrow), dim3(kThreads), 0,
                        stream, Hc, W, ids, count, c0, cap, cap, row_bytes, vocab, S, part, zy, logits, ld);
     return;
   }
   if (cap <= kNarrow128MaxTokens) {
-    hipLaunchKernelGGL((ce_partial_narrow_kernel<kDtype, kKeep, kNarrow128MaxTokens>), dim3((unsigned)S), dim3(kThreads), 0,
+    hipLaunchKernelGGL((ce_partial_narrow_kernel<0, kKeep, kNarrow128MaxTokens>), dim3((unsigned)S), dim3(kThreads), 0,
                        stream, Hc, W, ids, count, c0, cap, cap, row_bytes, vocab, S, part, zy, logits, ld);
     return;
   }
   const dim3 grid((unsigned)ntb * (unsigned)n_slice_groups(cap, vocab));
-  // the load schedule's rule, and its exception for fp32 kept logits, as in the logprob's forward
-  constexpr bool kFarOnly = kDtype == 1 && kKeep;
-  if (kFarOnly || row_bytes / kStepBytes > kNearBMaxSteps)
-    hipLaunchKernelGGL((ce_partial_kernel<kDtype, kKeep, true>), grid, dim3(kThreads8), 0, stream, Hc, W, ids, count, c0,
+  // the load schedule's rule as in the logprob's forward
+  if (row_bytes / kStepBytes > kNearBMaxSteps)
+    hipLaunchKernelGGL((ce_partial_kernel<0, kKeep, true>), grid, dim3(kThreads8), 0, stream, Hc, W, ids, count, c0,
                        cap, cap, row_bytes, vocab, S, G, part, zy, logits, ld);
-  else if constexpr (!kFarOnly)
-    hipLaunchKernelGGL((ce_partial_kernel<kDtype, kKeep, false>), grid, dim3(kThreads8), 0, stream, Hc, W, ids, count, c0,
+  else
+    hipLaunchKernelGGL((ce_partial_kernel<0, kKeep, false>), grid, dim3(kThreads8), 0, stream, Hc, W, ids, count, c0,
                        cap, cap, row_bytes, vocab, S, G, part, zy, logits, ld);
 }
 
@@ -923,11 +1025,10 @@ hipError_t run_cross_entropy(const CeCall& c, hipStream_t stream) {
   // not, so nothing is gathered.
   const bool direct = !grad && !wmean && n <= kNarrow128MaxTokens;
   if (!direct) {
-      hipLaunchKernelGGL(ce_select_kernel, dim3(1), dim3(kSelectThreads), 0, stream, c.targets, n, vocab, rows, ids, slot,
+    hipLaunchKernelGGL(ce_select_kernel, dim3(1), dim3(kSelectThreads), 0, stream, c.targets, n, vocab, rows, ids, slot,
                          count, grad ? reinterpret_cast<int32_t*>(at(L.splits)) : nullptr, L.cap, GradTile<kDtype>::kRows,
-                         (int)ceil_div(d, GradTile<kDtype>::kRows), L.vpad / GradTile<kDtype>::kStepK,
-                         kDtype);
-      ITL_CHECK_LAUNCH();
+                       L.parts, (int)ceil_div(d, GradTile<kDtype>::kRows), L.vpad / GradTile<kDtype>::kStepK, kDtype);
+    ITL_CHECK_LAUNCH();
   }
   if (wmean) {
     const int nb = (int)ceil_div(vocab, kMeanRows);
@@ -939,34 +1040,43 @@ hipError_t run_cross_entropy(const CeCall& c, hipStream_t stream) {
   }
   GradScale gs{c.smoothing, c.z_weight, c.grad_scale, 1.0f / (float)vocab, c.mean};
   const bool exact = grad && kDtype == 0 && c.grad_dtype == 1;
-  for (int c0 = 0; c0 < n; c0 += L.cap) {
+  for (long long first = 0; first < n; first += L.cap) {
+    const int c0 = (int)first;
     const int cap = std::min(L.cap, n - c0);
     if (!direct)
       hipLaunchKernelGGL(ce_gather_kernel, dim3((unsigned)(c0 == 0 ? n : cap)), dim3(256), 0, stream,
-                         reinterpret_cast<const uint4*>(H), rows, slot, count, c0, cap, row_chunks,
+                         reinterpret_cast<const uint4*>(H), rows, slot, count, c0, cap, L.parts, row_chunks,
                          reinterpret_cast<uint4*>(Hc), c0 == 0 ? static_cast<uint4*>(c.dH) : nullptr,
                          d * (c.grad_dtype == 0 ? 2 : 4) / 16);
-    float* z = grad ? reinterpret_cast<float*>(at(L.z)) : nullptr;
-    if (grad)
-      launch_ce_partial<kDtype, true>(Hc, reinterpret_cast<const char*>(W), ids + c0, count, c0, cap, d, vocab, part, zy,
-                                      z, L.vpad, stream);
-    else
-      launch_ce_partial<kDtype, false>(direct ? reinterpret_cast<const char*>(H) : Hc, reinterpret_cast<const char*>(W),
-                                       direct ? c.targets : ids + c0, direct ? nullptr : count, c0, cap, d, vocab, part, zy,
-                                       nullptr, 0, stream);
-    ITL_CHECK_LAUNCH();
-    e = launch_lse_combine(part, zy, cap, 2 * S, lp + c0, lse + c0, stream);
-    if (e != hipSuccess) return e;
+    float* z = reinterpret_cast<float*>(at(L.z));
+    const char* h_rows = direct ? reinterpret_cast<const char*>(H) : Hc;
+    const char* w_rows = reinterpret_cast<const char*>(W);
+    const int32_t* y = direct ? c.targets : ids + c0;
+    const int32_t* counted = direct ? nullptr : count;
+    if constexpr (kDtype == 0) {
+      if (grad) launch_ce_partial<true>(h_rows, w_rows, y, counted, c0, cap, d, vocab, part, zy, z, L.vpad, stream);
+      else launch_ce_partial<false>(h_rows, w_rows, y, counted, c0, cap, d, vocab, part, zy, nullptr, 0, stream);
+      ITL_CHECK_LAUNCH();
+      e = launch_lse_combine(part, zy, cap, 2 * S, lp + c0, lse + c0, stream);
+      if (e != hipSuccess) return e;
+    } else {
+      const int n_vt = (int)ceil_div(vocab, kF32Tile);
+      hipLaunchKernelGGL(ce_logits_f32_kernel, dim3((unsigned)(n_vt * ceil_div(cap, kF32Tile))), dim3(kF32Threads), 0, stream,
+                         h_rows, w_rows, counted, c0, cap, d * 4, vocab, n_vt, z, (long long)L.vpad);
+      hipLaunchKernelGGL(ce_lse_f32_kernel, dim3((unsigned)cap), dim3(256), 0, stream, z, (long long)L.vpad, y, counted, c0,
+                         cap, vocab, lp + c0, lse + c0);
+      ITL_CHECK_LAUNCH();
+    }
     if (!grad) continue;
 
     T* Gd = reinterpret_cast<T*>(at(L.gd));
     const dim3 g_grid((unsigned)ceil_div(L.vpad, 256 * kGradVec), (unsigned)cap);
     if (exact)
       hipLaunchKernelGGL((ce_grad_logits_kernel<kDtype, true>), g_grid, dim3(256), 0, stream, z, (long long)L.vpad,
-                         ids + c0, count, c0, cap, vocab, L.vpad, lse + c0, gs, Gd);
+                         ids + c0, count, c0, cap, L.parts, vocab, L.vpad, lse + c0, gs, Gd);
     else
       hipLaunchKernelGGL((ce_grad_logits_kernel<kDtype, false>), g_grid, dim3(256), 0, stream, z, (long long)L.vpad,
-                         ids + c0, count, c0, cap, vocab, L.vpad, lse + c0, gs, Gd);
+                         ids + c0, count, c0, cap, L.parts, vocab, L.vpad, lse + c0, gs, Gd);
     ITL_CHECK_LAUNCH();
     float* coef = nullptr;
     int32_t* cids = reinterpret_cast<int32_t*>(at(L.cids));
@@ -985,9 +1095,9 @@ hipError_t run_cross_entropy(const CeCall& c, hipStream_t stream) {
     const int32_t* splits = reinterpret_cast<const int32_t*>(at(L.splits)) + c0 / L.cap;
     hipLaunchKernelGGL(ce_dh_kernel<kDtype>, dim3((unsigned)L.dh_groups), g_block, 0, stream,
                        reinterpret_cast<const char*>(W), reinterpret_cast<const char*>(Gd), vocab, L.vpad, d, count, c0, cap,
-                       n_dt, splits, dhp);
+                       L.parts, n_dt, splits, dhp);
     ITL_CHECK_LAUNCH();
-    hipLaunchKernelGGL(ce_dh_finish_kernel<kDtype>, dim3((unsigned)cap), dim3(256), 0, stream, dhp, splits, cap, d, rows,
+    hipLaunchKernelGGL(ce_dh_finish_kernel<kDtype>, dim3((unsigned)cap), dim3(256), 0, stream, dhp, splits, cap, L.parts, d, rows,
                        ids + c0, count, c0, gs, coef, W, c.grad_dtype, c.dH);
     ITL_CHECK_LAUNCH();
     // dW
@@ -1009,7 +1119,8 @@ hipError_t run_cross_entropy(const CeCall& c, hipStream_t stream) {
         if (n <= kFewTokens) {
           const int n_dt2 = (int)ceil_div(d, kFewTile), n_vt2 = (int)ceil_div(vocab, kFewTile);
           hipLaunchKernelGGL((ce_dw_few_kernel<decltype(mode)::value>), dim3((unsigned)(n_vt2 * n_dt2)), dim3(kFewThreads), 0,
-                             stream, reinterpret_cast<const char*>(Gd), Hc, L.vpad, count, c0, cap, vocab, d, n_dt2, gs, out);
+                             stream, reinterpret_cast<const char*>(Gd), Hc, L.vpad, count, c0, cap, L.parts, vocab, d, n_dt2, gs,
+                             out);
           return;
         }
       }
@@ -1026,7 +1137,7 @@ hipError_t run_cross_entropy(const CeCall& c, hipStream_t stream) {
                          reinterpret_cast<const float4*>(acc), (long long)vocab * d / 4, static_cast<float4*>(c.dW));
       ITL_CHECK_LAUNCH();
     }
-    if (!exact && !single && c0 + L.cap >= n && c.grad_dtype == 0) {
+    if (!exact && !single && first + L.cap >= n && c.grad_dtype == 0) {
       hipLaunchKernelGGL(ce_round_kernel, dim3((unsigned)ceil_div((long long)vocab * d / 4, 256)), dim3(256), 0, stream,
                          reinterpret_cast<const float4*>(acc), (long long)vocab * d / 4, static_cast<uint2*>(c.dW));
       ITL_CHECK_LAUNCH();

@@ -317,10 +317,14 @@ constexpr int kF32Threads = 256;
 
 // acc = A B^T over nks steps of 32 k, 64 x 64: wavefront w holds A columns
 // 32 (w mod 2) .. against B 32 (w / 2) .., as 2 x 2 blocks; acc[bm][bn][i] is
-// A 32 (w & 1) + 16 bm + 4 quad + i, B 32 (w >> 1) + 16 bn + c16. A is
-// K-major, B K-major or K-contiguous. K-major rows are 256 bytes; their
-// 64-byte piece (16 columns) P of row k sits at P ^ ((k / 4) mod 4).
-template <bool kBMajor, class Epi>
+// A 32 (w & 1) + 16 bm + 4 quad + i, B 32 (w >> 1) + 16 bn + c16. Each operand
+// is K-major or K-contiguous. K-major rows are 256 bytes; their 64-byte piece
+// (16 columns) P of row k sits at P ^ ((k / 4) mod 4).
+// Sums of kF32Fold steps (64 k) are added to the total one by one: one chain
+// of k / 4 dependent additions of a growing sum lost up to 8e-6 of a logit at
+// 5056 k where the terms agree in sign; 16 additions, then k / 64 do not.
+constexpr int kF32Fold = 2;
+template <bool kAMajor, bool kBMajor, class Epi>
 __device__ __forceinline__ void run_tile_f32(uint4* smem, const KmOperand& A, const KmOperand& B, int nks, Epi&& epi) {
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -335,30 +339,40 @@ __device__ __forceinline__ void run_tile_f32(uint4* smem, const KmOperand& A, co
     const int lr = lane >> 3;  // rows 16 w + 8 j + lane / 8
     return (uint32_t)(16 * wave + 8 * j + lr) * row_bytes + (((lane & 7) ^ lr ^ (j & 1)) * 16);
   };
-  const uint32_t ao[2] = {offset(0, true, A.row_bytes), offset(1, true, A.row_bytes)};
+  const uint32_t ao[2] = {offset(0, kAMajor, A.row_bytes), offset(1, kAMajor, A.row_bytes)};
   const uint32_t bo[2] = {offset(0, kBMajor, B.row_bytes), offset(1, kBMajor, B.row_bytes)};
+  const int4v a_rows = rsrc_words(A.base, kAMajor ? 0u : (uint32_t)A.rows * A.row_bytes - A.skip);
   const int4v b_rows = rsrc_words(B.base, kBMajor ? 0u : (uint32_t)B.rows * B.row_bytes - B.skip);
   auto load = [&](int s) {
     const int st = s < nks ? s : nks - 1;
     const uint32_t slot = (uint32_t)(s % kF32Slots) * kF32SlotBytes + (uint32_t)wave * 2048u;
-    const int4v ar = km_step_rsrc(A, st, kF32StepK);
+    const int4v ar = kAMajor ? km_step_rsrc(A, st, kF32StepK) : a_rows;
     const int4v br = kBMajor ? km_step_rsrc(B, st, kF32StepK) : b_rows;
-    const uint32_t soff = kBMajor ? 0u : (uint32_t)st * kStepBytes;
+    const uint32_t a_off = kAMajor ? 0u : (uint32_t)st * kStepBytes, b_off = kBMajor ? 0u : (uint32_t)st * kStepBytes;
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
-      dma16(ar, ao[j], 0u, lds0 + slot + 1024u * j);
-      dma16(br, bo[j], soff, lds0 + kF32Slots * kF32SlotBytes + slot + 1024u * j);
+      dma16(ar, ao[j], a_off, lds0 + slot + 1024u * j);
+      dma16(br, bo[j], b_off, lds0 + kF32Slots * kF32SlotBytes + slot + 1024u * j);
     }
   };
   const float* lds_f = reinterpret_cast<const float*>(smem);
-  floatx4 acc[2][2];
+  floatx4 acc[2][2], total[2][2];
 #pragma unroll
   for (int bm = 0; bm < 2; ++bm)
 #pragma unroll
-    for (int bn = 0; bn < 2; ++bn) acc[bm][bn] = floatx4{};
+    for (int bn = 0; bn < 2; ++bn) acc[bm][bn] = total[bm][bn] = floatx4{};
   load(0);
   load(1);
   for (int s = 0; s < nks; ++s) {
+    if (s % kF32Fold == 0 && s > 0) {
+#pragma unroll
+      for (int bm = 0; bm < 2; ++bm)
+#pragma unroll
+        for (int bn = 0; bn < 2; ++bn) {
+          total[bm][bn] += acc[bm][bn];
+          acc[bm][bn] = floatx4{};
+        }
+    }
     // step s landed (step s + 1 may be in flight); every wavefront is done
     // with step s - 1, whose slot takes step s + 2
     wait_and_barrier<4>();
@@ -366,26 +380,28 @@ __device__ __forceinline__ void run_tile_f32(uint4* smem, const KmOperand& A, co
     const int slot = (s % kF32Slots) * (kF32SlotBytes / 4);
     const float* sa = lds_f + slot;
     const float* sb = lds_f + kF32Slots * (kF32SlotBytes / 4) + slot;
-    // value j of half kk: k = 16 kk + 4 lane_chunk(quad) + j
-    auto major = [&](const float* t, int block, int kk, int j) {
-      const int k = 16 * kk + 4 * lane_chunk(quad) + j;
-      return t[k * 64 + ((block ^ ((k >> 2) & 3)) * 16) + c16];
+    // the four values of a block's column (or row) c16 in half kk: k = 16 kk +
+    // 4 lane_chunk(quad) + j
+    auto fragment = [&](auto major, const float* t, int block, int kk, float (&v)[4]) {
+      if constexpr (decltype(major)::value) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int k = 16 * kk + 4 * lane_chunk(quad) + j;
+          v[j] = t[k * 64 + ((block ^ ((k >> 2) & 3)) * 16) + c16];
+        }
+      } else {
+        const int row = 16 * block + c16;
+        const float4 w = reinterpret_cast<const float4*>(t)[row * kRowChunks + ((4 * kk + lane_chunk(quad)) ^ swz(c16))];
+        v[0] = w.x, v[1] = w.y, v[2] = w.z, v[3] = w.w;
+      }
     };
 #pragma unroll
     for (int kk = 0; kk < 2; ++kk) {
       float a[2][4], b[2][4];
 #pragma unroll
       for (int t = 0; t < 2; ++t) {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) a[t][j] = major(sa, 2 * (wave & 1) + t, kk, j);
-        if constexpr (kBMajor) {
-#pragma unroll
-          for (int j = 0; j < 4; ++j) b[t][j] = major(sb, 2 * (wave >> 1) + t, kk, j);
-        } else {
-          const int row = 32 * (wave >> 1) + 16 * t + c16;
-          const float4 v = reinterpret_cast<const float4*>(sb)[row * kRowChunks + ((4 * kk + lane_chunk(quad)) ^ swz(c16))];
-          b[t][0] = v.x, b[t][1] = v.y, b[t][2] = v.z, b[t][3] = v.w;
-        }
+        fragment(std::integral_constant<bool, kAMajor>{}, sa, 2 * (wave & 1) + t, kk, a[t]);
+        fragment(std::integral_constant<bool, kBMajor>{}, sb, 2 * (wave >> 1) + t, kk, b[t]);
       }
 #pragma unroll
       for (int j = 0; j < 4; ++j)
@@ -397,7 +413,11 @@ __device__ __forceinline__ void run_tile_f32(uint4* smem, const KmOperand& A, co
     }
   }
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-  epi(acc, wave, quad, c16);
+#pragma unroll
+  for (int bm = 0; bm < 2; ++bm)
+#pragma unroll
+    for (int bn = 0; bn < 2; ++bn) total[bm][bn] += acc[bm][bn];
+  epi(total, wave, quad, c16);
 }
 
 }  // namespace itl

@@ -214,14 +214,17 @@ def test_nothing_and_refusals(cuda):
             call()
 
 
-def test_replay(cuda):
+@pytest.mark.parametrize("n,dtype,grad", [(500, torch.bfloat16, torch.bfloat16), (500, torch.bfloat16, torch.float32),
+                                          (70, torch.bfloat16, torch.bfloat16), (300, torch.float32, torch.float32)])
+def test_replay(cuda, n, dtype, grad):
+    """Another mask at each replay: how many tokens count is not fixed at the capture."""
     itl = _itl()
-    H, W, y = _head(500, 128, 3000, torch.bfloat16, 4, cuda, "some")
+    H, W, y = _head(n, 128, 3000, dtype, 4, cuda, "some")
     other = y.flip(0).contiguous()
+    other[: n // 2] = -100
     ids = y.clone()
-    ws = torch.empty(itl.cross_entropy_workspace_bytes(500, 128, 3000, torch.bfloat16, torch.bfloat16),
-                     dtype=torch.uint8, device=cuda)
-    call = lambda t: itl.cross_entropy_grad(H, W, t, grad_dtype=torch.bfloat16, label_smoothing=0.1, workspace=ws)
+    ws = torch.empty(itl.cross_entropy_workspace_bytes(n, 128, 3000, dtype, grad), dtype=torch.uint8, device=cuda)
+    call = lambda t: itl.cross_entropy_grad(H, W, t, grad_dtype=grad, label_smoothing=0.1, workspace=ws)
     want = [[a.clone() for a in call(t)] for t in (y, other)]
     torch.cuda.synchronize()
     graph = torch.cuda.CUDAGraph()

@@ -162,7 +162,7 @@ def test_column_sums_are_deterministic(cuda, n, d):
         assert same_bits(a, b)
 
 
-@pytest.mark.parametrize("d", [1001, 2560])
+@pytest.mark.parametrize("d", [1001, 2560, 5001, 7168, 9000, 16392])
 def test_in_place(cuda, d):
     """h may be x, and dx may be dh."""
     itl = _itl()

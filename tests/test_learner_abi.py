@@ -161,8 +161,8 @@ def test_bindings_refuse_host_tensors(itl):
 
 @needs_hipcc
 @pytest.mark.parametrize("src,kernels", [
-    ("cross_entropy.hip", ["ce_partial_kernelILi0E", "ce_partial_kernelILi1E", "ce_dh_kernelILi0E", "ce_dh_kernelILi1E",
-                           "ce_dw_kernelILi0E", "ce_dw_kernelILi1E"]),
+    ("cross_entropy.hip", ["ce_partial_kernelILi0E", "ce_partial_narrow_kernel", "ce_logits_f32_kernel", "ce_dh_kernelILi0E",
+                           "ce_dh_kernelILi1E", "ce_dw_kernelILi0E", "ce_dw_kernelILi1E", "ce_dw_few_kernel"]),
     ("norm.hip", ["norm_"]),
     ("adamw.hip", ["adamw_"]),
 ])
