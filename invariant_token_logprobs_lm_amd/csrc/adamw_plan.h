@@ -10,7 +10,7 @@ namespace itl {
 // state of tensor i - 1; an 8-bit state has one scale per kAdamBlock.
 constexpr int kAdamBlock = 256;
 // Elements of a piece: one workgroup's work, within one tensor.
-constexpr int kAdamPiece = 4096;
+constexpr int kAdamPiece = 2048;
 constexpr int kAdamThreads = 256;
 constexpr int kAdamVec = 8;  // consecutive elements of a thread
 static_assert(kAdamPiece % (kAdamThreads * kAdamVec) == 0 && kAdamPiece % kAdamBlock == 0, "whole passes and blocks");

@@ -19,7 +19,9 @@
 //      contraction and online log-sum-exp folds (the same bits; without the
 //      gradient nothing is kept), fp32 heads by 64 x 64 tiles and a pass over
 //      z for the log-sum-exp;
-//   2. G [chunk, Vpad] in the head's type;
+//   2. G [chunk, Vpad] in the head's type, like z in blocks of 256 vocabulary
+//      entries (all tokens of a block side by side): a tile's rows are then
+//      one piece of memory, for its writer and for both contractions;
 //   3. dH = G W, K = the vocabulary, split over several workgroups when the
 //      chunk has few tiles (fp32 partials added in order);
 //   4. dW += G^T H, K = the chunk's tokens.
@@ -76,6 +78,12 @@ __host__ __device__ inline int dh_splits(uint32_t tiles, uint32_t nks, bool f32)
     if (cost < best_cost) best = s, best_cost = cost;
   }
   return (int)best;
+}
+
+// Place of (token row t, vocabulary entry v) in a blocked array of `rows`
+// token rows: blocks of kBV entries.
+__host__ __device__ inline size_t block_at(int t, int v, int rows) {
+  return ((size_t)(v / kBV) * rows + t) * kBV + v % kBV;
 }
 
 // ---- which tokens count
@@ -155,7 +163,7 @@ template <int kDtype, bool kKeep, bool kBFar>
 __global__ __launch_bounds__(kThreads8, 1) void ce_partial_kernel(
     const char* __restrict__ H, const char* __restrict__ W, const int32_t* __restrict__ ids,
     const int32_t* __restrict__ count, int c0, int cap, int stride, int row_bytes, int vocab, int n_slices, int group,
-    float2* __restrict__ part, float* __restrict__ zy_out, float* __restrict__ logits, long long ld) {
+    float2* __restrict__ part, float* __restrict__ zy_out, float* __restrict__ logits) {
   __shared__ uint4 smem[kEngineSmemChunks];
   const Lanes8 L = lanes8();
   const int wv = L.wv, tq = L.tq, quad = L.quad, c16 = L.c16;
@@ -197,9 +205,11 @@ __global__ __launch_bounds__(kThreads8, 1) void ce_partial_kernel(
 #pragma unroll
       for (int bn = 0; bn < 4; ++bn) {
         if constexpr (kKeep) {
-          const LogitRows rows = logit_rows(logits, ld, t0 + tq * 64, 64, n_tok, c16, quad);
+          // (entries past the vocabulary are zeros and have their place)
+          const LogitRows rows = logit_rows(logits + (size_t)tile * kBV * cap, kBV, t0 + tq * 64, 64, n_tok, c16, quad);
 #pragma unroll
-          for (int bm = 0; bm < 8; ++bm) store_logits(rows, bn, vw + bm * 16, quad, vocab, acc[bm][bn], partial);
+          for (int bm = 0; bm < 8; ++bm)
+            store_logits(rows, bn, wv * 128 + bm * 16, quad, kBV, acc[bm][bn], std::false_type{});
         }
         floatx4 z[8];
 #pragma unroll
@@ -241,7 +251,7 @@ template <int kDtype, bool kKeep, int kBRows>
 __global__ __launch_bounds__(kThreads, 1) void ce_partial_narrow_kernel(
     const char* __restrict__ H, const char* __restrict__ W, const int32_t* __restrict__ ids,
     const int32_t* __restrict__ count, int c0, int cap, int stride, int row_bytes, int vocab, int n_slices,
-    float2* __restrict__ part, float* __restrict__ zy_out, float* __restrict__ logits, long long ld) {
+    float2* __restrict__ part, float* __restrict__ zy_out, float* __restrict__ logits) {
   __shared__ uint4 smem[kEngineSmemChunks];
   const Lanes L = lanes();
   const int wv = L.wv, wt = L.wt, quad = L.lane >> 4, c16 = L.lane & 15;
@@ -267,15 +277,17 @@ __global__ __launch_bounds__(kThreads, 1) void ce_partial_narrow_kernel(
     return rsrc_words(W + (size_t)v0 * row_bytes, (uint32_t)min(kBV, vocab - v0) * row_bytes);
   };
   const int4v hr = rsrc_words(H + (size_t)t0 * row_bytes, (uint32_t)min(kBRows, n_tok - t0) * row_bytes);
-  const LogitRows rows = logit_rows(logits, ld, t0 + wt * kWaveToks, kWaveToks, n_tok, c16, quad);
   auto epilogue = [&](int tile, floatx4 (&acc)[8][kBN]) {
     const int vw = tile * kBV + wv * 128;
     auto fold_tile = [&](auto partial) {
       if constexpr (kKeep) {
+        const LogitRows rows =
+            logit_rows(logits + (size_t)tile * kBV * cap, kBV, t0 + wt * kWaveToks, kWaveToks, n_tok, c16, quad);
 #pragma unroll
         for (int bn = 0; bn < kBN; ++bn)
 #pragma unroll
-          for (int bm = 0; bm < 8; ++bm) store_logits(rows, bn, vw + bm * 16, quad, vocab, acc[bm][bn], partial);
+          for (int bm = 0; bm < 8; ++bm)
+            store_logits(rows, bn, wv * 128 + bm * 16, quad, kBV, acc[bm][bn], std::false_type{});
       }
 #pragma unroll
       for (int bn = 0; bn < kBN; ++bn) {
@@ -297,13 +309,12 @@ __global__ __launch_bounds__(kThreads, 1) void ce_partial_narrow_kernel(
   }
 }
 
-// fp32 heads: z in 64 x 64 tiles (vocabulary tiles fastest), columns past the
-// vocabulary zero up to ld.
+// fp32 heads: z in 64 x 64 tiles (vocabulary tiles fastest).
 __global__ __launch_bounds__(kF32Threads, 1) void ce_logits_f32_kernel(const char* __restrict__ Hc,
                                                                        const char* __restrict__ W,
                                                                        const int32_t* __restrict__ count, int c0, int cap,
                                                                        int row_bytes, int vocab, int n_vt,
-                                                                       float* __restrict__ z, long long ld) {
+                                                                       float* __restrict__ z) {
   __shared__ __align__(1024) uint4 smem[kF32SmemChunks];
   const int live = __builtin_amdgcn_readfirstlane(chunk_live(count, c0, cap));
   const int vt = blockIdx.x % n_vt, t0 = blockIdx.x / n_vt * kF32Tile, v0 = vt * kF32Tile;
@@ -318,7 +329,7 @@ __global__ __launch_bounds__(kF32Threads, 1) void ce_logits_f32_kernel(const cha
 #pragma unroll
       for (int bm = 0; bm < 2; ++bm) {
         const floatx4& o = acc[bm][bn];
-        *reinterpret_cast<float4*>(z + (size_t)t * ld + v0 + 32 * (wave & 1) + 16 * bm + 4 * quad) =
+        *reinterpret_cast<float4*>(z + block_at(t, v0 + 32 * (wave & 1) + 16 * bm + 4 * quad, cap)) =
             make_float4(o[0], o[1], o[2], o[3]);
       }
     }
@@ -327,17 +338,16 @@ __global__ __launch_bounds__(kF32Threads, 1) void ce_logits_f32_kernel(const cha
 
 // lse and logprob of a row of z: each thread folds entries 4 (tid + 256 i) .. +
 // 3 into its (max, sum), then a fixed tree.
-__global__ __launch_bounds__(256) void ce_lse_f32_kernel(const float* __restrict__ z, long long ld,
+__global__ __launch_bounds__(256) void ce_lse_f32_kernel(const float* __restrict__ z,
                                                          const int32_t* __restrict__ ids, const int32_t* __restrict__ count,
                                                          int c0, int cap, int vocab, float* __restrict__ logprob,
                                                          float* __restrict__ lse) {
   __shared__ float2 lds[4];
   const int t = blockIdx.x;
   if (t >= chunk_live(count, c0, cap)) return;
-  const float* row = z + (size_t)t * ld;
   float m = -INFINITY, s = 0.0f;
   for (int v = 4 * threadIdx.x; v < vocab; v += 1024) {
-    const float4 q = *reinterpret_cast<const float4*>(row + v);  // (ld is a multiple of 256)
+    const float4 q = *reinterpret_cast<const float4*>(z + block_at(t, v, cap));
     float x[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) x[i] = v + i < vocab ? x[i] : -INFINITY;
@@ -362,7 +372,7 @@ __global__ __launch_bounds__(256) void ce_lse_f32_kernel(const float* __restrict
   // many times the loss. s >= 1, the maximum's own term is 1.
   const float ln_s = fast_log2(s) * kLn2;
   const int y = ids[t];  // (not gathered: it may not count)
-  logprob[t] = ((unsigned)y < (unsigned)vocab ? row[y] - m : 0.0f) - ln_s;
+  logprob[t] = ((unsigned)y < (unsigned)vocab ? z[block_at(t, y, cap)] - m : 0.0f) - ln_s;
   lse[t] = m + ln_s;
 }
 
@@ -572,38 +582,33 @@ constexpr int kPairTokens = 128;
 
 template <int kDtype, bool kExact>
 __global__ __launch_bounds__(256) void ce_grad_logits_kernel(
-    const float* __restrict__ logits, long long ld, const int32_t* __restrict__ ids, const int32_t* __restrict__ count,
-    int c0, int cap, int parts, int vocab, int vpad, const float* __restrict__ lse, GradScale gs,
+    const float* __restrict__ logits, const int32_t* __restrict__ ids, const int32_t* __restrict__ count,
+    int c0, int cap, int parts, int vocab, int g_rows, const float* __restrict__ lse, GradScale gs,
     typename Elem<kDtype>::T* __restrict__ Gd) {
   using E = Elem<kDtype>;
-  const int t = blockIdx.y;
-  const int v = (blockIdx.x * 256 + threadIdx.x) * kGradVec;
+  // a workgroup takes 8 tokens of one block: 8 KiB of z side by side
+  const int t = blockIdx.y * (256 * kGradVec / kBV) + threadIdx.x / (kBV / kGradVec);
+  const int v = blockIdx.x * kBV + threadIdx.x % (kBV / kGradVec) * kGradVec;
   const int live = chunk_live(count, c0, cap);
-  if (t >= live || v >= vpad) return;
+  if (t >= live) return;
   const float rest = 1.0f / (1.0f - gs.smoothing);
   const float cc = gs.smoothing * gs.inv_vocab * rest;
   const float s = lse[t];
   const float l2e_lse = s * kLog2e;
   const float a = rest * (1.0f + 2.0f * gs.z_weight * s);
   const int y = ids[t];
-  const float* row = logits + (size_t)t * (size_t)ld;
   float z[kGradVec];
-  if (v + kGradVec <= vocab) {
-    const floatx4 lo = __builtin_nontemporal_load(reinterpret_cast<const floatx4*>(row + v));
-    const floatx4 hi = __builtin_nontemporal_load(reinterpret_cast<const floatx4*>(row + v + 4));
+  const floatx4* at = reinterpret_cast<const floatx4*>(logits + block_at(t, v, cap));
+  const floatx4 lo = __builtin_nontemporal_load(at), hi = __builtin_nontemporal_load(at + 1);
 #pragma unroll
-    for (int r = 0; r < 4; ++r) z[r] = lo[r], z[4 + r] = hi[r];
-  } else {
-#pragma unroll
-    for (int r = 0; r < kGradVec; ++r) z[r] = v + r < vocab ? row[v + r] : 0.0f;
-  }
+  for (int r = 0; r < 4; ++r) z[r] = lo[r], z[4 + r] = hi[r];
 #pragma unroll
   for (int r = 0; r < kGradVec; ++r) {
     float x = a * fast_exp2(z[r] * kLog2e - l2e_lse) - cc;
     if (!kExact && v + r == y) x -= 1.0f;
     z[r] = v + r < vocab ? x : 0.0f;
   }
-  typename E::T* out = Gd + (size_t)t * vpad + v;
+  typename E::T* out = Gd + block_at(t, v, g_rows);
   if constexpr (kDtype == 0) {
     for (int part = 0; part < parts; ++part) {
       uint32_t w[4];
@@ -614,7 +619,7 @@ __global__ __launch_bounds__(256) void ce_grad_logits_kernel(
         z[2 * j + 1] -= __uint_as_float(w[j] & 0xffff0000u);
       }
       *reinterpret_cast<uint4*>(out) = make_uint4(w[0], w[1], w[2], w[3]);
-      out += (size_t)live * vpad;
+      out += (size_t)live * kBV;
     }
   } else {
     reinterpret_cast<float4*>(out)[0] = make_float4(z[0], z[1], z[2], z[3]);
@@ -654,7 +659,7 @@ __device__ __forceinline__ void store_grad4(void* out, int grad_f32, size_t at, 
 template <int kDtype>
 __global__ __launch_bounds__(kDtype == 0 ? kThreads8 : kF32Threads, 1) void ce_dh_kernel(
     const char* __restrict__ W, const char* __restrict__ Gd, int vocab, int vpad, int d, const int32_t* __restrict__ count,
-    int c0, int cap, int parts, int n_dt, const int32_t* __restrict__ splits_of, float* __restrict__ part) {
+    int c0, int cap, int parts, int g_rows, int n_dt, const int32_t* __restrict__ splits_of, float* __restrict__ part) {
   constexpr int kT = GradTile<kDtype>::kRows, kStepK = GradTile<kDtype>::kStepK, es = Elem<kDtype>::kSize;
   __shared__ __align__(1024) uint4 smem[kDtype == 0 ? kEngineSmemChunks : kF32SmemChunks];
   const int live = __builtin_amdgcn_readfirstlane(parts * chunk_live(count, c0, cap));
@@ -666,11 +671,12 @@ __global__ __launch_bounds__(kDtype == 0 ? kThreads8 : kF32Threads, 1) void ce_d
   const int t0 = tb * kT;
   const int nks_all = vpad / kStepK;
   const int ks0 = (int)((long long)nks_all * sp / splits), ks1 = (int)((long long)nks_all * (sp + 1) / splits);
-  const uint32_t w_row = (uint32_t)d * es, g_row = (uint32_t)vpad * es, d_off = (uint32_t)dt * kT * es;
+  const uint32_t w_row = (uint32_t)d * es, g_row = kBV * es, d_off = (uint32_t)dt * kT * es;
   const char* w_rows = W + (size_t)ks0 * kStepK * w_row;
   const int w_left = vocab - ks0 * kStepK;
-  const KmOperand B{Gd + (size_t)t0 * g_row + (size_t)ks0 * kStepBytes, g_row, min(kT, live - t0),
-                    (uint32_t)ks0 * kStepBytes};
+  const KmOperand B{Gd + (size_t)t0 * g_row, g_row, min(kT, live - t0), 0u, kDtype == 0 ? 2 : 3, ks0,
+                    (size_t)g_rows * g_row};
+  static_assert(kBV / kStepK == (kDtype == 0 ? 4 : 8), "K steps of a block of G");
   float* out = part + (size_t)sp * n_tb * kT * d;
   auto store = [&](int t, int k, const floatx4& o) {
     if (t < live && k < d) *reinterpret_cast<float4*>(out + (size_t)t * d + k) = make_float4(o[0], o[1], o[2], o[3]);
@@ -739,6 +745,12 @@ __global__ __launch_bounds__(256) void ce_dh_finish_kernel(const float* __restri
 
 // ---- dW
 
+// Columns v0 .. of G as a K-major operand (within one block), `live` rows.
+__device__ __forceinline__ KmOperand g_columns(const char* Gd, int v0, int g_rows, int es, int live) {
+  const uint32_t off = (uint32_t)(v0 % kBV * es);
+  return KmOperand{Gd + (size_t)(v0 / kBV) * g_rows * (kBV * es) + off, (uint32_t)(kBV * es), live, off};
+}
+
 // Tile of workgroup b of dW's contraction. Workgroups go to the 8 XCDs in
 // turn; XCD x takes the vocabulary tiles x, x + 8, ..., in blocks of 5 of them
 // by 3 walks of two tiles of d, so that the 30 or so workgroups it runs
@@ -774,7 +786,7 @@ enum { kDwRound = 0, kDwWrite = 1, kDwAdd = 2 };  // bf16 results; fp32 ones; fp
 
 template <int kDtype, int kMode>
 __global__ __launch_bounds__(kDtype == 0 ? kThreads8 : kF32Threads, 1) void ce_dw_kernel(
-    const char* __restrict__ Gd, const char* __restrict__ Hc, int vpad, const int32_t* __restrict__ count, int c0, int cap,
+    const char* __restrict__ Gd, const char* __restrict__ Hc, int g_rows, const int32_t* __restrict__ count, int c0, int cap,
     int vocab, int d, int n_vt, int n_dt, int walk, GradScale gs, void* __restrict__ dW) {
   constexpr int kT = GradTile<kDtype>::kRows, kStepK = GradTile<kDtype>::kStepK, es = Elem<kDtype>::kSize;
   __shared__ __align__(1024) uint4 smem[kDtype == 0 ? kEngineSmemChunks : kF32SmemChunks];
@@ -785,9 +797,9 @@ __global__ __launch_bounds__(kDtype == 0 ? kThreads8 : kF32Threads, 1) void ce_d
   dt *= walk;
   const int dt_end = min(dt + walk, n_dt);
   const int nks = max(1, (live + kStepK - 1) / kStepK);
-  const uint32_t h_row = (uint32_t)d * es, g_row = (uint32_t)vpad * es;
-  const uint32_t d_off = (uint32_t)dt * kT * es, v_off = (uint32_t)vt * kT * es;
-  const KmOperand B{Gd + v_off, g_row, live, v_off};
+  const uint32_t h_row = (uint32_t)d * es;
+  const uint32_t d_off = (uint32_t)dt * kT * es;
+  const KmOperand B = g_columns(Gd, vt * kT, g_rows, es, live);
   const float unit = grad_unit(gs, count);
   auto store = [&](int v, int k, const floatx4& o) {
     if (v >= vocab || k >= d) return;
@@ -827,16 +839,16 @@ __global__ __launch_bounds__(kDtype == 0 ? kThreads8 : kF32Threads, 1) void ce_d
 constexpr int kFewTokens = 256;
 template <int kMode>
 __global__ __launch_bounds__(kFewThreads, 4) void ce_dw_few_kernel(const char* __restrict__ Gd, const char* __restrict__ Hc,
-                                                                   int vpad, const int32_t* __restrict__ count, int c0,
+                                                                   int g_rows, const int32_t* __restrict__ count, int c0,
                                                                    int cap, int parts, int vocab, int d, int n_dt,
                                                                    GradScale gs, void* __restrict__ dW) {
   __shared__ __align__(1024) uint4 smem[kFewSmemChunks];
   const int live = __builtin_amdgcn_readfirstlane(parts * chunk_live(count, c0, cap));
   const int dt = blockIdx.x % n_dt, vt = blockIdx.x / n_dt;
-  const uint32_t d_off = (uint32_t)dt * kFewTile * 2, v_off = (uint32_t)vt * kFewTile * 2;
+  const uint32_t d_off = (uint32_t)dt * kFewTile * 2;
   const float unit = grad_unit(gs, count);
   run_tile_few(smem, KmOperand{Hc + d_off, (uint32_t)d * 2, live, d_off},
-               KmOperand{Gd + v_off, (uint32_t)vpad * 2, live, v_off},
+               g_columns(Gd, vt * kFewTile, g_rows, 2, live),
                [&](floatx4 (&acc)[4][4], int wave, int quad, int c16) {
 #pragma unroll
     for (int bn = 0; bn < 4; ++bn) {
@@ -959,7 +971,7 @@ CeLayout ce_layout(long long n_tok, long long d, long long vocab, int dtype, boo
 
 template <bool kKeep>
 void launch_ce_partial(const char* Hc, const char* W, const int32_t* ids, const int32_t* count, int c0, int cap, int d,
-                       int vocab, float2* part, float* zy, float* logits, long long ld, hipStream_t stream) {
+                       int vocab, float2* part, float* zy, float* logits, hipStream_t stream) {
   const int row_bytes = d * 2;
   const int S = n_slices(vocab), G = slices_per_group(cap, vocab), ntb = (int)ceil_div(cap, kBT);
   // Few workgroups: the narrow walk's blocks are a quarter of the wide one's
@@ -968,22 +980,22 @@ void launch_ce_partial(const char* Hc, const char* W, const int32_t* ids, const 
   const long long narrow = ceil_div(cap, kNarrowBRows) * S;
   if (cap <= kNarrowMaxTokens || narrow <= 512) {
     hipLaunchKernelGGL((ce_partial_narrow_kernel<0, kKeep, kNarrowBRows>), dim3((unsigned)narrow), dim3(kThreads), 0,
-                       stream, Hc, W, ids, count, c0, cap, cap, row_bytes, vocab, S, part, zy, logits, ld);
+                       stream, Hc, W, ids, count, c0, cap, cap, row_bytes, vocab, S, part, zy, logits);
     return;
   }
   if (cap <= kNarrow128MaxTokens) {
     hipLaunchKernelGGL((ce_partial_narrow_kernel<0, kKeep, kNarrow128MaxTokens>), dim3((unsigned)S), dim3(kThreads), 0,
-                       stream, Hc, W, ids, count, c0, cap, cap, row_bytes, vocab, S, part, zy, logits, ld);
+                       stream, Hc, W, ids, count, c0, cap, cap, row_bytes, vocab, S, part, zy, logits);
     return;
   }
   const dim3 grid((unsigned)ntb * (unsigned)n_slice_groups(cap, vocab));
   // the load schedule's rule as in the logprob's forward
   if (row_bytes / kStepBytes > kNearBMaxSteps)
     hipLaunchKernelGGL((ce_partial_kernel<0, kKeep, true>), grid, dim3(kThreads8), 0, stream, Hc, W, ids, count, c0,
-                       cap, cap, row_bytes, vocab, S, G, part, zy, logits, ld);
+                       cap, cap, row_bytes, vocab, S, G, part, zy, logits);
   else
     hipLaunchKernelGGL((ce_partial_kernel<0, kKeep, false>), grid, dim3(kThreads8), 0, stream, Hc, W, ids, count, c0,
-                       cap, cap, row_bytes, vocab, S, G, part, zy, logits, ld);
+                       cap, cap, row_bytes, vocab, S, G, part, zy, logits);
 }
 
 template <int kDtype>
@@ -1054,29 +1066,30 @@ hipError_t run_cross_entropy(const CeCall& c, hipStream_t stream) {
     const int32_t* y = direct ? c.targets : ids + c0;
     const int32_t* counted = direct ? nullptr : count;
     if constexpr (kDtype == 0) {
-      if (grad) launch_ce_partial<true>(h_rows, w_rows, y, counted, c0, cap, d, vocab, part, zy, z, L.vpad, stream);
-      else launch_ce_partial<false>(h_rows, w_rows, y, counted, c0, cap, d, vocab, part, zy, nullptr, 0, stream);
+      if (grad) launch_ce_partial<true>(h_rows, w_rows, y, counted, c0, cap, d, vocab, part, zy, z, stream);
+      else launch_ce_partial<false>(h_rows, w_rows, y, counted, c0, cap, d, vocab, part, zy, nullptr, stream);
       ITL_CHECK_LAUNCH();
       e = launch_lse_combine(part, zy, cap, 2 * S, lp + c0, lse + c0, stream);
       if (e != hipSuccess) return e;
     } else {
       const int n_vt = (int)ceil_div(vocab, kF32Tile);
       hipLaunchKernelGGL(ce_logits_f32_kernel, dim3((unsigned)(n_vt * ceil_div(cap, kF32Tile))), dim3(kF32Threads), 0, stream,
-                         h_rows, w_rows, counted, c0, cap, d * 4, vocab, n_vt, z, (long long)L.vpad);
-      hipLaunchKernelGGL(ce_lse_f32_kernel, dim3((unsigned)cap), dim3(256), 0, stream, z, (long long)L.vpad, y, counted, c0,
+                         h_rows, w_rows, counted, c0, cap, d * 4, vocab, n_vt, z);
+      hipLaunchKernelGGL(ce_lse_f32_kernel, dim3((unsigned)cap), dim3(256), 0, stream, z, y, counted, c0,
                          cap, vocab, lp + c0, lse + c0);
       ITL_CHECK_LAUNCH();
     }
     if (!grad) continue;
 
     T* Gd = reinterpret_cast<T*>(at(L.gd));
-    const dim3 g_grid((unsigned)ceil_div(L.vpad, 256 * kGradVec), (unsigned)cap);
+    const dim3 g_grid((unsigned)(L.vpad / kBV), (unsigned)ceil_div(cap, 256 * kGradVec / kBV));
+    const int g_rows = L.parts * cap;
     if (exact)
-      hipLaunchKernelGGL((ce_grad_logits_kernel<kDtype, true>), g_grid, dim3(256), 0, stream, z, (long long)L.vpad,
-                         ids + c0, count, c0, cap, L.parts, vocab, L.vpad, lse + c0, gs, Gd);
+      hipLaunchKernelGGL((ce_grad_logits_kernel<kDtype, true>), g_grid, dim3(256), 0, stream, z, ids + c0, count,
+                         c0, cap, L.parts, vocab, g_rows, lse + c0, gs, Gd);
     else
-      hipLaunchKernelGGL((ce_grad_logits_kernel<kDtype, false>), g_grid, dim3(256), 0, stream, z, (long long)L.vpad,
-                         ids + c0, count, c0, cap, L.parts, vocab, L.vpad, lse + c0, gs, Gd);
+      hipLaunchKernelGGL((ce_grad_logits_kernel<kDtype, false>), g_grid, dim3(256), 0, stream, z, ids + c0, count,
+                         c0, cap, L.parts, vocab, g_rows, lse + c0, gs, Gd);
     ITL_CHECK_LAUNCH();
     float* coef = nullptr;
     int32_t* cids = reinterpret_cast<int32_t*>(at(L.cids));
@@ -1095,7 +1108,7 @@ hipError_t run_cross_entropy(const CeCall& c, hipStream_t stream) {
     const int32_t* splits = reinterpret_cast<const int32_t*>(at(L.splits)) + c0 / L.cap;
     hipLaunchKernelGGL(ce_dh_kernel<kDtype>, dim3((unsigned)L.dh_groups), g_block, 0, stream,
                        reinterpret_cast<const char*>(W), reinterpret_cast<const char*>(Gd), vocab, L.vpad, d, count, c0, cap,
-                       L.parts, n_dt, splits, dhp);
+                       L.parts, g_rows, n_dt, splits, dhp);
     ITL_CHECK_LAUNCH();
     hipLaunchKernelGGL(ce_dh_finish_kernel<kDtype>, dim3((unsigned)cap), dim3(256), 0, stream, dhp, splits, cap, L.parts, d, rows,
                        ids + c0, count, c0, gs, coef, W, c.grad_dtype, c.dH);
@@ -1119,13 +1132,13 @@ hipError_t run_cross_entropy(const CeCall& c, hipStream_t stream) {
         if (n <= kFewTokens) {
           const int n_dt2 = (int)ceil_div(d, kFewTile), n_vt2 = (int)ceil_div(vocab, kFewTile);
           hipLaunchKernelGGL((ce_dw_few_kernel<decltype(mode)::value>), dim3((unsigned)(n_vt2 * n_dt2)), dim3(kFewThreads), 0,
-                             stream, reinterpret_cast<const char*>(Gd), Hc, L.vpad, count, c0, cap, L.parts, vocab, d, n_dt2, gs,
+                             stream, reinterpret_cast<const char*>(Gd), Hc, g_rows, count, c0, cap, L.parts, vocab, d, n_dt2, gs,
                              out);
           return;
         }
       }
       hipLaunchKernelGGL((ce_dw_kernel<kDtype, decltype(mode)::value>), dim3((unsigned)dw_groups(n_vt, ceil_div(n_dt, walk))),
-                         g_block, 0, stream, reinterpret_cast<const char*>(Gd), Hc, L.vpad, count, c0, cap, vocab, d, n_vt,
+                         g_block, 0, stream, reinterpret_cast<const char*>(Gd), Hc, g_rows, count, c0, cap, vocab, d, n_vt,
                          n_dt, walk, gs, out);
     };
     if (add) dw(std::integral_constant<int, kDwAdd>{});

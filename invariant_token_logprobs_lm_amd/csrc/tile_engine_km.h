@@ -32,12 +32,29 @@ typedef short shortx4 __attribute__((ext_vector_type(4)));
 // An operand of a tile: `base` its first row k (K-major: at the tile's first
 // column; K-contiguous: row 0 of the tile at the first k), rows or columns
 // past it never read.
+// A K-contiguous operand may lie in blocks of 2^block_shift K steps (rows of one
+// block side by side, block_bytes between blocks; 0: whole rows): base is the
+// tile's first row in block 0 then, and `first` the first step.
 struct KmOperand {
   const char* base;
   uint32_t row_bytes;  // between rows
   int rows;            // K-major: rows k in all; K-contiguous: the tile's rows
   uint32_t skip;       // bytes before base in its row (the range ends with the last row)
+  int block_shift = 0, first = 0;
+  size_t block_bytes = 0;
 };
+
+// Step s of a K-contiguous operand: its buffer range and the offset in a row.
+__device__ __forceinline__ int4v contiguous_rsrc(const KmOperand& o, int s, uint32_t* off) {
+  const uint32_t n = (uint32_t)o.rows * o.row_bytes - o.skip;
+  if (o.block_shift == 0) {
+    *off = (uint32_t)s * kStepBytes;
+    return rsrc_words(o.base, n);
+  }
+  const uint32_t at = (uint32_t)(o.first + s), block = at >> o.block_shift;
+  *off = (at - (block << o.block_shift)) * kStepBytes;
+  return rsrc_words(o.base + block * o.block_bytes, n);
+}
 
 // K-major rows 64 s .. of a K step as a buffer range: rows past the end load
 // zeros.
@@ -110,11 +127,15 @@ __device__ __forceinline__ void run_tiles_km(uint4* smem, const Lanes8& L, const
     a_ks = __builtin_amdgcn_readfirstlane(a_ks);
     a_tile = __builtin_amdgcn_readfirstlane(a_tile);
   };
-  const int4v b_rows = rsrc_words(B.base, kBMajor ? 0u : (uint32_t)B.rows * B.row_bytes - B.skip);
   auto b_load = [&](int s) {
     const uint32_t lds = lds0 + (uint32_t)(kAS + s % kBS) * kSlotBytes + my_rows;
-    if constexpr (kBMajor) load(km_step_rsrc(B, b_ks, 64), bvoff, 0u, lds, b_four);
-    else load(b_rows, bvoff, (uint32_t)b_ks * kStepBytes, lds, true);
+    if constexpr (kBMajor) {
+      load(km_step_rsrc(B, b_ks, 64), bvoff, 0u, lds, b_four);
+    } else {
+      uint32_t off;
+      const int4v r = contiguous_rsrc(B, b_ks, &off);
+      load(r, bvoff, off, lds, true);
+    }
     if (--b_left > 0) b_ks = b_ks + 1 < nks ? b_ks + 1 : 0;
     b_ks = __builtin_amdgcn_readfirstlane(b_ks);
   };
@@ -341,14 +362,12 @@ __device__ __forceinline__ void run_tile_f32(uint4* smem, const KmOperand& A, co
   };
   const uint32_t ao[2] = {offset(0, kAMajor, A.row_bytes), offset(1, kAMajor, A.row_bytes)};
   const uint32_t bo[2] = {offset(0, kBMajor, B.row_bytes), offset(1, kBMajor, B.row_bytes)};
-  const int4v a_rows = rsrc_words(A.base, kAMajor ? 0u : (uint32_t)A.rows * A.row_bytes - A.skip);
-  const int4v b_rows = rsrc_words(B.base, kBMajor ? 0u : (uint32_t)B.rows * B.row_bytes - B.skip);
   auto load = [&](int s) {
     const int st = s < nks ? s : nks - 1;
     const uint32_t slot = (uint32_t)(s % kF32Slots) * kF32SlotBytes + (uint32_t)wave * 2048u;
-    const int4v ar = kAMajor ? km_step_rsrc(A, st, kF32StepK) : a_rows;
-    const int4v br = kBMajor ? km_step_rsrc(B, st, kF32StepK) : b_rows;
-    const uint32_t a_off = kAMajor ? 0u : (uint32_t)st * kStepBytes, b_off = kBMajor ? 0u : (uint32_t)st * kStepBytes;
+    uint32_t a_off = 0u, b_off = 0u;
+    const int4v ar = kAMajor ? km_step_rsrc(A, st, kF32StepK) : contiguous_rsrc(A, st, &a_off);
+    const int4v br = kBMajor ? km_step_rsrc(B, st, kF32StepK) : contiguous_rsrc(B, st, &b_off);
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
       dma16(ar, ao[j], a_off, lds0 + slot + 1024u * j);

@@ -108,12 +108,12 @@ def _plan(itl, tensors):
 def test_adamw_plan_layout(itl):
     P, G = 1 << 20, 1 << 30
     st, nb, el, raw = _plan(itl, [(P, G, 10000, 0, 1, 0.5), (1 << 22, G, 0, 0, 0, 0.0), ((1 << 23) + 2, G, 300, 0, 0, 0.0)])
-    assert st == OK and nb == 4 * 40 and el == 10240 + 512
-    rows = [struct.unpack_from("<QQqiIfi", raw, 40 * i) for i in range(4)]
-    assert [r[:4] for r in rows] == [(P, G, 0, 4096), (P + 8192, G + 16384, 4096, 4096), (P + 16384, G + 32768, 8192, 1808),
-                                     ((1 << 23) + 2, G, 10240, 300)]
-    assert [r[4] for r in rows] == [2 | 4, 2 | 4, 2 | 4, 0]  # fp32 gradients, whole vectors; the last is misaligned
-    assert [r[5] for r in rows] == [0.5, 0.5, 0.5, 0.0]
+    assert st == OK and nb == 6 * 40 and el == 10240 + 512
+    rows = [struct.unpack_from("<QQqiIfi", raw, 40 * i) for i in range(6)]
+    assert [r[:4] for r in rows] == [(P + 4096 * i, G + 8192 * i, 2048 * i, 2048 if i < 4 else 1808) for i in range(5)] + [
+        ((1 << 23) + 2, G, 10240, 300)]
+    assert [r[4] for r in rows] == 5 * [2 | 4] + [0]  # fp32 gradients, whole vectors; the last is misaligned
+    assert [r[5] for r in rows] == 5 * [0.5] + [0.0]
 
 
 def test_adamw_plan_refusals(itl):
