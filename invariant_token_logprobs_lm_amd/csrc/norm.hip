@@ -80,6 +80,7 @@ struct NormArgs {
   long long n_rows, gate_stride;
   int d;
   float scale, eps;
+  bool stream;
 };
 
 // ---- rows in registers
@@ -133,8 +134,9 @@ __device__ __forceinline__ void load_group(const void* row, const Columns<kVec>&
   for (int j = 0; j < 8; ++j) v[j] = g[j];
 }
 
-// Stores group c rounded to the type; v becomes the stored values.
-template <int kDtype, bool kVec>
+// Stores group c rounded to the type; v becomes the stored values. kStream:
+// past the caches (see kStreamBytes).
+template <int kDtype, bool kStream = false, bool kVec>
 __device__ __forceinline__ void store_group(void* row, const Columns<kVec>& k, int c, float (&v)[8]) {
   using E = Elem<kDtype>;
   using T = typename E::T;
@@ -147,13 +149,24 @@ __device__ __forceinline__ void store_group(void* row, const Columns<kVec>& k, i
       v[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
     }
     const int at = k.at(c, 0);
-    if (at < k.d) *reinterpret_cast<uint4*>(static_cast<T*>(row) + at) = make_uint4(w[0], w[1], w[2], w[3]);
+    int4v* out = reinterpret_cast<int4v*>(static_cast<T*>(row) + at);
+    const int4v o = {(int)w[0], (int)w[1], (int)w[2], (int)w[3]};
+    if (at < k.d) {
+      if constexpr (kStream) __builtin_nontemporal_store(o, out);
+      else *out = o;
+    }
   } else if constexpr (kVec) {
     const int at = k.at(c, 0);
     if (at < k.d) {
-      float4* o = reinterpret_cast<float4*>(static_cast<float*>(row) + at);
-      o[0] = make_float4(v[0], v[1], v[2], v[3]);
-      o[1] = make_float4(v[4], v[5], v[6], v[7]);
+      floatx4* o = reinterpret_cast<floatx4*>(static_cast<float*>(row) + at);
+      const floatx4 lo = {v[0], v[1], v[2], v[3]}, hi = {v[4], v[5], v[6], v[7]};
+      if constexpr (kStream) {
+        __builtin_nontemporal_store(lo, o);
+        __builtin_nontemporal_store(hi, o + 1);
+      } else {
+        o[0] = lo;
+        o[1] = hi;
+      }
     }
   } else {
 #pragma unroll
@@ -167,7 +180,7 @@ __device__ __forceinline__ void store_group(void* row, const Columns<kVec>& k, i
 }
 
 // One row per kWaves wavefronts, kGroups groups of 8 values per thread.
-template <int kDtype, bool kFp8, bool kVec, int kWaves, int kGroups>
+template <int kDtype, bool kFp8, bool kVec, bool kStream, int kWaves, int kGroups>
 __global__ __launch_bounds__(kNormThreads) void norm_held_kernel(NormArgs a) {
   using T = typename Elem<kDtype>::T;
   __shared__ float lds[kWaves];
@@ -212,7 +225,7 @@ __global__ __launch_bounds__(kNormThreads) void norm_held_kernel(NormArgs a) {
     for (int c = 0; c < kGroups; ++c) {
 #pragma unroll
       for (int j = 0; j < 8; ++j) x[c][j] += a.scale * y[c][j];
-      store_group<kDtype>(static_cast<T*>(a.h) + base, k, c, x[c]);
+      store_group<kDtype, kStream>(static_cast<T*>(a.h) + base, k, c, x[c]);
     }
   }
   float ss = 0.0f;
@@ -228,7 +241,7 @@ __global__ __launch_bounds__(kNormThreads) void norm_held_kernel(NormArgs a) {
     load_group<kDtype>(a.w_pre, k, c, w);
 #pragma unroll
     for (int j = 0; j < 8; ++j) x[c][j] = x[c][j] * r_pre * w[j];
-    if constexpr (!kFp8) store_group<kDtype>(static_cast<T*>(a.u) + base, k, c, x[c]);
+    if constexpr (!kFp8) store_group<kDtype, kStream>(static_cast<T*>(a.u) + base, k, c, x[c]);
   }
   if constexpr (kFp8) {
     float amax = 0.0f;
@@ -579,6 +592,13 @@ __global__ __launch_bounds__(64 * kFinishWaves) void norm_backward_finish_kernel
   out[k] = s;
 }
 
+// Two results of more bytes than this together are stored past the caches: the
+// next reader would not find them there (the Infinity Cache holds 256 MiB),
+// and the operands still to come keep their place (16384 x 2560 bf16: 71 -> 64
+// us; 4096 x 7168 the same either way, and a decode step's rows stay cached).
+// The backward's gradients are not (137 us either way, 141 so).
+constexpr long long kStreamBytes = 128LL << 20;
+
 constexpr int kWaveWidth = 4096;      // widest row of one wavefront
 constexpr int kNormMaxWidth = 16384;  // widest row held in registers
 constexpr int kBwdMaxWidth = 8192;    // the same of the backward
@@ -605,18 +625,21 @@ template <int kDtype, bool kFp8, bool kVec>
 void run_norm(const NormArgs& a, hipStream_t stream) {
   const dim3 block(kNormThreads), one((unsigned)ceil_div(a.n_rows, kNormThreads / 64)), four((unsigned)a.n_rows);
   const int groups = (int)ceil_div(a.d, 8);
-#define ITL_NORM(waves, n, grid) \
-  hipLaunchKernelGGL((norm_held_kernel<kDtype, kFp8, kVec, waves, n>), grid, block, 0, stream, a)
+#define ITL_NORM(waves, n, grid)                                                                            \
+  if (kVec && !kFp8 && a.stream)                                                                            \
+    hipLaunchKernelGGL((norm_held_kernel<kDtype, kFp8, kVec, kVec && !kFp8, waves, n>), grid, block, 0, stream, a); \
+  else                                                                                                      \
+    hipLaunchKernelGGL((norm_held_kernel<kDtype, kFp8, kVec, false, waves, n>), grid, block, 0, stream, a)
   if (a.d <= kWaveWidth) {
-    if (groups <= 64) ITL_NORM(1, 1, one);
-    else if (groups <= 128) ITL_NORM(1, 2, one);
-    else if (groups <= 256) ITL_NORM(1, 4, one);
-    else if (groups <= 320) ITL_NORM(1, 5, one);
-    else ITL_NORM(1, 8, one);
+    if (groups <= 64) { ITL_NORM(1, 1, one); }
+    else if (groups <= 128) { ITL_NORM(1, 2, one); }
+    else if (groups <= 256) { ITL_NORM(1, 4, one); }
+    else if (groups <= 320) { ITL_NORM(1, 5, one); }
+    else { ITL_NORM(1, 8, one); }
   } else if (a.d <= kNormMaxWidth) {
-    if (groups <= 768) ITL_NORM(4, 3, four);
-    else if (groups <= 1024) ITL_NORM(4, 4, four);
-    else ITL_NORM(4, 8, four);
+    if (groups <= 768) { ITL_NORM(4, 3, four); }
+    else if (groups <= 1024) { ITL_NORM(4, 4, four); }
+    else { ITL_NORM(4, 8, four); }
   } else {
     hipLaunchKernelGGL((norm_rows_kernel<kDtype, kFp8>), four, block, 0, stream, a);
   }
@@ -633,7 +656,8 @@ hipError_t launch_residual_norm(const void* x, const void* y, const void* gate, 
                                 const void* w_post, const void* w_pre, int dtype, long long n_rows, int d, float scale,
                                 float eps, void* h, void* u, uint8_t* codes, float* u_scale, float* rstd_pre,
                                 float* rstd_post, hipStream_t stream) {
-  const NormArgs a{x, y, gate, w_post, w_pre, h, u, codes, u_scale, rstd_pre, rstd_post, n_rows, gate_stride, d, scale, eps};
+  const NormArgs a{x, y, gate, w_post, w_pre, h, u, codes, u_scale, rstd_pre, rstd_post, n_rows, gate_stride, d, scale, eps,
+                   2 * n_rows * d * (dtype == 0 ? 2 : 4) > kStreamBytes};
   if (codes) {
     if (dtype == 0) run_norm<0, true, true>(a, stream);
     else run_norm<1, true, true>(a, stream);

@@ -150,6 +150,20 @@ def test_rows_do_not_depend_on_the_batch(cuda, d):
         assert torch.equal(dx1, dx[i]) and torch.equal(dy1, dy[i])
 
 
+@pytest.mark.parametrize("dtype,d", [(torch.bfloat16, 4096), (torch.float32, 2048), (torch.bfloat16, 8192)])
+def test_rows_of_a_large_call(cuda, dtype, d):
+    """Results past the caches' size take another store: the same bits as the rows alone."""
+    itl = _itl()
+    n = (80 << 20) // (d * (2 if dtype == torch.bfloat16 else 4))
+    x = torch.randn(n, d, device=cuda).to(dtype)
+    y = torch.randn(n, d, device=cuda).to(dtype)
+    w = torch.randn(d, device=cuda).to(dtype)
+    h, u, r, _ = itl.residual_norm(x, y, w)
+    for i in (slice(0, 3), slice(n // 2, n // 2 + 50), slice(n - 1, n)):
+        h1, u1, r1, _ = itl.residual_norm(x[i], y[i], w)
+        assert torch.equal(h1, h[i]) and torch.equal(u1, u[i]) and same_bits(r1, r[i])
+
+
 @pytest.mark.parametrize("n,d", [(700, 2560), (64, 1001), (5000, 96), (257, 9000)])
 def test_column_sums_are_deterministic(cuda, n, d):
     itl = _itl()
