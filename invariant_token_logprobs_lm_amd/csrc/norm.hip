@@ -149,23 +149,23 @@ __device__ __forceinline__ void store_group(void* row, const Columns<kVec>& k, i
       v[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
     }
     const int at = k.at(c, 0);
-    int4v* out = reinterpret_cast<int4v*>(static_cast<T*>(row) + at);
-    const int4v o = {(int)w[0], (int)w[1], (int)w[2], (int)w[3]};
-    if (at < k.d) {
-      if constexpr (kStream) __builtin_nontemporal_store(o, out);
-      else *out = o;
+    if constexpr (kStream) {
+      const int4v o = {(int)w[0], (int)w[1], (int)w[2], (int)w[3]};
+      if (at < k.d) __builtin_nontemporal_store(o, reinterpret_cast<int4v*>(static_cast<T*>(row) + at));
+    } else {
+      if (at < k.d) *reinterpret_cast<uint4*>(static_cast<T*>(row) + at) = make_uint4(w[0], w[1], w[2], w[3]);
     }
   } else if constexpr (kVec) {
     const int at = k.at(c, 0);
     if (at < k.d) {
-      floatx4* o = reinterpret_cast<floatx4*>(static_cast<float*>(row) + at);
-      const floatx4 lo = {v[0], v[1], v[2], v[3]}, hi = {v[4], v[5], v[6], v[7]};
       if constexpr (kStream) {
-        __builtin_nontemporal_store(lo, o);
-        __builtin_nontemporal_store(hi, o + 1);
+        floatx4* o = reinterpret_cast<floatx4*>(static_cast<float*>(row) + at);
+        __builtin_nontemporal_store(floatx4{v[0], v[1], v[2], v[3]}, o);
+        __builtin_nontemporal_store(floatx4{v[4], v[5], v[6], v[7]}, o + 1);
       } else {
-        o[0] = lo;
-        o[1] = hi;
+        float4* o = reinterpret_cast<float4*>(static_cast<float*>(row) + at);
+        o[0] = make_float4(v[0], v[1], v[2], v[3]);
+        o[1] = make_float4(v[4], v[5], v[6], v[7]);
       }
     }
   } else {
