@@ -27,8 +27,14 @@
 //   4. dW += G^T H, K = the chunk's tokens.
 // 3 and 4 read W, G and H as they lie (tile_engine_km.h): no transposed copy.
 // That is three contractions, the least there is (keeping the logits saves
-// the fourth: a chunk's 12 bytes of traffic per logit cost less than a
+// the fourth: the 8 bytes written and read per logit of z cost less than a
 // contraction of 2 d operations each for d > about 1000, the widths here).
+//
+// Bound by the matrix cores for many tokens: 3072 of 4096 tokens, d = 2560, V
+// = 151936, bf16 take 6.5 ms (forward 2.05, dH 1.88, dW 2.08: 1.15 to 1.27
+// PFLOP/s; G from z 0.52 at 5.4 TB/s), 2188 of 2500, d = 7168, V = 129280 11.3
+// ms. Bound by reading W for few: the loss of 64 tokens, d = 1536, V = 151936
+// takes 109 us, 99 of them W at 4.7 TB/s.
 //
 // Every sum has a fixed order and there are no atomics: token losses depend
 // on the token alone, the loss and the gradients are run-to-run

@@ -32,6 +32,11 @@
 // the column sums (dw_pre, dw_post, a shared dgate) of its columns over all
 // rows of its workgroup in registers; the workgroups' sums are then added in
 // order: run-to-run deterministic, no atomics.
+//
+// Bound by memory: 16384 x 2560 bf16 with a post norm and a gate 64 to 71 us
+// forward (336 MB, 4.7 to 5.2 TB/s), 137 to 150 us backward (fp32 du; 590 MB,
+// 3.9 to 4.3 TB/s); 4096 x 7168 to E4M3 rows 39 to 44 us. One decode token
+// takes 4.2 us, launch and latency.
 
 #include <algorithm>
 
@@ -596,7 +601,7 @@ __global__ __launch_bounds__(64 * kFinishWaves) void norm_backward_finish_kernel
 // next reader would not find them there (the Infinity Cache holds 256 MiB),
 // and the operands still to come keep their place (16384 x 2560 bf16: 71 -> 64
 // us; 4096 x 7168 the same either way, and a decode step's rows stay cached).
-// The backward's gradients are not (137 us either way, 141 so).
+// The backward's gradients are not: 137 us with plain stores, 141 past them.
 constexpr long long kStreamBytes = 128LL << 20;
 
 constexpr int kWaveWidth = 4096;      // widest row of one wavefront
