@@ -449,8 +449,8 @@ size_t itl_adamw_step_workspace_bytes(void);
  * state_bits 32: exp_avg, exp_avg_sq fp32 [state_elements]. 8: uint8
  * [state_elements] holding E4M3 codes of m and of sqrt(v), with
  * exp_avg_scale, exp_avg_sq_scale fp32 [state_elements / 256], amax / 448 of
- * each 256 elements (1 for zeros); codes to nearest even, a root that is not
- * zero at least the smallest code. States start as zeros (codes and scales
+ * each 256 elements, at least 2^-126 (1 for zeros); codes to nearest even, a
+ * root that is not zero at least the smallest code. States start as zeros (codes and scales
  * too). Elements between the tensors' states are not used (in 32 bits not
  * touched; in 8 bits written as zeros up to the next multiple of 8).
  * master (nullable) fp32 [state_elements]: the weights of bf16 tensors, which

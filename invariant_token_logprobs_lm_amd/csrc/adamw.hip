@@ -10,7 +10,8 @@
 // fp32 on its own (nothing is fused), t and the powers are fp64.
 //
 // 8-bit states: m and sqrt(v) as E4M3 codes with an fp32 scale per 256
-// elements (the largest at 448; 1 for an all-zero block), to nearest even.
+// elements (the largest at 448, the scale no less than 2^-126; 1 for an
+// all-zero block), to nearest even.
 // The root is stored rather than v because its dynamic range is half of v's
 // in the exponent: the codes then hold v down to 2^-36 of a block's largest.
 // A root that is not zero never gets code 0 (the smallest code instead): a
@@ -232,7 +233,7 @@ __global__ __launch_bounds__(kAdamThreads) void adamw_update_kernel(AdamArgs a) 
       }
     } else {
       const float ma = block_amax(m), ra = block_amax(r);
-      const float ms = ma > 0.0f ? ma / 448.0f : 1.0f, vs = ra > 0.0f ? ra / 448.0f : 1.0f;
+      const float ms = e4m3_scale(ma), vs = e4m3_scale(ra);
       float q[8], o[8];
 #pragma unroll
       for (int j = 0; j < 8; ++j) {

@@ -38,6 +38,13 @@ __device__ __forceinline__ uint32_t e4m3_code(float x) {
   return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(x, x, 0, false) & 0xffu;
 }
 
+// Scale of values of at most amax: amax / 448, but no smaller than the least
+// normal number. A subnormal scale has few bits left or is 0, and quotients by
+// it pass the format's range or are 0 / 0: codes of NaN.
+__device__ __forceinline__ float e4m3_scale(float amax) {
+  return amax > 0.0f ? fmaxf(__fdiv_rn(amax, 448.0f), 0x1p-126f) : 1.0f;
+}
+
 // Four codes, the first in the low byte.
 __device__ __forceinline__ uint32_t e4m3_code4(float a, float b, float c, float d) {
   int w = __builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false);

@@ -260,3 +260,25 @@ def test_refusals(cuda):
     for error, call in bad:
         with pytest.raises(error):
             call()
+
+
+def test_eight_bit_states_fade_away(cuda):
+    """Gradients that stay zero: m shrinks by beta1 a step until a block's
+    amax / 448 would leave fp32's normal range (2^-126); codes, scales and
+    weights stay finite, and what never had a gradient never moves."""
+    itl = _itl()
+    g = torch.Generator().manual_seed(31)
+    p = torch.randn(600, generator=g).to(cuda)
+    grad = (torch.randn(600, generator=g) * 1e-3).to(cuda)
+    grad[::2] = 0.0
+    start = p.clone()
+    plan = itl.adamw_plan([p], [grad], lr=1e-3, state_bits=8)
+    itl.adamw_step(plan)
+    grad.zero_()
+    for _ in range(1100):  # 0.9^1100 = 5e-51, below fp32's smallest number
+        itl.adamw_step(plan)
+    assert bool(p.isfinite().all())
+    assert same_bits(p[::2].contiguous(), start[::2].contiguous())
+    for codes, scale in ((plan.exp_avg, plan.exp_avg_scale), (plan.exp_avg_sq, plan.exp_avg_sq_scale)):
+        assert not bool(((codes & 0x7F) == 0x7F).any())
+        assert bool((scale >= 2.0 ** -126).all())
