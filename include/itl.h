@@ -329,7 +329,8 @@ itl_status itl_residual_norm(const void* x, const void* y, const void* gate, int
                              void* h, void* u, float* rstd_pre, float* rstd_post, void* stream);
 
 /* The same with u as the FP8 head takes it [FP8]: E4M3 codes Uq [n_rows, d]
- * (8-byte aligned) with u_scale [n_rows] = amax_row / 448 (1 for a zero row),
+ * (8-byte aligned) with u_scale [n_rows] = amax_row / 448, at least 2^-126
+ * (1 for a zero row),
  * codes of u / u_scale (fp32 division, to nearest even) straight from the fp32
  * u: one rounding. d a multiple of 128 (ITL_ERR_UNSUPPORTED otherwise); the
  * rows must be finite. */

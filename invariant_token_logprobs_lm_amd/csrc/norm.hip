@@ -8,8 +8,8 @@
 // u is taken from the kept (rounded) h, so the fused call gives the bits of
 // a call that norms a stored h. All arithmetic between loads and stores is
 // fp32; h and u are rounded once each, to nearest even. The FP8 form writes
-// u as E4M3 codes with a scale per row, amax / 448, straight from the fp32
-// u (one rounding, not two).
+// u as E4M3 codes with a scale per row, amax / 448 (no less than 2^-126),
+// straight from the fp32 u (one rounding, not two).
 //
 // Backward, with n = h r_pre, q = y r_post and a row mean <.>:
 //   dn = du w_pre,  dx = dh + r_pre (dn - n <dn n>)
@@ -255,7 +255,7 @@ __global__ __launch_bounds__(kNormThreads) void norm_held_kernel(NormArgs a) {
 #pragma unroll
       for (int j = 0; j < 8; ++j) amax = fmaxf(amax, fabsf(x[c][j]));
     amax = block_max<kWaves>(amax, lds);
-    const float s = amax > 0.0f ? __fdiv_rn(amax, 448.0f) : 1.0f;
+    const float s = e4m3_scale(amax);
     if (k.lane == 0) a.u_scale[row] = s;
 #pragma unroll
     for (int c = 0; c < kGroups; ++c) {
@@ -322,7 +322,7 @@ __global__ __launch_bounds__(kNormThreads) void norm_rows_kernel(NormArgs a) {
     float amax = 0.0f;
     for (int k = threadIdx.x; k < d; k += kNormThreads) amax = fmaxf(amax, fabsf(E::to_f(hr[k]) * r_pre * E::to_f(w_pre[k])));
     amax = block_max<kW>(amax, lds);
-    const float s = amax > 0.0f ? __fdiv_rn(amax, 448.0f) : 1.0f;
+    const float s = e4m3_scale(amax);
     if (threadIdx.x == 0) a.u_scale[row] = s;
     for (int k = threadIdx.x; k < d; k += kNormThreads)
       a.codes[base + k] = (uint8_t)e4m3_code(__fdiv_rn(E::to_f(hr[k]) * r_pre * E::to_f(w_pre[k]), s));

@@ -270,3 +270,23 @@ def test_side_stream_and_replay(cuda, d):
             assert torch.equal(a, b)
         step()
         torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("d", [256, 7168, 16512])
+def test_fp8_rows_that_nearly_vanish(cuda, d):
+    """Rows whose amax / 448 would leave fp32's normal range: the scale is at
+    least 2^-126. A code is off by half a step of E4M3, 2^-4 of its value or
+    2^-10 of the scale; u by a few roundings (2^-20 of it, 2^-148 below the
+    normal range)."""
+    itl = _itl()
+    g = torch.Generator().manual_seed(5)
+    x = torch.randn(12, d, generator=g).to(cuda)
+    for e in (-110, -122, -128, -134, -140, -149):
+        w = torch.full((d,), 2.0 ** e, dtype=torch.float64).to(torch.float32).to(cuda)
+        w[::3] = 0.0
+        h, q, s, r, _ = itl.residual_norm_fp8(x, None, w)
+        assert bool((s >= 2.0 ** -126).all()), e
+        got = q.view(torch.float8_e4m3fn).double() * s.double()[:, None]
+        u = x.double() * r.double()[:, None] * w.double()
+        tol = u.abs() * (2.0 ** -4 + 2.0 ** -20) + s.double()[:, None] * 2.0 ** -10 + 2.0 ** -148
+        assert bool(((got - u).abs() <= tol).all()), e
