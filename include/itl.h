@@ -320,7 +320,8 @@ itl_status itl_lmhead_logprob_mxfp4(const uint8_t* Hq, const float* h_scale,
  * `dtype` (ITL_BF16 or ITL_F32), any d in [1, 2^24]; 16-byte aligned where d
  * is a multiple of 8, else aligned to their elements (ITL_ERR_INVALID_ARG
  * otherwise). rstd_pre, rstd_post (nullable) fp32 [n_rows]: r_pre, r_post, for
- * the backward. h may be x. eps in (0, 1).
+ * the backward. h may be x; other outputs that share memory with inputs or
+ * each other are refused (ITL_ERR_INVALID_ARG). eps in (0, 1).
  * A row's results depend on the row, d and dtype alone, as everything of this
  * library's forward [BC]. */
 itl_status itl_residual_norm(const void* x, const void* y, const void* gate, int64_t gate_stride,
@@ -354,7 +355,8 @@ size_t itl_residual_norm_backward_workspace_bytes(int64_t n_rows, int64_t d);
  *   dy = r_post (dp w_post - q <dp w_post q>)         (w_post NULL: dy = dp)
  * dx is the whole gradient of h and so of x. dx, dy of dtype; dw_pre, dw_post
  * fp32 [d]; dgate fp32 [d] for gate_stride 0, else [n_rows, d] of dtype.
- * dy, dgate, dw_post only where y, gate, w_post are given. dx may be dh.
+ * dy, dgate, dw_post only where y, gate, w_post are given. dx may be dh; other
+ * outputs that share memory with inputs or each other are refused.
  * n_rows == 0: the sums are zeros. Row results depend on the row alone; the
  * column sums are run-to-run deterministic. workspace 256-byte aligned. */
 itl_status itl_residual_norm_backward(const void* du, itl_dtype du_dtype, const void* dh, const void* h,
@@ -389,7 +391,9 @@ size_t itl_cross_entropy_workspace_bytes(int64_t n_tok, int64_t d, int64_t vocab
  * loss fp32 [1], token_loss, lse (nullable) fp32 [n_tok]. The losses are summed
  * in fp64 in a fixed order. A token's loss does not depend on its batch-mates
  * (bf16 heads: its z and lse have itl_lmhead_logprob's bits). fp32 heads with a
- * vocab above about 2.1e6 return ITL_ERR_UNSUPPORTED. */
+ * vocab above about 2.1e6 return ITL_ERR_UNSUPPORTED. Outputs that share memory
+ * with inputs or each other are refused (ITL_ERR_INVALID_ARG), with the
+ * gradient too. */
 itl_status itl_cross_entropy(const void* H, const void* W, itl_dtype dtype,
                              int64_t n_tok, int64_t d, int64_t vocab, const int32_t* targets,
                              float label_smoothing, float z_weight, int32_t reduction,
@@ -433,7 +437,8 @@ itl_status itl_adamw_plan_sizes(const itl_adamw_tensor* tensors, int32_t n_tenso
  * aligned) and passes that copy to every step as long as the tensors stay
  * where they are. The tensors may have any mix of dtypes and any element
  * alignment (16-byte aligned ones are moved in whole vectors); two of them
- * that share weights are refused (ITL_ERR_INVALID_ARG). */
+ * that share weights, and gradients that share memory with weights, are
+ * refused (ITL_ERR_INVALID_ARG). */
 itl_status itl_adamw_plan(const itl_adamw_tensor* tensors, int32_t n_tensors,
                           void* host_plan, size_t host_plan_bytes);
 

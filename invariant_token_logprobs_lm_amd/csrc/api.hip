@@ -371,6 +371,29 @@ constexpr int64_t kMaxNormWidth = 1 << 24;
 
 bool known_dtype(itl_dtype dt) { return dt == ITL_BF16 || dt == ITL_F32; }
 
+// Arrays of a call by their bytes; a null or empty one shares nothing.
+struct Span {
+  const void* p;
+  int64_t bytes;
+};
+
+bool shares(const Span& a, const Span& b) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
+  return a.p && b.p && a.bytes > 0 && b.bytes > 0 && x < y + (uintptr_t)b.bytes && y < x + (uintptr_t)a.bytes;
+}
+
+// Whether an output shares memory with an input or another output: other
+// workgroups may still read what one has written.
+bool outputs_share(std::initializer_list<Span> outs, std::initializer_list<Span> ins) {
+  for (auto o = outs.begin(); o != outs.end(); ++o) {
+    for (const Span& i : ins)
+      if (shares(*o, i)) return true;
+    for (auto p = outs.begin(); p != o; ++p)
+      if (shares(*o, *p)) return true;
+  }
+  return false;
+}
+
 // Rows the norms move in 16-byte pieces (widths of a multiple of 8) have to
 // start at one; other widths are read value by value.
 bool rows_misaligned(std::initializer_list<const void*> ps, int64_t d, itl_dtype dtype) {
@@ -405,6 +428,15 @@ itl_status residual_norm(const void* x, const void* y, const void* gate, int64_t
   if (rows_misaligned({x, y, gate, w_post, w_pre, y ? h : nullptr, u}, d, dtype))
     return fail(ITL_ERR_INVALID_ARG, "arrays must be 16-byte aligned where d is a multiple of 8, else by element");
   if (fp8 && (reinterpret_cast<uintptr_t>(codes) & 7) != 0) return fail(ITL_ERR_INVALID_ARG, "Uq must be 8-byte aligned");
+  const int64_t row_bytes = d * elem_size(dtype), all = n_rows * row_bytes, one = n_rows * 4;
+  // (h may be x, row for row)
+  if (outputs_share({{u, all}, {codes, n_rows * d}, {u_scale, one}, {rstd_pre, one}, {w_post ? rstd_post : nullptr, one},
+                     {y ? h : nullptr, all}},
+                    {{h == x ? nullptr : x, all}, {y, all}, {gate, gate_stride ? all : row_bytes}, {w_post, row_bytes},
+                     {w_pre, row_bytes}}) ||
+      (h == x && outputs_share({{u, all}, {codes, n_rows * d}, {u_scale, one}, {rstd_pre, one},
+                                {w_post ? rstd_post : nullptr, one}}, {{x, all}})))
+    return fail(ITL_ERR_INVALID_ARG, "outputs share memory with inputs or each other (only h may be x)");
   hipError_t e = itl::launch_residual_norm(x, y, gate, gate_stride, w_post, w_pre, (int)dtype, n_rows, (int)d, scale, eps,
                                            h, u, codes, u_scale, rstd_pre, rstd_post, static_cast<hipStream_t>(stream));
   return e == hipSuccess ? ITL_OK : hip_fail(e, name);
@@ -453,6 +485,15 @@ itl_status itl_residual_norm_backward(const void* du, itl_dtype du_dtype, const 
   if (!workspace || workspace_bytes < itl::norm_backward_workspace_bytes(n_rows, d))
     return fail(ITL_ERR_WORKSPACE, "workspace missing or smaller than itl_residual_norm_backward_workspace_bytes()");
   if (misaligned(workspace)) return fail(ITL_ERR_WORKSPACE, "workspace must be 256-byte aligned");
+  const int64_t row_bytes = d * elem_size(dtype), all = n_rows * row_bytes;
+  // (dx may be dh, row for row)
+  if (outputs_share({{dx, all}, {y ? dy : nullptr, all}, {gate ? dgate : nullptr, gate_stride ? all : d * 4},
+                     {dw_pre, d * 4}, {w_post ? dw_post : nullptr, d * 4},
+                     {workspace, (int64_t)itl::norm_backward_workspace_bytes(n_rows, d)}},
+                    {{du, n_rows * d * elem_size(du_dtype)}, {dh == dx ? nullptr : dh, all}, {h, all}, {y, all},
+                     {gate, gate_stride ? all : row_bytes}, {w_post, row_bytes}, {w_pre, row_bytes},
+                     {rstd_pre, n_rows * 4}, {w_post ? rstd_post : nullptr, n_rows * 4}}))
+    return fail(ITL_ERR_INVALID_ARG, "outputs share memory with inputs or each other (only dx may be dh)");
   hipError_t e = itl::launch_residual_norm_backward(du, (int)du_dtype, dh, h, y, gate, gate_stride, w_post, w_pre,
                                                     rstd_pre, rstd_post, (int)dtype, n_rows, (int)d, scale, dx, dy, dgate,
                                                     dw_pre, dw_post, workspace, static_cast<hipStream_t>(stream));
@@ -482,6 +523,11 @@ itl_status cross_entropy(const itl::CeCall& c, bool grad, size_t workspace_bytes
   if (need > 0 && (!c.workspace || workspace_bytes < need))
     return fail(ITL_ERR_WORKSPACE, "workspace missing or smaller than itl_cross_entropy_workspace_bytes()");
   if (need > 0 && misaligned(c.workspace)) return fail(ITL_ERR_WORKSPACE, "workspace must be 256-byte aligned");
+  const int64_t es = elem_size((itl_dtype)c.dtype), gs = elem_size((itl_dtype)c.grad_dtype);
+  if (outputs_share({{c.loss, 4}, {c.token_loss, c.n_tok * 4}, {c.lse, c.n_tok * 4}, {c.dH, c.n_tok * c.d * gs},
+                     {c.dW, c.vocab * c.d * gs}, {c.workspace, (int64_t)need}},
+                    {{c.H, c.n_tok * c.d * es}, {c.W, c.vocab * c.d * es}, {c.targets, c.n_tok * 4}}))
+    return fail(ITL_ERR_INVALID_ARG, "outputs share memory with inputs or each other");
   hipError_t e = itl::launch_cross_entropy(c, static_cast<hipStream_t>(stream));
   return e == hipSuccess ? ITL_OK : hip_fail(e, name);
 }
@@ -562,7 +608,8 @@ itl_status itl_adamw_plan(const itl_adamw_tensor* tensors, int32_t n_tensors, vo
   if (pieces == 0) return ITL_OK;
   if (!host_plan || host_plan_bytes < (size_t)pieces * sizeof(itl::AdamPiece))
     return fail(ITL_ERR_WORKSPACE, "host_plan missing or smaller than itl_adamw_plan_sizes() says");
-  // two entries that share weights would be written by two workgroups at once
+  // two entries that share weights would be written by two workgroups at
+  // once, and gradients among the weights read after they are written
   try {
     std::vector<std::pair<uintptr_t, uintptr_t>> spans;
     for (int32_t i = 0; i < n_tensors; ++i)
@@ -573,6 +620,15 @@ itl_status itl_adamw_plan(const itl_adamw_tensor* tensors, int32_t n_tensors, vo
     std::sort(spans.begin(), spans.end());
     for (size_t i = 1; i < spans.size(); ++i)
       if (spans[i].first < spans[i - 1].second) return fail(ITL_ERR_INVALID_ARG, "two tensors share weights");
+    for (int32_t i = 0; i < n_tensors; ++i) {
+      if (tensors[i].n == 0) continue;
+      const uintptr_t g = reinterpret_cast<uintptr_t>(tensors[i].grad);
+      const uintptr_t end = g + (uintptr_t)tensors[i].n * elem_size(tensors[i].grad_dtype);
+      // the last weights that begin before the gradient's end
+      auto s = std::lower_bound(spans.begin(), spans.end(), std::make_pair(end, (uintptr_t)0));
+      if (s != spans.begin() && (--s)->second > g)
+        return fail(ITL_ERR_INVALID_ARG, "a gradient and weights share memory");
+    }
   } catch (const std::bad_alloc&) {
     return fail(ITL_ERR_INVALID_ARG, "out of host memory");
   }

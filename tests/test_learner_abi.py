@@ -93,6 +93,57 @@ def test_cross_entropy_arguments(itl):
     assert 16384 * 50000 * 4 < one < ten < one + 163840 * 64 + 50000 * 128 * 4 + (1 << 20)
 
 
+def _refused_as_shared(itl, status):
+    return status == INVALID and "share" in itl.lib.itl_last_error().decode()
+
+
+def test_shared_memory_is_refused(itl):
+    """Outputs over inputs or other outputs (but h over x, dx over dh, row for row)."""
+    MB = 1 << 20
+
+    def norm(**over):
+        a = dict(x=1, y=2, gate=3, w_post=4, w_pre=5, h=6, u=7, r=8, rp=9)
+        at = {k: over.get(k, n * MB) for k, n in a.items()}
+        return itl.lib.itl_residual_norm(v(at["x"]), v(at["y"]), v(at["gate"]), 64, v(at["w_post"]), v(at["w_pre"]), 0, 4, 64,
+                                         1.0, 1e-6, v(at["h"]), v(at["u"]), v(at["r"]), v(at["rp"]), None)
+
+    for over in (dict(u=MB), dict(u=2 * MB), dict(u=6 * MB), dict(u=3 * MB + 496), dict(u=5 * MB), dict(h=2 * MB),
+                 dict(h=MB + 16), dict(r=7 * MB), dict(rp=8 * MB + 12), dict(h=MB, u=MB), dict(h=MB, x=MB, y=MB)):
+        assert _refused_as_shared(itl, norm(**over)), over
+
+    def backward(d=64, **over):
+        names = ("du", "dh", "h", "y", "gate", "w_post", "w_pre", "r", "rp", "dx", "dy", "dgate", "dw_pre", "dw_post", "ws")
+        p = {k: v(over.get(k, (16 + n) * 16 * MB)) for n, k in enumerate(names)}
+        return itl.lib.itl_residual_norm_backward(p["du"], 0, p["dh"], p["h"], p["y"], p["gate"], d, p["w_post"], p["w_pre"],
+                                                  p["r"], p["rp"], 0, 4, d, 1.0, p["dx"], p["dy"], p["dgate"], p["dw_pre"],
+                                                  p["dw_post"], p["ws"], 1 << 30, None)
+
+    at = lambda n: (16 + n) * 16 * MB
+    for d in (64, 16384):
+        for over in (dict(dx=at(0)), dict(dx=at(2)), dict(dx=at(3)), dict(dy=at(1)), dict(dy=at(3)), dict(dy=at(9)),
+                     dict(dx=at(1) + 16), dict(dgate=at(4)), dict(dw_pre=at(6)), dict(dw_post=at(12)), dict(ws=at(0)),
+                     dict(dx=at(1), dy=at(1))):
+            assert _refused_as_shared(itl, backward(d, **over)), (d, over)
+
+    def entropy(**over):
+        names = ("H", "W", "y", "loss", "tok", "lse", "dH", "dW", "ws")
+        p = {k: v(over.get(k, (n + 1) * 16 * MB)) for n, k in enumerate(names)}
+        return itl.lib.itl_cross_entropy_grad(p["H"], p["W"], 0, 4, 64, 300, p["y"], 0.0, 0.0, 1, 1.0, 0, p["loss"], p["tok"],
+                                              p["lse"], p["dH"], p["dW"], p["ws"], 1 << 40, None)
+
+    at = lambda n: (n + 1) * 16 * MB
+    for over in (dict(dH=at(0)), dict(dW=at(1)), dict(dW=at(6)), dict(tok=at(2)), dict(lse=at(4)), dict(loss=at(4) + 12),
+                 dict(dH=at(1) + 256), dict(ws=at(0))):
+        assert _refused_as_shared(itl, entropy(**over)), over
+
+    P, G = 1 << 20, 1 << 30
+    for g in (P, P + 198, P - 2, (1 << 22) + 64):
+        st = _plan(itl, [(P, G, 100, 0, 0, 0.0), (1 << 22, g, 100, 0, 0, 0.0)])[0]
+        assert _refused_as_shared(itl, st), g
+    for g in (P + 200, P - 200, (1 << 22) - 200):
+        assert _plan(itl, [(P, G, 100, 0, 0, 0.0), (1 << 22, g, 100, 0, 0, 0.0)])[0] == OK
+
+
 def _plan(itl, tensors):
     T = itl._AdamWTensor
     table = (T * max(1, len(tensors)))(*[T(*t) for t in tensors])
