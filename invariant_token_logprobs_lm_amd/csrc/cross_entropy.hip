@@ -30,10 +30,10 @@
 // the fourth: the 8 bytes written and read per logit of z cost less than a
 // contraction of 2 d operations each for d > about 1000, the widths here).
 //
-// Bound by the matrix cores for many tokens: 3072 of 4096 tokens, d = 2560, V
-// = 151936, bf16 take 6.5 ms (forward 2.05, dH 1.88, dW 2.08: 1.15 to 1.27
-// PFLOP/s; G from z 0.52 at 5.4 TB/s), 2188 of 2500, d = 7168, V = 129280 11.3
-// ms. Bound by reading W for few: the loss of 64 tokens, d = 1536, V = 151936
+// Bound by the matrix cores for many tokens: 4096 tokens, three quarters of
+// them counted, d = 2560, V = 151936, bf16 take 6.5 ms (forward 2.05, dH 1.88,
+// dW 2.08: 1.15 to 1.27 PFLOP/s; G from z 0.52 at 5.4 TB/s), 2188 of 2500, d =
+// 7168, V = 129280 11.3 ms. Bound by reading W for few: the loss of 64 tokens, d = 1536, V = 151936
 // takes 109 us, 99 of them W at 4.7 TB/s.
 //
 // Every sum has a fixed order and there are no atomics: token losses depend
@@ -177,8 +177,8 @@ __global__ __launch_bounds__(kThreads8, 1) void ce_partial_kernel(
   const int S = n_slices;
   const int n_tok = __builtin_amdgcn_readfirstlane(chunk_live(count, c0, cap));
   // The walk is that of the live token blocks, workgroups past it leave: dead
-  // blocks in between would leave some XCDs idle (3072 of 4096 tokens: 2.32 ms
-  // so, 2.0 ms without).
+  // blocks in between would leave some XCDs idle (three quarters of 4096 tokens
+  // counted: 2.32 ms so, 2.0 ms without).
   const int n_tb = (n_tok + kBT - 1) / kBT;
   if ((long long)blockIdx.x >= (long long)n_tb * ((S + group - 1) / group)) return;
   const WideWork work = wide_work(blockIdx.x, n_tb, S, group);
