@@ -373,7 +373,8 @@ enum { ITL_SUM = 0, ITL_MEAN = 1 };
 /* Bytes of device workspace itl_cross_entropy (with_grad 0) or
  * itl_cross_entropy_grad (with_grad 1) needs. With the gradient it holds the
  * logits (fp32) and their gradients (dtype) of at most 16,384 tokens, whatever
- * n_tok, and one fp32 copy of dW where a bf16 head has more tokens than that;
+ * n_tok, one fp32 copy of dW where a bf16 head has more tokens than that, and
+ * fp32 partial sums of dH (of dW too where it is small and the tokens are many);
  * without it the logits of at most 4,096 tokens of an fp32 head, none of a
  * bf16 one. SIZE_MAX for invalid sizes or dtypes. */
 size_t itl_cross_entropy_workspace_bytes(int64_t n_tok, int64_t d, int64_t vocab, itl_dtype dtype,

@@ -68,22 +68,34 @@ struct GradTile {
   static constexpr int kStepK = kStepBytes / Elem<kDtype>::kSize;
 };
 
-// Workgroups that share the K steps of a dH tile (each at least 4 steps): the
-// count that takes the fewest K steps of time, rounds over the CUs x steps per
-// workgroup, beside each round's start and end (12 steps' worth) and the fp32
-// partials' traffic (a step's time moves those of about 4 tiles). fp32: three
+// Workgroups that share the K steps of a tile of dH or dW (each at least 4
+// steps): the count that takes the fewest K steps of time, rounds over the CUs
+// x steps per workgroup, beside each round's start and end (12 steps' worth)
+// and the fp32 partials' traffic (a step's time moves those of about 4 tiles;
+// of a single block of tokens, its `rows` of `tile` only). fp32: three
 // workgroups fit a CU and share its matrix cores; one alone waits for its loads
 // (a step takes 1.6 times as long), starts and ends overlap, and the partials
 // are a sixteenth.
-__host__ __device__ inline int dh_splits(uint32_t tiles, uint32_t nks, bool f32) {
+constexpr uint32_t kMaxSplits = 16, kMaxSplitsOneBlock = 64;  // (few rows' partials cost little)
+__host__ __device__ inline int k_splits(uint32_t tiles, uint32_t nks, bool f32, uint32_t rows, uint32_t tile) {
   uint32_t best = 1, best_cost = 0xffffffffu;
-  for (uint32_t s = 1; s <= 16 && (s == 1 || nks / s >= 4); ++s) {
+  const uint32_t most = rows < tile ? kMaxSplitsOneBlock : kMaxSplits;
+  for (uint32_t s = 1; s <= most && (s == 1 || nks / s >= 4); ++s) {
     const uint32_t rounds = (tiles * s + 255) / 256, steps = (nks + s - 1) / s;
-    const uint32_t cost = f32 ? rounds * (steps + 4) + (rounds == 1 ? steps * 3 / 5 : 0) + s * tiles / 64
-                              : rounds * (steps + 12) + s * tiles / 4;
+    const uint32_t part = s * tiles * rows / tile;
+    const uint32_t cost = f32 ? rounds * (steps + 4) + (rounds == 1 ? steps * 3 / 5 : 0) + part / 64
+                              : rounds * (steps + 12) + part / 4;
     if (cost < best_cost) best = s, best_cost = cost;
   }
   return (int)best;
+}
+
+// dH's: `live` rows of G in blocks of `tile`, n_dt tiles of d. A single
+// block's rows count in quarters of it.
+__host__ __device__ inline int dh_splits(uint32_t live, uint32_t n_dt, uint32_t nks, bool f32, uint32_t tile) {
+  const uint32_t quarter = tile / 4;
+  const uint32_t rows = live >= tile ? tile : (live + quarter - 1) / quarter * quarter;
+  return k_splits((live + tile - 1) / tile * n_dt, nks, f32, rows, tile);
 }
 
 // Place of (token row t, vocabulary entry v) in a blocked array of `rows`
@@ -130,7 +142,7 @@ __global__ __launch_bounds__(kSelectThreads) void ce_select_kernel(const int32_t
   if (splits)
     for (int c = threadIdx.x; (long long)c * chunk < n; c += kSelectThreads) {
       const int live = parts * max(0, min(base - c * chunk, chunk));
-      splits[c] = dh_splits((uint32_t)((live + rows_per_tile - 1) / rows_per_tile * n_dt), (uint32_t)nks, f32 != 0);
+      splits[c] = dh_splits((uint32_t)live, (uint32_t)n_dt, (uint32_t)nks, f32 != 0, (uint32_t)rows_per_tile);
     }
 }
 
@@ -660,7 +672,7 @@ __device__ __forceinline__ void store_grad4(void* out, int grad_f32, size_t at, 
 
 // Partial sp of dH for the chunk: A = W (columns d0 .. of rows v), B = rows of
 // Gd, K = the vocabulary steps [nks sp / splits, nks (sp + 1) / splits). Writes
-// fp32 rows part[sp, t, :] (tile rows of the live tokens per split). Token
+// fp32 rows part[sp, t, :] (the live tokens' rows per split). Token
 // blocks fastest: workgroups that run together share W's rows.
 template <int kDtype>
 __global__ __launch_bounds__(kDtype == 0 ? kThreads8 : kF32Threads, 1) void ce_dh_kernel(
@@ -683,7 +695,7 @@ __global__ __launch_bounds__(kDtype == 0 ? kThreads8 : kF32Threads, 1) void ce_d
   const KmOperand B{Gd + (size_t)t0 * g_row, g_row, min(kT, live - t0), 0u, kDtype == 0 ? 2 : 3, ks0,
                     (size_t)g_rows * g_row};
   static_assert(kBV / kStepK == (kDtype == 0 ? 4 : 8), "K steps of a block of G");
-  float* out = part + (size_t)sp * n_tb * kT * d;
+  float* out = part + (size_t)sp * live * d;
   auto store = [&](int t, int k, const floatx4& o) {
     if (t < live && k < d) *reinterpret_cast<float4*>(out + (size_t)t * d + k) = make_float4(o[0], o[1], o[2], o[3]);
   };
@@ -709,44 +721,48 @@ __global__ __launch_bounds__(kDtype == 0 ? kThreads8 : kF32Threads, 1) void ce_d
 }
 
 // dH rows: the splits added in order (plus, with coef, the exact one-hot
-// term coef[j] W[y]), four values per thread, to the token's own row.
+// term coef[j] W[y]), four values per thread, to the token's own row. 256
+// columns per workgroup: with few tokens and many splits, waiting for the
+// partials is all there is (2 tokens, d = 3904, 16 splits: 39 us by one
+// workgroup per token).
+constexpr int kDhFinish = 64;
 template <int kDtype>
-__global__ __launch_bounds__(256) void ce_dh_finish_kernel(const float* __restrict__ part,
-                                                           const int32_t* __restrict__ splits_of, int cap, int parts, int d,
-                                                           const int32_t* __restrict__ rows, const int32_t* __restrict__ ids,
-                                                           const int32_t* __restrict__ count, int c0, GradScale gs,
-                                                           const float* __restrict__ coef,
-                                                           const typename Elem<kDtype>::T* __restrict__ W, int grad_f32,
-                                                           void* __restrict__ dH) {
+__global__ __launch_bounds__(kDhFinish) void ce_dh_finish_kernel(
+    const float* __restrict__ part, const int32_t* __restrict__ splits_of, int cap, int parts, int d,
+    const int32_t* __restrict__ rows, const int32_t* __restrict__ ids, const int32_t* __restrict__ count, int c0, GradScale gs,
+    const float* __restrict__ coef, const typename Elem<kDtype>::T* __restrict__ W, int grad_f32, void* __restrict__ dH) {
   using E = Elem<kDtype>;
-  const int j = blockIdx.x;
+  const int j = blockIdx.x, k = (blockIdx.y * kDhFinish + threadIdx.x) * 4;
   const int live = chunk_live(count, c0, cap);
-  if (j >= live) return;
-  constexpr int kT = GradTile<kDtype>::kRows;
+  if (j >= live || k >= d) return;
   const int splits = *splits_of;
-  const size_t per_split = (size_t)((parts * live + kT - 1) / kT * kT) * d;
+  const size_t per_split = (size_t)(parts * live) * d;
   const float unit = grad_unit(gs, count);
-  for (int k = threadIdx.x * 4; k < d; k += 1024) {
-    float o[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+  const float* at = part + (size_t)j * d + k;
+  float o[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+  auto add = [&](const float* p) {
+    const float4 v = *reinterpret_cast<const float4*>(p);
+    o[0] += v.x, o[1] += v.y, o[2] += v.z, o[3] += v.w;
+  };
+  if (parts == 2) {
+#pragma unroll 8
     for (int s = 0; s < splits; ++s) {
-      const float* at = part + s * per_split + (size_t)j * d + k;
-      float4 v = *reinterpret_cast<const float4*>(at);
-      o[0] += v.x, o[1] += v.y, o[2] += v.z, o[3] += v.w;
-      if (parts == 2) {
-        v = *reinterpret_cast<const float4*>(at + (size_t)live * d);
-        o[0] += v.x, o[1] += v.y, o[2] += v.z, o[3] += v.w;
-      }
+      add(at + s * per_split);
+      add(at + s * per_split + (size_t)live * d);
     }
-#pragma unroll
-    for (int r = 0; r < 4; ++r) o[r] *= unit;
-    if (coef) {
-      const float c = coef[j];
-      const typename E::T* w = W + (size_t)ids[j] * d + k;
-#pragma unroll
-      for (int r = 0; r < 4; ++r) o[r] += c * E::to_f(w[r]);
-    }
-    store_grad4(dH, grad_f32, (size_t)rows[c0 + j] * d + k, o);
+  } else {
+#pragma unroll 8
+    for (int s = 0; s < splits; ++s) add(at + s * per_split);
   }
+#pragma unroll
+  for (int r = 0; r < 4; ++r) o[r] *= unit;
+  if (coef) {
+    const float c = coef[j];
+    const typename E::T* w = W + (size_t)ids[j] * d + k;
+#pragma unroll
+    for (int r = 0; r < 4; ++r) o[r] += c * E::to_f(w[r]);
+  }
+  store_grad4(dH, grad_f32, (size_t)rows[c0 + j] * d + k, o);
 }
 
 // ---- dW
@@ -788,7 +804,9 @@ inline long long dw_groups(long long n_vt, long long n_dt) {
 // the chunk's live tokens.
 // A workgroup walks up to `walk` tiles of d (fp32: one), so that a
 // tile's first loads and last stores run under its neighbours' products.
-enum { kDwRound = 0, kDwWrite = 1, kDwAdd = 2 };  // bf16 results; fp32 ones; fp32 ones on top of dW
+// Where there are few tiles (small vocabularies) the tokens are split over
+// blockIdx.y: partial sums [split, vocab, d] in fp32, without the unit.
+enum { kDwRound = 0, kDwWrite = 1, kDwAdd = 2, kDwPart = 3 };  // bf16 results; fp32; fp32 on top of dW; partials
 
 template <int kDtype, int kMode>
 __global__ __launch_bounds__(kDtype == 0 ? kThreads8 : kF32Threads, 1) void ce_dw_kernel(
@@ -797,18 +815,32 @@ __global__ __launch_bounds__(kDtype == 0 ? kThreads8 : kF32Threads, 1) void ce_d
   constexpr int kT = GradTile<kDtype>::kRows, kStepK = GradTile<kDtype>::kStepK, es = Elem<kDtype>::kSize;
   __shared__ __align__(1024) uint4 smem[kDtype == 0 ? kEngineSmemChunks : kF32SmemChunks];
   const int live = __builtin_amdgcn_readfirstlane(chunk_live(count, c0, cap));
-  if (live == 0 && c0 > 0) return;  // (the first chunk writes its zeros)
+  if (live == 0 && c0 > 0 && kMode != kDwPart) return;  // (the first chunk writes its zeros; partials are read)
   int vt, dt;
   if (!dw_work(blockIdx.x, n_vt, (n_dt + walk - 1) / walk, vt, dt)) return;
   dt *= walk;
   const int dt_end = min(dt + walk, n_dt);
-  const int nks = max(1, (live + kStepK - 1) / kStepK);
+  const int nks_all = (live + kStepK - 1) / kStepK;
+  int ks0 = 0, ks1 = nks_all;
+  if constexpr (kMode == kDwPart) {
+    ks0 = (int)((long long)nks_all * blockIdx.y / gridDim.y);
+    ks1 = (int)((long long)nks_all * (blockIdx.y + 1) / gridDim.y);
+  }
+  const int nks = max(1, ks1 - ks0);  // (a split without steps sums zeros: its range of rows is empty)
+  const int first = ks0 * kStepK, left = min(live, ks1 * kStepK) - first;
   const uint32_t h_row = (uint32_t)d * es;
   const uint32_t d_off = (uint32_t)dt * kT * es;
-  const KmOperand B = g_columns(Gd, vt * kT, g_rows, es, live);
-  const float unit = grad_unit(gs, count);
+  KmOperand B = g_columns(Gd, vt * kT, g_rows, es, left);
+  B.base += (size_t)first * B.row_bytes;
+  Hc += (size_t)first * h_row;
+  const float unit = kMode == kDwPart ? 1.0f : grad_unit(gs, count);
   auto store = [&](int v, int k, const floatx4& o) {
     if (v >= vocab || k >= d) return;
+    if constexpr (kMode == kDwPart) {
+      char* part = static_cast<char*>(dW) + (size_t)blockIdx.y * vocab * d * 4;  // (one split's is less than 2^31 bytes)
+      *reinterpret_cast<floatx4*>(part + ((uint32_t)v * (uint32_t)d + (uint32_t)k) * 4u) = o;
+      return;
+    }
     const size_t at = (size_t)v * d + k;
     float x[4] = {o[0] * unit, o[1] * unit, o[2] * unit, o[3] * unit};
     if constexpr (kMode == kDwAdd) {
@@ -819,7 +851,7 @@ __global__ __launch_bounds__(kDtype == 0 ? kThreads8 : kF32Threads, 1) void ce_d
   };
   if constexpr (kDtype == 0) {
     const Lanes8 L = lanes8();
-    run_tiles_km<true, true>(smem, L, KmOperand{Hc, h_row, live, 0u}, B, dt, dt_end, nks, [&](int tile, floatx4 (&acc)[8][4]) {
+    run_tiles_km<true, true>(smem, L, KmOperand{Hc, h_row, left, 0u}, B, dt, dt_end, nks, [&](int tile, floatx4 (&acc)[8][4]) {
       int lane = L.lane;  // made opaque: addresses formed here, not kept live across the K loop
       asm volatile("" : "+v"(lane));
       const int v0 = vt * kT + L.tq * 64 + (lane & 15), k0 = tile * kT + L.wv * 128 + 4 * (lane >> 4);
@@ -831,7 +863,7 @@ __global__ __launch_bounds__(kDtype == 0 ? kThreads8 : kF32Threads, 1) void ce_d
       }
     });
   } else {
-    run_tile_f32<true, true>(smem, KmOperand{Hc + d_off, h_row, live, d_off}, B, nks, [&](floatx4 (&acc)[2][2], int wave, int quad, int c16) {
+    run_tile_f32<true, true>(smem, KmOperand{Hc + d_off, h_row, left, d_off}, B, nks, [&](floatx4 (&acc)[2][2], int wave, int quad, int c16) {
 #pragma unroll
       for (int bn = 0; bn < 2; ++bn)
 #pragma unroll
@@ -839,6 +871,29 @@ __global__ __launch_bounds__(kDtype == 0 ? kThreads8 : kF32Threads, 1) void ce_d
           store(vt * kT + 32 * (wave >> 1) + 16 * bn + c16, dt * kT + 32 * (wave & 1) + 16 * bm + 4 * quad, acc[bm][bn]);
     });
   }
+}
+
+// The splits' partials added in order, times the unit: as kMode says.
+template <int kMode>
+__global__ __launch_bounds__(256) void ce_dw_finish_kernel(const float* __restrict__ part, int splits, long long n,
+                                                           const int32_t* __restrict__ count, GradScale gs,
+                                                           void* __restrict__ dW) {
+  const long long i = ((long long)blockIdx.x * 256 + threadIdx.x) * 4;
+  if (i >= n) return;
+  const float unit = grad_unit(gs, count);
+  float o[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 8
+  for (int s = 0; s < splits; ++s) {
+    const float4 v = *reinterpret_cast<const float4*>(part + s * n + i);
+    o[0] += v.x, o[1] += v.y, o[2] += v.z, o[3] += v.w;
+  }
+#pragma unroll
+  for (int r = 0; r < 4; ++r) o[r] *= unit;
+  if constexpr (kMode == kDwAdd) {
+    const float4 old = *reinterpret_cast<const float4*>(static_cast<const float*>(dW) + i);
+    o[0] += old.x, o[1] += old.y, o[2] += old.z, o[3] += old.w;
+  }
+  store_grad4(dW, kMode != kDwRound, i, o);
 }
 
 // dW of a chunk of few tokens (bf16): 128 x 128 tiles, the tiles of d fastest.
@@ -904,24 +959,35 @@ __global__ __launch_bounds__(256) void ce_clear_kernel(uint4* __restrict__ out, 
 
 // ---- workspace
 
-// The most workgroups, and fp32 partial rows, that a chunk of up to cap tokens
-// can take in dH's contraction, over all live counts.
+// The most workgroups, and fp32 partial rows, that a chunk of up to `cap` rows
+// of G can take in dH's contraction, over all live counts.
 void dh_most(long long cap, long long d, long long vpad, int dtype, long long* groups, long long* rows) {
   const long long tile = dtype == 0 ? GradTile<0>::kRows : GradTile<1>::kRows;
   const long long nks = vpad / (dtype == 0 ? GradTile<0>::kStepK : GradTile<1>::kStepK), n_dt = ceil_div(d, tile);
   *groups = *rows = 0;
-  for (long long n_tb = 1; n_tb <= ceil_div(cap, tile); ++n_tb) {
-    const long long s = dh_splits((uint32_t)(n_tb * n_dt), (uint32_t)nks, dtype == 1);
-    *groups = std::max(*groups, n_tb * n_dt * s);
-    *rows = std::max(*rows, n_tb * tile * s);
-  }
+  auto take = [&](long long live) {
+    const long long s = dh_splits((uint32_t)live, (uint32_t)n_dt, (uint32_t)nks, dtype == 1, (uint32_t)tile);
+    *groups = std::max(*groups, ceil_div(live, tile) * n_dt * s);
+    *rows = std::max(*rows, live * s);
+  };
+  for (int quarter = 1; quarter < 4; ++quarter) take(quarter * tile / 4);
+  for (long long n_tb = 1; n_tb <= ceil_div(cap, tile); ++n_tb) take(n_tb * tile);
+}
+
+// Splits of the tokens of a chunk of cap in dW's contraction.
+int dw_splits(long long cap, long long d, long long vocab, int dtype) {
+  const long long tile = dtype == 0 ? GradTile<0>::kRows : GradTile<1>::kRows;
+  const long long nks = ceil_div(cap, dtype == 0 ? GradTile<0>::kStepK : GradTile<1>::kStepK);
+  const long long tiles = ceil_div(d, tile) * ceil_div(vocab, tile);
+  if (tiles > 512 * (dtype == 0 ? 1 : 3)) return 1;  // the CUs have two rounds without
+  return k_splits((uint32_t)tiles, (uint32_t)nks, dtype == 1, (uint32_t)tile, (uint32_t)tile);
 }
 
 struct CeLayout {
   int cap, vpad, parts;
   long long dh_groups;
-  size_t rows, ids, slot, count, splits, lp, lse, zy, part, loss, wmean, wpart, hc, z, gd, dhp, coef, cids, dwacc, sampled,
-      total;
+  size_t rows, ids, slot, count, splits, lp, lse, zy, part, loss, wmean, wpart, hc, z, gd, dhp, dwp, coef, cids, dwacc,
+      sampled, total;
 };
 
 CeLayout ce_layout(long long n_tok, long long d, long long vocab, int dtype, bool grad, int grad_dtype) {
@@ -958,6 +1024,11 @@ CeLayout ce_layout(long long n_tok, long long d, long long vocab, int dtype, boo
     L.splits = take((size_t)ceil_div(n_tok, L.cap) * 4);
     L.gd = take((size_t)L.parts * L.cap * L.vpad * es);
     L.dhp = take((size_t)rows * d * 4);
+    if (dtype == 1 || n_tok > kFewTokens) {
+      const long long last = n_tok % L.cap ? n_tok % L.cap : L.cap;
+      const int s = std::max(dw_splits(L.cap, d, vocab, dtype), dw_splits(last, d, vocab, dtype));
+      if (s > 1) L.dwp = take((size_t)s * vocab * d * 4);
+    }
     if (dtype == 0 && grad_dtype == 1) {
       L.coef = take((size_t)L.cap * 4);
       L.cids = take((size_t)L.cap * 4);
@@ -1116,7 +1187,8 @@ hipError_t run_cross_entropy(const CeCall& c, hipStream_t stream) {
                        reinterpret_cast<const char*>(W), reinterpret_cast<const char*>(Gd), vocab, L.vpad, d, count, c0, cap,
                        L.parts, g_rows, n_dt, splits, dhp);
     ITL_CHECK_LAUNCH();
-    hipLaunchKernelGGL(ce_dh_finish_kernel<kDtype>, dim3((unsigned)cap), dim3(256), 0, stream, dhp, splits, cap, L.parts, d, rows,
+    hipLaunchKernelGGL(ce_dh_finish_kernel<kDtype>, dim3((unsigned)cap, (unsigned)ceil_div(d, 4 * kDhFinish)),
+                       dim3(kDhFinish), 0, stream, dhp, splits, cap, L.parts, d, rows,
                        ids + c0, count, c0, gs, coef, W, c.grad_dtype, c.dH);
     ITL_CHECK_LAUNCH();
     // dW
@@ -1142,6 +1214,17 @@ hipError_t run_cross_entropy(const CeCall& c, hipStream_t stream) {
                              out);
           return;
         }
+      }
+      const int splits = dw_splits(cap, d, vocab, kDtype);
+      if (splits > 1) {
+        float* dwp = reinterpret_cast<float*>(at(L.dwp));
+        hipLaunchKernelGGL((ce_dw_kernel<kDtype, kDwPart>), dim3((unsigned)dw_groups(n_vt, n_dt), (unsigned)splits), g_block, 0,
+                           stream, reinterpret_cast<const char*>(Gd), Hc, g_rows, count, c0, cap, vocab, d, n_vt, n_dt, 1, gs,
+                           dwp);
+        hipLaunchKernelGGL((ce_dw_finish_kernel<decltype(mode)::value>),
+                           dim3((unsigned)ceil_div((long long)vocab * d, 1024)), dim3(256), 0, stream, dwp, splits,
+                           (long long)vocab * d, count, gs, out);
+        return;
       }
       hipLaunchKernelGGL((ce_dw_kernel<kDtype, decltype(mode)::value>), dim3((unsigned)dw_groups(n_vt, ceil_div(n_dt, walk))),
                          g_block, 0, stream, reinterpret_cast<const char*>(Gd), Hc, g_rows, count, c0, cap, vocab, d, n_vt,
