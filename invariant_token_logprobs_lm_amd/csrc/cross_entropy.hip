@@ -71,31 +71,49 @@ struct GradTile {
 // Workgroups that share the K steps of a tile of dH or dW (each at least 4
 // steps): the count that takes the fewest K steps of time, rounds over the CUs
 // x steps per workgroup, beside each round's start and end (12 steps' worth)
-// and the fp32 partials' traffic (a step's time moves those of about 4 tiles;
+// and the fp32 partials' traffic (a step's time moves those of about 8 tiles;
 // of a single block of tokens, its `rows` of `tile` only). fp32: three
 // workgroups fit a CU and share its matrix cores; one alone waits for its loads
 // (a step takes 1.6 times as long), starts and ends overlap, and the partials
 // are a sixteenth.
-constexpr uint32_t kMaxSplits = 16, kMaxSplitsOneBlock = 64;  // (few rows' partials cost little)
-__host__ __device__ inline int k_splits(uint32_t tiles, uint32_t nks, bool f32, uint32_t rows, uint32_t tile) {
-  uint32_t best = 1, best_cost = 0xffffffffu;
-  const uint32_t most = rows < tile ? kMaxSplitsOneBlock : kMaxSplits;
-  for (uint32_t s = 1; s <= most && (s == 1 || nks / s >= 4); ++s) {
+struct KSplits {
+  uint32_t tiles, nks, rows, tile;
+  bool f32;
+  // a single block's partials are few: more splits pay
+  __host__ __device__ uint32_t most() const { return tiles == 0 ? 1 : rows <= tile ? 64 : 16; }
+  __host__ __device__ uint32_t cost(uint32_t s) const {
+    if (s > most() || (s > 1 && nks / s < 4)) return 0xffffffffu;
     const uint32_t rounds = (tiles * s + 255) / 256, steps = (nks + s - 1) / s;
-    const uint32_t part = s * tiles * rows / tile;
-    const uint32_t cost = f32 ? rounds * (steps + 4) + (rounds == 1 ? steps * 3 / 5 : 0) + part / 64
-                              : rounds * (steps + 12) + part / 4;
-    if (cost < best_cost) best = s, best_cost = cost;
+    const uint32_t part = s * tiles * (rows < tile ? rows : tile) / tile;
+    return f32 ? rounds * (steps + 4) + (rounds == 1 ? steps * 3 / 5 : 0) + part / 64 : rounds * (steps + 12) + part / 8;
   }
+};
+
+inline int k_splits(const KSplits& k) {
+  uint32_t best = 1;
+  for (uint32_t s = 2; s <= k.most(); ++s)
+    if (k.cost(s) < k.cost(best)) best = s;
   return (int)best;
+}
+
+// The same by a wavefront, a count per lane.
+__device__ __forceinline__ int k_splits_wave(const KSplits& k) {
+  const uint32_t s = (threadIdx.x & 63) + 1;
+  uint64_t key = ((uint64_t)k.cost(s) << 32) | s;
+#pragma unroll
+  for (int off = 32; off >= 1; off >>= 1) {
+    const uint64_t other = (uint64_t)__shfl_xor((unsigned long long)key, off, 64);
+    key = other < key ? other : key;
+  }
+  return (int)(uint32_t)key;
 }
 
 // dH's: `live` rows of G in blocks of `tile`, n_dt tiles of d. A single
 // block's rows count in quarters of it.
-__host__ __device__ inline int dh_splits(uint32_t live, uint32_t n_dt, uint32_t nks, bool f32, uint32_t tile) {
+__host__ __device__ inline KSplits dh_split_sizes(uint32_t live, uint32_t n_dt, uint32_t nks, bool f32, uint32_t tile) {
   const uint32_t quarter = tile / 4;
-  const uint32_t rows = live >= tile ? tile : (live + quarter - 1) / quarter * quarter;
-  return k_splits((live + tile - 1) / tile * n_dt, nks, f32, rows, tile);
+  const uint32_t rows = (live + quarter - 1) / quarter * quarter;
+  return KSplits{(live + tile - 1) / tile * n_dt, nks, rows, tile, f32};
 }
 
 // Place of (token row t, vocabulary entry v) in a blocked array of `rows`
@@ -138,11 +156,12 @@ __global__ __launch_bounds__(kSelectThreads) void ce_select_kernel(const int32_t
     __syncthreads();
   }
   if (threadIdx.x == 0) *count = base;
-  // dH's splits of every chunk
+  // dH's splits of every chunk, a wavefront each
   if (splits)
-    for (int c = threadIdx.x; (long long)c * chunk < n; c += kSelectThreads) {
+    for (int c = wave; (long long)c * chunk < n; c += kSelectThreads / 64) {
       const int live = parts * max(0, min(base - c * chunk, chunk));
-      splits[c] = dh_splits((uint32_t)live, (uint32_t)n_dt, (uint32_t)nks, f32 != 0, (uint32_t)rows_per_tile);
+      const int s = k_splits_wave(dh_split_sizes((uint32_t)live, (uint32_t)n_dt, (uint32_t)nks, f32 != 0, (uint32_t)rows_per_tile));
+      if (lane == 0) splits[c] = s;
     }
 }
 
@@ -805,7 +824,8 @@ inline long long dw_groups(long long n_vt, long long n_dt) {
 // A workgroup walks up to `walk` tiles of d (fp32: one), so that a
 // tile's first loads and last stores run under its neighbours' products.
 // Where there are few tiles (small vocabularies) the tokens are split over
-// blockIdx.y: partial sums [split, vocab, d] in fp32, without the unit.
+// gridDim.x / tiles workgroups each: partial sums [split, vocab, d] in fp32,
+// without the unit.
 enum { kDwRound = 0, kDwWrite = 1, kDwAdd = 2, kDwPart = 3 };  // bf16 results; fp32; fp32 on top of dW; partials
 
 template <int kDtype, int kMode>
@@ -817,14 +837,22 @@ __global__ __launch_bounds__(kDtype == 0 ? kThreads8 : kF32Threads, 1) void ce_d
   const int live = __builtin_amdgcn_readfirstlane(chunk_live(count, c0, cap));
   if (live == 0 && c0 > 0 && kMode != kDwPart) return;  // (the first chunk writes its zeros; partials are read)
   int vt, dt;
-  if (!dw_work(blockIdx.x, n_vt, (n_dt + walk - 1) / walk, vt, dt)) return;
-  dt *= walk;
+  int split = 0;
+  if constexpr (kMode == kDwPart) {  // one tile each, in turn over the XCDs: few vocabulary tiles would fill few of them
+    const int tiles = n_vt * n_dt;
+    split = blockIdx.x / tiles;
+    vt = blockIdx.x % tiles / n_dt, dt = blockIdx.x % n_dt;
+  } else {
+    if (!dw_work(blockIdx.x, n_vt, (n_dt + walk - 1) / walk, vt, dt)) return;
+    dt *= walk;
+  }
   const int dt_end = min(dt + walk, n_dt);
   const int nks_all = (live + kStepK - 1) / kStepK;
   int ks0 = 0, ks1 = nks_all;
   if constexpr (kMode == kDwPart) {
-    ks0 = (int)((long long)nks_all * blockIdx.y / gridDim.y);
-    ks1 = (int)((long long)nks_all * (blockIdx.y + 1) / gridDim.y);
+    const int splits = gridDim.x / (n_vt * n_dt);
+    ks0 = (int)((long long)nks_all * split / splits);
+    ks1 = (int)((long long)nks_all * (split + 1) / splits);
   }
   const int nks = max(1, ks1 - ks0);  // (a split without steps sums zeros: its range of rows is empty)
   const int first = ks0 * kStepK, left = min(live, ks1 * kStepK) - first;
@@ -837,7 +865,7 @@ __global__ __launch_bounds__(kDtype == 0 ? kThreads8 : kF32Threads, 1) void ce_d
   auto store = [&](int v, int k, const floatx4& o) {
     if (v >= vocab || k >= d) return;
     if constexpr (kMode == kDwPart) {
-      char* part = static_cast<char*>(dW) + (size_t)blockIdx.y * vocab * d * 4;  // (one split's is less than 2^31 bytes)
+      char* part = static_cast<char*>(dW) + (size_t)split * vocab * d * 4;  // (one split's is less than 2^31 bytes)
       *reinterpret_cast<floatx4*>(part + ((uint32_t)v * (uint32_t)d + (uint32_t)k) * 4u) = o;
       return;
     }
@@ -897,7 +925,10 @@ __global__ __launch_bounds__(256) void ce_dw_finish_kernel(const float* __restri
 }
 
 // dW of a chunk of few tokens (bf16): 128 x 128 tiles, the tiles of d fastest.
-constexpr int kFewTokens = 256;
+// d = 2560, V = 50000: 500 tokens 188 us in 256 x 256 tiles, 156 so; 1020 282
+// and 267. 705 (449 counted), d = 4864, V = 340: 26 us split, 16 so. 2 tokens, d =
+// 3904, V = 87112: 125 us, dW written at 5.4 TB/s.
+constexpr int kFewTokens = 1024;
 template <int kMode>
 __global__ __launch_bounds__(kFewThreads, 4) void ce_dw_few_kernel(const char* __restrict__ Gd, const char* __restrict__ Hc,
                                                                    int g_rows, const int32_t* __restrict__ count, int c0,
@@ -911,6 +942,32 @@ __global__ __launch_bounds__(kFewThreads, 4) void ce_dw_few_kernel(const char* _
   run_tile_few(smem, KmOperand{Hc + d_off, (uint32_t)d * 2, live, d_off},
                g_columns(Gd, vt * kFewTile, g_rows, 2, live),
                [&](floatx4 (&acc)[4][4], int wave, int quad, int c16) {
+    if constexpr (kMode == kDwRound) {
+      // Through LDS (the operands are done with): rows of 256 bytes, 16-byte
+      // piece P of row r at P ^ (r mod 16), so that a store moves whole rows.
+      // Straight from the accumulators it moves 32 bytes of 16 rows.
+      char* tile = reinterpret_cast<char*>(smem);
+#pragma unroll
+      for (int bn = 0; bn < 4; ++bn)
+#pragma unroll
+        for (int bm = 0; bm < 4; ++bm) {
+          const floatx4& o = acc[bm][bn];
+          const int row = 64 * (wave >> 1) + 16 * bn + c16, col = 64 * (wave & 1) + 16 * bm + 4 * quad;
+          *reinterpret_cast<uint2*>(tile + row * 256 + (((col >> 3) ^ c16) << 4) + (col & 4) * 2) =
+              make_uint2((uint32_t)Elem<0>::from_f(o[0] * unit) | ((uint32_t)Elem<0>::from_f(o[1] * unit) << 16),
+                         (uint32_t)Elem<0>::from_f(o[2] * unit) | ((uint32_t)Elem<0>::from_f(o[3] * unit) << 16));
+        }
+      __syncthreads();
+      const int piece = threadIdx.x & 15, k = dt * kFewTile + piece * 8;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int row = 16 * i + (threadIdx.x >> 4), v = vt * kFewTile + row;
+        if (v < vocab && k < d)
+          *reinterpret_cast<uint4*>(static_cast<uint16_t*>(dW) + (size_t)v * d + k) =
+              *reinterpret_cast<const uint4*>(tile + row * 256 + ((piece ^ (row & 15)) << 4));
+      }
+      return;
+    }
 #pragma unroll
     for (int bn = 0; bn < 4; ++bn) {
       const int v = vt * kFewTile + 64 * (wave >> 1) + 16 * bn + c16;
@@ -966,7 +1023,7 @@ void dh_most(long long cap, long long d, long long vpad, int dtype, long long* g
   const long long nks = vpad / (dtype == 0 ? GradTile<0>::kStepK : GradTile<1>::kStepK), n_dt = ceil_div(d, tile);
   *groups = *rows = 0;
   auto take = [&](long long live) {
-    const long long s = dh_splits((uint32_t)live, (uint32_t)n_dt, (uint32_t)nks, dtype == 1, (uint32_t)tile);
+    const long long s = k_splits(dh_split_sizes((uint32_t)live, (uint32_t)n_dt, (uint32_t)nks, dtype == 1, (uint32_t)tile));
     *groups = std::max(*groups, ceil_div(live, tile) * n_dt * s);
     *rows = std::max(*rows, live * s);
   };
@@ -980,7 +1037,7 @@ int dw_splits(long long cap, long long d, long long vocab, int dtype) {
   const long long nks = ceil_div(cap, dtype == 0 ? GradTile<0>::kStepK : GradTile<1>::kStepK);
   const long long tiles = ceil_div(d, tile) * ceil_div(vocab, tile);
   if (tiles > 512 * (dtype == 0 ? 1 : 3)) return 1;  // the CUs have two rounds without
-  return k_splits((uint32_t)tiles, (uint32_t)nks, dtype == 1, (uint32_t)tile, (uint32_t)tile);
+  return k_splits(KSplits{(uint32_t)tiles, (uint32_t)nks, 2 * (uint32_t)tile, (uint32_t)tile, dtype == 1});
 }
 
 struct CeLayout {
@@ -1181,7 +1238,8 @@ hipError_t run_cross_entropy(const CeCall& c, hipStream_t stream) {
     constexpr int kT = GradTile<kDtype>::kRows;
     const dim3 g_block(kDtype == 0 ? kThreads8 : kF32Threads);
     const int n_dt = (int)ceil_div(d, kT), n_vt = (int)ceil_div(vocab, kT);
-    const int walk = kDtype == 0 ? kDwWalk : 1;
+    // (a walk each for fewer than four rounds over the CUs leaves some idle at the end)
+    const int walk = kDtype == 0 && (long long)n_vt * ceil_div(n_dt, kDwWalk) >= 1024 ? kDwWalk : 1;
     const int32_t* splits = reinterpret_cast<const int32_t*>(at(L.splits)) + c0 / L.cap;
     hipLaunchKernelGGL(ce_dh_kernel<kDtype>, dim3((unsigned)L.dh_groups), g_block, 0, stream,
                        reinterpret_cast<const char*>(W), reinterpret_cast<const char*>(Gd), vocab, L.vpad, d, count, c0, cap,
@@ -1218,7 +1276,7 @@ hipError_t run_cross_entropy(const CeCall& c, hipStream_t stream) {
       const int splits = dw_splits(cap, d, vocab, kDtype);
       if (splits > 1) {
         float* dwp = reinterpret_cast<float*>(at(L.dwp));
-        hipLaunchKernelGGL((ce_dw_kernel<kDtype, kDwPart>), dim3((unsigned)dw_groups(n_vt, n_dt), (unsigned)splits), g_block, 0,
+        hipLaunchKernelGGL((ce_dw_kernel<kDtype, kDwPart>), dim3((unsigned)(n_vt * n_dt * splits)), g_block, 0,
                            stream, reinterpret_cast<const char*>(Gd), Hc, g_rows, count, c0, cap, vocab, d, n_vt, n_dt, 1, gs,
                            dwp);
         hipLaunchKernelGGL((ce_dw_finish_kernel<decltype(mode)::value>),

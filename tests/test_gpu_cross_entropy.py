@@ -105,6 +105,30 @@ def test_loss_and_gradient(cuda, n, d, V, mask, dtype, grad):
             assert same_bits(a, b)
 
 
+# dW's tiles by the number of tokens and tiles: whole (walks of one and of
+# two), its tokens split (one token left: most splits are empty), and dH's
+# vocabulary over as many workgroups as one block of tokens takes
+SIZES = [
+    (1100, 1024, 17000, "some"), (1100, 2048, 70000, "all"), (4030, 256, 1330, "some"), (2100, 320, 300, "one left"),
+    (1025, 64, 700, "all"), (3, 192, 70000, "some"), (200, 128, 40000, "some"),
+]
+
+
+@pytest.mark.parametrize("dtype,grad", [(torch.bfloat16, torch.bfloat16), (torch.bfloat16, torch.float32),
+                                        (torch.float32, torch.float32)])
+@pytest.mark.parametrize("n,d,V,mask", SIZES)
+def test_how_the_gradients_are_split(cuda, n, d, V, mask, dtype, grad):
+    itl = _itl()
+    say("cross entropy", n, d, V, mask, dtype, grad)
+    H, W, y = _head(n, d, V, dtype, n + d + V, cuda, mask)
+    H *= 0.25  # (logits that leave several ids some probability at these widths)
+    got = itl.cross_entropy_grad(H, W, y, grad_dtype=grad, label_smoothing=0.1)
+    _check(got, H, W, y, grad, smoothing=0.1)
+    again = itl.cross_entropy_grad(H, W, y, grad_dtype=grad, label_smoothing=0.1)
+    for a, b in zip(got, again):
+        assert same_bits(a, b)
+
+
 def test_agrees_with_the_logprob(cuda):
     """Without smoothing and z-loss a token's loss is minus its logprob, bit for bit."""
     itl = _itl()
