@@ -81,8 +81,8 @@ struct KSplits {
   bool f32;
   // a single block's partials are few: more splits pay
   __host__ __device__ uint32_t most() const { return tiles == 0 ? 1 : rows <= tile ? 64 : 16; }
+  __host__ __device__ bool may(uint32_t s) const { return s == 1 || (s <= most() && nks >= 4 * s); }
   __host__ __device__ uint32_t cost(uint32_t s) const {
-    if (s > most() || (s > 1 && nks / s < 4)) return 0xffffffffu;
     const uint32_t rounds = (tiles * s + 255) / 256, steps = (nks + s - 1) / s;
     const uint32_t part = s * tiles * (rows < tile ? rows : tile) / tile;
     return f32 ? rounds * (steps + 4) + (rounds == 1 ? steps * 3 / 5 : 0) + part / 64 : rounds * (steps + 12) + part / 8;
@@ -90,16 +90,18 @@ struct KSplits {
 };
 
 inline int k_splits(const KSplits& k) {
-  uint32_t best = 1;
-  for (uint32_t s = 2; s <= k.most(); ++s)
-    if (k.cost(s) < k.cost(best)) best = s;
+  uint32_t best = 1, least = 0xffffffffu;
+  for (uint32_t s = 1; k.may(s); ++s) {
+    const uint32_t cost = k.cost(s);
+    if (cost < least) best = s, least = cost;
+  }
   return (int)best;
 }
 
 // The same by a wavefront, a count per lane.
 __device__ __forceinline__ int k_splits_wave(const KSplits& k) {
   const uint32_t s = (threadIdx.x & 63) + 1;
-  uint64_t key = ((uint64_t)k.cost(s) << 32) | s;
+  uint64_t key = ((uint64_t)(k.may(s) ? k.cost(s) : 0xffffffffu) << 32) | s;
 #pragma unroll
   for (int off = 32; off >= 1; off >>= 1) {
     const uint64_t other = (uint64_t)__shfl_xor((unsigned long long)key, off, 64);
@@ -373,12 +375,45 @@ __global__ __launch_bounds__(kF32Threads, 1) void ce_logits_f32_kernel(const cha
   });
 }
 
+// G is held in units of u = (1 - e) s / N, which the contractions' epilogues
+// apply in fp32: a p - [v = y] - c with a = (1 + 2 lam lse) / (1 - e) and
+// c = e / (V (1 - e)). The target's entry is then near -1, which bf16 holds
+// to 2^-10 or better; with u folded in, every target's entry would carry the
+// same rounding error of u, up to 2^-9 of the whole gradient (measured:
+// dH and dW 0.0027 off at d = 2560, V = 151936 with 16-bit results; 0.0020 so).
+struct GradScale {
+  float smoothing, z_weight, scale, inv_vocab;
+  int mean;
+};
+
+__device__ __forceinline__ float grad_unit(const GradScale& g, const int32_t* count) {
+  const double u = (double)g.scale * (1.0 - (double)g.smoothing);
+  return (float)(g.mean ? u / (double)max(1, *count) : u);
+}
+
+// One token's row of G from its logits.
+struct GradRow {
+  float l2e_lse, a, cc;
+  __device__ __forceinline__ GradRow(const GradScale& gs, float lse) {
+    const float rest = 1.0f / (1.0f - gs.smoothing);
+    l2e_lse = lse * kLog2e;
+    a = rest * (1.0f + 2.0f * gs.z_weight * lse);
+    cc = gs.smoothing * gs.inv_vocab * rest;
+  }
+  __device__ __forceinline__ float at(float z) const { return a * fast_exp2(z * kLog2e - l2e_lse) - cc; }
+};
+
 // lse and logprob of a row of z: each thread folds entries 4 (tid + 256 i) .. +
-// 3 into its (max, sum), then a fixed tree.
+// 3 into its (max, sum), then a fixed tree. kGrad: then the row's G too (as
+// ce_grad_logits_kernel writes it), of vocabularies up to kGradRowVocab: a
+// launch less (177 tokens, d = 128, V = 1024: 37 -> 35 us); larger ones
+// want more than a workgroup per token for it.
+constexpr int kGradRowVocab = 4096;
+template <bool kGrad>
 __global__ __launch_bounds__(256) void ce_lse_f32_kernel(const float* __restrict__ z,
                                                          const int32_t* __restrict__ ids, const int32_t* __restrict__ count,
                                                          int c0, int cap, int vocab, float* __restrict__ logprob,
-                                                         float* __restrict__ lse) {
+                                                         float* __restrict__ lse, GradScale gs, float* __restrict__ Gd) {
   __shared__ float2 lds[4];
   const int t = blockIdx.x;
   if (t >= chunk_live(count, c0, cap)) return;
@@ -403,14 +438,32 @@ __global__ __launch_bounds__(256) void ce_lse_f32_kernel(const float* __restrict
   }
   if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = make_float2(m, s);
   __syncthreads();
-  if (threadIdx.x != 0) return;
+  if (!kGrad && threadIdx.x != 0) return;
+  m = lds[0].x, s = lds[0].y;
   for (int w = 1; w < 4; ++w) lse_merge(m, s, lds[w].x, lds[w].y);
   // (z_y - m) - ln s: lse itself is rounded to a step of its size, which may be
   // many times the loss. s >= 1, the maximum's own term is 1.
   const float ln_s = fast_log2(s) * kLn2;
   const int y = ids[t];  // (not gathered: it may not count)
-  logprob[t] = ((unsigned)y < (unsigned)vocab ? z[block_at(t, y, cap)] - m : 0.0f) - ln_s;
-  lse[t] = m + ln_s;
+  if (threadIdx.x == 0) {
+    logprob[t] = ((unsigned)y < (unsigned)vocab ? z[block_at(t, y, cap)] - m : 0.0f) - ln_s;
+    lse[t] = m + ln_s;
+  }
+  if constexpr (kGrad) {
+    const GradRow row(gs, m + ln_s);
+    for (int v = 4 * threadIdx.x; v < (vocab + kBV - 1) / kBV * kBV; v += 1024) {
+      const float4 q = *reinterpret_cast<const float4*>(z + block_at(t, v, cap));
+      const float x[4] = {q.x, q.y, q.z, q.w};
+      float o[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        float e = row.at(x[i]);
+        if (v + i == y) e -= 1.0f;
+        o[i] = v + i < vocab ? e : 0.0f;
+      }
+      *reinterpret_cast<float4*>(Gd + block_at(t, v, cap)) = make_float4(o[0], o[1], o[2], o[3]);
+    }
+  }
 }
 
 // ---- mean of the logits (label smoothing): z's mean over v is H . mean_v W[v]
@@ -588,22 +641,6 @@ __global__ __launch_bounds__(1024) void ce_small_loss_kernel(const int32_t* __re
 
 // ---- G
 
-// G is held in units of u = (1 - e) s / N, which the contractions' epilogues
-// apply in fp32: a p - [v = y] - c with a = (1 + 2 lam lse) / (1 - e) and
-// c = e / (V (1 - e)). The target's entry is then near -1, which bf16 holds
-// to 2^-10 or better; with u folded in, every target's entry would carry the
-// same rounding error of u, up to 2^-9 of the whole gradient (measured:
-// dH and dW 0.0027 off at d = 2560, V = 151936 with 16-bit results; 0.0020 so).
-struct GradScale {
-  float smoothing, z_weight, scale, inv_vocab;
-  int mean;
-};
-
-__device__ __forceinline__ float grad_unit(const GradScale& g, const int32_t* count) {
-  const double u = (double)g.scale * (1.0 - (double)g.smoothing);
-  return (float)(g.mean ? u / (double)max(1, *count) : u);
-}
-
 // G from the kept logits: 8 vocabulary entries of one token per thread; past
 // the vocabulary zeros. With kExact the target's entry is stored without its
 // -1, which dH and dW then take in fp32.
@@ -628,11 +665,7 @@ __global__ __launch_bounds__(256) void ce_grad_logits_kernel(
   const int v = blockIdx.x * kBV + threadIdx.x % (kBV / kGradVec) * kGradVec;
   const int live = chunk_live(count, c0, cap);
   if (t >= live) return;
-  const float rest = 1.0f / (1.0f - gs.smoothing);
-  const float cc = gs.smoothing * gs.inv_vocab * rest;
-  const float s = lse[t];
-  const float l2e_lse = s * kLog2e;
-  const float a = rest * (1.0f + 2.0f * gs.z_weight * s);
+  const GradRow row(gs, lse[t]);
   const int y = ids[t];
   float z[kGradVec];
   const floatx4* at = reinterpret_cast<const floatx4*>(logits + block_at(t, v, cap));
@@ -641,7 +674,7 @@ __global__ __launch_bounds__(256) void ce_grad_logits_kernel(
   for (int r = 0; r < 4; ++r) z[r] = lo[r], z[4 + r] = hi[r];
 #pragma unroll
   for (int r = 0; r < kGradVec; ++r) {
-    float x = a * fast_exp2(z[r] * kLog2e - l2e_lse) - cc;
+    float x = row.at(z[r]);
     if (!kExact && v + r == y) x -= 1.0f;
     z[r] = v + r < vocab ? x : 0.0f;
   }
@@ -1186,6 +1219,7 @@ hipError_t run_cross_entropy(const CeCall& c, hipStream_t stream) {
   }
   GradScale gs{c.smoothing, c.z_weight, c.grad_scale, 1.0f / (float)vocab, c.mean};
   const bool exact = grad && kDtype == 0 && c.grad_dtype == 1;
+  const bool row_grad = grad && kDtype == 1 && vocab <= kGradRowVocab;
   for (long long first = 0; first < n; first += L.cap) {
     const int c0 = (int)first;
     const int cap = std::min(L.cap, n - c0);
@@ -1209,22 +1243,28 @@ hipError_t run_cross_entropy(const CeCall& c, hipStream_t stream) {
       const int n_vt = (int)ceil_div(vocab, kF32Tile);
       hipLaunchKernelGGL(ce_logits_f32_kernel, dim3((unsigned)(n_vt * ceil_div(cap, kF32Tile))), dim3(kF32Threads), 0, stream,
                          h_rows, w_rows, counted, c0, cap, d * 4, vocab, n_vt, z);
-      hipLaunchKernelGGL(ce_lse_f32_kernel, dim3((unsigned)cap), dim3(256), 0, stream, z, y, counted, c0,
-                         cap, vocab, lp + c0, lse + c0);
+      if (row_grad)
+        hipLaunchKernelGGL((ce_lse_f32_kernel<true>), dim3((unsigned)cap), dim3(256), 0, stream, z, y, counted, c0, cap, vocab,
+                           lp + c0, lse + c0, gs, reinterpret_cast<float*>(at(L.gd)));
+      else
+        hipLaunchKernelGGL((ce_lse_f32_kernel<false>), dim3((unsigned)cap), dim3(256), 0, stream, z, y, counted, c0, cap, vocab,
+                           lp + c0, lse + c0, gs, nullptr);
       ITL_CHECK_LAUNCH();
     }
     if (!grad) continue;
 
     T* Gd = reinterpret_cast<T*>(at(L.gd));
-    const dim3 g_grid((unsigned)(L.vpad / kBV), (unsigned)ceil_div(cap, 256 * kGradVec / kBV));
     const int g_rows = L.parts * cap;
-    if (exact)
-      hipLaunchKernelGGL((ce_grad_logits_kernel<kDtype, true>), g_grid, dim3(256), 0, stream, z, ids + c0, count,
-                         c0, cap, L.parts, vocab, g_rows, lse + c0, gs, Gd);
-    else
-      hipLaunchKernelGGL((ce_grad_logits_kernel<kDtype, false>), g_grid, dim3(256), 0, stream, z, ids + c0, count,
-                         c0, cap, L.parts, vocab, g_rows, lse + c0, gs, Gd);
-    ITL_CHECK_LAUNCH();
+    if (!row_grad) {
+      const dim3 g_grid((unsigned)(L.vpad / kBV), (unsigned)ceil_div(cap, 256 * kGradVec / kBV));
+      if (exact)
+        hipLaunchKernelGGL((ce_grad_logits_kernel<kDtype, true>), g_grid, dim3(256), 0, stream, z, ids + c0, count,
+                           c0, cap, L.parts, vocab, g_rows, lse + c0, gs, Gd);
+      else
+        hipLaunchKernelGGL((ce_grad_logits_kernel<kDtype, false>), g_grid, dim3(256), 0, stream, z, ids + c0, count,
+                           c0, cap, L.parts, vocab, g_rows, lse + c0, gs, Gd);
+      ITL_CHECK_LAUNCH();
+    }
     float* coef = nullptr;
     int32_t* cids = reinterpret_cast<int32_t*>(at(L.cids));
     if (exact) {
