@@ -84,7 +84,7 @@ struct KSplits {
   __host__ __device__ bool may(uint32_t s) const { return s == 1 || (s <= most() && nks >= 4 * s); }
   __host__ __device__ uint32_t cost(uint32_t s) const {
     const uint32_t rounds = (tiles * s + 255) / 256, steps = (nks + s - 1) / s;
-    const uint32_t part = s * tiles * (rows < tile ? rows : tile) / tile;
+    const uint32_t part = rows < tile ? s * tiles * rows / tile : s * tiles;
     return f32 ? rounds * (steps + 4) + (rounds == 1 ? steps * 3 / 5 : 0) + part / 64 : rounds * (steps + 12) + part / 8;
   }
 };

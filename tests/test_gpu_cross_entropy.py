@@ -239,7 +239,9 @@ def test_nothing_and_refusals(cuda):
 
 
 @pytest.mark.parametrize("n,dtype,grad", [(500, torch.bfloat16, torch.bfloat16), (500, torch.bfloat16, torch.float32),
-                                          (70, torch.bfloat16, torch.bfloat16), (300, torch.float32, torch.float32)])
+                                          (70, torch.bfloat16, torch.bfloat16), (300, torch.float32, torch.float32),
+                                          (2500, torch.bfloat16, torch.bfloat16), (2500, torch.bfloat16, torch.float32),
+                                          (2500, torch.float32, torch.float32)])
 def test_replay(cuda, n, dtype, grad):
     """Another mask at each replay: how many tokens count is not fixed at the capture."""
     itl = _itl()
@@ -262,3 +264,24 @@ def test_replay(cuda, n, dtype, grad):
             assert torch.equal(a, b), rep
         call(other)
         torch.cuda.synchronize()
+
+
+def test_two_calls_at_once(cuda):
+    """Calls on two streams, each with its own workspace, while neither has ended."""
+    itl = _itl()
+    calls = []
+    for n, V, dtype in ((2500, 3000, torch.bfloat16), (40, 60000, torch.bfloat16), (500, 2000, torch.float32)):
+        H, W, y = _head(n, 256, V, dtype, n, cuda, "some")
+        calls.append(lambda H=H, W=W, y=y: itl.cross_entropy_grad(H, W, y, grad_dtype=H.dtype, label_smoothing=0.1))
+    want = [c() for c in calls]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(device=cuda) for _ in calls]
+    got = []
+    for _ in range(3):
+        for s, c in zip(streams, calls):
+            with torch.cuda.stream(s):
+                got.append(c())
+    torch.cuda.synchronize()
+    for i, out in enumerate(got):
+        for a, b in zip(want[i % len(calls)], out):
+            assert same_bits(a, b)
