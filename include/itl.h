@@ -409,7 +409,7 @@ itl_status itl_cross_entropy(const void* H, const void* W, itl_dtype dtype,
  * logits are kept for one chunk of at most 16,384 tokens at a time, in the
  * workspace. G enters its contractions in the head's dtype (bf16: each entry
  * within 2^-8 of itself, calls of at most 128 tokens 2^-16; with fp32 gradients
- * the one-hot term is applied exactly in fp32). Sums in fp32; fixed orders, no
+ * what the target's entry loses to that is added in fp32). Sums in fp32; fixed orders, no
  * atomics: run-to-run deterministic. n_tok == 0: loss 0, dW zeros. vocab above
  * about 2.1e6 returns ITL_ERR_UNSUPPORTED. */
 itl_status itl_cross_entropy_grad(const void* H, const void* W, itl_dtype dtype,

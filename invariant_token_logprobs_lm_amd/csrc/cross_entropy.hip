@@ -381,6 +381,8 @@ __global__ __launch_bounds__(kF32Threads, 1) void ce_logits_f32_kernel(const cha
 // to 2^-10 or better; with u folded in, every target's entry would carry the
 // same rounding error of u, up to 2^-9 of the whole gradient (measured:
 // dH and dW 0.0027 off at d = 2560, V = 151936 with 16-bit results; 0.0020 so).
+// The -1 is taken off in fp32, before any rounding to bf16: for a sure token p
+// is near 1, and rounded first it would leave of p - 1 its rounding error alone.
 struct GradScale {
   float smoothing, z_weight, scale, inv_vocab;
   int mean;
@@ -642,8 +644,8 @@ __global__ __launch_bounds__(1024) void ce_small_loss_kernel(const int32_t* __re
 // ---- G
 
 // G from the kept logits: 8 vocabulary entries of one token per thread; past
-// the vocabulary zeros. With kExact the target's entry is stored without its
-// -1, which dH and dW then take in fp32.
+// the vocabulary zeros. rest (bf16, nullable): what the target's entry lost to
+// its rounding, which fp32 gradients then take in fp32.
 constexpr int kGradVec = 8;
 
 // Up to this many tokens (bf16), G is held as two bf16 rows per token, its
@@ -654,11 +656,11 @@ constexpr int kGradVec = 8;
 // with many they average out.)
 constexpr int kPairTokens = 128;
 
-template <int kDtype, bool kExact>
+template <int kDtype>
 __global__ __launch_bounds__(256) void ce_grad_logits_kernel(
     const float* __restrict__ logits, const int32_t* __restrict__ ids, const int32_t* __restrict__ count,
     int c0, int cap, int parts, int vocab, int g_rows, const float* __restrict__ lse, GradScale gs,
-    typename Elem<kDtype>::T* __restrict__ Gd) {
+    typename Elem<kDtype>::T* __restrict__ Gd, float* __restrict__ rest) {
   using E = Elem<kDtype>;
   // a workgroup takes 8 tokens of one block: 8 KiB of z side by side
   const int t = blockIdx.y * (256 * kGradVec / kBV) + threadIdx.x / (kBV / kGradVec);
@@ -675,7 +677,7 @@ __global__ __launch_bounds__(256) void ce_grad_logits_kernel(
 #pragma unroll
   for (int r = 0; r < kGradVec; ++r) {
     float x = row.at(z[r]);
-    if (!kExact && v + r == y) x -= 1.0f;
+    if (v + r == y) x -= 1.0f;
     z[r] = v + r < vocab ? x : 0.0f;
   }
   typename E::T* out = Gd + block_at(t, v, g_rows);
@@ -691,21 +693,26 @@ __global__ __launch_bounds__(256) void ce_grad_logits_kernel(
       *reinterpret_cast<uint4*>(out) = make_uint4(w[0], w[1], w[2], w[3]);
       out += (size_t)live * kBV;
     }
+    if (rest) {
+#pragma unroll
+      for (int r = 0; r < kGradVec; ++r)
+        if (v + r == y) rest[t] = z[r];
+    }
   } else {
     reinterpret_cast<float4*>(out)[0] = make_float4(z[0], z[1], z[2], z[3]);
     reinterpret_cast<float4*>(out)[1] = make_float4(z[4], z[5], z[6], z[7]);
   }
 }
 
-// coef[j] = -u for the chunk's live tokens, 0 (and id -1) past them: the
-// exact one-hot term of the fp32 gradients.
-__global__ __launch_bounds__(256) void ce_onehot_kernel(const int32_t* __restrict__ ids, const int32_t* __restrict__ count,
-                                                        int c0, int cap, GradScale gs, float* __restrict__ coef,
-                                                        int32_t* __restrict__ chunk_ids) {
+// The chunk's live tokens' rest in the gradient's unit, 0 (and id -1) past
+// them: the targets' term of the fp32 gradients.
+__global__ __launch_bounds__(256) void ce_rest_kernel(const int32_t* __restrict__ ids, const int32_t* __restrict__ count,
+                                                      int c0, int cap, GradScale gs, float* __restrict__ coef,
+                                                      int32_t* __restrict__ chunk_ids) {
   const int j = blockIdx.x * 256 + threadIdx.x;
   if (j >= cap) return;
   const bool in = j < chunk_live(count, c0, cap);
-  coef[j] = in ? -grad_unit(gs, count) : 0.0f;
+  coef[j] = in ? coef[j] * grad_unit(gs, count) : 0.0f;
   chunk_ids[j] = in ? ids[j] : -1;
 }
 
@@ -772,8 +779,8 @@ __global__ __launch_bounds__(kDtype == 0 ? kThreads8 : kF32Threads, 1) void ce_d
   }
 }
 
-// dH rows: the splits added in order (plus, with coef, the exact one-hot
-// term coef[j] W[y]), four values per thread, to the token's own row. 256
+// dH rows: the splits added in order (plus, with coef, the target's rest
+// coef[j] W[y]), four values per thread, to the token's own row. 256
 // columns per workgroup: with few tokens and many splits, waiting for the
 // partials is all there is (2 tokens, d = 3904, 16 splits: 39 us by one
 // workgroup per token).
@@ -1255,21 +1262,16 @@ hipError_t run_cross_entropy(const CeCall& c, hipStream_t stream) {
 
     T* Gd = reinterpret_cast<T*>(at(L.gd));
     const int g_rows = L.parts * cap;
+    float* coef = exact ? reinterpret_cast<float*>(at(L.coef)) : nullptr;
     if (!row_grad) {
-      const dim3 g_grid((unsigned)(L.vpad / kBV), (unsigned)ceil_div(cap, 256 * kGradVec / kBV));
-      if (exact)
-        hipLaunchKernelGGL((ce_grad_logits_kernel<kDtype, true>), g_grid, dim3(256), 0, stream, z, ids + c0, count,
-                           c0, cap, L.parts, vocab, g_rows, lse + c0, gs, Gd);
-      else
-        hipLaunchKernelGGL((ce_grad_logits_kernel<kDtype, false>), g_grid, dim3(256), 0, stream, z, ids + c0, count,
-                           c0, cap, L.parts, vocab, g_rows, lse + c0, gs, Gd);
+      hipLaunchKernelGGL(ce_grad_logits_kernel<kDtype>,
+                         dim3((unsigned)(L.vpad / kBV), (unsigned)ceil_div(cap, 256 * kGradVec / kBV)), dim3(256), 0, stream,
+                         z, ids + c0, count, c0, cap, L.parts, vocab, g_rows, lse + c0, gs, Gd, coef);
       ITL_CHECK_LAUNCH();
     }
-    float* coef = nullptr;
     int32_t* cids = reinterpret_cast<int32_t*>(at(L.cids));
     if (exact) {
-      coef = reinterpret_cast<float*>(at(L.coef));
-      hipLaunchKernelGGL(ce_onehot_kernel, dim3((unsigned)ceil_div(cap, 256)), dim3(256), 0, stream, ids + c0, count, c0,
+      hipLaunchKernelGGL(ce_rest_kernel, dim3((unsigned)ceil_div(cap, 256)), dim3(256), 0, stream, ids + c0, count, c0,
                          cap, gs, coef, cids);
       ITL_CHECK_LAUNCH();
     }
@@ -1295,7 +1297,7 @@ hipError_t run_cross_entropy(const CeCall& c, hipStream_t stream) {
     void* out = c.dW;
     int add = 0, out_f32 = c.grad_dtype;
     if (exact) {
-      // the chunk's one-hot rows first (every row of the target is written), then the contraction on top
+      // the chunk's targets' rests first (every row of the target is written), then the contraction on top
       float* target = single ? static_cast<float*>(c.dW) : c0 == 0 ? static_cast<float*>(c.dW) : acc;
       e = launch_sampled_dw(Hc, kDtype, cap, d, vocab, cids, coef, target, at(L.sampled), stream);
       if (e != hipSuccess) return e;
