@@ -10,6 +10,16 @@
 
 namespace itl {
 
+// A grid dimension holds less than 2^32 threads: a launch of more (a wavefront
+// for each of 2^26 rows) wraps without an error and leaves the rest undone.
+// flat_grid lays any number of workgroups out in two dimensions, flat_group is
+// a workgroup's number; the last ones may lie past the end.
+inline dim3 flat_grid(long long groups) {
+  const long long x = groups < (1LL << 20) ? groups : 1LL << 20;
+  return dim3((unsigned)x, (unsigned)((groups + x - 1) / x));
+}
+__device__ __forceinline__ long long flat_group() { return (long long)blockIdx.y * gridDim.x + blockIdx.x; }
+
 template <int kDtype>
 struct Elem;
 

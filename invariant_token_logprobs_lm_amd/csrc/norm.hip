@@ -189,8 +189,8 @@ template <int kDtype, bool kFp8, bool kVec, bool kStream, int kWaves, int kGroup
 __global__ __launch_bounds__(kNormThreads) void norm_held_kernel(NormArgs a) {
   using T = typename Elem<kDtype>::T;
   __shared__ float lds[kWaves];
-  const long long row = kWaves == 1 ? (long long)blockIdx.x * (kNormThreads / 64) + (threadIdx.x >> 6) : blockIdx.x;
-  if (row >= a.n_rows) return;  // (whole wavefronts, and only where a wavefront is alone)
+  const long long row = kWaves == 1 ? flat_group() * (kNormThreads / 64) + (threadIdx.x >> 6) : flat_group();
+  if (row >= a.n_rows) return;  // (whole wavefronts where one is alone, else whole workgroups)
   const Columns<kVec> k{a.d, 64 * kWaves, kWaves == 1 ? (int)(threadIdx.x & 63) : (int)threadIdx.x};
   const size_t base = (size_t)row * a.d;
   const float inv_d = (float)a.d;
@@ -280,7 +280,8 @@ __global__ __launch_bounds__(kNormThreads) void norm_rows_kernel(NormArgs a) {
   using T = typename E::T;
   __shared__ float lds[kNormThreads / 64];
   constexpr int kW = kNormThreads / 64;
-  const long long row = blockIdx.x;
+  const long long row = flat_group();
+  if (row >= a.n_rows) return;
   const int d = a.d;
   const size_t base = (size_t)row * d;
   const T* x = static_cast<const T*>(a.x) + base;
@@ -628,7 +629,7 @@ int norm_runs(long long n_rows, long long d) {
 
 template <int kDtype, bool kFp8, bool kVec>
 void run_norm(const NormArgs& a, hipStream_t stream) {
-  const dim3 block(kNormThreads), one((unsigned)ceil_div(a.n_rows, kNormThreads / 64)), four((unsigned)a.n_rows);
+  const dim3 block(kNormThreads), one = flat_grid(ceil_div(a.n_rows, kNormThreads / 64)), four = flat_grid(a.n_rows);
   const int groups = (int)ceil_div(a.d, 8);
 #define ITL_NORM(waves, n, grid)                                                                            \
   if (kVec && !kFp8 && a.stream)                                                                            \
