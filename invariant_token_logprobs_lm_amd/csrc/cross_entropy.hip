@@ -56,6 +56,9 @@ namespace {
 
 constexpr int kCeChunk = 16384;    // tokens per chunk with the gradient (a multiple of kBT)
 constexpr int kCeF32Chunk = 4096;  // the same of fp32 heads without it (their logits are kept too)
+// bf16 heads without it: the forward's workgroups of 512 threads, up to 256 per
+// 256 tokens, and the merge's 16 threads per token then fit a grid dimension
+constexpr int kCeLossChunk = 1 << 22;
 static_assert(kCeChunk % kBT == 0, "chunks hold whole token blocks");
 
 long long round_up(long long x, long long m) { return (x + m - 1) / m * m; }
@@ -179,8 +182,9 @@ __device__ __forceinline__ int chunk_live(const int32_t* count, int c0, int cap)
 __global__ __launch_bounds__(256) void ce_gather_kernel(const uint4* __restrict__ H, const int32_t* __restrict__ rows,
                                                         const int32_t* __restrict__ slot, const int32_t* __restrict__ count,
                                                         int c0, int cap, int parts, int row_chunks, uint4* __restrict__ Hc,
-                                                        uint4* __restrict__ dH, int grad_chunks) {
-  const int j = blockIdx.x;
+                                                        uint4* __restrict__ dH, int grad_chunks, long long n) {
+  const long long j = flat_group();
+  if (j >= n) return;
   if (dH && slot[j] < 0)
     for (int i = threadIdx.x; i < grad_chunks; i += 256) dH[(size_t)j * grad_chunks + i] = make_uint4(0u, 0u, 0u, 0u);
   const int live = chunk_live(count, c0, cap);
@@ -542,7 +546,7 @@ __global__ __launch_bounds__(256) void ce_token_loss_kernel(const typename Elem<
   using E = Elem<kDtype>;
   __shared__ double lds[4];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int t = blockIdx.x * 4 + wave;
+  const long long group = flat_group(), t = group * 4 + wave;
   const int j = t < n ? slot[t] : -1;
   float l = 0.0f, s = 0.0f;
   if (j >= 0) {
@@ -579,7 +583,7 @@ __global__ __launch_bounds__(256) void ce_token_loss_kernel(const typename Elem<
     lds[wave] = (double)l;
   }
   __syncthreads();
-  if (threadIdx.x == 0) part[blockIdx.x] = ((lds[0] + lds[1]) + lds[2]) + lds[3];
+  if (threadIdx.x == 0 && group * 4 < n) part[group] = ((lds[0] + lds[1]) + lds[2]) + lds[3];
 }
 
 // The fp64 sums in a fixed order, over N (0 when no token counts).
@@ -1031,7 +1035,7 @@ __global__ __launch_bounds__(kFewThreads, 4) void ce_dw_few_kernel(const char* _
 
 // The accumulated fp32 dW rounded to bf16.
 __global__ __launch_bounds__(256) void ce_round_kernel(const float4* __restrict__ in, long long n4, uint2* __restrict__ out) {
-  const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
+  const long long i = flat_group() * 256 + threadIdx.x;
   if (i >= n4) return;
   const float4 v = in[i];
   out[i] = make_uint2((uint32_t)Elem<0>::from_f(v.x) | ((uint32_t)Elem<0>::from_f(v.y) << 16),
@@ -1039,7 +1043,7 @@ __global__ __launch_bounds__(256) void ce_round_kernel(const float4* __restrict_
 }
 
 __global__ __launch_bounds__(256) void ce_add_kernel(const float4* __restrict__ in, long long n4, float4* __restrict__ out) {
-  const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
+  const long long i = flat_group() * 256 + threadIdx.x;
   if (i >= n4) return;
   const float4 v = in[i];
   float4 o = out[i];
@@ -1049,7 +1053,7 @@ __global__ __launch_bounds__(256) void ce_add_kernel(const float4* __restrict__ 
 
 // out = 0 in 16-byte pieces; *one = 0 where given.
 __global__ __launch_bounds__(256) void ce_clear_kernel(uint4* __restrict__ out, long long n16, float* __restrict__ one) {
-  const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
+  const long long i = flat_group() * 256 + threadIdx.x;
   if (i < n16) out[i] = make_uint4(0u, 0u, 0u, 0u);
   if (one && i == 0) *one = 0.0f;
 }
@@ -1091,8 +1095,7 @@ CeLayout ce_layout(long long n_tok, long long d, long long vocab, int dtype, boo
   CeLayout L{};
   const int es = dtype == 0 ? 2 : 4;
   L.vpad = (int)round_up(vocab, kBV);
-  // bf16 without the gradient keeps no logits: one chunk
-  L.cap = (int)(grad ? std::min<long long>(kCeChunk, n_tok) : dtype == 1 ? std::min<long long>(kCeF32Chunk, n_tok) : n_tok);
+  L.cap = (int)std::min<long long>(grad ? kCeChunk : dtype == 1 ? kCeF32Chunk : kCeLossChunk, n_tok);
   L.parts = dtype == 0 && grad && n_tok <= kPairTokens ? 2 : 1;
   size_t off = 0;
   auto take = [&](size_t bytes) {
@@ -1181,7 +1184,7 @@ hipError_t run_cross_entropy(const CeCall& c, hipStream_t stream) {
     hipLaunchKernelGGL(ce_clear_kernel, dim3(1), dim3(256), 0, stream, reinterpret_cast<uint4*>(c.loss), 0LL, c.loss);
     if (grad) {
       const long long n16 = c.vocab * c.d * (c.grad_dtype == 0 ? 2 : 4) / 16;
-      hipLaunchKernelGGL(ce_clear_kernel, dim3((unsigned)ceil_div(n16, 256)), dim3(256), 0, stream,
+      hipLaunchKernelGGL(ce_clear_kernel, flat_grid(ceil_div(n16, 256)), dim3(256), 0, stream,
                          static_cast<uint4*>(c.dW), n16, nullptr);
     }
     return hipGetLastError();
@@ -1231,10 +1234,10 @@ hipError_t run_cross_entropy(const CeCall& c, hipStream_t stream) {
     const int c0 = (int)first;
     const int cap = std::min(L.cap, n - c0);
     if (!direct)
-      hipLaunchKernelGGL(ce_gather_kernel, dim3((unsigned)(c0 == 0 ? n : cap)), dim3(256), 0, stream,
+      hipLaunchKernelGGL(ce_gather_kernel, flat_grid(c0 == 0 ? n : cap), dim3(256), 0, stream,
                          reinterpret_cast<const uint4*>(H), rows, slot, count, c0, cap, L.parts, row_chunks,
                          reinterpret_cast<uint4*>(Hc), c0 == 0 ? static_cast<uint4*>(c.dH) : nullptr,
-                         d * (c.grad_dtype == 0 ? 2 : 4) / 16);
+                         d * (c.grad_dtype == 0 ? 2 : 4) / 16, (long long)(c0 == 0 ? n : cap));
     float* z = reinterpret_cast<float*>(at(L.z));
     const char* h_rows = direct ? reinterpret_cast<const char*>(H) : Hc;
     const char* w_rows = reinterpret_cast<const char*>(W);
@@ -1335,12 +1338,12 @@ hipError_t run_cross_entropy(const CeCall& c, hipStream_t stream) {
     else dw(std::integral_constant<int, kDwRound>{});
     ITL_CHECK_LAUNCH();
     if (exact && !single && c0 > 0) {
-      hipLaunchKernelGGL(ce_add_kernel, dim3((unsigned)ceil_div((long long)vocab * d / 4, 256)), dim3(256), 0, stream,
+      hipLaunchKernelGGL(ce_add_kernel, flat_grid(ceil_div((long long)vocab * d / 4, 256)), dim3(256), 0, stream,
                          reinterpret_cast<const float4*>(acc), (long long)vocab * d / 4, static_cast<float4*>(c.dW));
       ITL_CHECK_LAUNCH();
     }
     if (!exact && !single && first + L.cap >= n && c.grad_dtype == 0) {
-      hipLaunchKernelGGL(ce_round_kernel, dim3((unsigned)ceil_div((long long)vocab * d / 4, 256)), dim3(256), 0, stream,
+      hipLaunchKernelGGL(ce_round_kernel, flat_grid(ceil_div((long long)vocab * d / 4, 256)), dim3(256), 0, stream,
                          reinterpret_cast<const float4*>(acc), (long long)vocab * d / 4, static_cast<uint2*>(c.dW));
       ITL_CHECK_LAUNCH();
     }
@@ -1349,7 +1352,7 @@ hipError_t run_cross_entropy(const CeCall& c, hipStream_t stream) {
     hipLaunchKernelGGL(ce_small_loss_kernel, dim3(1), dim3(1024), 0, stream, c.targets, n, vocab, direct ? nullptr : slot,
                        direct ? nullptr : count, lp, lse, c.z_weight, c.mean, c.token_loss, c.lse, c.loss);
   } else {
-    hipLaunchKernelGGL(ce_token_loss_kernel<kDtype>, dim3((unsigned)ceil_div(n, 4)), dim3(256), 0, stream, H, n, d, slot, lp,
+    hipLaunchKernelGGL(ce_token_loss_kernel<kDtype>, flat_grid(ceil_div(n, 4)), dim3(256), 0, stream, H, n, d, slot, lp,
                        lse, wmean, c.smoothing, c.z_weight, c.token_loss, c.lse, loss_part);
     hipLaunchKernelGGL(ce_loss_kernel, dim3(1), dim3(1024), 0, stream, loss_part, (int)ceil_div(n, 4), count, c.mean,
                        c.loss);
