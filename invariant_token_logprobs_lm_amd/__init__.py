@@ -781,7 +781,9 @@ def adamw_plan(params, grads, *, lr, weight_decay=0.0, state_bits=32, step=None,
     else:
         plan.master = None if master is False else state("master", master, torch.float32, total)
     plan.step = state("step", step, torch.int64, 1)
-    plan.lr = torch.full((1,), float(lr), device=dev) if not isinstance(lr, torch.Tensor) else state("lr", lr, torch.float32, 1)
+    if not isinstance(lr, torch.Tensor):  # (the default dtype may be another)
+        lr = torch.full((1,), float(lr), dtype=torch.float32, device=dev)
+    plan.lr = state("lr", lr, torch.float32, 1)
     plan._table = host[:nbytes.value].to(dev)
     plan._workspace = torch.empty(int(lib.itl_adamw_step_workspace_bytes()), dtype=torch.uint8, device=dev)
     plan._args = (_ptr(plan._table), nbytes.value, state_bits, _ptr(plan.exp_avg), _ptr(plan.exp_avg_sq),
