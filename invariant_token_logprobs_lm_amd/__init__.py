@@ -28,6 +28,7 @@ Entry points (same names as the C ABI without the ``itl_`` prefix):
 """
 
 import ctypes
+import operator
 import os
 
 import torch
@@ -709,10 +710,50 @@ class AdamWPlan:
     exp_avg_scale, exp_avg_sq_scale (fp32, one per 256). master: fp32 weights
     of the bf16 tensors, or None. step (int64 [1]) and lr (fp32 [1]) are device
     tensors: a captured step sees what they hold when it is replayed.
+
+    The step uses the addresses that the tensors had when the plan was made. So
+    plan.lr = x and plan.step = n write into the tensors that the plan holds,
+    everything else is fixed (its tensors may be written in place), a plan is
+    not copied or pickled (save its tensors), and a step whose tensors lie
+    elsewhere by then (``.data`` assigned, storage resized) is refused; a
+    replayed one cannot look.
     """
 
     __slots__ = ("params", "grads", "offsets", "state_bits", "exp_avg", "exp_avg_sq", "exp_avg_scale",
-                 "exp_avg_sq_scale", "master", "lr", "step", "device", "_table", "_workspace", "_args")
+                 "exp_avg_sq_scale", "master", "lr", "step", "device", "_table", "_workspace", "_args", "_tensors",
+                 "_addresses")
+
+    def __setattr__(self, name, value):
+        try:
+            held = getattr(self, name)
+        except AttributeError:  # being made
+            return object.__setattr__(self, name, value)
+        if value is held:  # (plan.lr *= 0.5)
+            return
+        if name not in ("lr", "step"):
+            raise AttributeError(f"{name} of an AdamWPlan is fixed: write into its tensors, or make another plan")
+        if isinstance(value, torch.Tensor) and value.numel() != 1:
+            raise ValueError(f"{name} must have 1 element, got {value.numel()}")
+        with torch.no_grad():
+            if isinstance(value, torch.Tensor):
+                held.copy_(value.reshape(1))
+            else:
+                held.fill_(float(value) if name == "lr" else operator.index(value))
+
+    def __delattr__(self, name):
+        raise AttributeError(f"{name} of an AdamWPlan is fixed")
+
+    def __reduce_ex__(self, protocol):
+        raise TypeError("an AdamWPlan holds device addresses: save its tensors and make another plan from them")
+
+    def _named(self):
+        """(name, tensor) of everything whose address a step uses."""
+        for name in ("params", "grads"):
+            yield from ((f"{name}[{i}]", t) for i, t in enumerate(getattr(self, name)))
+        for name in ("exp_avg", "exp_avg_sq", "exp_avg_scale", "exp_avg_sq_scale", "master", "lr", "step", "_table",
+                     "_workspace"):
+            if getattr(self, name) is not None:
+                yield name, getattr(self, name)
 
 
 def adamw_plan(params, grads, *, lr, weight_decay=0.0, state_bits=32, step=None, master=None, exp_avg=None,
@@ -751,7 +792,8 @@ def adamw_plan(params, grads, *, lr, weight_decay=0.0, state_bits=32, step=None,
     _check(lib.itl_adamw_plan(table, len(params), _ptr(host), nbytes.value))
 
     plan = AdamWPlan()
-    plan.params, plan.grads, plan.offsets, plan.state_bits, plan.device = params, grads, offsets, state_bits, dev
+    plan.params, plan.grads, plan.offsets = tuple(params), tuple(grads), tuple(offsets)
+    plan.state_bits, plan.device = state_bits, dev
 
     def state(name, given, dtype, n):
         if given is None:
@@ -789,6 +831,8 @@ def adamw_plan(params, grads, *, lr, weight_decay=0.0, state_bits=32, step=None,
     plan._args = (_ptr(plan._table), nbytes.value, state_bits, _ptr(plan.exp_avg), _ptr(plan.exp_avg_sq),
                   _ptr(plan.exp_avg_scale), _ptr(plan.exp_avg_sq_scale), _ptr(plan.master), _ptr(plan.lr),
                   _ptr(plan.step))
+    plan._tensors = [t for _, t in plan._named()]
+    plan._addresses = [*map(torch.Tensor.data_ptr, plan._tensors)]
     return plan
 
 
@@ -799,6 +843,9 @@ def adamw_step(plan, *, betas=(0.9, 0.999), eps=1e-8, max_norm=None, grad_norm=N
     norm that is not finite skips the step."""
     if not isinstance(plan, AdamWPlan):
         raise TypeError("plan must come from adamw_plan")
+    if [*map(torch.Tensor.data_ptr, plan._tensors)] != plan._addresses:
+        moved = [name for (name, t), at in zip(plan._named(), plan._addresses) if t.data_ptr() != at]
+        raise ValueError(f"{', '.join(moved)} moved since the plan was made: make another plan")
     if grad_norm is not None:
         _need(grad_norm, "grad_norm", (torch.float32,), device=plan.device, ndim=1)
         if grad_norm.shape[0] != 1:

@@ -2,6 +2,9 @@
 learning rate and the count by assignment, everything else fixed; tensors that
 have moved; autograd's view of updated weights; states that share memory."""
 
+import copy
+import pickle
+
 import pytest
 import torch
 
@@ -38,3 +41,78 @@ def test_rate_is_fp32_whatever_the_default_type(cuda, default):
         torch.set_default_dtype(before)
     assert same_bits(norm, itl.adamw_step(want, max_norm=1.0))
     assert torch.equal(p[0], q[0]) and same_bits(p[1], q[1])
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_rate_and_count_are_assigned_into_the_plans_tensors(cuda, bits):
+    itl = _itl()
+    p, g = _tensors(cuda)
+    q, h = _tensors(cuda)
+    plan = itl.adamw_plan(p, g, lr=1e-2, state_bits=bits)
+    lr, step = plan.lr, plan.step
+    plan.lr = 5e-6
+    assert plan.lr is lr and float(lr) == float(torch.tensor(5e-6))
+    plan.lr = torch.tensor(2e-3, device=cuda, dtype=torch.float64)
+    assert plan.lr is lr and lr.dtype == torch.float32 and float(lr) == float(torch.tensor(2e-3))
+    plan.lr *= 0.5
+    plan.step = 7
+    plan.step += 2
+    assert plan.lr is lr and plan.step is step and int(step) == 9
+    for bad in (torch.zeros(2, device=cuda), [0.1, 0.2], "rate", None):
+        with pytest.raises((TypeError, ValueError)):
+            plan.lr = bad
+    other = itl.adamw_plan(q, h, lr=lr.clone(), step=step.clone(), state_bits=bits)
+    itl.adamw_step(plan)
+    itl.adamw_step(other)
+    assert int(plan.step) == 10 and torch.equal(p[0], q[0]) and same_bits(p[1], q[1])
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_the_rest_of_a_plan_is_fixed(cuda, bits):
+    itl = _itl()
+    p, g = _tensors(cuda)
+    plan = itl.adamw_plan(p, g, lr=1e-2, state_bits=bits)
+    names = [n for n in type(plan).__slots__ if n not in ("lr", "step")]
+    for name in names:
+        held = getattr(plan, name)
+        with pytest.raises(AttributeError):
+            setattr(plan, name, held.clone() if isinstance(held, torch.Tensor) else 0)
+        assert getattr(plan, name) is held
+    for name in names + ["lr", "step"]:
+        with pytest.raises(AttributeError):
+            delattr(plan, name)
+    for seq in (plan.params, plan.grads, plan.offsets):
+        with pytest.raises(TypeError):
+            seq[0] = seq[1]
+    plan.exp_avg *= 0  # (in place: the same tensor)
+    for make in (copy.copy, copy.deepcopy, pickle.dumps):
+        with pytest.raises(TypeError):
+            make(plan)
+    itl.adamw_step(plan)
+
+
+@pytest.mark.parametrize("which", ["params", "grads", "exp_avg", "exp_avg_sq", "master", "lr", "step"])
+def test_a_tensor_that_moved_is_refused(cuda, which):
+    itl = _itl()
+    p, g = _tensors(cuda)
+    plan = itl.adamw_plan(p, g, lr=1e-2)
+    t = getattr(plan, which)
+    t = t[1] if isinstance(t, tuple) else t
+    kept, before = t.data, [x.clone() for x in (*p, plan.exp_avg, plan.step)]
+    t.data = kept.clone()
+    with pytest.raises(ValueError, match=which):
+        itl.adamw_step(plan)
+    t.data = kept
+    for a, b in zip((*p, plan.exp_avg, plan.step), before):
+        assert torch.equal(a, b)
+    itl.adamw_step(plan)
+    assert int(plan.step) == 1
+
+
+def test_freed_storage_is_refused(cuda):
+    itl = _itl()
+    p, g = _tensors(cuda)
+    plan = itl.adamw_plan(p, g, lr=1e-2)
+    g[0].untyped_storage().resize_(0)
+    with pytest.raises(ValueError, match="grads"):
+        itl.adamw_step(plan)
