@@ -855,6 +855,8 @@ def adamw_step(plan, *, betas=(0.9, 0.999), eps=1e-8, max_norm=None, grad_norm=N
     _launch(plan.device, lib.itl_adamw_step, *plan._args, betas[0], betas[1], eps,
             float("inf") if max_norm is None else max_norm, _ptr(grad_norm), _ptr(plan._workspace),
             plan._workspace.numel())
+    # graphs that saved the weights before the step must not go backward with the new ones
+    torch.autograd.graph.increment_version(plan.params)
     return grad_norm
 
 

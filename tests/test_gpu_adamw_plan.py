@@ -116,3 +116,19 @@ def test_freed_storage_is_refused(cuda):
     g[0].untyped_storage().resize_(0)
     with pytest.raises(ValueError, match="grads"):
         itl.adamw_step(plan)
+
+
+def test_autograd_sees_that_the_weights_changed(cuda):
+    itl = _itl()
+    p, g = _tensors(cuda)
+    w = p[1].requires_grad_()
+    plan = itl.adamw_plan(p, g, lr=1e-2)
+    x = torch.ones_like(w, requires_grad=True)
+    y = (x * w).sum()  # saves w
+    version = p[0]._version, w._version
+    itl.adamw_step(plan)
+    assert p[0]._version > version[0] and w._version > version[1]
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        y.backward()
+    (x * w).sum().backward()
+    assert same_bits(x.grad, w.detach())
