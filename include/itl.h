@@ -463,8 +463,11 @@ size_t itl_adamw_step_workspace_bytes(void);
  * master (nullable) fp32 [state_elements]: the weights of bf16 tensors, which
  * then get its rounding (without it a bf16 weight is its own; fp32 weights
  * never use it). lr fp32 [1] and step int64 [1] are device memory, so that a
- * captured step replays with the values of the time of the replay. Run-to-run
- * deterministic. Two steps of one plan, or two that share a workspace, must be
+ * captured step replays with the values of the time of the replay. Whatever
+ * the step writes must not share memory with anything else of the call; of
+ * states, master, step, grad_norm, workspace, lr and the plan it is refused
+ * (ITL_ERR_INVALID_ARG) as far as 256 elements per piece of the plan tell.
+ * Run-to-run deterministic. Two steps of one plan, or two that share a workspace, must be
  * ordered by the caller. */
 itl_status itl_adamw_step(const void* plan, size_t plan_bytes, int32_t state_bits,
                           void* exp_avg, void* exp_avg_sq, float* exp_avg_scale, float* exp_avg_sq_scale,

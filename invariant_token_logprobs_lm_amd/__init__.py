@@ -756,13 +756,28 @@ class AdamWPlan:
                 yield name, getattr(self, name)
 
 
+def _refuse_shared(plan):
+    """What a step writes (all but gradients and rate) may share memory with nothing else."""
+    spans = sorted((t.data_ptr(), t.data_ptr() + t.numel() * t.element_size(), name) for name, t in plan._named() if t.numel())
+    any_end = written_end = 0, None
+    for start, end, name in spans:
+        written = not name.startswith("grads") and name != "lr"
+        last = any_end if written else written_end
+        if start < last[0]:
+            raise ValueError(f"{last[1]} and {name} share memory")
+        any_end = max(any_end, (end, name))
+        if written:
+            written_end = max(written_end, (end, name))
+
+
 def adamw_plan(params, grads, *, lr, weight_decay=0.0, state_bits=32, step=None, master=None, exp_avg=None,
                exp_avg_sq=None, exp_avg_scale=None, exp_avg_sq_scale=None):
     """Lay out an AdamW step over many tensors (any mix of bf16 and fp32).
 
     params and grads: lists of contiguous tensors of equal sizes, kept by the
     plan and used where they lie: the gradients of every step are written into
-    them. lr: a float or a device tensor fp32 [1]; weight_decay: a float or one
+    them. Nothing that a step writes may share memory with another tensor of the
+    plan. lr: a float or a device tensor fp32 [1]; weight_decay: a float or one
     per tensor. States start as zeros (step 0) unless given, as from a
     checkpoint; master: fp32 flat weights, True (from the params; the default
     where any is bf16) or False for none.
@@ -831,6 +846,7 @@ def adamw_plan(params, grads, *, lr, weight_decay=0.0, state_bits=32, step=None,
     plan._args = (_ptr(plan._table), nbytes.value, state_bits, _ptr(plan.exp_avg), _ptr(plan.exp_avg_sq),
                   _ptr(plan.exp_avg_scale), _ptr(plan.exp_avg_sq_scale), _ptr(plan.master), _ptr(plan.lr),
                   _ptr(plan.step))
+    _refuse_shared(plan)
     plan._tensors = [t for _, t in plan._named()]
     plan._addresses = [*map(torch.Tensor.data_ptr, plan._tensors)]
     return plan

@@ -678,6 +678,14 @@ itl_status itl_adamw_step(const void* plan, size_t plan_bytes, int32_t state_bit
   if (!workspace || workspace_bytes < itl::adamw_workspace_bytes())
     return fail(ITL_ERR_WORKSPACE, "workspace missing or smaller than itl_adamw_step_workspace_bytes()");
   if (misaligned(workspace)) return fail(ITL_ERR_WORKSPACE, "workspace must be 256-byte aligned");
+  // (the states' sizes are in the plan, on the device: 256 elements a piece are there at least)
+  const int64_t least = pieces * itl::kAdamBlock, code = state_bits == 8 ? 1 : 4;
+  const bool scales = state_bits == 8;
+  if (outputs_share({{exp_avg, least * code}, {exp_avg_sq, least * code}, {scales ? exp_avg_scale : nullptr, pieces * 4},
+                     {scales ? exp_avg_sq_scale : nullptr, pieces * 4}, {master, least * 4}, {step, 8}, {grad_norm, 4},
+                     {workspace, (int64_t)itl::adamw_workspace_bytes()}},
+                    {{lr, 4}, {plan, (int64_t)plan_bytes}}))
+    return fail(ITL_ERR_INVALID_ARG, "states, step, grad_norm or workspace share memory with each other, lr or the plan");
   const bool with_norm = grad_norm || max_norm < __builtin_inff();
   hipError_t e = itl::launch_adamw_step(plan, pieces, state_bits, exp_avg, exp_avg_sq, exp_avg_scale, exp_avg_sq_scale,
                                         master, lr, step, beta1, beta2, eps, with_norm, max_norm, grad_norm, workspace,

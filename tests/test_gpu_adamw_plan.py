@@ -132,3 +132,30 @@ def test_autograd_sees_that_the_weights_changed(cuda):
         y.backward()
     (x * w).sum().backward()
     assert same_bits(x.grad, w.detach())
+
+
+def test_states_that_share_memory_are_refused(cuda):
+    itl = _itl()
+    p, g = _tensors(cuda, dtypes=(torch.bfloat16, torch.bfloat16))
+    total = 5120 + 512
+    f32 = lambda n=total: torch.zeros(n, device=cuda)
+    u8 = lambda n=total: torch.zeros(n, dtype=torch.uint8, device=cuda)
+    s, long = f32(), f32(2 * total)
+    scales = f32(2 * total // 256)
+    w32 = f32()
+    bad = [
+        dict(exp_avg=s, exp_avg_sq=s), dict(exp_avg=s, master=s), dict(exp_avg_sq=long[:total], master=long[256:256 + total]),
+        dict(exp_avg=s, lr=s[5:6]), dict(exp_avg=s, step=s.view(torch.int64)[9:10]),
+        dict(state_bits=8, exp_avg=u8(), exp_avg_scale=scales[:total // 256], exp_avg_sq_scale=scales[8:8 + total // 256]),
+        dict(state_bits=8, exp_avg=s.view(torch.uint8)[:total], exp_avg_sq=s.view(torch.uint8)[1024:1024 + total]),
+    ]
+    for kw in bad:
+        with pytest.raises(ValueError, match="share"):
+            itl.adamw_plan(p, g, **{"lr": 0.1, **kw})
+    with pytest.raises(ValueError, match="share"):  # a state over the weights, or over a gradient
+        itl.adamw_plan([w32[:5000]], [g[0]], lr=0.1, exp_avg=w32[:5120])
+    with pytest.raises(ValueError, match="share"):
+        itl.adamw_plan([p[0]], [w32[:5000]], lr=0.1, exp_avg_sq=w32[:5120])
+    plan = itl.adamw_plan(p, g, lr=0.1, exp_avg=long[:total], exp_avg_sq=long[total:], master=s)  # neighbours do not
+    itl.adamw_step(plan)
+    assert bool(s[:5000].any())
