@@ -606,12 +606,13 @@ def residual_norm_backward_workspace_bytes(n_rows, d):
 
 
 def residual_norm_backward(du, dh, h, y, w_pre, rstd_pre, *, w_post=None, rstd_post=None, gate=None, scale=1.0,
-                           dx=None, dy=None, workspace=None):
+                           dx=None, dy=None, dw_pre=None, dw_post=None, dgate=None, workspace=None):
     """Gradients of residual_norm: du [n, d] (h's dtype or fp32) and dh [n, d]
     (h's dtype, or None) are those of u and h. Returns (dx, dy, dw_pre fp32
     [d], dw_post fp32 [d], dgate: fp32 [d] for a shared gate, else like gate);
-    dy, dw_post, dgate are None where y, w_post, gate are. dx is the gradient
-    of the residual stream x (all of h's)."""
+    dy, dw_post, dgate are None where y, w_post, gate are. Each may be given as
+    a tensor to write into (the gradients that an adamw_plan holds). dx is the
+    gradient of the residual stream x (all of h's)."""
     n, d, stride = _norm_operands(h, y, w_pre, w_post, gate, "h")
     dev = h.device
     _need(du, "du", (h.dtype, torch.float32), device=dev, ndim=2)
@@ -628,11 +629,12 @@ def residual_norm_backward(du, dh, h, y, w_pre, rstd_pre, *, w_post=None, rstd_p
             raise ValueError(f"{name} must have {n} elements")
     dx = _new((n, d), h.dtype, h, "dx", dx)
     dy = None if y is None else _new((n, d), h.dtype, h, "dy", dy)
-    dw_pre = torch.empty(d, dtype=torch.float32, device=dev)
-    dw_post = None if w_post is None else torch.empty(d, dtype=torch.float32, device=dev)
-    dgate = None
-    if gate is not None:
-        dgate = torch.empty(d, dtype=torch.float32, device=dev) if stride == 0 else torch.empty_like(gate)
+    dw_pre = _new((d,), torch.float32, h, "dw_pre", dw_pre)
+    dw_post = None if w_post is None else _new((d,), torch.float32, h, "dw_post", dw_post)
+    if gate is None:
+        dgate = None
+    else:
+        dgate = _new((d,), torch.float32, h, "dgate", dgate) if stride == 0 else _new((n, d), h.dtype, h, "dgate", dgate)
     workspace = _workspace(workspace, residual_norm_backward_workspace_bytes(n, d), dev)
     _launch(dev, lib.itl_residual_norm_backward, _ptr(du), _HEAD_DTYPES[du.dtype], _ptr(dh), _ptr(h), _ptr(y),
             _ptr(gate), stride, _ptr(w_post), _ptr(w_pre), _ptr(rstd_pre),
