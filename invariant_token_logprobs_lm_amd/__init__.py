@@ -567,6 +567,22 @@ def _norm_operands(x, y, w_pre, w_post, gate, first):
     return n, d, 0 if gate.dim() == 1 else d
 
 
+def _refuse_unwritten(**outputs):
+    """name=(tensor, its operand, the operand's name): an output given without its operand."""
+    for name, (out, operand, needed) in outputs.items():
+        if out is not None and operand is None:
+            raise ValueError(f"{name} needs {needed}")
+
+
+def _stream_rows(x, y, h, n, d):
+    """residual_norm's h: x itself without y."""
+    if y is None:
+        if h is not x:
+            _refuse_unwritten(h=(h, y, "y"))
+        return x
+    return _new((n, d), x.dtype, x, "h", h)
+
+
 def residual_norm(x, y, w_pre, *, w_post=None, gate=None, scale=1.0, eps=1e-6, h=None, u=None):
     """h = x + scale * gate * p and u = rmsnorm(h) * w_pre, where p = y, or
     rmsnorm(y) * w_post with w_post given.
@@ -576,7 +592,7 @@ def residual_norm(x, y, w_pre, *, w_post=None, gate=None, scale=1.0, eps=1e-6, h
     [n] or None).
     """
     n, d, stride = _norm_operands(x, y, w_pre, w_post, gate, "x")
-    h = x if y is None else _new((n, d), x.dtype, x, "h", h)
+    h = _stream_rows(x, y, h, n, d)
     u = _new((n, d), x.dtype, x, "u", u)
     rstd_pre = torch.empty(n, dtype=torch.float32, device=x.device)
     rstd_post = None if w_post is None else torch.empty(n, dtype=torch.float32, device=x.device)
@@ -590,7 +606,7 @@ def residual_norm_fp8(x, y, w_pre, *, w_post=None, gate=None, scale=1.0, eps=1e-
     (fp32 [n]), as lmhead_logprob_fp8 takes them; d a multiple of 128. Returns
     (h, Uq, u_scale, rstd_pre, rstd_post)."""
     n, d, stride = _norm_operands(x, y, w_pre, w_post, gate, "x")
-    h = x if y is None else _new((n, d), x.dtype, x, "h", h)
+    h = _stream_rows(x, y, h, n, d)
     Uq = _new((n, d), torch.uint8, x, "Uq", Uq)
     u_scale = _new((n,), torch.float32, x, "u_scale", u_scale)
     rstd_pre = torch.empty(n, dtype=torch.float32, device=x.device)
@@ -627,6 +643,7 @@ def residual_norm_backward(du, dh, h, y, w_pre, rstd_pre, *, w_post=None, rstd_p
         _need(t, name, (torch.float32,), device=dev, ndim=1)
         if t.shape[0] != n:
             raise ValueError(f"{name} must have {n} elements")
+    _refuse_unwritten(dy=(dy, y, "y"), dw_post=(dw_post, w_post, "w_post"), dgate=(dgate, gate, "gate"))
     dx = _new((n, d), h.dtype, h, "dx", dx)
     dy = None if y is None else _new((n, d), h.dtype, h, "dy", dy)
     dw_pre = _new((d,), torch.float32, h, "dw_pre", dw_pre)

@@ -1,5 +1,6 @@
 """The training loop as the README writes it: one plan over gradients that every
-step's backward writes into, with no copies."""
+step's backward writes into, with no copies; outputs that have no operand are
+refused rather than left unwritten."""
 
 import pytest
 import torch
@@ -69,3 +70,18 @@ def test_column_gradients_given(cuda):
     got = call(dw_pre=f(128), dw_post=f(128), dgate=f(128))
     for a, b in zip(want, got):
         assert torch.equal(a, b)
+def test_outputs_without_their_operand_are_refused(cuda):
+    import invariant_token_logprobs_lm_amd as itl
+
+    t, batches = _model(cuda)
+    x = batches[0][0]
+    f = lambda *s, dt=torch.float32: torch.empty(*s, dtype=dt, device=cuda)
+    b = f(200, 128, dt=torch.bfloat16)
+    with pytest.raises(ValueError, match="h needs y"):
+        itl.residual_norm(x, None, t["w_pre"], h=b)
+    with pytest.raises(ValueError, match="h needs y"):
+        itl.residual_norm_fp8(x, None, t["w_pre"], h=b)
+    h, u, r_pre, _ = itl.residual_norm(x, None, t["w_pre"], h=x)  # (h is x either way)
+    for kw in (dict(dy=b), dict(dw_post=f(128)), dict(dgate=f(128))):
+        with pytest.raises(ValueError, match="needs"):
+            itl.residual_norm_backward(b, None, h, None, t["w_pre"], r_pre, **kw)
