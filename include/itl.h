@@ -462,7 +462,7 @@ size_t itl_adamw_step_workspace_bytes(void);
  * touched; in 8 bits written as zeros up to the next multiple of 8).
  * master (nullable) fp32 [state_elements]: the weights of bf16 tensors, which
  * then get its rounding (without it a bf16 weight is its own; fp32 weights
- * never use it). lr fp32 [1] and step int64 [1] are device memory, so that a
+ * never use it). eps in (0, 1), in fp32 too. lr fp32 [1] and step int64 [1] are device memory, so that a
  * captured step replays with the values of the time of the replay. Whatever
  * the step writes must not share memory with anything else of the call; of
  * states, master, step, grad_norm, workspace, lr and the plan it is refused

@@ -666,7 +666,7 @@ itl_status itl_adamw_step(const void* plan, size_t plan_bytes, int32_t state_bit
   if (state_bits != 8 && state_bits != 32) return fail(ITL_ERR_UNSUPPORTED, "state_bits must be 8 or 32");
   if (!(beta1 >= 0.0 && beta1 < 1.0) || !(beta2 >= 0.0 && beta2 < 1.0))
     return fail(ITL_ERR_INVALID_ARG, "beta1 and beta2 must be in [0, 1)");
-  if (!(eps > 0.0 && eps < 1.0)) return fail(ITL_ERR_INVALID_ARG, "eps must be in (0, 1)");
+  if (!((float)eps > 0.0f && eps < 1.0)) return fail(ITL_ERR_INVALID_ARG, "eps must be in (0, 1) in fp32");
   if (!(max_norm > 0.0f)) return fail(ITL_ERR_INVALID_ARG, "max_norm must be > 0 (infinity: no clipping)");
   const int64_t pieces = (int64_t)(plan_bytes / sizeof(itl::AdamPiece));
   if (pieces > INT32_MAX) return fail(ITL_ERR_UNSUPPORTED, "too many elements for one plan");

@@ -33,3 +33,10 @@ def test_shared_states_are_refused(itl):
             assert _step(itl, bits=32, **over) == INVALID and "share" in itl.lib.itl_last_error().decode()
         assert _step(itl, **over) == INVALID and "share" in itl.lib.itl_last_error().decode(), over
     assert _step(itl, bits=32, v=at(1) + 64 * 1024 - 16) == INVALID
+
+
+def test_eps_that_vanishes_in_fp32_is_refused(itl):
+    """The kernel adds eps in fp32: where it is 0 a weight without a gradient becomes 0 / 0."""
+    for eps in (1e-46, 1e-300, 0.0, float("nan")):
+        assert _step(itl, eps=eps) == INVALID and "eps" in itl.lib.itl_last_error().decode(), eps
+    assert _step(itl, eps=1e-44, ws=0) == WORKSPACE  # (a subnormal eps is one: the next check answers)
