@@ -430,7 +430,9 @@ typedef struct itl_adamw_tensor {
 } itl_adamw_tensor;
 
 /* Sizes of a plan over these tensors: the plan's bytes, and the elements of
- * each flat state (every tensor's state starts at the next multiple of 256). */
+ * each flat state (every tensor's state starts at the next multiple of 256).
+ * More than 2^24 - 1 pieces of 2048 elements of one tensor (34e9 elements)
+ * return ITL_ERR_UNSUPPORTED: two plans. */
 itl_status itl_adamw_plan_sizes(const itl_adamw_tensor* tensors, int32_t n_tensors,
                                 int64_t* plan_bytes, int64_t* state_elements);
 

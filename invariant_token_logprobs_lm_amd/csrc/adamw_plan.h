@@ -13,6 +13,8 @@ constexpr int kAdamBlock = 256;
 constexpr int kAdamPiece = 2048;
 constexpr int kAdamThreads = 256;
 constexpr int kAdamVec = 8;  // consecutive elements of a thread
+// A workgroup per piece in one grid dimension, which holds less than 2^32 threads.
+constexpr int64_t kAdamMaxPieces = (1LL << 32) / kAdamThreads - 1;
 static_assert(kAdamPiece % (kAdamThreads * kAdamVec) == 0 && kAdamPiece % kAdamBlock == 0, "whole passes and blocks");
 
 enum : uint32_t {

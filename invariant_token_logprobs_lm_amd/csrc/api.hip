@@ -581,7 +581,7 @@ itl_status adamw_layout(const itl_adamw_tensor* tensors, int32_t n_tensors, int6
       return fail(ITL_ERR_INVALID_ARG, "param and grad must be aligned to their elements");
     pieces += itl::ceil_div(t.n, itl::kAdamPiece);
     state += itl::ceil_div(t.n, itl::kAdamBlock) * itl::kAdamBlock;
-    if (pieces > INT32_MAX) return fail(ITL_ERR_UNSUPPORTED, "too many elements for one plan");
+    if (pieces > itl::kAdamMaxPieces) return fail(ITL_ERR_UNSUPPORTED, "too many elements for one plan");
   }
   *n_pieces = pieces;
   *n_state = state;
@@ -669,7 +669,7 @@ itl_status itl_adamw_step(const void* plan, size_t plan_bytes, int32_t state_bit
   if (!((float)eps > 0.0f && eps < 1.0)) return fail(ITL_ERR_INVALID_ARG, "eps must be in (0, 1) in fp32");
   if (!(max_norm > 0.0f)) return fail(ITL_ERR_INVALID_ARG, "max_norm must be > 0 (infinity: no clipping)");
   const int64_t pieces = (int64_t)(plan_bytes / sizeof(itl::AdamPiece));
-  if (pieces > INT32_MAX) return fail(ITL_ERR_UNSUPPORTED, "too many elements for one plan");
+  if (pieces > itl::kAdamMaxPieces) return fail(ITL_ERR_UNSUPPORTED, "too many elements for one plan");
   if (!lr || !step) return fail(ITL_ERR_INVALID_ARG, "null lr or step");
   if (pieces > 0 && (!plan || !exp_avg || !exp_avg_sq || (state_bits == 8 && (!exp_avg_scale || !exp_avg_sq_scale))))
     return fail(ITL_ERR_INVALID_ARG, "null plan or state");

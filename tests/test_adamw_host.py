@@ -40,3 +40,17 @@ def test_eps_that_vanishes_in_fp32_is_refused(itl):
     for eps in (1e-46, 1e-300, 0.0, float("nan")):
         assert _step(itl, eps=eps) == INVALID and "eps" in itl.lib.itl_last_error().decode(), eps
     assert _step(itl, eps=1e-44, ws=0) == WORKSPACE  # (a subnormal eps is one: the next check answers)
+
+
+def test_more_pieces_than_a_launch_has_threads_for_are_refused(itl):
+    """A workgroup of 256 threads per piece: 2^24 pieces are a grid dimension's 2^32
+    threads, and the launch would wrap without an error."""
+    def sizes(n):
+        t = itl._AdamWTensor(MB, 1 << 50, n, 0, 0, 0.0)
+        nb, el = ctypes.c_int64(), ctypes.c_int64()
+        return itl.lib.itl_adamw_plan_sizes(ctypes.byref(t), 1, ctypes.byref(nb), ctypes.byref(el)), nb.value
+
+    most = (1 << 24) - 1
+    assert sizes(most * 2048) == (OK, most * 40)
+    assert sizes(most * 2048 + 1)[0] == UNSUPPORTED
+    assert _step(itl, pieces=most + 1) == UNSUPPORTED
