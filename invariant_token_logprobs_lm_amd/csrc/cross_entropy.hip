@@ -1152,16 +1152,11 @@ void launch_ce_partial(const char* Hc, const char* W, const int32_t* ids, const 
   const int row_bytes = d * 2;
   const int S = n_slices(vocab), G = slices_per_group(cap, vocab), ntb = (int)ceil_div(cap, kBT);
   // Few workgroups: the narrow walk's blocks are a quarter of the wide one's
-  // (two rounds of them over the CUs still half its time), of 128 tokens a
-  // half. The bits are the same.
+  // (two rounds of them over the CUs still half its time). The bits are the
+  // same.
   const long long narrow = ceil_div(cap, kNarrowBRows) * S;
-  if (cap <= kNarrowMaxTokens || narrow <= 512) {
+  if (narrow <= 512) {
     hipLaunchKernelGGL((ce_partial_narrow_kernel<0, kKeep, kNarrowBRows>), dim3((unsigned)narrow), dim3(kThreads), 0,
-                       stream, Hc, W, ids, count, c0, cap, cap, row_bytes, vocab, S, part, zy, logits);
-    return;
-  }
-  if (cap <= kNarrow128MaxTokens) {
-    hipLaunchKernelGGL((ce_partial_narrow_kernel<0, kKeep, kNarrow128MaxTokens>), dim3((unsigned)S), dim3(kThreads), 0,
                        stream, Hc, W, ids, count, c0, cap, cap, row_bytes, vocab, S, part, zy, logits);
     return;
   }
@@ -1210,8 +1205,8 @@ hipError_t run_cross_entropy(const CeCall& c, hipStream_t stream) {
   const int row_chunks = d * E::kSize / 16;
   hipError_t e;
 
-  // A few tokens without their gradient: one block holds them all, counted or
-  // not, so nothing is gathered.
+  // A few tokens without their gradient: a block or two hold them all, counted
+  // or not, so nothing is gathered.
   const bool direct = !grad && !wmean && n <= kNarrow128MaxTokens;
   if (!direct) {
     hipLaunchKernelGGL(ce_select_kernel, dim3(1), dim3(kSelectThreads), 0, stream, c.targets, n, vocab, rows, ids, slot,
@@ -1309,7 +1304,7 @@ hipError_t run_cross_entropy(const CeCall& c, hipStream_t stream) {
       out = acc, out_f32 = 1, add = c0 > 0;
     }
     auto dw = [&](auto mode) {
-      if constexpr (kDtype == 0) {
+      if constexpr (kDtype == 0 && decltype(mode)::value != kDwWrite) {  // (kDwWrite: of several chunks)
         if (n <= kFewTokens) {
           const int n_dt2 = (int)ceil_div(d, kFewTile), n_vt2 = (int)ceil_div(vocab, kFewTile);
           hipLaunchKernelGGL((ce_dw_few_kernel<decltype(mode)::value>), dim3((unsigned)(n_vt2 * n_dt2)), dim3(kFewThreads), 0,
@@ -1334,8 +1329,8 @@ hipError_t run_cross_entropy(const CeCall& c, hipStream_t stream) {
                          n_dt, walk, gs, out);
     };
     if (add) dw(std::integral_constant<int, kDwAdd>{});
-    else if (out_f32) dw(std::integral_constant<int, kDwWrite>{});
-    else dw(std::integral_constant<int, kDwRound>{});
+    else if (kDtype == 1 || out_f32) dw(std::integral_constant<int, kDwWrite>{});
+    else if constexpr (kDtype == 0) dw(std::integral_constant<int, kDwRound>{});
     ITL_CHECK_LAUNCH();
     if (exact && !single && c0 > 0) {
       hipLaunchKernelGGL(ce_add_kernel, flat_grid(ceil_div((long long)vocab * d / 4, 256)), dim3(256), 0, stream,
