@@ -53,7 +53,10 @@
  *  - dtype selects the element type of H and W: ITL_BF16 (bfloat16 bits)
  *    or ITL_F32. Accumulation is always fp32. d must be a positive
  *    multiple of 64 (otherwise ITL_ERR_UNSUPPORTED); vocab is any value in
- *    [1, 2^31 - 256].
+ *    [1, 2^31 - 256]. Calls whose kernels would pass the 2^32 threads of a
+ *    launch return ITL_ERR_UNSUPPORTED: forwards from 2^28 (small vocab) or
+ *    2^23 tokens on (vocab above about 196,000; 2^24 at 151,936; the MXFP4
+ *    head twice that), itl_quantize_rows_fp8 from 2^26 rows.
  *  - n_tok == 0 (or n_resp / n_groups == 0) is a no-op returning ITL_OK.
  *  - Host-detectable errors return before anything is launched.
  *    A failed launch returns ITL_ERR_HIP; itl_last_error() describes it.

@@ -57,6 +57,17 @@ itl_status check_head(itl_dtype dtype, int64_t n_tok, int64_t d, int64_t vocab) 
   return ITL_OK;
 }
 
+// A grid dimension holds less than 2^32 threads; a launch of more wraps without
+// an error. The forwards have 16 threads per token to merge the slices and
+// `threads` per token block and slice group.
+constexpr int64_t kGridThreads = (int64_t)1 << 32;
+itl_status check_forward_launch(int64_t n_tok, int64_t vocab, int threads) {
+  const int64_t grid = itl::ceil_div(n_tok, itl::kBT) * itl::n_slice_groups(n_tok, vocab);
+  if (16 * itl::ceil_div(n_tok, 64) * 64 >= kGridThreads || grid * threads >= kGridThreads)
+    return fail(ITL_ERR_UNSUPPORTED, "n_tok too large for one launch");
+  return ITL_OK;
+}
+
 bool misaligned(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 255) != 0; }
 
 // The head kernels move H and W rows in 16-byte pieces per lane.
@@ -121,6 +132,7 @@ itl_status itl_lmhead_logprob(const void* H, const void* W, itl_dtype dtype, int
                               size_t workspace_bytes, void* stream) {
   g_last_error.clear();
   itl_status st = check_head(dtype, n_tok, d, vocab);
+  if (st == ITL_OK) st = check_forward_launch(n_tok, vocab, itl::kThreads8);
   if (st != ITL_OK) return st;
   if (n_tok == 0) return ITL_OK;
   if (!H || !W || !tokens || !logprob) return fail(ITL_ERR_INVALID_ARG, "null H, W, tokens or logprob");
@@ -176,6 +188,7 @@ itl_status itl_lmhead_logprob_keep_logits(const void* H, const void* W, itl_dtyp
                                           void* stream) {
   g_last_error.clear();
   itl_status st = check_head(dtype, n_tok, d, vocab);
+  if (st == ITL_OK) st = check_forward_launch(n_tok, vocab, itl::kThreads8);
   if (st != ITL_OK) return st;
   if (n_tok == 0) return ITL_OK;
   if (!H || !W || !tokens || !logprob) return fail(ITL_ERR_INVALID_ARG, "null H, W, tokens or logprob");
@@ -286,7 +299,8 @@ itl_status itl_quantize_rows_fp8(const void* X, itl_dtype dtype, int64_t n_rows,
   if (n_rows < 0 || d <= 0) return fail(ITL_ERR_INVALID_ARG, "n_rows must be >= 0 and d > 0");
   if (dtype != ITL_BF16 && dtype != ITL_F32) return fail(ITL_ERR_UNSUPPORTED, "dtype must be ITL_BF16 or ITL_F32");
   if (d % kFp8DMultiple != 0) return fail(ITL_ERR_UNSUPPORTED, "d must be a multiple of 128");
-  if (n_rows > (int64_t)INT32_MAX * 4 || d > INT32_MAX) return fail(ITL_ERR_UNSUPPORTED, "too many rows or columns");
+  if (n_rows > kGridThreads / 64 - 4 || d > INT32_MAX)  // (a wavefront per row, four a workgroup)
+    return fail(ITL_ERR_UNSUPPORTED, "too many rows or columns");
   if (n_rows == 0) return ITL_OK;
   if (!X || !Xq || !scale) return fail(ITL_ERR_INVALID_ARG, "null X, Xq or scale");
   if ((reinterpret_cast<uintptr_t>(Xq) & 3) != 0) return fail(ITL_ERR_INVALID_ARG, "Xq must be 4-byte aligned");
@@ -310,6 +324,8 @@ itl_status itl_lmhead_logprob_fp8(const uint8_t* Hq, const float* h_scale, const
   const int64_t grid = narrow ? itl::ceil_div(n_tok, itl::kNarrowBRows) * itl::n_slices(vocab)
                               : itl::ceil_div(n_tok, itl::kBT) * itl::n_slice_groups(n_tok, vocab);
   if (grid > INT32_MAX) return fail(ITL_ERR_UNSUPPORTED, "problem too large for one launch");
+  const itl_status fits = check_forward_launch(n_tok, vocab, itl::kThreads8);
+  if (fits != ITL_OK) return fits;
   if (n_tok == 0) return ITL_OK;
   if (!Hq || !h_scale || !Wq || !w_scale || !tokens || !logprob)
     return fail(ITL_ERR_INVALID_ARG, "null Hq, h_scale, Wq, w_scale, tokens or logprob");
@@ -329,7 +345,7 @@ itl_status itl_quantize_rows_mxfp4(const void* X, itl_dtype dtype, int64_t n_row
   if (n_rows < 0 || d <= 0) return fail(ITL_ERR_INVALID_ARG, "n_rows must be >= 0 and d > 0");
   if (dtype != ITL_BF16 && dtype != ITL_F32) return fail(ITL_ERR_UNSUPPORTED, "dtype must be ITL_BF16 or ITL_F32");
   if (d % kFp8DMultiple != 0) return fail(ITL_ERR_UNSUPPORTED, "d must be a multiple of 128");
-  if (d > INT32_MAX || n_rows > ((int64_t)INT32_MAX * 256) / (d / 32)) return fail(ITL_ERR_UNSUPPORTED, "too many rows");
+  if (d > INT32_MAX || n_rows > (kGridThreads - 256) / (d / 32)) return fail(ITL_ERR_UNSUPPORTED, "too many rows");
   if (n_rows == 0) return ITL_OK;
   if (!X || !Xq || !scale_codes) return fail(ITL_ERR_INVALID_ARG, "null X, Xq or scale_codes");
   if ((reinterpret_cast<uintptr_t>(Xq) & 15) != 0) return fail(ITL_ERR_INVALID_ARG, "Xq must be 16-byte aligned");
@@ -350,6 +366,8 @@ itl_status itl_lmhead_logprob_mxfp4(const uint8_t* Hq, const float* h_scale, con
   if (d >= ((int64_t)1 << 31) / (int64_t)itl::kBT) return fail(ITL_ERR_UNSUPPORTED, "d too large");
   const int64_t grid = itl::ceil_div(n_tok, itl::kBT) * itl::n_slice_groups(n_tok, vocab);
   if (grid > INT32_MAX) return fail(ITL_ERR_UNSUPPORTED, "problem too large for one launch");
+  const itl_status fits = check_forward_launch(n_tok, vocab, itl::kThreads);
+  if (fits != ITL_OK) return fits;
   if (n_tok == 0) return ITL_OK;
   if (!Hq || !h_scale || !Wq4 || !w_scale_codes || !tokens || !logprob)
     return fail(ITL_ERR_INVALID_ARG, "null Hq, h_scale, Wq4, w_scale_codes, tokens or logprob");
