@@ -572,18 +572,11 @@ def _norm_operands(x, y, w_pre, w_post, gate, first):
     return n, d, 0 if gate.dim() == 1 else d
 
 
-def _refuse_unwritten(**outputs):
-    """name=(tensor, its operand, the operand's name): an output given without its operand."""
-    for name, (out, operand, needed) in outputs.items():
-        if out is not None and operand is None:
-            raise ValueError(f"{name} needs {needed}")
-
-
 def _stream_rows(x, y, h, n, d):
     """residual_norm's h: x itself without y."""
     if y is None:
-        if h is not x:
-            _refuse_unwritten(h=(h, y, "y"))
+        if h is not None and h is not x:
+            raise ValueError("h needs y")
         return x
     return _new((n, d), x.dtype, x, "h", h)
 
@@ -648,7 +641,12 @@ def residual_norm_backward(du, dh, h, y, w_pre, rstd_pre, *, w_post=None, rstd_p
         _need(t, name, (torch.float32,), device=dev, ndim=1)
         if t.shape[0] != n:
             raise ValueError(f"{name} must have {n} elements")
-    _refuse_unwritten(dy=(dy, y, "y"), dw_post=(dw_post, w_post, "w_post"), dgate=(dgate, gate, "gate"))
+    if dy is not None and y is None:
+        raise ValueError("dy needs y")
+    if dw_post is not None and w_post is None:
+        raise ValueError("dw_post needs w_post")
+    if dgate is not None and gate is None:
+        raise ValueError("dgate needs gate")
     dx = _new((n, d), h.dtype, h, "dx", dx)
     dy = None if y is None else _new((n, d), h.dtype, h, "dy", dy)
     dw_pre = _new((d,), torch.float32, h, "dw_pre", dw_pre)

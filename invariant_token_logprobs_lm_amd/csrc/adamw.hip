@@ -28,9 +28,9 @@
 // adds the workgroups in order, in fp64: run-to-run deterministic.
 //
 // Bound by memory: 252 M bf16 weights with fp32 masters and states, 7.1 GB,
-// update in 1.30 ms (5.4 TB/s; a large copy moves 4.7), with the norm's 0.5 GB
-// 1.46 ms; 389 M with 8-bit states and fp32 gradients 7.0 GB in 1.30 ms, with
-// the norm 1.63 ms. Pieces of 2048 elements, one pass of 8 per thread, beat
+// update in 1.20 to 1.31 ms (5.4 to 5.9 TB/s; a large copy moves 4.7), with the
+// norm's 0.5 GB 1.33 to 1.46 ms; 389 M with 8-bit states and fp32 gradients 7.0
+// GB in 1.18 to 1.32 ms, with the norm 1.53 to 1.64 ms. Pieces of 2048 elements, one pass of 8 per thread, beat
 // 4096 (two passes; 9 % slower) and 1024 on 128 threads (3 %): many short
 // workgroups keep loads and stores of different pieces in flight together.
 
