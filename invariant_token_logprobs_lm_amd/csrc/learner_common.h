@@ -12,11 +12,11 @@ namespace itl {
 
 // A grid dimension holds less than 2^32 threads: a launch of more (a wavefront
 // for each of 2^26 rows) wraps without an error and leaves the rest undone.
-// flat_grid lays any number of workgroups out in two dimensions, flat_group is
-// a workgroup's number; the last ones may lie past the end.
+// flat_grid lays any number of workgroups out in rows of at most 2^20, flat_group
+// is a workgroup's number; fewer than there are rows lie past the end.
 inline dim3 flat_grid(long long groups) {
-  const long long x = groups < (1LL << 20) ? groups : 1LL << 20;
-  return dim3((unsigned)x, (unsigned)((groups + x - 1) / x));
+  const long long y = (groups + (1LL << 20) - 1) >> 20;
+  return dim3((unsigned)((groups + y - 1) / y), (unsigned)y);
 }
 __device__ __forceinline__ long long flat_group() { return (long long)blockIdx.y * gridDim.x + blockIdx.x; }
 

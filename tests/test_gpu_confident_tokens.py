@@ -14,6 +14,8 @@ half a step of fp32, a = 1 + 2 lam lse, c = e / V):
   to a few steps of fp32, as the documentation has it;
 * the contractions add half a step of fp32 per addition, the results half a
   step of their type.
+
+The last case is more than one chunk of tokens.
 """
 
 import pytest
@@ -63,7 +65,7 @@ def bounds(H, W, y, dtype, grad_dtype, smoothing=0.0, z_weight=0.0):
     return want, {k: b + R.half_step(grad_dtype) * want[k].abs() for k, b in bound.items()}, p[rows, at], G[rows, at]
 
 
-CASES = [(80, 256, 4000), (129, 128, 700), (400, 256, 4000), (1500, 256, 4000), (1500, 64, 300)]
+CASES = [(80, 256, 4000), (129, 128, 700), (400, 256, 4000), (1500, 256, 4000), (1500, 64, 300), (16684, 64, 300)]
 TYPES = [(torch.bfloat16, torch.float32), (torch.bfloat16, torch.bfloat16), (torch.float32, torch.float32)]
 
 
