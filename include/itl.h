@@ -370,6 +370,98 @@ itl_status itl_residual_norm_backward(const void* du, itl_dtype du_dtype, const 
                                       float* dw_pre, float* dw_post,
                                       void* workspace, size_t workspace_bytes, void* stream);
 
+/* Dropout of the block's output, from a counter-based generator: no mask is
+ * stored, the backward takes the same one from the same numbers. Value (r, c)
+ * of a call's rows is dropped where its 16-bit number is below p 65536 (p to the
+ * nearest 2^-16), the others are multiplied by 65536 / (65536 - that) in fp32. The
+ * number is half c mod 2 (low first) of word (c mod 8) / 2 of Philox 4 x 32 with
+ * ten rounds (Salmon et al., "Parallel random numbers: as easy as 1, 2, 3",
+ * 2011) at the counter (c / 8, low and high word of first_row + r, site) under the
+ * key (low and high word of *seed): it depends on nothing else, so that a batch
+ * in pieces (first_row) has the bits of the whole.
+ * p in [0, 1]; seed: int64 on the device, read when the kernel runs (a captured
+ * call takes what it holds at each replay; let each step have its own); site: which
+ * dropout of the model. A dropped value's result is 0 whatever the value is. */
+typedef struct {
+  const int64_t* seed;
+  int64_t first_row;
+  uint32_t site;
+  float p;
+} itl_dropout_spec;
+
+/* y = x with dropout, [n_rows, d] of dtype; y may be x. Its gradient is the
+ * same call on y's gradient. Sizes and alignment as for itl_residual_norm. */
+itl_status itl_dropout(const void* x, itl_dtype dtype, int64_t n_rows, int64_t d,
+                       const itl_dropout_spec* dropout, void* y, void* stream);
+
+/* itl_residual_norm and its backward with dropout of the block's output: with
+ * D the keep factors (0 or the scale) of itl_dropout_spec,
+ *   h = x + scale gate D p
+ *   dp = scale gate D dx, dgate = scale D p dx, the rest as there.
+ * y must be given. */
+itl_status itl_residual_norm_dropout(const void* x, const void* y, const void* gate, int64_t gate_stride,
+                                     const void* w_post, const void* w_pre, itl_dtype dtype,
+                                     int64_t n_rows, int64_t d, float scale, float eps,
+                                     const itl_dropout_spec* dropout,
+                                     void* h, void* u, float* rstd_pre, float* rstd_post, void* stream);
+itl_status itl_residual_norm_dropout_backward(const void* du, itl_dtype du_dtype, const void* dh, const void* h,
+                                              const void* y, const void* gate, int64_t gate_stride,
+                                              const void* w_post, const void* w_pre,
+                                              const float* rstd_pre, const float* rstd_post, itl_dtype dtype,
+                                              int64_t n_rows, int64_t d, float scale,
+                                              const itl_dropout_spec* dropout, void* dx, void* dy, void* dgate,
+                                              float* dw_pre, float* dw_post,
+                                              void* workspace, size_t workspace_bytes, void* stream);
+
+/* itl_residual_norm, or with dropout (nullable) itl_residual_norm_dropout, with
+ * u as itl_matmul_fp8_blocks takes its first operand: E4M3 codes Uq [n_rows, d]
+ * (8-byte aligned) with u_scale [d / 128, n_rows], the codes and scales that
+ * itl_quantize_blocks_fp8 makes of the fp32 u (one rounding). d a multiple of 128
+ * (ITL_ERR_UNSUPPORTED otherwise); the rows must be finite. */
+itl_status itl_residual_norm_blocks_fp8(const void* x, const void* y, const void* gate, int64_t gate_stride,
+                                        const void* w_post, const void* w_pre, itl_dtype dtype,
+                                        int64_t n_rows, int64_t d, float scale, float eps,
+                                        const itl_dropout_spec* dropout,
+                                        void* h, uint8_t* Uq, float* u_scale, float* rstd_pre, float* rstd_post,
+                                        void* stream);
+
+/* E4M3 codes with a scale for each 128 values of a row of X [n_rows, d] (bf16
+ * or fp32), the product's first operand:
+ *   scale[b, r] = amax over columns 128 b .. 128 b + 127 of row r / 448, at least
+ *                 2^-126 (1 for zeros)                     [ceil(d / 128), n_rows]
+ *   Xq[r, c]    = E4M3 code of X[r, c] / scale (fp32 division, to nearest even)
+ * with rows of codes padded by zeros to whole blocks: Xq [n_rows, 128 ceil(d / 128)].
+ * Xtq [d, 128 ceil(n_rows / 128)] and t_scale [ceil(n_rows / 128), d]: the same of
+ * X's transpose, for the product whose contraction runs over the rows (a weight
+ * gradient). Either pair may be NULL; both together read X once. Xq, Xtq 16-byte
+ * aligned. X must be finite. A row's codes do not depend on the other rows
+ * (Xtq's do, on the 128 of their block). n_rows == 0 writes nothing. Outputs
+ * that share memory with X or each other are refused. d up to 2^23. */
+itl_status itl_quantize_blocks_fp8(const void* X, itl_dtype dtype, int64_t n_rows, int64_t d,
+                                   uint8_t* Xq, float* scale, uint8_t* Xtq, float* t_scale, void* stream);
+
+/* The same with one scale for each 128 x 128 tile, the product's second operand:
+ * scale [ceil(n_rows / 128), ceil(d / 128)], t_scale its transpose; Xtq holds Xq's
+ * codes. For weights (both directions: the forward and the input gradient) and
+ * for the activations of a weight gradient (Xtq). */
+itl_status itl_quantize_tiles_fp8(const void* X, itl_dtype dtype, int64_t n_rows, int64_t d,
+                                  uint8_t* Xq, float* scale, uint8_t* Xtq, float* t_scale, void* stream);
+
+/* The product of block-scaled E4M3 operands on the FP8 matrix cores:
+ *   C[i, j] = sum_b a_scale[b, i] b_scale[j / 128, b] sum_{c in block b} e4m3(Aq[i, c]) e4m3(Bq[j, c])
+ * Aq [m, k], a_scale fp32 [k / 128, m], Bq [n, k], b_scale fp32 [ceil(n / 128), k / 128],
+ * C [m, n] of out_dtype, rounded once. A linear layer Y = X W^T takes it three times:
+ *   Y = matmul(blocks(X), tiles(W)),  dX = matmul(blocks(dY), transposed tiles(W)),
+ *   dW = matmul(transposed blocks(dY), transposed tiles(X)).
+ * Each block's product and the sum over blocks are fp32, blocks in ascending
+ * order: C's row i depends on row i of Aq and a_scale, Bq and b_scale alone, whatever
+ * m [BC]. k a multiple of 128 (ITL_ERR_UNSUPPORTED otherwise), up to 2^23; 0: C is
+ * zeros. Aq, Bq 16-byte aligned, C by element; C that shares memory with an operand
+ * is refused. */
+itl_status itl_matmul_fp8_blocks(const uint8_t* Aq, const float* a_scale,
+                                 const uint8_t* Bq, const float* b_scale,
+                                 int64_t m, int64_t n, int64_t k, itl_dtype out_dtype, void* C, void* stream);
+
 /* What itl_cross_entropy's loss is over the counted tokens. */
 enum { ITL_SUM = 0, ITL_MEAN = 1 };
 

@@ -23,6 +23,10 @@ Entry points (same names as the C ABI without the ``itl_`` prefix):
   ``residual_norm_backward(du, dh, h, y, w_pre, rstd_pre) -> (dx, dy, dw_pre, dw_post, dgate)``
 * ``cross_entropy(H, W, targets) -> (loss, token_loss, lse)``,
   ``cross_entropy_grad(H, W, targets) -> (loss, token_loss, lse, dH, dW)``
+* ``dropout(x, Dropout(p, seed)) -> y``; ``dropout=`` of the norms above, and
+  ``residual_norm_blocks_fp8(x, y, w_pre) -> (h, Uq, u_scale, rstd_pre, rstd_post)``
+* ``quantize_blocks_fp8(X)``, ``quantize_tiles_fp8(X) -> (Xq, scale, Xtq, t_scale)``,
+  ``matmul_fp8_blocks(Aq, a_scale, Bq, b_scale) -> C``
 * ``adamw_plan(params, grads, lr=...) -> plan``, ``adamw_step(plan) -> grad_norm``
 * ``check_inputs(tokens, vocab, resp_offsets=None)``, ``build_info()``
 """
@@ -30,6 +34,7 @@ Entry points (same names as the C ABI without the ``itl_`` prefix):
 import ctypes
 import operator
 import os
+import typing
 
 import torch
 
@@ -57,6 +62,12 @@ class _AdamWTensor(ctypes.Structure):
                 ("weight_decay", _f32)]
 
 
+class _DropoutSpec(ctypes.Structure):
+    """itl_dropout_spec."""
+
+    _fields_ = [("seed", _c_void_p), ("first_row", _i64), ("site", ctypes.c_uint32), ("p", _f32)]
+
+
 class ItlError(RuntimeError):
     """A non-OK status from the library."""
 
@@ -72,6 +83,7 @@ def _load():
             "(there is no fallback implementation)"
         )
     lib = ctypes.CDLL(LIB_PATH)
+    _spec = ctypes.POINTER(_DropoutSpec)
     sig = {
         "itl_lmhead_logprob_workspace_bytes": (_size, [_i64, _i64]),
         "itl_lmhead_logprob": (ctypes.c_int, [_c_void_p, _c_void_p, ctypes.c_int, _i64, _i64, _i64, _c_void_p,
@@ -112,6 +124,24 @@ def _load():
                                                       _c_void_p, _i64, _c_void_p, _c_void_p, _c_void_p, _c_void_p,
                                                       ctypes.c_int, _i64, _i64, _f32, _c_void_p, _c_void_p, _c_void_p,
                                                       _c_void_p, _c_void_p, _c_void_p, _size, _c_void_p]),
+        "itl_dropout": (ctypes.c_int, [_c_void_p, ctypes.c_int, _i64, _i64, _spec, _c_void_p, _c_void_p]),
+        "itl_residual_norm_dropout": (ctypes.c_int, [_c_void_p, _c_void_p, _c_void_p, _i64, _c_void_p, _c_void_p,
+                                                     ctypes.c_int, _i64, _i64, _f32, _f32, _spec, _c_void_p, _c_void_p,
+                                                     _c_void_p, _c_void_p, _c_void_p]),
+        "itl_residual_norm_dropout_backward": (ctypes.c_int, [_c_void_p, ctypes.c_int, _c_void_p, _c_void_p, _c_void_p,
+                                                              _c_void_p, _i64, _c_void_p, _c_void_p, _c_void_p,
+                                                              _c_void_p, ctypes.c_int, _i64, _i64, _f32, _spec,
+                                                              _c_void_p, _c_void_p, _c_void_p, _c_void_p, _c_void_p,
+                                                              _c_void_p, _size, _c_void_p]),
+        "itl_residual_norm_blocks_fp8": (ctypes.c_int, [_c_void_p, _c_void_p, _c_void_p, _i64, _c_void_p, _c_void_p,
+                                                        ctypes.c_int, _i64, _i64, _f32, _f32, _spec, _c_void_p,
+                                                        _c_void_p, _c_void_p, _c_void_p, _c_void_p, _c_void_p]),
+        "itl_quantize_blocks_fp8": (ctypes.c_int, [_c_void_p, ctypes.c_int, _i64, _i64, _c_void_p, _c_void_p, _c_void_p,
+                                                   _c_void_p, _c_void_p]),
+        "itl_quantize_tiles_fp8": (ctypes.c_int, [_c_void_p, ctypes.c_int, _i64, _i64, _c_void_p, _c_void_p, _c_void_p,
+                                                  _c_void_p, _c_void_p]),
+        "itl_matmul_fp8_blocks": (ctypes.c_int, [_c_void_p, _c_void_p, _c_void_p, _c_void_p, _i64, _i64, _i64,
+                                                 ctypes.c_int, _c_void_p, _c_void_p]),
         "itl_cross_entropy_workspace_bytes": (_size, [_i64, _i64, _i64, ctypes.c_int, _i32, ctypes.c_int]),
         "itl_cross_entropy": (ctypes.c_int, [_c_void_p, _c_void_p, ctypes.c_int, _i64, _i64, _i64, _c_void_p, _f32,
                                              _f32, _i32, _c_void_p, _c_void_p, _c_void_p, _c_void_p, _size,
@@ -162,6 +192,13 @@ EXPORTS = (
     "itl_residual_norm_fp8",
     "itl_residual_norm_backward_workspace_bytes",
     "itl_residual_norm_backward",
+    "itl_dropout",
+    "itl_residual_norm_dropout",
+    "itl_residual_norm_dropout_backward",
+    "itl_residual_norm_blocks_fp8",
+    "itl_quantize_blocks_fp8",
+    "itl_quantize_tiles_fp8",
+    "itl_matmul_fp8_blocks",
     "itl_cross_entropy_workspace_bytes",
     "itl_cross_entropy",
     "itl_cross_entropy_grad",
@@ -581,9 +618,51 @@ def _stream_rows(x, y, h, n, d):
     return _new((n, d), x.dtype, x, "h", h)
 
 
-def residual_norm(x, y, w_pre, *, w_post=None, gate=None, scale=1.0, eps=1e-6, h=None, u=None):
+class Dropout(typing.NamedTuple):
+    """Which values of a tensor's rows dropout drops: each with probability p (to
+    the nearest 2^-16), by a number that depends on the seed (int64 tensor [1] on
+    the tensor's device, read when the kernel runs: give each step its own, as by
+    ``seed += 1``), the site (which dropout of the model, below 2^32), its column
+    and its row's number, first_row and up. No mask is stored: the backward is
+    given the same Dropout."""
+
+    p: float
+    seed: torch.Tensor
+    site: int = 0
+    first_row: int = 0
+
+
+def _dropout_spec(drop, device):
+    if not isinstance(drop, Dropout):
+        raise TypeError("dropout must be a Dropout")
+    _need(drop.seed, "the dropout seed", (torch.int64,), device=device, ndim=1)
+    if drop.seed.shape[0] != 1:
+        raise ValueError("the dropout seed must have 1 element")
+    site, first_row = operator.index(drop.site), operator.index(drop.first_row)
+    if not 0 <= site < 1 << 32:
+        raise ValueError(f"the dropout site must be in [0, 2^32), got {site}")
+    if not 0 <= first_row < 1 << 63:
+        raise ValueError(f"dropout's first_row must be in [0, 2^63), got {first_row}")
+    return _DropoutSpec(drop.seed.data_ptr(), first_row, site, drop.p)
+
+
+def dropout(x, drop, *, y=None):
+    """x [n, d] (bf16 or fp32) with dropout: 0 where dropped, else x / (1 - p).
+    Its gradient is dropout of y's gradient with the same Dropout. y: a tensor to
+    write into, x itself among them."""
+    _need(x, "x", tuple(_HEAD_DTYPES), ndim=2)
+    n, d = x.shape
+    if d == 0:
+        raise ValueError("x must have at least one column")
+    spec = _dropout_spec(drop, x.device)
+    y = _new((n, d), x.dtype, x, "y", y)
+    _launch(x.device, lib.itl_dropout, _ptr(x), _HEAD_DTYPES[x.dtype], n, d, spec, _ptr(y))
+    return y
+
+
+def residual_norm(x, y, w_pre, *, w_post=None, gate=None, scale=1.0, eps=1e-6, h=None, u=None, dropout=None):
     """h = x + scale * gate * p and u = rmsnorm(h) * w_pre, where p = y, or
-    rmsnorm(y) * w_post with w_post given.
+    rmsnorm(y) * w_post with w_post given, with dropout (a Dropout) of gate * p.
 
     x, y [n, d] (bf16 or fp32; y None: h is x), w_pre, w_post [d], gate [d] or
     [n, d], all of one dtype. Returns (h, u, rstd_pre fp32 [n], rstd_post fp32
@@ -594,8 +673,12 @@ def residual_norm(x, y, w_pre, *, w_post=None, gate=None, scale=1.0, eps=1e-6, h
     u = _new((n, d), x.dtype, x, "u", u)
     rstd_pre = torch.empty(n, dtype=torch.float32, device=x.device)
     rstd_post = None if w_post is None else torch.empty(n, dtype=torch.float32, device=x.device)
-    _launch(x.device, lib.itl_residual_norm, _ptr(x), _ptr(y), _ptr(gate), stride, _ptr(w_post), _ptr(w_pre),
-            _HEAD_DTYPES[x.dtype], n, d, scale, eps, _ptr(h), _ptr(u), _ptr(rstd_pre), _ptr(rstd_post))
+    operands = (_ptr(x), _ptr(y), _ptr(gate), stride, _ptr(w_post), _ptr(w_pre), _HEAD_DTYPES[x.dtype], n, d, scale, eps)
+    outputs = (_ptr(h), _ptr(u), _ptr(rstd_pre), _ptr(rstd_post))
+    if dropout is None:
+        _launch(x.device, lib.itl_residual_norm, *operands, *outputs)
+    else:
+        _launch(x.device, lib.itl_residual_norm_dropout, *operands, _dropout_spec(dropout, x.device), *outputs)
     return h, u, rstd_pre, rstd_post
 
 
@@ -615,13 +698,30 @@ def residual_norm_fp8(x, y, w_pre, *, w_post=None, gate=None, scale=1.0, eps=1e-
     return h, Uq, u_scale, rstd_pre, rstd_post
 
 
+def residual_norm_blocks_fp8(x, y, w_pre, *, w_post=None, gate=None, scale=1.0, eps=1e-6, h=None, Uq=None, u_scale=None,
+                             dropout=None):
+    """residual_norm with u as matmul_fp8_blocks takes its first operand: E4M3
+    codes (uint8 [n, d]) and a scale for each 128 columns (fp32 [d / 128, n]); d a
+    multiple of 128. Returns (h, Uq, u_scale, rstd_pre, rstd_post)."""
+    n, d, stride = _norm_operands(x, y, w_pre, w_post, gate, "x")
+    h = _stream_rows(x, y, h, n, d)
+    Uq = _new((n, d), torch.uint8, x, "Uq", Uq)
+    u_scale = _new((d // 128, n), torch.float32, x, "u_scale", u_scale)
+    rstd_pre = torch.empty(n, dtype=torch.float32, device=x.device)
+    rstd_post = None if w_post is None else torch.empty(n, dtype=torch.float32, device=x.device)
+    _launch(x.device, lib.itl_residual_norm_blocks_fp8, _ptr(x), _ptr(y), _ptr(gate), stride, _ptr(w_post), _ptr(w_pre),
+            _HEAD_DTYPES[x.dtype], n, d, scale, eps, None if dropout is None else _dropout_spec(dropout, x.device),
+            _ptr(h), _ptr(Uq), _ptr(u_scale), _ptr(rstd_pre), _ptr(rstd_post))
+    return h, Uq, u_scale, rstd_pre, rstd_post
+
+
 def residual_norm_backward_workspace_bytes(n_rows, d):
     return int(lib.itl_residual_norm_backward_workspace_bytes(n_rows, d))
 
 
 def residual_norm_backward(du, dh, h, y, w_pre, rstd_pre, *, w_post=None, rstd_post=None, gate=None, scale=1.0,
-                           dx=None, dy=None, dw_pre=None, dw_post=None, dgate=None, workspace=None):
-    """Gradients of residual_norm: du [n, d] (h's dtype or fp32) and dh [n, d]
+                           dx=None, dy=None, dw_pre=None, dw_post=None, dgate=None, workspace=None, dropout=None):
+    """Gradients of residual_norm (with the forward's dropout): du [n, d] (h's dtype or fp32) and dh [n, d]
     (h's dtype, or None) are those of u and h. Returns (dx, dy, dw_pre fp32
     [d], dw_post fp32 [d], dgate: fp32 [d] for a shared gate, else like gate);
     dy, dw_post, dgate are None where y, w_post, gate are. Each may be given as
@@ -656,11 +756,90 @@ def residual_norm_backward(du, dh, h, y, w_pre, rstd_pre, *, w_post=None, rstd_p
     else:
         dgate = _new((d,), torch.float32, h, "dgate", dgate) if stride == 0 else _new((n, d), h.dtype, h, "dgate", dgate)
     workspace = _workspace(workspace, residual_norm_backward_workspace_bytes(n, d), dev)
-    _launch(dev, lib.itl_residual_norm_backward, _ptr(du), _HEAD_DTYPES[du.dtype], _ptr(dh), _ptr(h), _ptr(y),
-            _ptr(gate), stride, _ptr(w_post), _ptr(w_pre), _ptr(rstd_pre),
-            _ptr(rstd_post if w_post is not None else None), _HEAD_DTYPES[h.dtype], n, d, scale, _ptr(dx), _ptr(dy),
-            _ptr(dgate), _ptr(dw_pre), _ptr(dw_post), _ptr(workspace), workspace.numel())
+    operands = (_ptr(du), _HEAD_DTYPES[du.dtype], _ptr(dh), _ptr(h), _ptr(y), _ptr(gate), stride, _ptr(w_post),
+                _ptr(w_pre), _ptr(rstd_pre), _ptr(rstd_post if w_post is not None else None), _HEAD_DTYPES[h.dtype], n, d,
+                scale)
+    outputs = (_ptr(dx), _ptr(dy), _ptr(dgate), _ptr(dw_pre), _ptr(dw_post), _ptr(workspace), workspace.numel())
+    if dropout is None:
+        _launch(dev, lib.itl_residual_norm_backward, *operands, *outputs)
+    else:
+        _launch(dev, lib.itl_residual_norm_dropout_backward, *operands, _dropout_spec(dropout, dev), *outputs)
     return dx, dy, dw_pre, dw_post, dgate
+
+
+_FP8_BLOCK = 128
+
+
+def _whole(n):
+    """n in whole blocks."""
+    return -(-n // _FP8_BLOCK) * _FP8_BLOCK
+
+
+def _quantize(call, X, tiles, rows, columns, Xq, scale, Xtq, t_scale):
+    _need(X, "X", tuple(_HEAD_DTYPES), ndim=2)
+    n, d = X.shape
+    if d == 0:
+        raise ValueError("X must have at least one column")
+    if not rows and not columns:
+        raise ValueError("at least one of rows and columns must be asked for")
+    if not rows and (Xq is not None or scale is not None) or not columns and (Xtq is not None or t_scale is not None):
+        raise ValueError("Xq and scale need rows, Xtq and t_scale columns")
+    across, down = _whole(d), _whole(n)
+    if rows:
+        Xq = _new((n, across), torch.uint8, X, "Xq", Xq)
+        scale = _new((down // _FP8_BLOCK, across // _FP8_BLOCK) if tiles else (across // _FP8_BLOCK, n), torch.float32, X,
+                     "scale", scale)
+    if columns:
+        Xtq = _new((d, down), torch.uint8, X, "Xtq", Xtq)
+        t_scale = _new((across // _FP8_BLOCK, down // _FP8_BLOCK) if tiles else (down // _FP8_BLOCK, d), torch.float32, X,
+                       "t_scale", t_scale)
+    _launch(X.device, call, _ptr(X), _HEAD_DTYPES[X.dtype], n, d, _ptr(Xq), _ptr(scale), _ptr(Xtq), _ptr(t_scale))
+    return Xq, scale, Xtq, t_scale
+
+
+def quantize_blocks_fp8(X, *, rows=True, columns=False, Xq=None, scale=None, Xtq=None, t_scale=None):
+    """E4M3 codes of X [n, d] (bf16 or fp32) with a scale for each 128 values of a
+    row: matmul_fp8_blocks' first operand. Returns (Xq uint8 [n, d in whole
+    blocks], scale fp32 [blocks, n], Xtq, t_scale); with columns the last two are
+    the same of X's transpose ([d, n in whole blocks], [blocks, d]), else None, as
+    the first two are without rows."""
+    return _quantize(lib.itl_quantize_blocks_fp8, X, False, rows, columns, Xq, scale, Xtq, t_scale)
+
+
+def quantize_tiles_fp8(X, *, rows=True, columns=False, Xq=None, scale=None, Xtq=None, t_scale=None):
+    """quantize_blocks_fp8 with a scale for each 128 x 128 tile: matmul_fp8_blocks'
+    second operand. scale is [blocks of rows, blocks of columns], t_scale its
+    transpose."""
+    return _quantize(lib.itl_quantize_tiles_fp8, X, True, rows, columns, Xq, scale, Xtq, t_scale)
+
+
+def matmul_fp8_blocks(Aq, a_scale, Bq, b_scale, *, out_dtype=torch.bfloat16, out=None):
+    """A B^T [m, n] of block-scaled E4M3 codes Aq [m, k], Bq [n, k] (uint8, k whole
+    blocks of 128) with a_scale [k / 128, m], b_scale [n in blocks, k / 128] (fp32),
+    as quantize_blocks_fp8 and quantize_tiles_fp8 write them; out_dtype bf16 or fp32.
+
+    A linear layer Y = X W^T: Y from blocks of X and tiles of W; dX from blocks of
+    dY and the transposed tiles of W; dW from the transposed blocks of dY and the
+    transposed tiles of X.
+    """
+    _need(Aq, "Aq", (torch.uint8,), ndim=2)
+    dev = Aq.device
+    _need(a_scale, "a_scale", (torch.float32,), device=dev, ndim=2)
+    _need(Bq, "Bq", (torch.uint8,), device=dev, ndim=2)
+    _need(b_scale, "b_scale", (torch.float32,), device=dev, ndim=2)
+    if out_dtype not in _HEAD_DTYPES:
+        raise ValueError(f"out_dtype must be one of {tuple(_HEAD_DTYPES)}, got {out_dtype}")
+    (m, k), n = Aq.shape, Bq.shape[0]
+    if Bq.shape[1] != k:
+        raise ValueError(f"shape mismatch: Aq {tuple(Aq.shape)}, Bq {tuple(Bq.shape)}")
+    for name, t, want in (("a_scale", a_scale, (_whole(k) // _FP8_BLOCK, m)),
+                          ("b_scale", b_scale, (_whole(n) // _FP8_BLOCK, _whole(k) // _FP8_BLOCK))):
+        if tuple(t.shape) != want:
+            raise ValueError(f"{name} must have shape {want}, got {tuple(t.shape)}")
+    out = _new((m, n), out_dtype, Aq, "out", out)
+    _launch(dev, lib.itl_matmul_fp8_blocks, _ptr(Aq), _ptr(a_scale), _ptr(Bq), _ptr(b_scale), m, n, k,
+            _HEAD_DTYPES[out_dtype], _ptr(out))
+    return out
 
 
 _REDUCTIONS = {"sum": 0, "mean": 1}

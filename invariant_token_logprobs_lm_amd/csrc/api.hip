@@ -5,6 +5,7 @@
 
 #include <stdint.h>
 #include <stdio.h>
+#include <math.h>
 #include <string.h>
 
 #include <algorithm>
@@ -16,6 +17,7 @@
 #include <vector>
 
 #include "adamw_plan.h"
+#include "dropout.h"
 #include "itl.h"
 #include "itl_config.h"
 #include "itl_launch.h"
@@ -433,12 +435,36 @@ itl_status check_norm(itl_dtype dtype, int64_t n_rows, int64_t d, int64_t gate_s
   return ITL_OK;
 }
 
+// A call's dropout: its threshold and scale from p; none (seed null) without one.
+itl_status read_dropout(const itl_dropout_spec* drop, int64_t n_rows, itl::DropoutArgs* out) {
+  *out = itl::DropoutArgs{};
+  if (!drop) return ITL_OK;
+  if (!(drop->p >= 0.0f && drop->p <= 1.0f)) return fail(ITL_ERR_INVALID_ARG, "dropout's p must be in [0, 1]");
+  if (!drop->seed) return fail(ITL_ERR_INVALID_ARG, "null dropout seed");
+  if ((reinterpret_cast<uintptr_t>(drop->seed) & 7) != 0)
+    return fail(ITL_ERR_INVALID_ARG, "the dropout seed must be 8-byte aligned");
+  if (drop->first_row < 0 || drop->first_row > INT64_MAX - n_rows)
+    return fail(ITL_ERR_INVALID_ARG, "dropout's first_row must be >= 0, and no row's number past int64");
+  const uint32_t threshold = (uint32_t)lrint((double)drop->p * 65536.0);
+  *out = itl::DropoutArgs{drop->seed, drop->first_row, drop->site, threshold,
+                          threshold < 65536 ? (float)(65536.0 / (65536 - threshold)) : 0.0f};
+  return ITL_OK;
+}
+
+// What u becomes (the row codes' scale is one per row, the block codes' one per 128 columns).
+enum NormOutput { kNormOwn, kNormRowCodes, kNormBlockCodes };
+
 itl_status residual_norm(const void* x, const void* y, const void* gate, int64_t gate_stride, const void* w_post,
                          const void* w_pre, itl_dtype dtype, int64_t n_rows, int64_t d, float scale, float eps, void* h,
-                         void* u, uint8_t* codes, float* u_scale, bool fp8, float* rstd_pre, float* rstd_post,
-                         void* stream, const char* name) {
+                         void* u, uint8_t* codes, float* u_scale, NormOutput output, float* rstd_pre, float* rstd_post,
+                         const itl_dropout_spec* dropout, void* stream, const char* name) {
   itl_status st = check_norm(dtype, n_rows, d, gate_stride, gate, y, w_post, scale, eps);
   if (st != ITL_OK) return st;
+  const bool fp8 = output != kNormOwn;
+  itl::DropoutArgs drop;
+  st = read_dropout(dropout, n_rows, &drop);
+  if (st != ITL_OK) return st;
+  if (n_rows > 0 && drop.seed && !y) return fail(ITL_ERR_INVALID_ARG, "dropout needs y");
   if (fp8 && d % kFp8DMultiple != 0) return fail(ITL_ERR_UNSUPPORTED, "d must be a multiple of 128");
   if (n_rows == 0) return ITL_OK;
   if (!x || !w_pre || (y && !h) || (fp8 ? !codes || !u_scale : !u))
@@ -447,16 +473,26 @@ itl_status residual_norm(const void* x, const void* y, const void* gate, int64_t
     return fail(ITL_ERR_INVALID_ARG, "arrays must be 16-byte aligned where d is a multiple of 8, else by element");
   if (fp8 && (reinterpret_cast<uintptr_t>(codes) & 7) != 0) return fail(ITL_ERR_INVALID_ARG, "Uq must be 8-byte aligned");
   const int64_t row_bytes = d * elem_size(dtype), all = n_rows * row_bytes, one = n_rows * 4;
+  const int64_t scales = output == kNormBlockCodes ? d / kFp8DMultiple * one : one;
   // (h may be x, row for row)
-  if (outputs_share({{u, all}, {codes, n_rows * d}, {u_scale, one}, {rstd_pre, one}, {w_post ? rstd_post : nullptr, one},
+  if (outputs_share({{u, all}, {codes, n_rows * d}, {u_scale, scales}, {rstd_pre, one}, {w_post ? rstd_post : nullptr, one},
                      {y ? h : nullptr, all}},
                     {{h == x ? nullptr : x, all}, {y, all}, {gate, gate_stride ? all : row_bytes}, {w_post, row_bytes},
-                     {w_pre, row_bytes}}) ||
-      (h == x && outputs_share({{u, all}, {codes, n_rows * d}, {u_scale, one}, {rstd_pre, one},
+                     {w_pre, row_bytes}, {drop.seed, 8}}) ||
+      (h == x && outputs_share({{u, all}, {codes, n_rows * d}, {u_scale, scales}, {rstd_pre, one},
                                 {w_post ? rstd_post : nullptr, one}}, {{x, all}})))
     return fail(ITL_ERR_INVALID_ARG, "outputs share memory with inputs or each other (only h may be x)");
-  hipError_t e = itl::launch_residual_norm(x, y, gate, gate_stride, w_post, w_pre, (int)dtype, n_rows, (int)d, scale, eps,
-                                           h, u, codes, u_scale, rstd_pre, rstd_post, static_cast<hipStream_t>(stream));
+  hipStream_t on = static_cast<hipStream_t>(stream);
+  hipError_t e;
+  if (output == kNormBlockCodes)
+    e = itl::launch_residual_norm_blocks(x, y, gate, gate_stride, w_post, w_pre, (int)dtype, n_rows, (int)d, scale, eps, drop,
+                                         h, codes, u_scale, rstd_pre, rstd_post, on);
+  else if (drop.seed)
+    e = itl::launch_residual_norm_dropout(x, y, gate, gate_stride, w_post, w_pre, (int)dtype, n_rows, (int)d, scale, eps,
+                                          drop, h, u, rstd_pre, rstd_post, on);
+  else
+    e = itl::launch_residual_norm(x, y, gate, gate_stride, w_post, w_pre, (int)dtype, n_rows, (int)d, scale, eps, h, u,
+                                  codes, u_scale, rstd_pre, rstd_post, on);
   return e == hipSuccess ? ITL_OK : hip_fail(e, name);
 }
 
@@ -466,16 +502,56 @@ itl_status itl_residual_norm(const void* x, const void* y, const void* gate, int
                              const void* w_pre, itl_dtype dtype, int64_t n_rows, int64_t d, float scale, float eps,
                              void* h, void* u, float* rstd_pre, float* rstd_post, void* stream) {
   g_last_error.clear();
-  return residual_norm(x, y, gate, gate_stride, w_post, w_pre, dtype, n_rows, d, scale, eps, h, u, nullptr, nullptr, false,
-                       rstd_pre, rstd_post, stream, "itl_residual_norm");
+  return residual_norm(x, y, gate, gate_stride, w_post, w_pre, dtype, n_rows, d, scale, eps, h, u, nullptr, nullptr,
+                       kNormOwn, rstd_pre, rstd_post, nullptr, stream, "itl_residual_norm");
 }
 
 itl_status itl_residual_norm_fp8(const void* x, const void* y, const void* gate, int64_t gate_stride, const void* w_post,
                                  const void* w_pre, itl_dtype dtype, int64_t n_rows, int64_t d, float scale, float eps,
                                  void* h, uint8_t* Uq, float* u_scale, float* rstd_pre, float* rstd_post, void* stream) {
   g_last_error.clear();
-  return residual_norm(x, y, gate, gate_stride, w_post, w_pre, dtype, n_rows, d, scale, eps, h, nullptr, Uq, u_scale, true,
-                       rstd_pre, rstd_post, stream, "itl_residual_norm_fp8");
+  return residual_norm(x, y, gate, gate_stride, w_post, w_pre, dtype, n_rows, d, scale, eps, h, nullptr, Uq, u_scale,
+                       kNormRowCodes, rstd_pre, rstd_post, nullptr, stream, "itl_residual_norm_fp8");
+}
+
+itl_status itl_residual_norm_dropout(const void* x, const void* y, const void* gate, int64_t gate_stride,
+                                     const void* w_post, const void* w_pre, itl_dtype dtype, int64_t n_rows, int64_t d,
+                                     float scale, float eps, const itl_dropout_spec* dropout, void* h, void* u,
+                                     float* rstd_pre, float* rstd_post, void* stream) {
+  g_last_error.clear();
+  if (!dropout) return fail(ITL_ERR_INVALID_ARG, "null dropout");
+  return residual_norm(x, y, gate, gate_stride, w_post, w_pre, dtype, n_rows, d, scale, eps, h, u, nullptr, nullptr,
+                       kNormOwn, rstd_pre, rstd_post, dropout, stream, "itl_residual_norm_dropout");
+}
+
+itl_status itl_residual_norm_blocks_fp8(const void* x, const void* y, const void* gate, int64_t gate_stride,
+                                        const void* w_post, const void* w_pre, itl_dtype dtype, int64_t n_rows, int64_t d,
+                                        float scale, float eps, const itl_dropout_spec* dropout, void* h, uint8_t* Uq,
+                                        float* u_scale, float* rstd_pre, float* rstd_post, void* stream) {
+  g_last_error.clear();
+  return residual_norm(x, y, gate, gate_stride, w_post, w_pre, dtype, n_rows, d, scale, eps, h, nullptr, Uq, u_scale,
+                       kNormBlockCodes, rstd_pre, rstd_post, dropout, stream, "itl_residual_norm_blocks_fp8");
+}
+
+itl_status itl_dropout(const void* x, itl_dtype dtype, int64_t n_rows, int64_t d, const itl_dropout_spec* dropout, void* y,
+                       void* stream) {
+  g_last_error.clear();
+  if (n_rows < 0 || d <= 0) return fail(ITL_ERR_INVALID_ARG, "n_rows must be >= 0 and d > 0");
+  if (!known_dtype(dtype)) return fail(ITL_ERR_UNSUPPORTED, "dtype must be ITL_BF16 or ITL_F32");
+  if (n_rows > INT32_MAX || d > kMaxNormWidth) return fail(ITL_ERR_UNSUPPORTED, "too many rows or columns");
+  if (!dropout) return fail(ITL_ERR_INVALID_ARG, "null dropout");
+  itl::DropoutArgs drop;
+  const itl_status st = read_dropout(dropout, n_rows, &drop);
+  if (st != ITL_OK) return st;
+  if (n_rows == 0) return ITL_OK;
+  if (!x || !y) return fail(ITL_ERR_INVALID_ARG, "null x or y");
+  if (rows_misaligned({x, y}, d, dtype))
+    return fail(ITL_ERR_INVALID_ARG, "arrays must be 16-byte aligned where d is a multiple of 8, else by element");
+  const int64_t all = n_rows * d * elem_size(dtype);
+  if (outputs_share({{y, all}}, {{y == x ? nullptr : x, all}, {drop.seed, 8}}))
+    return fail(ITL_ERR_INVALID_ARG, "y shares memory with x (without being x) or the seed");
+  hipError_t e = itl::launch_dropout(x, (int)dtype, n_rows, (int)d, drop, y, static_cast<hipStream_t>(stream));
+  return e == hipSuccess ? ITL_OK : hip_fail(e, "itl_dropout");
 }
 
 size_t itl_residual_norm_backward_workspace_bytes(int64_t n_rows, int64_t d) {
@@ -483,21 +559,27 @@ size_t itl_residual_norm_backward_workspace_bytes(int64_t n_rows, int64_t d) {
   return itl::norm_backward_workspace_bytes(n_rows, d);
 }
 
-itl_status itl_residual_norm_backward(const void* du, itl_dtype du_dtype, const void* dh, const void* h, const void* y,
-                                      const void* gate, int64_t gate_stride, const void* w_post, const void* w_pre,
-                                      const float* rstd_pre, const float* rstd_post, itl_dtype dtype, int64_t n_rows,
-                                      int64_t d, float scale, void* dx, void* dy, void* dgate, float* dw_pre,
-                                      float* dw_post, void* workspace, size_t workspace_bytes, void* stream) {
-  g_last_error.clear();
+namespace {
+
+itl_status residual_norm_backward(const void* du, itl_dtype du_dtype, const void* dh, const void* h, const void* y,
+                                  const void* gate, int64_t gate_stride, const void* w_post, const void* w_pre,
+                                  const float* rstd_pre, const float* rstd_post, itl_dtype dtype, int64_t n_rows,
+                                  int64_t d, float scale, const itl_dropout_spec* dropout, void* dx, void* dy,
+                                  void* dgate, float* dw_pre, float* dw_post, void* workspace, size_t workspace_bytes,
+                                  void* stream, const char* name) {
   itl_status st = check_norm(dtype, n_rows, d, gate_stride, gate, y, w_post, scale, 0.5f);
   if (st != ITL_OK) return st;
+  itl::DropoutArgs drop;
+  st = read_dropout(dropout, n_rows, &drop);
+  if (st != ITL_OK) return st;
+  if (n_rows > 0 && drop.seed && !y) return fail(ITL_ERR_INVALID_ARG, "dropout needs y");
   if (du_dtype != dtype && du_dtype != ITL_F32) return fail(ITL_ERR_UNSUPPORTED, "du_dtype must be dtype or ITL_F32");
   if (!w_pre || !dw_pre || (gate && !dgate) || (w_post && !dw_post))
     return fail(ITL_ERR_INVALID_ARG, "null w_pre, dw_pre, dgate (with gate) or dw_post (with w_post)");
   if (n_rows > 0 && (!du || !h || !dx || !rstd_pre || (y && !dy) || (w_post && !rstd_post)))
     return fail(ITL_ERR_INVALID_ARG, "null du, h, dx, rstd_pre, dy (with y) or rstd_post (with w_post)");
   if (n_rows > 0 && (rows_misaligned({dh, h, y, gate, w_post, w_pre, dx, y ? dy : nullptr,
-                                      gate && gate_stride ? dgate : nullptr}, d, dtype) ||
+                                  gate && gate_stride ? dgate : nullptr}, d, dtype) ||
                      rows_misaligned({du}, d, du_dtype)))
     return fail(ITL_ERR_INVALID_ARG, "arrays must be 16-byte aligned where d is a multiple of 8, else by element");
   if (!workspace || workspace_bytes < itl::norm_backward_workspace_bytes(n_rows, d))
@@ -510,12 +592,108 @@ itl_status itl_residual_norm_backward(const void* du, itl_dtype du_dtype, const 
                      {workspace, (int64_t)itl::norm_backward_workspace_bytes(n_rows, d)}},
                     {{du, n_rows * d * elem_size(du_dtype)}, {dh == dx ? nullptr : dh, all}, {h, all}, {y, all},
                      {gate, gate_stride ? all : row_bytes}, {w_post, row_bytes}, {w_pre, row_bytes},
-                     {rstd_pre, n_rows * 4}, {w_post ? rstd_post : nullptr, n_rows * 4}}))
+                     {rstd_pre, n_rows * 4}, {w_post ? rstd_post : nullptr, n_rows * 4},
+                     {drop.seed, 8}}))
     return fail(ITL_ERR_INVALID_ARG, "outputs share memory with inputs or each other (only dx may be dh)");
-  hipError_t e = itl::launch_residual_norm_backward(du, (int)du_dtype, dh, h, y, gate, gate_stride, w_post, w_pre,
-                                                    rstd_pre, rstd_post, (int)dtype, n_rows, (int)d, scale, dx, dy, dgate,
-                                                    dw_pre, dw_post, workspace, static_cast<hipStream_t>(stream));
-  return e == hipSuccess ? ITL_OK : hip_fail(e, "itl_residual_norm_backward");
+  hipStream_t on = static_cast<hipStream_t>(stream);
+  hipError_t e;
+  if (drop.seed)
+    e = itl::launch_residual_norm_dropout_backward(du, (int)du_dtype, dh, h, y, gate, gate_stride, w_post, w_pre, rstd_pre,
+                                                   rstd_post, (int)dtype, n_rows, (int)d, scale, drop, dx, dy, dgate, dw_pre,
+                                                   dw_post, workspace, on);
+  else
+    e = itl::launch_residual_norm_backward(du, (int)du_dtype, dh, h, y, gate, gate_stride, w_post, w_pre, rstd_pre, rstd_post,
+                                           (int)dtype, n_rows, (int)d, scale, dx, dy, dgate, dw_pre, dw_post, workspace, on);
+  return e == hipSuccess ? ITL_OK : hip_fail(e, name);
+}
+
+}  // namespace
+
+itl_status itl_residual_norm_backward(const void* du, itl_dtype du_dtype, const void* dh, const void* h, const void* y,
+                                      const void* gate, int64_t gate_stride, const void* w_post, const void* w_pre,
+                                      const float* rstd_pre, const float* rstd_post, itl_dtype dtype, int64_t n_rows,
+                                      int64_t d, float scale, void* dx, void* dy, void* dgate, float* dw_pre,
+                                      float* dw_post, void* workspace, size_t workspace_bytes, void* stream) {
+  g_last_error.clear();
+  return residual_norm_backward(du, du_dtype, dh, h, y, gate, gate_stride, w_post, w_pre, rstd_pre, rstd_post, dtype, n_rows,
+                                d, scale, nullptr, dx, dy, dgate, dw_pre, dw_post, workspace, workspace_bytes, stream,
+                                "itl_residual_norm_backward");
+}
+
+itl_status itl_residual_norm_dropout_backward(const void* du, itl_dtype du_dtype, const void* dh, const void* h, const void* y,
+                                              const void* gate, int64_t gate_stride, const void* w_post, const void* w_pre,
+                                              const float* rstd_pre, const float* rstd_post, itl_dtype dtype, int64_t n_rows,
+                                              int64_t d, float scale, const itl_dropout_spec* dropout,
+                                              void* dx, void* dy, void* dgate, float* dw_pre, float* dw_post,
+                                              void* workspace, size_t workspace_bytes, void* stream) {
+  g_last_error.clear();
+  if (!dropout) return fail(ITL_ERR_INVALID_ARG, "null dropout");
+  return residual_norm_backward(du, du_dtype, dh, h, y, gate, gate_stride, w_post, w_pre, rstd_pre, rstd_post, dtype, n_rows,
+                                d, scale, dropout, dx, dy, dgate, dw_pre, dw_post, workspace, workspace_bytes, stream,
+                                "itl_residual_norm_dropout_backward");
+}
+
+namespace {
+
+// Operands of the block-scaled product: 32-bit offsets over 256 rows, and sizes whose products fit.
+constexpr int64_t kMaxBlockWidth = (int64_t)1 << 23;
+
+int64_t whole_blocks(int64_t n) { return (n + kFp8DMultiple - 1) / kFp8DMultiple; }
+
+itl_status quantize(const void* X, itl_dtype dtype, int64_t n_rows, int64_t d, bool tiles, uint8_t* Xq, float* scale,
+                    uint8_t* Xtq, float* t_scale, void* stream, const char* name) {
+  if (n_rows < 0 || d <= 0) return fail(ITL_ERR_INVALID_ARG, "n_rows must be >= 0 and d > 0");
+  if (!known_dtype(dtype)) return fail(ITL_ERR_UNSUPPORTED, "dtype must be ITL_BF16 or ITL_F32");
+  if (n_rows > INT32_MAX || d > kMaxBlockWidth) return fail(ITL_ERR_UNSUPPORTED, "too many rows or columns");
+  if (n_rows == 0) return ITL_OK;
+  if (!X || (!Xq && !Xtq) || (Xq && !scale) || (Xtq && !t_scale))
+    return fail(ITL_ERR_INVALID_ARG, "null X, both of Xq and Xtq, or the scale of one");
+  if ((reinterpret_cast<uintptr_t>(X) & (elem_size(dtype) - 1)) != 0) return fail(ITL_ERR_INVALID_ARG, "X must be aligned by element");
+  if (misaligned16(Xq, Xtq)) return fail(ITL_ERR_INVALID_ARG, "Xq and Xtq must be 16-byte aligned");
+  const int64_t across = whole_blocks(d), down = whole_blocks(n_rows);
+  if (outputs_share({{Xq, n_rows * across * kFp8DMultiple}, {Xq ? scale : nullptr, 4 * across * (tiles ? down : n_rows)},
+                     {Xtq, d * down * kFp8DMultiple}, {Xtq ? t_scale : nullptr, 4 * down * (tiles ? across : d)}},
+                    {{X, n_rows * d * elem_size(dtype)}}))
+    return fail(ITL_ERR_INVALID_ARG, "outputs share memory with X or each other");
+  hipError_t e = itl::launch_quantize_blocks(X, (int)dtype, n_rows, d, tiles, Xq, scale, Xtq, t_scale,
+                                             static_cast<hipStream_t>(stream));
+  return e == hipSuccess ? ITL_OK : hip_fail(e, name);
+}
+
+}  // namespace
+
+itl_status itl_quantize_blocks_fp8(const void* X, itl_dtype dtype, int64_t n_rows, int64_t d, uint8_t* Xq, float* scale,
+                                   uint8_t* Xtq, float* t_scale, void* stream) {
+  g_last_error.clear();
+  return quantize(X, dtype, n_rows, d, false, Xq, scale, Xtq, t_scale, stream, "itl_quantize_blocks_fp8");
+}
+
+itl_status itl_quantize_tiles_fp8(const void* X, itl_dtype dtype, int64_t n_rows, int64_t d, uint8_t* Xq, float* scale,
+                                  uint8_t* Xtq, float* t_scale, void* stream) {
+  g_last_error.clear();
+  return quantize(X, dtype, n_rows, d, true, Xq, scale, Xtq, t_scale, stream, "itl_quantize_tiles_fp8");
+}
+
+itl_status itl_matmul_fp8_blocks(const uint8_t* Aq, const float* a_scale, const uint8_t* Bq, const float* b_scale, int64_t m,
+                                 int64_t n, int64_t k, itl_dtype out_dtype, void* C, void* stream) {
+  g_last_error.clear();
+  if (m < 0 || n < 0 || k < 0) return fail(ITL_ERR_INVALID_ARG, "m, n and k must be >= 0");
+  if (!known_dtype(out_dtype)) return fail(ITL_ERR_UNSUPPORTED, "out_dtype must be ITL_BF16 or ITL_F32");
+  if (k % kFp8DMultiple != 0) return fail(ITL_ERR_UNSUPPORTED, "k must be a multiple of 128");
+  if (m > INT32_MAX || n > INT32_MAX || k > kMaxBlockWidth) return fail(ITL_ERR_UNSUPPORTED, "m, n or k too large");
+  if (m == 0 || n == 0) return ITL_OK;
+  if (!C || (k > 0 && (!Aq || !a_scale || !Bq || !b_scale)))
+    return fail(ITL_ERR_INVALID_ARG, "null Aq, a_scale, Bq, b_scale or C");
+  if (k > 0 && misaligned16(Aq, Bq)) return fail(ITL_ERR_INVALID_ARG, "Aq and Bq must be 16-byte aligned");
+  if ((reinterpret_cast<uintptr_t>(C) & (elem_size(out_dtype) - 1)) != 0)
+    return fail(ITL_ERR_INVALID_ARG, "C must be aligned by element");
+  const int64_t blocks = k / kFp8DMultiple;
+  if (outputs_share({{C, m * n * elem_size(out_dtype)}},
+                    {{Aq, m * k}, {a_scale, 4 * m * blocks}, {Bq, n * k}, {b_scale, 4 * whole_blocks(n) * blocks}}))
+    return fail(ITL_ERR_INVALID_ARG, "C shares memory with an operand");
+  hipError_t e = itl::launch_matmul_fp8_blocks(itl::MatmulFp8{Aq, Bq, a_scale, b_scale, m, n, k, C, (int)out_dtype},
+                                               static_cast<hipStream_t>(stream));
+  return e == hipSuccess ? ITL_OK : hip_fail(e, "itl_matmul_fp8_blocks");
 }
 
 namespace {
@@ -773,7 +951,7 @@ const char* itl_build_info(void) {
     snprintf(buf, sizeof buf,
              "itl 0.3 arch=gfx950 threads=%d wide_threads=%d token_block=%d vocab_tile=%d k_step_bytes=%d w_slots=%d h_slots=%d "
              "swap_slots_over_k_steps=%d max_slices=%d slices=balanced narrow_max_tokens=%d narrow_token_block=%d narrow128_max_tokens=%d "
-             "mfma_bf16=16x16x32 mfma_f32=16x16x4 fp8=e4m3_row_scaled mfma_fp8=16x16x128 mxfp4=e2m1_e8m0_32 mfma_mxfp4=32x32x64 "
+             "mfma_bf16=16x16x32 mfma_f32=16x16x4 fp8=e4m3_row_scaled mfma_fp8=16x16x128 fp8_blocks=128_f32_scales dropout=philox4x32_10_u16 mxfp4=e2m1_e8m0_32 mfma_mxfp4=32x32x64 "
              "bwd_chunk_tokens=%d loss_segment_tokens=%d loss_lane_segment=%d loss_wave_segment=%d loss_threads=%d "
              "loss_mean_chunk=%d loss_sums=f64 bwd_sampled_sort=stable_counting bwd_sampled_segment=%d "
              "bwd_sampled_group=%d",

@@ -98,6 +98,50 @@ hipError_t launch_residual_norm_backward(const void* du, int grad_dtype, const v
                                          long long n_rows, int d, float scale, void* dx, void* dy, void* dgate,
                                          float* dw_pre, float* dw_post, void* workspace, hipStream_t stream);
 
+// The end of a norm's backward: the runs' column sums added (norm.hip). Null outputs are left out.
+hipError_t launch_norm_backward_finish(const float* part, int runs, int d, float* dw_pre, float* dw_post, float* dgate,
+                                       hipStream_t stream);
+
+struct DropoutArgs;
+
+// y = x with dropout (dropout.hip); y may be x.
+hipError_t launch_dropout(const void* x, int dtype, long long n_rows, int d, const DropoutArgs& drop, void* y,
+                          hipStream_t stream);
+
+// The norms with dropout of y (norm_dropout.hip) and with u as block-scaled E4M3
+// rows, u_scale [d / 128, n_rows] (norm_codes.hip; drop.seed null: no dropout).
+hipError_t launch_residual_norm_dropout(const void* x, const void* y, const void* gate, long long gate_stride,
+                                        const void* w_post, const void* w_pre, int dtype, long long n_rows, int d,
+                                        float scale, float eps, const DropoutArgs& drop, void* h, void* u, float* rstd_pre,
+                                        float* rstd_post, hipStream_t stream);
+hipError_t launch_residual_norm_blocks(const void* x, const void* y, const void* gate, long long gate_stride,
+                                       const void* w_post, const void* w_pre, int dtype, long long n_rows, int d,
+                                       float scale, float eps, const DropoutArgs& drop, void* h, uint8_t* codes,
+                                       float* u_scale, float* rstd_pre, float* rstd_post, hipStream_t stream);
+hipError_t launch_residual_norm_dropout_backward(const void* du, int grad_dtype, const void* dh, const void* h, const void* y,
+                                                 const void* gate, long long gate_stride, const void* w_post,
+                                                 const void* w_pre, const float* rstd_pre, const float* rstd_post,
+                                                 int dtype, long long n_rows, int d, float scale, const DropoutArgs& drop,
+                                                 void* dx, void* dy, void* dgate, float* dw_pre, float* dw_post,
+                                                 void* workspace, hipStream_t stream);
+
+// E4M3 codes with a scale for each 128 values of a row (tiles false) or each 128 x 128
+// tile (quantize_blocks.hip): Xq [n_rows, d rounded up to 128], scale [d / 128, n_rows]
+// (tiles: [n_rows / 128, d / 128]), and of the transpose: Xtq [d, n_rows rounded up],
+// t_scale [n_rows / 128, d] (tiles: [d / 128, n_rows / 128]). Either pair may be null.
+hipError_t launch_quantize_blocks(const void* X, int dtype, long long n_rows, long long d, bool tiles, uint8_t* Xq,
+                                  float* scale, uint8_t* Xtq, float* t_scale, hipStream_t stream);
+
+// C [m, n] = A B^T of block-scaled E4M3 operands (matmul_fp8.hip).
+struct MatmulFp8 {
+  const uint8_t *A, *B;
+  const float *a_scale, *b_scale;
+  long long m, n, k;
+  void* C;
+  int out_dtype;
+};
+hipError_t launch_matmul_fp8_blocks(const MatmulFp8& c, hipStream_t stream);
+
 // The vocabulary cross entropy (cross_entropy.hip), with the gradient where dH is given.
 struct CeCall {
   const void *H, *W;
