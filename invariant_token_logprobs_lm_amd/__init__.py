@@ -245,6 +245,9 @@ def _stream(device):
 
 
 def _need(t, name, dtypes, device=None, ndim=None):
+    if (isinstance(t, torch.Tensor) and t.dtype in dtypes and t.is_cuda and (device is None or t.device == device)
+            and (ndim is None or t.dim() == ndim) and t.is_contiguous()):
+        return
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dtype not in dtypes:

@@ -681,6 +681,7 @@ itl_status itl_matmul_fp8_blocks(const uint8_t* Aq, const float* a_scale, const 
   if (!known_dtype(out_dtype)) return fail(ITL_ERR_UNSUPPORTED, "out_dtype must be ITL_BF16 or ITL_F32");
   if (k % kFp8DMultiple != 0) return fail(ITL_ERR_UNSUPPORTED, "k must be a multiple of 128");
   if (m > INT32_MAX || n > INT32_MAX || k > kMaxBlockWidth) return fail(ITL_ERR_UNSUPPORTED, "m, n or k too large");
+  if (n > 0 && m > ((int64_t)1 << 40) / n) return fail(ITL_ERR_UNSUPPORTED, "m n too large");  // (tiles are counted in 32 bits)
   if (m == 0 || n == 0) return ITL_OK;
   if (!C || (k > 0 && (!Aq || !a_scale || !Bq || !b_scale)))
     return fail(ITL_ERR_INVALID_ARG, "null Aq, a_scale, Bq, b_scale or C");

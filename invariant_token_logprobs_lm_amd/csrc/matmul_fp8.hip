@@ -30,6 +30,7 @@
 #include "itl_launch.h"
 #include "learner_common.h"
 #include "tile_engine.h"
+#include "tile_engine8.h"
 
 namespace itl {
 
@@ -96,27 +97,45 @@ struct ProductArgs {
   int k, tiles_n;
   long long tiles;
   bool quads;  // C's rows are whole fours of columns, aligned as such
+  bool lines;  // C's rows are whole 16-byte pieces, aligned as such
 };
 
-// Four consecutive columns of a row of C.
+// Four consecutive columns of a row of C, aligned as such.
+template <int kOut>
+__device__ __forceinline__ void put4(typename Elem<kOut>::T* out, const floatx4& v) {
+  using E = Elem<kOut>;
+  if constexpr (kOut == 0) {
+    *reinterpret_cast<uint2*>(out) = make_uint2((uint32_t)E::from_f(v[0]) | ((uint32_t)E::from_f(v[1]) << 16),
+                                                (uint32_t)E::from_f(v[2]) | ((uint32_t)E::from_f(v[3]) << 16));
+  } else {
+    *reinterpret_cast<float4*>(out) = make_float4(v[0], v[1], v[2], v[3]);
+  }
+}
+
+// The same within C, of any alignment.
 template <int kOut>
 __device__ __forceinline__ void store4(const ProductArgs& a, long long row, long long col, const floatx4& v) {
   using E = Elem<kOut>;
   using T = typename E::T;
   if (row >= a.m || col >= a.n) return;
   T* out = static_cast<T*>(a.C) + row * a.n + col;
-  if (a.quads) {
-    if constexpr (kOut == 0) {
-      *reinterpret_cast<uint2*>(out) = make_uint2((uint32_t)E::from_f(v[0]) | ((uint32_t)E::from_f(v[1]) << 16),
-                                                  (uint32_t)E::from_f(v[2]) | ((uint32_t)E::from_f(v[3]) << 16));
-    } else {
-      *reinterpret_cast<float4*>(out) = make_float4(v[0], v[1], v[2], v[3]);
-    }
-    return;
-  }
+  if (a.quads) return put4<kOut>(out, v);
 #pragma unroll
   for (int i = 0; i < 4; ++i)
     if (col + i < a.n) out[i] = E::from_f(v[i]);
+}
+
+// Eight bf16 columns of a row within C, of any alignment.
+__device__ __forceinline__ void store8(const ProductArgs& a, uint16_t* to, uint4 v, long long row, long long col) {
+  if (row >= a.m || col >= a.n) return;
+  if (a.lines) {
+    *reinterpret_cast<uint4*>(to) = v;
+    return;
+  }
+  uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int e = 0; e < 8; ++e)
+    if (col + e < a.n) to[e] = (uint16_t)(w[e >> 1] >> (16 * (e & 1)));
 }
 
 // kBR columns of C (rows of B) by kAR rows, a grid of kWB x kWA wavefronts, both
@@ -228,6 +247,248 @@ __global__ __launch_bounds__(64 * kWB * kWA) void product_tile_kernel(ProductArg
       store4<kOut>(a, i0 + wa * (kAR / kWA) + an * 16 + c16, j0 + wb * (kBR / kWB) + bm * 16 + 4 * quad, acc[bm][an]);
 }
 
+// 256 x 256 tiles for large products: eight wavefronts, each 128 columns of C by
+// 64 rows, one workgroup per CU that walks its tiles without letting the loads
+// run dry between them.
+//
+// Wavefronts w and w + 4 share a SIMD, so that one's waits lie under the other's
+// instructions. A step is 32 of them. The first 16 take B's blocks 0 .. 3 one after
+// the other against A's four, the last 16 A's blocks one after the other against
+// B's 4 .. 7: each of the eight fragments in registers is refilled right after its
+// last use, three instructions or more before its next. The step's last reads are
+// under way after the first half, so its one barrier comes a little after that; it
+// publishes the next step (loaded one step before) and frees this step's slot,
+// whose loads for the step after next are spread over the second half. An
+// instruction's sums are scaled into the accumulators three instructions later,
+// when they are there.
+constexpr int kWide = 256;
+constexpr int kWideRows = kWide * kRowChunks;          // chunks of an operand's rows of a step
+constexpr int kWideSlot = 2 * kWideRows + 64 + 16;     // and A's 256 scales, B's two (of 64 lanes)
+constexpr int kTurnPitch = 128 + 16;                   // bytes of a row of a wavefront's turned results
+constexpr int kTurnChunks = 16 * kTurnPitch / 16;      // of 16 rows
+constexpr int kCUs = 256;
+
+// Tile t's place, in tiles. Four rows of tiles are walked together, column by
+// column: the 32 tiles that a die works on at a time share 12 strips of operands.
+__device__ __forceinline__ int2 wide_tile(int tiles_m, int tiles_n, int t) {
+  const int band = t / (4 * tiles_n), in = t - band * 4 * tiles_n;
+  const int rows = min(4, tiles_m - band * 4);
+  const int j = in / rows;
+  return make_int2(__builtin_amdgcn_readfirstlane(band * 4 + in - j * rows), __builtin_amdgcn_readfirstlane(j));
+}
+
+__global__ __launch_bounds__(kThreads8, 2) void product_wide_kernel(ProductArgs a) {
+  __shared__ uint4 smem[2 * kWideSlot + 8 * kTurnChunks];
+  const Lanes8 L = lanes8();
+  const int lane = L.lane, quad = L.quad, c16 = L.c16;
+  const int steps = a.k / kBlock;
+  // A die (every eighth workgroup) has a run of consecutive tiles, its workgroups
+  // take them in turn.
+  const int die = blockIdx.x & 7, seats = gridDim.x >> 3;
+  const int tiles = (int)a.tiles, tiles_m = (int)((a.m + kWide - 1) / kWide);
+  const int t_end = (int)((long long)tiles * (die + 1) / 8);
+  int t = (int)((long long)tiles * die / 8) + (blockIdx.x >> 3);
+  if (t >= t_end) return;
+
+  const int lr = lane >> 3;
+  uint32_t voff[kDma8PerWave];
+#pragma unroll
+  for (int j = 0; j < kDma8PerWave; ++j)
+    voff[j] = (uint32_t)(L.wave * 32 + j * kDmaRows + lr) * (uint32_t)a.k + (((lane & 7) ^ lr ^ (j & 1)) * 16);
+  const uint32_t lds0 = (uint32_t)(size_t)((__attribute__((address_space(3))) uint4*)smem);
+  const uint32_t my_rows = (uint32_t)L.wave * 32 * kStepBytes;
+  // Wavefronts 0 .. 3 fetch 64 of A's scales each, the others B's two (all four the
+  // same ones; lanes past the two lie past the range).
+  const bool of_a = L.wave < 4;
+  const uint32_t scale_off = of_a ? (uint32_t)(L.wave * 64 + lane) * 4u : lane < 2 ? (uint32_t)(lane * steps) * 4u : 0x80000000u;
+  const uint32_t scale_lds = 2 * kWideRows * 16 + (of_a ? (uint32_t)L.wave * 256u : 1024u);
+  const uint64_t scale_step = of_a ? (uint64_t)a.m * 4 : 4;
+  // A tile's operands and scales. With no tile the ranges are empty: zeros are
+  // written into slots that nothing reads.
+  struct Source {
+    uint64_t b, a, scale;
+    uint32_t b_bytes, a_bytes, scale_bytes;
+  };
+  auto source = [&](int2 at, bool any) {
+    const long long i0 = (long long)at.x * kWide, j0 = (long long)at.y * kWide;
+    const uint32_t rows = (uint32_t)min((long long)kWide, a.m - i0), cols = (uint32_t)min((long long)kWide, a.n - j0);
+    const uint32_t tiles_b = cols > kBlock ? 2 : 1;
+    Source f;
+    f.b = (uint64_t)a.B + (uint64_t)j0 * (uint32_t)a.k;
+    f.a = (uint64_t)a.A + (uint64_t)i0 * (uint32_t)a.k;
+    f.scale = of_a ? (uint64_t)(a.a_scale + i0) : (uint64_t)(a.b_scale + (uint64_t)(2 * at.y) * (uint32_t)steps);
+    f.b_bytes = any ? cols * (uint32_t)a.k : 0;
+    f.a_bytes = any ? rows * (uint32_t)a.k : 0;
+    f.scale_bytes = any ? (of_a ? rows : tiles_b * (uint32_t)steps) * 4u : 0;
+    return f;
+  };
+  // The loads' own walk over the steps, two ahead: with three steps or more, in the
+  // next tile at most. (No branch: a step is one block, whose order stands as written.)
+  int2 at = wide_tile(tiles_m, a.tiles_n, t);
+  Source from = source(at, true), ahead = from;
+  int ld_s = 0;
+  auto words = [](uint64_t base, uint32_t bytes) {
+    return int4v{(int)(uint32_t)base, (int)((uint32_t)(base >> 32) & 0xffffu), (int)bytes, 0x00020000};
+  };
+  auto load = [&](int slot, int j) {  // the j-th of a step's nine loads
+    const uint32_t base = lds0 + (uint32_t)slot * kWideSlot * 16;
+    if (j < 4) {
+      dma16(words(from.b, from.b_bytes), voff[j & 3], (uint32_t)ld_s * kBlock, base + my_rows + j * 1024);
+    } else if (j < 8) {
+      dma16(words(from.a, from.a_bytes), voff[j & 3], (uint32_t)ld_s * kBlock, base + kWideRows * 16 + my_rows + (j & 3) * 1024);
+    } else {
+      dma4(words(from.scale, from.scale_bytes), scale_off, 0, base + scale_lds);
+      const bool last = ld_s + 1 == steps;
+      ld_s = last ? 0 : ld_s + 1;
+      from.b = last ? ahead.b : from.b;
+      from.a = last ? ahead.a : from.a;
+      from.scale = last ? ahead.scale : from.scale + scale_step;
+      from.b_bytes = last ? ahead.b_bytes : from.b_bytes;
+      from.a_bytes = last ? ahead.a_bytes : from.a_bytes;
+      from.scale_bytes = last ? ahead.scale_bytes : from.scale_bytes;
+    }
+  };
+  auto load_all = [&](int slot) {
+#pragma unroll
+    for (int j = 0; j < 9; ++j) load(slot, j);
+  };
+
+  int b_off[2], a_off[2];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int pc = (4 * h + lane_chunk(quad)) ^ swz(c16);
+    b_off[h] = (L.wv * 128 + c16) * kRowChunks + pc;
+    a_off[h] = kWideRows + (L.tq * 64 + c16) * kRowChunks + pc;
+  }
+  Frag8 FB[4], FA[4];
+  float xs[4], sb;
+  auto read_b = [&](int slot, int bm) {
+    FB[bm & 3].lo = smem[slot * kWideSlot + b_off[0] + bm * 16 * kRowChunks];
+    FB[bm & 3].hi = smem[slot * kWideSlot + b_off[1] + bm * 16 * kRowChunks];
+  };
+  auto read_a = [&](int slot, int an) {
+    FA[an].lo = smem[slot * kWideSlot + a_off[0] + an * 16 * kRowChunks];
+    FA[an].hi = smem[slot * kWideSlot + a_off[1] + an * 16 * kRowChunks];
+  };
+  auto read_scales = [&](int slot) {
+    const float* f = reinterpret_cast<const float*>(smem + slot * kWideSlot + 2 * kWideRows);
+#pragma unroll
+    for (int an = 0; an < 4; ++an) xs[an] = f[L.tq * 64 + an * 16 + c16];
+    sb = f[256 + L.wv];
+  };
+  floatx4 acc[8][4];
+  constexpr int kLag = 3;  // instructions between one and the use of its result
+  // One step. kNext: the next step's first fragments are read in it (not in a
+  // tile's last: they are read after its results are stored). kPending: loads and
+  // stores issued after the next step's loads that may be in flight at the barrier.
+  auto step = [&](auto next, auto pending, int slot) {
+    floatx4 R[32];
+    float sab[4];
+#pragma unroll
+    for (int an = 0; an < 4; ++an) sab[an] = xs[an] * sb;
+    auto place = [](int i) { return i < 16 ? make_int2(i >> 2, i & 3) : make_int2(4 + (i & 3), (i - 16) >> 2); };
+    auto scale = [&](int i) {
+      const int2 at = place(i);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) acc[at.x][at.y][e] = __builtin_fmaf(R[i][e], sab[at.y], acc[at.x][at.y][e]);
+    };
+#pragma unroll
+    for (int i = 0; i < 32; ++i) {
+      const int2 at = place(i);
+      R[i] = floatx4{};
+      mma_f8_16(R[i], FB[at.x & 3], FA[at.y]);
+      if (i >= kLag) scale(i - kLag);
+      if (i < 16 && (i & 3) == 3) read_b(slot, 4 + (i >> 2));
+      if (i == 19) wait_and_barrier<decltype(pending)::value>();
+      if (i >= 20 && i < 29) load(slot, i - 20);
+      if constexpr (decltype(next)::value) {
+        if (i >= 19 && (i & 3) == 3) read_a(slot ^ 1, (i - 19) >> 2);
+        if (i >= 28) read_b(slot ^ 1, i - 28);
+        if (i == 27) read_scales(slot ^ 1);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    }
+#pragma unroll
+    for (int i = 32 - kLag; i < 32; ++i) scale(i);
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  auto read_first = [&](int slot) {
+    read_scales(slot);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      read_b(slot, i);
+      read_a(slot, i);
+    }
+  };
+  using Yes = std::true_type;
+  using No = std::false_type;
+  constexpr int kStores = 16;  // of a whole tile, per wavefront
+  using AfterStores = std::integral_constant<int, kStores>;
+  using None = std::integral_constant<int, 0>;
+
+  load_all(0);
+  load_all(1);
+  wait_and_barrier<0>();
+  int slot = 0;
+  for (;;) {
+    const bool more = t + seats < t_end;
+    const int2 to = more ? wide_tile(tiles_m, a.tiles_n, t + seats) : at;
+    ahead = source(to, more);
+    read_first(slot);
+#pragma unroll
+    for (int bm = 0; bm < 8; ++bm)
+#pragma unroll
+      for (int an = 0; an < 4; ++an) acc[bm][an] = floatx4{};
+    // (the tile before has left at most its stores behind this one's loads)
+    step(Yes{}, AfterStores{}, slot);
+    slot ^= 1;
+    for (int s = 1; s + 1 < steps; ++s, slot ^= 1) step(Yes{}, None{}, slot);
+    step(No{}, None{}, slot);
+    slot ^= 1;
+    // (the last step stays before the branches below, which its results alone would sink into)
+#pragma unroll
+    for (int bm = 0; bm < 8; ++bm)
+#pragma unroll
+      for (int an = 0; an < 4; ++an) asm volatile("" : "+v"(acc[bm][an]));
+    int ln = lane;
+    asm volatile("" : "+v"(ln));  // (per-lane addresses formed here, not kept across the steps)
+    // 16 rows by 64 columns at a time through LDS, so that whole 128-byte lines are
+    // written (8 bytes per lane in 32-byte pieces took twice as long)
+    char* turn = reinterpret_cast<char*>(smem + 2 * kWideSlot + L.wave * kTurnChunks);
+    char* put = turn + (ln & 15) * kTurnPitch + (ln >> 4) * 8;
+    const char* get = turn + (ln >> 3) * kTurnPitch + (ln & 7) * 16;
+    const long long row0 = (long long)at.x * kWide + L.tq * 64 + (ln >> 3), col0 = (long long)at.y * kWide + L.wv * 128 + (ln & 7) * 8;
+    uint16_t* out = static_cast<uint16_t*>(a.C) + row0 * a.n + col0;
+    const bool whole = a.lines && (long long)(at.x + 1) * kWide <= a.m && (long long)(at.y + 1) * kWide <= a.n;
+#pragma unroll
+    for (int an = 0; an < 4; ++an) {
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+#pragma unroll
+        for (int b = 0; b < 4; ++b) put4<0>(reinterpret_cast<uint16_t*>(put + b * 32), acc[4 * half + b][an]);
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          const uint4 v = *reinterpret_cast<const uint4*>(get + r * 8 * kTurnPitch);
+          uint16_t* to = out + (an * 16 + r * 8) * a.n + half * 64;
+          if (whole) *reinterpret_cast<uint4*>(to) = v;
+          else store8(a, to, v, row0 + an * 16 + r * 8, col0 + half * 64);
+        }
+      }
+    }
+    if (!whole) asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // (how many there were is not known)
+    if (!more) break;
+    t += seats;
+    at = to;
+  }
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // (no load into LDS outlives the workgroup)
+}
+
+void run_wide(ProductArgs a, hipStream_t stream) {
+  a.tiles_n = (int)ceil_div(a.n, kWide);
+  a.tiles = ceil_div(a.m, kWide) * a.tiles_n;
+  hipLaunchKernelGGL((product_wide_kernel), dim3((unsigned)std::min<long long>(ceil_div(a.tiles, 8) * 8, kCUs)), dim3(kThreads8), 0, stream, a);
+}
+
 template <int kOut, int kBR, int kAR, int kWB, int kWA, int kSlots>
 void run_tiles(ProductArgs a, hipStream_t stream) {
   a.tiles_n = (int)ceil_div(a.n, kBR);
@@ -235,9 +496,139 @@ void run_tiles(ProductArgs a, hipStream_t stream) {
   hipLaunchKernelGGL((product_tile_kernel<kOut, kBR, kAR, kWB, kWA, kSlots>), flat_grid(a.tiles), dim3(64 * kWB * kWA), 0, stream, a);
 }
 
+// Few rows of A (16 kAN at most): B is read once, straight into registers, and a
+// workgroup's eight wavefronts share the blocks of its 16 kBM columns of C, so that
+// many loads are under way wherever there are few columns. A block's unscaled sums
+// go to LDS, and each element's chain over the blocks is then walked in order by
+// one thread: the bits of the tiles' kernels. kHeld blocks of a wavefront are
+// loaded at a time, the next ones while the chain is walked.
+constexpr int kFewWaves = 8;
+
+template <int kOut, int kBM, int kAN>
+__global__ __launch_bounds__(64 * kFewWaves) void product_few_kernel(ProductArgs a) {
+  constexpr int kHeld = 8 / (kBM * kAN), kRound = kHeld * kFewWaves;  // blocks of a round
+  constexpr int kEach = kBM * kAN * 256 / (64 * kFewWaves) > 0 ? kBM * kAN * 256 / (64 * kFewWaves) : 1;  // elements per thread
+  static_assert(kHeld >= 1, "a wavefront holds a block at least");
+  __shared__ floatx4 part[kRound][kBM * kAN][64];
+  __shared__ float scales[kRound][16 * kAN];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int quad = lane >> 4, c16 = lane & 15;
+  const long long group = flat_group();
+  if (group >= a.tiles) return;
+  const long long j0 = group * 16 * kBM;
+  const int blocks = a.k / kBlock, m = (int)a.m;
+  const int at0 = lane_chunk(quad) * 16, at1 = (4 + lane_chunk(quad)) * 16;
+  const float* b_scale = a.b_scale + j0 / kBlock * blocks;
+
+  uint4 vb[kHeld][kBM][2], va[kHeld][kAN][2];
+  auto load = [&](int first) {
+#pragma unroll
+    for (int h = 0; h < kHeld; ++h) {
+      const int b = first + h * kFewWaves + wave;
+#pragma unroll
+      for (int i = 0; i < kBM; ++i) {
+        const long long row = j0 + 16 * i + c16;
+        const uint8_t* p = a.B + row * a.k + (long long)b * kBlock;
+        const bool in = b < blocks && row < a.n;
+        vb[h][i][0] = in ? *reinterpret_cast<const uint4*>(p + at0) : make_uint4(0u, 0u, 0u, 0u);
+        vb[h][i][1] = in ? *reinterpret_cast<const uint4*>(p + at1) : make_uint4(0u, 0u, 0u, 0u);
+      }
+#pragma unroll
+      for (int i = 0; i < kAN; ++i) {
+        const int row = 16 * i + c16;
+        const uint8_t* p = a.A + (long long)row * a.k + (long long)b * kBlock;
+        const bool in = b < blocks && row < m;
+        va[h][i][0] = in ? *reinterpret_cast<const uint4*>(p + at0) : make_uint4(0u, 0u, 0u, 0u);
+        va[h][i][1] = in ? *reinterpret_cast<const uint4*>(p + at1) : make_uint4(0u, 0u, 0u, 0u);
+      }
+    }
+  };
+  // Element e of this thread: float (64 kFewWaves e + threadIdx.x) of a block's sums.
+  float acc[kEach];
+#pragma unroll
+  for (int e = 0; e < kEach; ++e) acc[e] = 0.0f;
+
+  load(0);
+  for (int first = 0; first < blocks; first += kRound) {
+    for (int i = threadIdx.x; i < kRound * 16 * kAN; i += 64 * kFewWaves) {
+      const int b = first + i / (16 * kAN), row = i % (16 * kAN);
+      (&scales[0][0])[i] = b < blocks && row < m ? a.a_scale[(long long)b * m + row] * b_scale[b] : 0.0f;
+    }
+#pragma unroll
+    for (int h = 0; h < kHeld; ++h) {
+      Operand<kOut> fa[kAN];
+#pragma unroll
+      for (int i = 0; i < kAN; ++i) fa[i].set(va[h][i][0], va[h][i][1]);
+#pragma unroll
+      for (int j = 0; j < kBM; ++j) {
+        Operand<kOut> fb;
+        fb.set(vb[h][j][0], vb[h][j][1]);
+        floatx4 p[kAN];
+        Operand<kOut>::products(fb, fa, p);
+#pragma unroll
+        for (int i = 0; i < kAN; ++i) part[h * kFewWaves + wave][j * kAN + i][lane] = p[i];
+      }
+    }
+    if (first + kRound < blocks) load(first + kRound);
+    __syncthreads();
+    const int count = min(kRound, blocks - first);
+#pragma unroll
+    for (int e = 0; e < kEach; ++e) {
+      const int f = 64 * kFewWaves * e + threadIdx.x;
+      if (f < kBM * kAN * 256) {
+        const float* p = reinterpret_cast<const float*>(part) + f;
+        const float* s = &scales[0][16 * ((f >> 8) % kAN) + ((f >> 2) & 15)];
+#pragma unroll 8
+        for (int b = 0; b < count; ++b) acc[e] = __builtin_fmaf(p[b * kBM * kAN * 256], s[b * 16 * kAN], acc[e]);
+      }
+    }
+    __syncthreads();
+  }
+#pragma unroll
+  for (int e = 0; e < kEach; ++e) {
+    const int f = 64 * kFewWaves * e + threadIdx.x, which = f >> 8;
+    const long long row = 16 * (which % kAN) + ((f >> 2) & 15), col = j0 + 16 * (which / kAN) + 4 * ((f >> 6) & 3) + (f & 3);
+    if (f < kBM * kAN * 256 && row < a.m && col < a.n)
+      static_cast<typename Elem<kOut>::T*>(a.C)[row * a.n + col] = Elem<kOut>::from_f(acc[e]);
+  }
+}
+
+template <int kOut, int kBM, int kAN>
+void run_few(ProductArgs a, hipStream_t stream) {
+  a.tiles = ceil_div(a.n, 16 * kBM);
+  hipLaunchKernelGGL((product_few_kernel<kOut, kBM, kAN>), flat_grid(a.tiles), dim3(64 * kFewWaves), 0, stream, a);
+}
+
+// Which kernel: all give the same bits. us measured on both sides of each border
+// (bf16 results; m x n x k).
 template <int kOut>
 void run_product(const ProductArgs& a, hipStream_t stream) {
-  run_tiles<kOut, 128, 128, 2, 2, 2>(a, stream);
+  // Few rows and so few columns that a CU has one workgroup of 16, 32 or 64 columns
+  // (more columns per workgroup read A less often): the blocks are shared by the
+  // wavefronts. 16 x 2560 x 7168 9.5, in 64 x 64 tiles 21.8; 16 x 10240 x 7168 19.0
+  // and 28.2; 16 x 20480 x 7168 35.5 and 29.6. 32 x 5120 x 7168 17.4 and 27.3;
+  // 32 x 10240 x 7168 29.5 and 28.9.
+  if (a.m <= 16 && a.n <= 16 * kCUs) return run_few<kOut, 1, 1>(a, stream);
+  if (a.m <= 16 && a.n <= 32 * kCUs) return run_few<kOut, 2, 1>(a, stream);
+  if (a.m <= 16 && a.n <= 64 * kCUs) return run_few<kOut, 4, 1>(a, stream);
+  if (a.m <= 32 && a.n <= 16 * kCUs) return run_few<kOut, 1, 2>(a, stream);
+  if (a.m <= 32 && a.n <= 32 * kCUs) return run_few<kOut, 2, 2>(a, stream);
+  // Half the CUs or more with a 256 x 256 tile: 1024 x 10240 x 2560 (160 tiles) 35.7,
+  // in 64 x 128 tiles 44.2; 4096 x 1536 x 2560 (96) 35.7 and 27.8.
+  if constexpr (kOut == 0) {
+    if (a.m > 128 && a.k >= 3 * kBlock && ceil_div(a.m, kWide) * ceil_div(a.n, kWide) >= kCUs / 2) return run_wide(a, stream);
+  }
+  // Tiles of 64 x 64 while they run at once, four per CU: 1024 x 2560 x 2560 (640) 16.8,
+  // in 64 x 128 tiles 17.9; 2048 x 2560 x 2560 (1280) 28.9 and 26.6.
+  if (ceil_div(a.m, 64) * ceil_div(a.n, 64) <= 4 * kCUs) return run_tiles<kOut, 64, 64, 2, 2, 2>(a, stream);
+  // Many columns for few rows are a matter of B's bytes: 64 x 61440 x 7168 85.5 in tiles
+  // of 128 columns, 97.1 of 64; 128 x 61440 x 7168 102 (128 x 128 tiles), 137 (64 x 128).
+  if (a.m <= 64) return run_tiles<kOut, 128, 64, 2, 2, 3>(a, stream);
+  // fp32 results (no larger tiles): 2048 x 10240 x 7168 (1280 tiles) 286, in 64 x 128 tiles
+  // 329; 1024 x 10240 x 7168 (640) 177 and 171.
+  if (a.m <= 128 || ceil_div(a.m, 128) * ceil_div(a.n, 128) >= 4 * kCUs) return run_tiles<kOut, 128, 128, 2, 2, 2>(a, stream);
+  run_tiles<kOut, 64, 128, 2, 2, 2>(a, stream);
 }
 
 }  // namespace
@@ -245,7 +636,8 @@ void run_product(const ProductArgs& a, hipStream_t stream) {
 hipError_t launch_matmul_fp8_blocks(const MatmulFp8& c, hipStream_t stream) {
   const uintptr_t four = c.out_dtype == 0 ? 7 : 15;
   const ProductArgs a{c.A, c.B, c.a_scale, c.b_scale, c.C, c.m, c.n, (int)c.k, 0, 0,
-                      c.n % 4 == 0 && (reinterpret_cast<uintptr_t>(c.C) & four) == 0};
+                      c.n % 4 == 0 && (reinterpret_cast<uintptr_t>(c.C) & four) == 0,
+                      c.n % (c.out_dtype == 0 ? 8 : 4) == 0 && (reinterpret_cast<uintptr_t>(c.C) & 15) == 0};
   if (c.out_dtype == 0) run_product<0>(a, stream);
   else run_product<1>(a, stream);
   return hipGetLastError();

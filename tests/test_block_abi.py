@@ -89,7 +89,7 @@ def test_product_arguments(itl):
     assert f(m=0, A=0, C=0) == OK and f(n=0, B=0, C=0) == OK
     assert f(m=-1) == INVALID and f(n=-1) == INVALID and f(k=-128) == INVALID
     assert f(k=64) == UNSUPPORTED and f(dt=7) == UNSUPPORTED and f(k=(1 << 23) + 128) == UNSUPPORTED
-    assert f(m=1 << 31) == UNSUPPORTED and f(n=1 << 31) == UNSUPPORTED
+    assert f(m=1 << 31) == UNSUPPORTED and f(n=1 << 31) == UNSUPPORTED and f(m=1 << 30, n=1 << 11) == UNSUPPORTED
     for name in ("A", "sa", "B", "sb", "C"):
         assert f(**{name: 0}) == INVALID, name
     assert f(A=M + 8) == INVALID and f(B=3 * M + 8) == INVALID and f(C=5 * M + 1) == INVALID and f(dt=1, C=5 * M + 2) == INVALID

@@ -26,7 +26,8 @@ DTYPES = [torch.bfloat16, torch.float32]
 SIZES = [(1, 1, 128), (1, 16, 256), (1, 1536, 1536), (2, 100, 384), (5, 127, 128), (15, 129, 1024), (16, 300, 8960),
          (17, 65, 512), (31, 1000, 256), (33, 128, 640), (64, 129, 384), (65, 250, 1536), (100, 77, 128), (127, 255, 256),
          (128, 256, 512), (129, 257, 384), (200, 1001, 1536), (256, 256, 128), (257, 513, 256), (300, 200, 8448),
-         (777, 1001, 1536), (1024, 1536, 640), (8, 40, 16640)]
+         (777, 1001, 1536), (1024, 1536, 640), (8, 40, 16640), (3, 5000, 256), (16, 9000, 384), (30, 8000, 128),
+         (33, 70000, 128), (90, 70000, 256), (4000, 1100, 128), (2100, 4100, 384), (4353, 4097, 640), (16900, 600, 512)]
 
 
 @pytest.fixture(scope="module")
@@ -162,6 +163,25 @@ def test_rows_do_not_depend_on_their_batch(cuda, itl, n, k, dtype):
         assert torch.equal(_bits(some), _bits(whole[i:i + m])), (i, m)
 
 
+@pytest.mark.parametrize("k", [384, 512])
+def test_rows_of_a_large_product(cuda, itl, k):
+    """Rows that large tiles made, several per workgroup, and those of smaller calls: the same bits."""
+    m, n = 4300, 4000
+    a, sa, b, sb = _operands(itl, m, n, k, cuda)
+    whole = itl.matmul_fp8_blocks(a, sa, b, sb)
+    for i, some in ((0, 1), (4200, 100), (1000, 700), (255, 33)):
+        got = itl.matmul_fp8_blocks(a[i:i + some].contiguous(), sa[:, i:i + some].contiguous(), b, sb)
+        assert torch.equal(_bits(got), _bits(whole[i:i + some])), i
+    # run to run, beside another stream's work
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        other = itl.matmul_fp8_blocks(a, sa, b, sb)
+    again = itl.matmul_fp8_blocks(a, sa, b, sb)
+    torch.cuda.synchronize()
+    assert torch.equal(_bits(other), _bits(whole)) and torch.equal(_bits(again), _bits(whole))
+
+
 def test_columns_do_not_depend_on_the_width(cuda, itl):
     """The first columns of a wider B, down to a few: the same bits."""
     for m in (3, 40, 300):
@@ -174,10 +194,10 @@ def test_columns_do_not_depend_on_the_width(cuda, itl):
 
 @pytest.mark.parametrize("dtype", DTYPES)
 def test_outputs_of_any_alignment_and_nothing_beyond(cuda, itl, dtype):
-    for m, n in ((1, 12), (3, 13), (20, 64), (130, 260), (300, 258)):
-        ops = _operands(itl, m, n, 256, cuda)
+    for m, n in ((1, 12), (3, 13), (20, 64), (130, 260), (300, 258), (2048, 4090), (2048, 4096), (2050, 4092)):
+        ops = _operands(itl, m, n, 384, cuda)
         want = itl.matmul_fp8_blocks(*ops, out_dtype=dtype)
-        for at in (8, 9, 10):
+        for at in (8, 9, 10, 12):
             flat = torch.full((m * n + 32,), 7.0, dtype=dtype, device=cuda)
             out = flat[at:at + m * n].view(m, n)
             assert itl.matmul_fp8_blocks(*ops, out_dtype=dtype, out=out) is out
@@ -231,7 +251,7 @@ def test_linear_layer_and_its_gradients(cuda, itl):
         assert float((R.f64(got) - want).norm()) <= 0.05 * float(want.norm())
 
 
-@pytest.mark.parametrize("m", [1, 40, 300])
+@pytest.mark.parametrize("m", [1, 40, 300, 33000])
 def test_replays_and_other_streams(cuda, itl, m):
     x, w = torch.randn(m, 1000, device=cuda), torch.randn(520, 1000, device=cuda).mul_(0.02)
     wq, ws, _, _ = itl.quantize_tiles_fp8(w)
