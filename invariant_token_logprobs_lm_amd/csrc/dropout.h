@@ -46,9 +46,9 @@ __device__ __forceinline__ uint4 dropout_numbers(const DropoutArgs& a, DropoutKe
 #pragma unroll
   for (int r = 0; r < 10; ++r) {
     const uint64_t p0 = (uint64_t)c0 * 0xD2511F53u, p1 = (uint64_t)c2 * 0xCD9E8D57u;
-    c0 = (uint32_t)(p1 >> 32) ^ c1 ^ k0;
+    c0 = __builtin_amdgcn_bitop3_b32((uint32_t)(p1 >> 32), c1, k0, 0x96);  // all three, exclusive or
     c1 = (uint32_t)p1;
-    c2 = (uint32_t)(p0 >> 32) ^ c3 ^ k1;
+    c2 = __builtin_amdgcn_bitop3_b32((uint32_t)(p0 >> 32), c3, k1, 0x96);
     c3 = (uint32_t)p0;
     k0 += 0x9E3779B9u;
     k1 += 0xBB67AE85u;
@@ -62,22 +62,25 @@ __device__ __forceinline__ bool dropout_keeps(const uint4& u, int j, uint32_t th
   return ((j & 1) ? w >> 16 : w & 0xffffu) >= threshold;
 }
 
-// Bit j: whether column 8 group + j is kept.
-__device__ __forceinline__ uint32_t dropout_bits(const DropoutArgs& a, DropoutKey key, uint32_t group, long long row) {
+// Whether columns 8 group + j are kept.
+struct Kept8 {
+  bool at[8];
+};
+__device__ __forceinline__ Kept8 dropout_kept(const DropoutArgs& a, DropoutKey key, uint32_t group, long long row) {
   const uint4 u = dropout_numbers(a, key, group, row);
-  uint32_t bits = 0;
+  Kept8 k;
 #pragma unroll
-  for (int j = 0; j < 8; ++j) bits |= dropout_keeps(u, j, a.threshold) ? 1u << j : 0u;
-  return bits;
+  for (int j = 0; j < 8; ++j) k.at[j] = dropout_keeps(u, j, a.threshold);
+  return k;
 }
 
-// Bit j: whether column first + j step + lane of this wavefront is kept (first,
+// Whether columns first + j step + lane of this wavefront are kept (first,
 // step: multiples of 8, the same in all lanes; every lane takes part). A column's
 // group has eight lanes, and the wavefront's eight columns per lane are 64
 // groups: lane l makes one call, for the group of lanes 8 (l / 8) .. + 7 at
 // j = l mod 8; ballots over the numbers' places then hand each lane its byte.
-__device__ __forceinline__ uint32_t dropout_bits_across(const DropoutArgs& a, DropoutKey key, uint32_t first,
-                                                        uint32_t step, long long row) {
+__device__ __forceinline__ Kept8 dropout_kept_across(const DropoutArgs& a, DropoutKey key, uint32_t first, uint32_t step,
+                                                     long long row) {
   const uint32_t l = threadIdx.x & 63;
   const uint4 u = dropout_numbers(a, key, (first + (l & 7) * step) / 8 + (l >> 3), row);
   const bool high = l >= 32;
@@ -90,7 +93,11 @@ __device__ __forceinline__ uint32_t dropout_bits_across(const DropoutArgs& a, Dr
   const uint32_t x0 = (l & 1) ? w[1] : w[0], x1 = (l & 1) ? w[3] : w[2];
   const uint32_t x2 = (l & 1) ? w[5] : w[4], x3 = (l & 1) ? w[7] : w[6];
   const uint32_t y0 = (l & 2) ? x1 : x0, y1 = (l & 2) ? x3 : x2;
-  return (((l & 4) ? y1 : y0) >> (8 * ((l >> 3) & 3))) & 0xffu;
+  const uint32_t bits = ((l & 4) ? y1 : y0) >> (8 * ((l >> 3) & 3));
+  Kept8 k;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) k.at[j] = (bits >> j) & 1;
+  return k;
 }
 
 // Whether one value is kept (a call for it alone).

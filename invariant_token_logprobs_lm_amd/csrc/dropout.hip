@@ -97,10 +97,10 @@ __global__ __launch_bounds__(kDropThreads) void dropout_any_kernel(DropoutCall a
   T v[8];
 #pragma unroll
   for (int j = 0; j < 8; ++j) v[j] = k0 + 64 * j < a.d ? x[k0 + 64 * j] : T(0);
-  const uint32_t bits = dropout_bits_across(a.drop, dropout_key(a.drop), first, 64, a.drop.first_row + row);
+  const Kept8 kept = dropout_kept_across(a.drop, dropout_key(a.drop), first, 64, a.drop.first_row + row);
 #pragma unroll
   for (int j = 0; j < 8; ++j)
-    if (k0 + 64 * j < a.d) y[k0 + 64 * j] = E::from_f(dropped(E::to_f(v[j]), (bits >> j) & 1, a.drop.scale));
+    if (k0 + 64 * j < a.d) y[k0 + 64 * j] = E::from_f(dropped(E::to_f(v[j]), kept.at[j], a.drop.scale));
 }
 
 }  // namespace

@@ -48,6 +48,7 @@
 #include <algorithm>
 #include <type_traits>
 
+#include "block_codes.h"
 #include "dropout.h"
 #include "itl_launch.h"
 #include "learner_common.h"
@@ -106,14 +107,6 @@ using FwdArgs = std::conditional_t<kDrop, NormDropArgs, NormArgs>;
 // one for each 128 columns.
 enum NormOut { kOwn, kRowCodes, kBlockCodes };
 
-// Largest of 16 lanes, the same in all of them.
-__device__ __forceinline__ float max16(float x) {
-  x = fmaxf(x, lane_move<0xB1>(x));
-  x = fmaxf(x, lane_move<0x4E>(x));
-  x = fmaxf(x, lane_move<0x141>(x));
-  return fmaxf(x, lane_move<0x140>(x));
-}
-
 // ---- rows in registers
 
 // Eight columns of a thread: group c of a row of T threads. Whole vectors:
@@ -122,10 +115,10 @@ template <bool kVec>
 struct Columns {
   int d, T, lane;
   __device__ __forceinline__ int at(int c, int j) const { return kVec ? 8 * (c * T + lane) + j : (8 * c + j) * T + lane; }
-  // Bit j: whether dropout keeps column at(c, j) of a row (all lanes of a wavefront take part).
-  __device__ __forceinline__ uint32_t kept(const DropoutArgs& drop, DropoutKey key, int c, long long row) const {
-    if constexpr (kVec) return dropout_bits(drop, key, (uint32_t)(c * T + lane), drop.first_row + row);
-    else return dropout_bits_across(drop, key, (uint32_t)(8 * c * T + (lane & ~63)), (uint32_t)T, drop.first_row + row);
+  // Whether dropout keeps columns at(c, j) of a row (all lanes of a wavefront take part).
+  __device__ __forceinline__ Kept8 kept(const DropoutArgs& drop, DropoutKey key, int c, long long row) const {
+    if constexpr (kVec) return dropout_kept(drop, key, (uint32_t)(c * T + lane), drop.first_row + row);
+    else return dropout_kept_across(drop, key, (uint32_t)(8 * c * T + (lane & ~63)), (uint32_t)T, drop.first_row + row);
   }
 };
 
@@ -261,9 +254,9 @@ __global__ __launch_bounds__(kNormThreads) void norm_held_kernel(FwdArgs<kDrop> 
       const DropoutKey key = dropout_key(a.drop);
 #pragma unroll
       for (int c = 0; c < kGroups; ++c) {
-        const uint32_t bits = k.kept(a.drop, key, c, row);
+        const Kept8 kept = k.kept(a.drop, key, c, row);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) y[c][j] = dropped(y[c][j], (bits >> j) & 1, a.drop.scale);
+        for (int j = 0; j < 8; ++j) y[c][j] = dropped(y[c][j], kept.at[j], a.drop.scale);
       }
     }
 #pragma unroll
@@ -312,16 +305,9 @@ __global__ __launch_bounds__(kNormThreads) void norm_held_kernel(FwdArgs<kDrop> 
 #pragma unroll
     for (int c = 0; c < kGroups; ++c) {
       const int at = k.at(c, 0);
-      float amax = 0.0f;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) amax = fmaxf(amax, fabsf(x[c][j]));
-      const float s = e4m3_scale(max16(amax));
-      float q[8];
-#pragma unroll
-      for (int j = 0; j < 8; ++j) q[j] = __fdiv_rn(x[c][j], s);
+      const float s = e4m3_scale(largest16(largest8(x[c])));
       if (at < k.d) {
-        *reinterpret_cast<uint2*>(a.codes + base + at) =
-            make_uint2(e4m3_code4(q[0], q[1], q[2], q[3]), e4m3_code4(q[4], q[5], q[6], q[7]));
+        *reinterpret_cast<uint2*>(a.codes + base + at) = codes8(x[c], Quotient(s));
         if ((k.lane & 15) == 0) a.u_scale[(size_t)(at >> 7) * a.n_rows + row] = s;
       }
     }
@@ -425,8 +411,10 @@ using BwdArgs = std::conditional_t<kDrop, NormBwdDropArgs, NormBwdArgs>;
 // part[blockIdx.x].
 constexpr int kBwdMaxWaves = 8;
 
+// (Dropout's bits leave the registers of three wavefronts per SIMD short: with two,
+// 16384 x 2560 fp32 takes 218 us, spilling with three 259; bf16 the same either way.)
 template <int kDtype, int kGrad, bool kDrop, bool kVec, int kGroups>
-__global__ __launch_bounds__(64 * kBwdMaxWaves, kGroups == 1 ? 3 : 2) void norm_backward_held_kernel(BwdArgs<kDrop> a) {
+__global__ __launch_bounds__(64 * kBwdMaxWaves, kGroups == 1 && !kDrop ? 3 : 2) void norm_backward_held_kernel(BwdArgs<kDrop> a) {
   using T = typename Elem<kDtype>::T;
   using TG = typename Elem<kGrad>::T;
   __shared__ float lds[2][kBwdMaxWaves][3];
@@ -440,7 +428,11 @@ __global__ __launch_bounds__(64 * kBwdMaxWaves, kGroups == 1 ? 3 : 2) void norm_
 #pragma unroll
     for (int j = 0; j < 8; ++j) s_pre[c][j] = s_post[c][j] = s_gate[c][j] = 0.0f;
   DropoutKey key;
-  if constexpr (kDrop) key = dropout_key(a.drop);
+  float scale = a.scale;  // of the gate's and the branch's gradients, where the value is kept
+  if constexpr (kDrop) {
+    key = dropout_key(a.drop);
+    scale *= a.drop.scale;
+  }
   using G = Group<kDtype, kVec>;
   G w_pre[kGroups], w_post[kGroups], gate[kGroups];
 #pragma unroll
@@ -469,16 +461,6 @@ __global__ __launch_bounds__(64 * kBwdMaxWaves, kGroups == 1 ? 3 : 2) void norm_
   };
   constexpr bool kAhead = kGroups == 1;  // (two groups have no registers left for it)
   if (kAhead && blockIdx.x < a.n_rows) fetch(blockIdx.x);
-  // A row's keep bits, taken at the end of the one before, when few registers are
-  // held and the row's loads are under way.
-  uint32_t bits[kGroups];
-  auto draw = [&](long long row) {
-    if constexpr (kDrop) {
-#pragma unroll
-      for (int c = 0; c < kGroups; ++c) bits[c] = k.kept(a.drop, key, c, row);
-    }
-  };
-  draw(blockIdx.x);
   int flip = 0;
   for (long long row = blockIdx.x; row < a.n_rows; row += gridDim.x, flip ^= 1) {
     const size_t base = (size_t)row * a.d;
@@ -487,6 +469,11 @@ __global__ __launch_bounds__(64 * kBwdMaxWaves, kGroups == 1 ? 3 : 2) void norm_
     // g = dx without the mean's part, n, q
     float g[kGroups][8], n[kGroups][8], q[kGroups][8];
     float A = 0.0f, B = 0.0f, C = 0.0f;
+    Kept8 kept[kGroups];
+    if constexpr (kDrop) {
+#pragma unroll
+      for (int c = 0; c < kGroups; ++c) kept[c] = k.kept(a.drop, key, c, row);
+    }
 #pragma unroll
     for (int c = 0; c < kGroups; ++c) {
       if (!shared_gate) gate[c] = r_gate[c];
@@ -504,9 +491,7 @@ __global__ __launch_bounds__(64 * kBwdMaxWaves, kGroups == 1 ? 3 : 2) void norm_
       if (a.w_post) {
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-          const float all = a.scale * (a.gate ? gate[c][j] : 1.0f) * w_post[c][j] * q[c][j];
-          float s = all;
-          if constexpr (kDrop) s = dropped(all, (bits[c] >> j) & 1, a.drop.scale);
+          const float s = (kDrop ? kept[c].at[j] ? scale : 0.0f : scale) * (a.gate ? gate[c][j] : 1.0f) * w_post[c][j] * q[c][j];
           B += s * g[c][j];
           C += s * (r_pre * n[c][j]);
         }
@@ -534,12 +519,12 @@ __global__ __launch_bounds__(64 * kBwdMaxWaves, kGroups == 1 ? 3 : 2) void norm_
         float dy[8], dg[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-          float sdx = a.scale * g[c][j];
-          if constexpr (kDrop) sdx = dropped(sdx, (bits[c] >> j) & 1, a.drop.scale);
+          float sdx = scale * g[c][j];
+          if constexpr (kDrop) sdx = kept[c].at[j] ? sdx : 0.0f;
           const float dp = a.gate ? sdx * gate[c][j] : sdx;
           if (a.gate) {
             dg[j] = sdx * (a.w_post ? q[c][j] * w_post[c][j] : q[c][j]);
-            if constexpr (kDrop) dg[j] = (bits[c] >> j) & 1 ? dg[j] : 0.0f;
+            if constexpr (kDrop) dg[j] = kept[c].at[j] ? dg[j] : 0.0f;
             s_gate[c][j] += dg[j];
           }
           if (a.w_post) {
@@ -554,7 +539,6 @@ __global__ __launch_bounds__(64 * kBwdMaxWaves, kGroups == 1 ? 3 : 2) void norm_
       }
       store_group<kDtype>(static_cast<T*>(a.dx) + base, k, c, g[c]);
     }
-    draw(row + gridDim.x);
   }
   float* part = a.part + (size_t)blockIdx.x * 3 * a.d;
 #pragma unroll

@@ -18,15 +18,14 @@
 
 #include <algorithm>
 
+#include "block_codes.h"
 #include "itl_launch.h"
-#include "learner_common.h"
 
 namespace itl {
 
 namespace {
 
 constexpr int kQuantThreads = 256;
-constexpr int kBlock = 128;
 
 struct QuantArgs {
   const void* X;
@@ -62,35 +61,13 @@ __device__ __forceinline__ void load8(const void* X, long long row, long long d,
   }
 }
 
-__device__ __forceinline__ float largest8(const float (&v)[8]) {
-  float m = 0.0f;
-#pragma unroll
-  for (int j = 0; j < 8; ++j) m = fmaxf(m, fabsf(v[j]));
-  return m;
-}
-
-// Largest of 16 lanes, the same in all of them.
-__device__ __forceinline__ float largest16(float x) {
-  x = fmaxf(x, lane_move<0xB1>(x));
-  x = fmaxf(x, lane_move<0x4E>(x));
-  x = fmaxf(x, lane_move<0x141>(x));
-  return fmaxf(x, lane_move<0x140>(x));
-}
-
-__device__ __forceinline__ uint2 codes8(const float (&v)[8], float s) {
-  float q[8];
-#pragma unroll
-  for (int j = 0; j < 8; ++j) q[j] = __fdiv_rn(v[j], s);
-  return make_uint2(e4m3_code4(q[0], q[1], q[2], q[3]), e4m3_code4(q[4], q[5], q[6], q[7]));
-}
-
 // Blocks of rows alone: 16 lanes have a block, a thread kQuantGroups of them,
 // all read before the first is dealt with.
 constexpr int kQuantGroups = 4;
 
 template <int kDtype, bool kWhole>
 __global__ __launch_bounds__(kQuantThreads) void quantize_block_rows_kernel(QuantArgs a) {
-  const int blocks = (int)((a.d + kBlock - 1) / kBlock);
+  const int blocks = (int)((a.d + kCodeBlock - 1) / kCodeBlock);
   const long long all = a.n_rows * blocks;
   const long long first = flat_group() * (kQuantGroups * kQuantThreads / 16) + (threadIdx.x >> 4);
   const int lane16 = threadIdx.x & 15;
@@ -102,14 +79,14 @@ __global__ __launch_bounds__(kQuantThreads) void quantize_block_rows_kernel(Quan
     const long long f = first + g * (kQuantThreads / 16);
     row[g] = f < (1LL << 32) ? (uint32_t)f / (uint32_t)blocks : f / blocks;
     block[g] = (int)(f - row[g] * blocks);
-    load8<kDtype, kWhole>(a.X, row[g], a.d, (long long)block[g] * kBlock + lane16 * 8, f < all, v[g]);
+    load8<kDtype, kWhole>(a.X, row[g], a.d, (long long)block[g] * kCodeBlock + lane16 * 8, f < all, v[g]);
   }
 #pragma unroll
   for (int g = 0; g < kQuantGroups; ++g) {
     const long long f = first + g * (kQuantThreads / 16);
     const float s = e4m3_scale(largest16(largest8(v[g])));
     if (f < all) {
-      *reinterpret_cast<uint2*>(a.Xq + (size_t)f * kBlock + lane16 * 8) = codes8(v[g], s);
+      *reinterpret_cast<uint2*>(a.Xq + (size_t)f * kCodeBlock + lane16 * 8) = codes8(v[g], Quotient(s));
       if (lane16 == 0) a.scale[(size_t)block[g] * a.n_rows + row[g]] = s;
     }
   }
@@ -118,16 +95,16 @@ __global__ __launch_bounds__(kQuantThreads) void quantize_block_rows_kernel(Quan
 // A 128 x 128 tile per workgroup: rows' codes (Xq), the transpose's (Xtq), or both.
 template <int kDtype, bool kWhole, bool kTiles>
 __global__ __launch_bounds__(kQuantThreads) void quantize_tile_kernel(QuantArgs a) {
-  __shared__ float tops[4][kBlock];
-  __shared__ uint2 turned[kBlock * 16];  // [column][8 rows], chunk c of column k at c ^ (k / 8)
-  const int across = (int)((a.d + kBlock - 1) / kBlock);
-  const long long down = (a.n_rows + kBlock - 1) / kBlock;
+  __shared__ float tops[4][kCodeBlock];
+  __shared__ uint2 turned[kCodeBlock * 16];  // [column][8 rows], chunk c of column k at c ^ (k / 8)
+  const int across = (int)((a.d + kCodeBlock - 1) / kCodeBlock);
+  const long long down = (a.n_rows + kCodeBlock - 1) / kCodeBlock;
   const long long tile = flat_group();
   if (tile >= across * down) return;
   const long long ti = tile / across;
   const int tj = (int)(tile - ti * across);
   const int cg = threadIdx.x & 15, rg = threadIdx.x >> 4;  // columns 8 cg .., rows 8 rg ..
-  const long long r0 = ti * kBlock + 8 * rg, k0 = (long long)tj * kBlock + 8 * cg;
+  const long long r0 = ti * kCodeBlock + 8 * rg, k0 = (long long)tj * kCodeBlock + 8 * cg;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   float x[8][8];
 #pragma unroll
@@ -165,13 +142,14 @@ __global__ __launch_bounds__(kQuantThreads) void quantize_tile_kernel(QuantArgs 
       if (rg == 0 && k0 + j < a.d) a.t_scale[(size_t)ti * a.d + k0 + j] = s_column[j];
     }
   }
-  const size_t width = (size_t)across * kBlock;
+  const size_t width = (size_t)across * kCodeBlock;
+  const Quotient one(s);
   if (a.Xq) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       if constexpr (!kTiles) s = e4m3_scale(largest16(largest8(x[i])));
       if (r0 + i >= a.n_rows) continue;
-      *reinterpret_cast<uint2*>(a.Xq + (size_t)(r0 + i) * width + k0) = codes8(x[i], s);
+      *reinterpret_cast<uint2*>(a.Xq + (size_t)(r0 + i) * width + k0) = codes8(x[i], kTiles ? one : Quotient(s));
       if (!kTiles && cg == 0) a.scale[(size_t)tj * a.n_rows + r0 + i] = s;
     }
   }
@@ -181,23 +159,23 @@ __global__ __launch_bounds__(kQuantThreads) void quantize_tile_kernel(QuantArgs 
     float v[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] = x[i][j];
-    turned[(8 * cg + j) * 16 + (rg ^ cg)] = codes8(v, kTiles ? s : s_column[j]);
+    turned[(8 * cg + j) * 16 + (rg ^ cg)] = codes8(v, kTiles ? one : Quotient(s_column[j]));
   }
   __syncthreads();
-  const size_t height = (size_t)down * kBlock;
+  const size_t height = (size_t)down * kCodeBlock;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int k = (threadIdx.x >> 3) + 32 * i, c = 2 * (threadIdx.x & 7), x8 = k >> 3;
-    const long long column = (long long)tj * kBlock + k;
+    const long long column = (long long)tj * kCodeBlock + k;
     const uint2 lo = turned[k * 16 + (c ^ x8)], hi = turned[k * 16 + ((c + 1) ^ x8)];
     if (column < a.d)
-      *reinterpret_cast<uint4*>(a.Xtq + (size_t)column * height + (size_t)ti * kBlock + 8 * c) = make_uint4(lo.x, lo.y, hi.x, hi.y);
+      *reinterpret_cast<uint4*>(a.Xtq + (size_t)column * height + (size_t)ti * kCodeBlock + 8 * c) = make_uint4(lo.x, lo.y, hi.x, hi.y);
   }
 }
 
 template <int kDtype, bool kWhole>
 void run_quantize(const QuantArgs& a, bool tiles, hipStream_t stream) {
-  const long long across = ceil_div(a.d, kBlock), down = ceil_div(a.n_rows, kBlock);
+  const long long across = ceil_div(a.d, kCodeBlock), down = ceil_div(a.n_rows, kCodeBlock);
   const dim3 block(kQuantThreads);
   if (tiles)
     hipLaunchKernelGGL((quantize_tile_kernel<kDtype, kWhole, true>), flat_grid(across * down), block, 0, stream, a);
