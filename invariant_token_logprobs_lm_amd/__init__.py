@@ -240,6 +240,10 @@ def _stream_handle(index):
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _stream_handle)
 
 
+# The current device's index, by the query below torch.cuda.current_device where there is one.
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+
+
 def _stream(device):
     return _raw_stream(device.index)
 
@@ -562,9 +566,7 @@ def lmhead_logprob_mxfp4(Hq, h_scale, Wq4, w_scale_codes, tokens, *, logprob=Non
 def _new(shape, dtype, like, name, given):
     """`given`, checked, or a new tensor of that shape and dtype on like's device."""
     if given is None:
-        if like.dtype == dtype and like.shape == shape:
-            return torch.empty_like(like)
-        return torch.empty(shape, dtype=dtype, device=like.device)
+        return like.new_empty(shape, dtype=dtype)
     _need(given, name, (dtype,), device=like.device, ndim=len(shape))
     if tuple(given.shape) != tuple(shape):
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(given.shape)}")
@@ -580,7 +582,7 @@ def _workspace(given, need, device):
 
 def _launch(device, call, *args):
     """call(*args, the current stream of `device`), with `device` the current one."""
-    if torch.cuda.current_device() == device.index:
+    if _current_device() == device.index:
         return _check(call(*args, _raw_stream(device.index)))
     with torch.cuda.device(device):
         return _check(call(*args, _raw_stream(device.index)))
@@ -773,11 +775,6 @@ def residual_norm_backward(du, dh, h, y, w_pre, rstd_pre, *, w_post=None, rstd_p
 _FP8_BLOCK = 128
 
 
-def _whole(n):
-    """n in whole blocks."""
-    return -(-n // _FP8_BLOCK) * _FP8_BLOCK
-
-
 def _quantize(call, X, tiles, rows, columns, Xq, scale, Xtq, t_scale):
     _need(X, "X", tuple(_HEAD_DTYPES), ndim=2)
     n, d = X.shape
@@ -787,15 +784,13 @@ def _quantize(call, X, tiles, rows, columns, Xq, scale, Xtq, t_scale):
         raise ValueError("at least one of rows and columns must be asked for")
     if not rows and (Xq is not None or scale is not None) or not columns and (Xtq is not None or t_scale is not None):
         raise ValueError("Xq and scale need rows, Xtq and t_scale columns")
-    across, down = _whole(d), _whole(n)
+    across, down = -(-d // _FP8_BLOCK), -(-n // _FP8_BLOCK)
     if rows:
-        Xq = _new((n, across), torch.uint8, X, "Xq", Xq)
-        scale = _new((down // _FP8_BLOCK, across // _FP8_BLOCK) if tiles else (across // _FP8_BLOCK, n), torch.float32, X,
-                     "scale", scale)
+        Xq = _new((n, across * _FP8_BLOCK), torch.uint8, X, "Xq", Xq)
+        scale = _new((down, across) if tiles else (across, n), torch.float32, X, "scale", scale)
     if columns:
-        Xtq = _new((d, down), torch.uint8, X, "Xtq", Xtq)
-        t_scale = _new((across // _FP8_BLOCK, down // _FP8_BLOCK) if tiles else (down // _FP8_BLOCK, d), torch.float32, X,
-                       "t_scale", t_scale)
+        Xtq = _new((d, down * _FP8_BLOCK), torch.uint8, X, "Xtq", Xtq)
+        t_scale = _new((across, down) if tiles else (down, d), torch.float32, X, "t_scale", t_scale)
     _launch(X.device, call, _ptr(X), _HEAD_DTYPES[X.dtype], n, d, _ptr(Xq), _ptr(scale), _ptr(Xtq), _ptr(t_scale))
     return Xq, scale, Xtq, t_scale
 
@@ -832,13 +827,15 @@ def matmul_fp8_blocks(Aq, a_scale, Bq, b_scale, *, out_dtype=torch.bfloat16, out
     _need(b_scale, "b_scale", (torch.float32,), device=dev, ndim=2)
     if out_dtype not in _HEAD_DTYPES:
         raise ValueError(f"out_dtype must be one of {tuple(_HEAD_DTYPES)}, got {out_dtype}")
-    (m, k), n = Aq.shape, Bq.shape[0]
-    if Bq.shape[1] != k:
+    m, k = Aq.shape
+    n, kb = Bq.shape
+    if kb != k:
         raise ValueError(f"shape mismatch: Aq {tuple(Aq.shape)}, Bq {tuple(Bq.shape)}")
-    for name, t, want in (("a_scale", a_scale, (_whole(k) // _FP8_BLOCK, m)),
-                          ("b_scale", b_scale, (_whole(n) // _FP8_BLOCK, _whole(k) // _FP8_BLOCK))):
-        if tuple(t.shape) != want:
-            raise ValueError(f"{name} must have shape {want}, got {tuple(t.shape)}")
+    blocks = -(-k // _FP8_BLOCK)
+    if a_scale.shape != (blocks, m):
+        raise ValueError(f"a_scale must have shape {(blocks, m)}, got {tuple(a_scale.shape)}")
+    if b_scale.shape != (-(-n // _FP8_BLOCK), blocks):
+        raise ValueError(f"b_scale must have shape {(-(-n // _FP8_BLOCK), blocks)}, got {tuple(b_scale.shape)}")
     out = _new((m, n), out_dtype, Aq, "out", out)
     _launch(dev, lib.itl_matmul_fp8_blocks, _ptr(Aq), _ptr(a_scale), _ptr(Bq), _ptr(b_scale), m, n, k,
             _HEAD_DTYPES[out_dtype], _ptr(out))

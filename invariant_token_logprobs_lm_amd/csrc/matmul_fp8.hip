@@ -496,12 +496,12 @@ void run_tiles(ProductArgs a, hipStream_t stream) {
   hipLaunchKernelGGL((product_tile_kernel<kOut, kBR, kAR, kWB, kWA, kSlots>), flat_grid(a.tiles), dim3(64 * kWB * kWA), 0, stream, a);
 }
 
-// Few rows of A (16 kAN at most): B is read once, straight into registers, and a
-// workgroup's eight wavefronts share the blocks of its 16 kBM columns of C, so that
-// many loads are under way wherever there are few columns. A block's unscaled sums
-// go to LDS, and each element's chain over the blocks is then walked in order by
-// one thread: the bits of the tiles' kernels. kHeld blocks of a wavefront are
-// loaded at a time, the next ones while the chain is walked.
+// Small products, however long the contraction: tiles of 16 kBM columns by 16 kAN
+// rows of C, whose blocks a workgroup's eight wavefronts share, straight from memory
+// into registers, so that many loads are under way with few tiles. A block's
+// unscaled sums go to LDS, and each element's chain over the blocks is then walked
+// in order by one thread: the bits of the other kernels. kHeld blocks of a wavefront
+// are loaded at a time, the next ones while the chain is walked.
 constexpr int kFewWaves = 8;
 
 template <int kOut, int kBM, int kAN>
@@ -516,8 +516,8 @@ __global__ __launch_bounds__(64 * kFewWaves) void product_few_kernel(ProductArgs
   const int quad = lane >> 4, c16 = lane & 15;
   const long long group = flat_group();
   if (group >= a.tiles) return;
-  const long long j0 = group * 16 * kBM;
-  const int blocks = a.k / kBlock, m = (int)a.m;
+  const long long i0 = group / a.tiles_n * 16 * kAN, j0 = group % a.tiles_n * 16 * kBM;
+  const int blocks = a.k / kBlock;
   const int at0 = lane_chunk(quad) * 16, at1 = (4 + lane_chunk(quad)) * 16;
   const float* b_scale = a.b_scale + j0 / kBlock * blocks;
 
@@ -536,9 +536,9 @@ __global__ __launch_bounds__(64 * kFewWaves) void product_few_kernel(ProductArgs
       }
 #pragma unroll
       for (int i = 0; i < kAN; ++i) {
-        const int row = 16 * i + c16;
-        const uint8_t* p = a.A + (long long)row * a.k + (long long)b * kBlock;
-        const bool in = b < blocks && row < m;
+        const long long row = i0 + 16 * i + c16;
+        const uint8_t* p = a.A + row * a.k + (long long)b * kBlock;
+        const bool in = b < blocks && row < a.m;
         va[h][i][0] = in ? *reinterpret_cast<const uint4*>(p + at0) : make_uint4(0u, 0u, 0u, 0u);
         va[h][i][1] = in ? *reinterpret_cast<const uint4*>(p + at1) : make_uint4(0u, 0u, 0u, 0u);
       }
@@ -552,8 +552,9 @@ __global__ __launch_bounds__(64 * kFewWaves) void product_few_kernel(ProductArgs
   load(0);
   for (int first = 0; first < blocks; first += kRound) {
     for (int i = threadIdx.x; i < kRound * 16 * kAN; i += 64 * kFewWaves) {
-      const int b = first + i / (16 * kAN), row = i % (16 * kAN);
-      (&scales[0][0])[i] = b < blocks && row < m ? a.a_scale[(long long)b * m + row] * b_scale[b] : 0.0f;
+      const int b = first + i / (16 * kAN);
+      const long long row = i0 + i % (16 * kAN);
+      (&scales[0][0])[i] = b < blocks && row < a.m ? a.a_scale[b * a.m + row] * b_scale[b] : 0.0f;
     }
 #pragma unroll
     for (int h = 0; h < kHeld; ++h) {
@@ -588,7 +589,7 @@ __global__ __launch_bounds__(64 * kFewWaves) void product_few_kernel(ProductArgs
 #pragma unroll
   for (int e = 0; e < kEach; ++e) {
     const int f = 64 * kFewWaves * e + threadIdx.x, which = f >> 8;
-    const long long row = 16 * (which % kAN) + ((f >> 2) & 15), col = j0 + 16 * (which / kAN) + 4 * ((f >> 6) & 3) + (f & 3);
+    const long long row = i0 + 16 * (which % kAN) + ((f >> 2) & 15), col = j0 + 16 * (which / kAN) + 4 * ((f >> 6) & 3) + (f & 3);
     if (f < kBM * kAN * 256 && row < a.m && col < a.n)
       static_cast<typename Elem<kOut>::T*>(a.C)[row * a.n + col] = Elem<kOut>::from_f(acc[e]);
   }
@@ -596,7 +597,8 @@ __global__ __launch_bounds__(64 * kFewWaves) void product_few_kernel(ProductArgs
 
 template <int kOut, int kBM, int kAN>
 void run_few(ProductArgs a, hipStream_t stream) {
-  a.tiles = ceil_div(a.n, 16 * kBM);
+  a.tiles_n = (int)ceil_div(a.n, 16 * kBM);
+  a.tiles = ceil_div(a.m, 16 * kAN) * a.tiles_n;
   hipLaunchKernelGGL((product_few_kernel<kOut, kBM, kAN>), flat_grid(a.tiles), dim3(64 * kFewWaves), 0, stream, a);
 }
 
@@ -604,30 +606,29 @@ void run_few(ProductArgs a, hipStream_t stream) {
 // (bf16 results; m x n x k).
 template <int kOut>
 void run_product(const ProductArgs& a, hipStream_t stream) {
-  // Few rows and so few columns that a CU has one workgroup of 16, 32 or 64 columns
-  // (more columns per workgroup read A less often): the blocks are shared by the
-  // wavefronts. 16 x 2560 x 7168 9.5, in 64 x 64 tiles 21.8; 16 x 10240 x 7168 19.0
-  // and 28.2; 16 x 20480 x 7168 35.5 and 29.6. 32 x 5120 x 7168 17.4 and 27.3;
-  // 32 x 10240 x 7168 29.5 and 28.9.
-  if (a.m <= 16 && a.n <= 16 * kCUs) return run_few<kOut, 1, 1>(a, stream);
-  if (a.m <= 16 && a.n <= 32 * kCUs) return run_few<kOut, 2, 1>(a, stream);
-  if (a.m <= 16 && a.n <= 64 * kCUs) return run_few<kOut, 4, 1>(a, stream);
-  if (a.m <= 32 && a.n <= 16 * kCUs) return run_few<kOut, 1, 2>(a, stream);
-  if (a.m <= 32 && a.n <= 32 * kCUs) return run_few<kOut, 2, 2>(a, stream);
+  // No more tiles of 16 to 64 columns by 16 or 32 rows than CUs (the smallest that are
+  // so few: larger ones read less): the wavefronts share the blocks. 16 x 2560 x 7168
+  // 9.5, in 64 x 64 tiles 21.8; 16 x 10240 x 7168 19.0 and 28.2; 16 x 20480 x 7168
+  // 35.5 and 29.6; 32 x 5120 x 7168 17.4 and 27.3; 32 x 10240 x 7168 29.5 and 28.9.
+  auto tiles = [&](int cols, int rows) { return ceil_div(a.n, cols) * ceil_div(a.m, rows); };
+  if (tiles(16, 16) <= kCUs) return run_few<kOut, 1, 1>(a, stream);
+  if (tiles(32, 16) <= kCUs) return run_few<kOut, 2, 1>(a, stream);
+  if (a.m <= 16 && tiles(64, 16) <= kCUs) return run_few<kOut, 4, 1>(a, stream);
+  if (a.m > 16 && tiles(32, 32) <= kCUs) return run_few<kOut, 2, 2>(a, stream);
   // Half the CUs or more with a 256 x 256 tile: 1024 x 10240 x 2560 (160 tiles) 35.7,
   // in 64 x 128 tiles 44.2; 4096 x 1536 x 2560 (96) 35.7 and 27.8.
   if constexpr (kOut == 0) {
-    if (a.m > 128 && a.k >= 3 * kBlock && ceil_div(a.m, kWide) * ceil_div(a.n, kWide) >= kCUs / 2) return run_wide(a, stream);
+    if (a.m > 128 && a.k >= 3 * kBlock && tiles(kWide, kWide) >= kCUs / 2) return run_wide(a, stream);
   }
   // Tiles of 64 x 64 while they run at once, four per CU: 1024 x 2560 x 2560 (640) 16.8,
   // in 64 x 128 tiles 17.9; 2048 x 2560 x 2560 (1280) 28.9 and 26.6.
-  if (ceil_div(a.m, 64) * ceil_div(a.n, 64) <= 4 * kCUs) return run_tiles<kOut, 64, 64, 2, 2, 2>(a, stream);
+  if (tiles(64, 64) <= 4 * kCUs) return run_tiles<kOut, 64, 64, 2, 2, 2>(a, stream);
   // Many columns for few rows are a matter of B's bytes: 64 x 61440 x 7168 85.5 in tiles
   // of 128 columns, 97.1 of 64; 128 x 61440 x 7168 102 (128 x 128 tiles), 137 (64 x 128).
   if (a.m <= 64) return run_tiles<kOut, 128, 64, 2, 2, 3>(a, stream);
   // fp32 results (no larger tiles): 2048 x 10240 x 7168 (1280 tiles) 286, in 64 x 128 tiles
   // 329; 1024 x 10240 x 7168 (640) 177 and 171.
-  if (a.m <= 128 || ceil_div(a.m, 128) * ceil_div(a.n, 128) >= 4 * kCUs) return run_tiles<kOut, 128, 128, 2, 2, 2>(a, stream);
+  if (a.m <= 128 || tiles(128, 128) >= 4 * kCUs) return run_tiles<kOut, 128, 128, 2, 2, 2>(a, stream);
   run_tiles<kOut, 64, 128, 2, 2, 2>(a, stream);
 }
 
