@@ -92,13 +92,12 @@ def test_nothing_beyond_the_rows_is_written(cuda, itl):
 
 
 def test_more_rows_than_a_part_of_the_grid_holds(cuda, itl):
-    """Rows of one value: 2^25 wavefronts and more, in several parts."""
-    n, k = (1 << 25) + 1000, 1 << 20
-    x = torch.ones(n, 1, dtype=torch.bfloat16, device=cuda)
-    got = itl.dropout(x, _drop(itl, cuda))
-    for a in (0, (1 << 25) - k // 2, n - k):
-        m = min(k, n - a)
-        assert torch.equal(got[a:a + m].cpu() == 0, _factors(m, 1, _drop(itl, cuda, first_row=a)) == 0), a
+    """Rows of two groups: 2^31 groups and more, in two parts (19 GB, in place)."""
+    n, d, k = (1 << 30) + 1000, 9, 1 << 16
+    x = torch.ones(n, d, dtype=torch.bfloat16, device=cuda)
+    itl.dropout(x, _drop(itl, cuda), y=x)
+    for a in (0, (1 << 30) - k // 2, n - k):
+        assert torch.equal(x[a:a + k].cpu() == 0, _factors(k, d, _drop(itl, cuda, first_row=a)) == 0), a
 
 
 def test_dropped_values_are_zero_whatever_they_are(cuda, itl):
