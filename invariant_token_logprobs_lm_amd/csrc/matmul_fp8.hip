@@ -94,6 +94,7 @@ struct ProductArgs {
   const float *a_scale, *b_scale;
   void* C;
   long long m, n;
+  long long scale_rows;  // of a_scale: m, or more where these are some of its rows
   int k, tiles_n;
   long long tiles;
   bool quads;  // C's rows are whole fours of columns, aligned as such
@@ -186,7 +187,7 @@ __global__ __launch_bounds__(64 * kWB * kWA) void product_tile_kernel(ProductArg
     for (int j = 0; j < kBDma; ++j) dma16(b_rsrc, b_off[j], at, slot + (uint32_t)(wave * kBDma + j) * 1024);
 #pragma unroll
     for (int j = 0; j < kADma; ++j) dma16(a_rsrc, a_off[j], at, slot + kBChunks * 16 + (uint32_t)(wave * kADma + j) * 1024);
-    dma4(rsrc_words(a.a_scale + (size_t)s * a.m + i0, rows * 4), (uint32_t)(sc * 64 + lane) * 4, 0,
+    dma4(rsrc_words(a.a_scale + (size_t)s * a.scale_rows + i0, rows * 4), (uint32_t)(sc * 64 + lane) * 4, 0,
          slot + (kBChunks + kAChunks) * 16 + (uint32_t)sc * 256);
   };
   constexpr int kLoads = kBDma + kADma + 1;
@@ -302,7 +303,7 @@ __global__ __launch_bounds__(kThreads8, 2) void product_wide_kernel(ProductArgs 
   const bool of_a = L.wave < 4;
   const uint32_t scale_off = of_a ? (uint32_t)(L.wave * 64 + lane) * 4u : lane < 2 ? (uint32_t)(lane * steps) * 4u : 0x80000000u;
   const uint32_t scale_lds = 2 * kWideRows * 16 + (of_a ? (uint32_t)L.wave * 256u : 1024u);
-  const uint64_t scale_step = of_a ? (uint64_t)a.m * 4 : 4;
+  const uint64_t scale_step = of_a ? (uint64_t)a.scale_rows * 4 : 4;
   // A tile's operands and scales. With no tile the ranges are empty: zeros are
   // written into slots that nothing reads.
   struct Source {
@@ -554,7 +555,7 @@ __global__ __launch_bounds__(64 * kFewWaves) void product_few_kernel(ProductArgs
     for (int i = threadIdx.x; i < kRound * 16 * kAN; i += 64 * kFewWaves) {
       const int b = first + i / (16 * kAN);
       const long long row = i0 + i % (16 * kAN);
-      (&scales[0][0])[i] = b < blocks && row < a.m ? a.a_scale[b * a.m + row] * b_scale[b] : 0.0f;
+      (&scales[0][0])[i] = b < blocks && row < a.m ? a.a_scale[b * a.scale_rows + row] * b_scale[b] : 0.0f;
     }
 #pragma unroll
     for (int h = 0; h < kHeld; ++h) {
@@ -602,23 +603,52 @@ void run_few(ProductArgs a, hipStream_t stream) {
   hipLaunchKernelGGL((product_few_kernel<kOut, kBM, kAN>), flat_grid(a.tiles), dim3(64 * kFewWaves), 0, stream, a);
 }
 
+// Rows first .. first + count of a product.
+ProductArgs rows_of(ProductArgs a, long long first, long long count, size_t elem) {
+  a.A += first * a.k;
+  a.a_scale += first;
+  a.C = static_cast<char*>(a.C) + (size_t)first * a.n * elem;
+  a.m = count;
+  return a;
+}
+
 // Which kernel: all give the same bits. us measured on both sides of each border
-// (bf16 results; m x n x k).
+// (bf16 results where not said otherwise; m x n x k).
 template <int kOut>
 void run_product(const ProductArgs& a, hipStream_t stream) {
+  auto tiles = [&](int cols, int rows) { return ceil_div(a.n, cols) * ceil_div(a.m, rows); };
   // No more tiles of 16 to 64 columns by 16 or 32 rows than CUs (the smallest that are
   // so few: larger ones read less): the wavefronts share the blocks. 16 x 2560 x 7168
   // 9.5, in 64 x 64 tiles 21.8; 16 x 10240 x 7168 19.0 and 28.2; 16 x 20480 x 7168
-  // 35.5 and 29.6; 32 x 5120 x 7168 17.4 and 27.3; 32 x 10240 x 7168 29.5 and 28.9.
-  auto tiles = [&](int cols, int rows) { return ceil_div(a.n, cols) * ceil_div(a.m, rows); };
+  // 35.5 and 29.6; 128 x 2048 x 16384 36.4 and 58.4; 256 x 2048 x 16384 64.2 and 58.9.
   if (tiles(16, 16) <= kCUs) return run_few<kOut, 1, 1>(a, stream);
   if (tiles(32, 16) <= kCUs) return run_few<kOut, 2, 1>(a, stream);
   if (a.m <= 16 && tiles(64, 16) <= kCUs) return run_few<kOut, 4, 1>(a, stream);
   if (a.m > 16 && tiles(32, 32) <= kCUs) return run_few<kOut, 2, 2>(a, stream);
+  // Rows whose tiles fill the CUs a whole number of times, and what is left: a few tiles
+  // more than whole rounds take as long as another round, or a third of it in smaller
+  // tiles of their own. 6000 x 3000 x 7168 (288 tiles of 256 x 256) 130, all in those 169.
+  struct Rounds {
+    long long rounds, rows, left;  // whole rounds, their rows, the tiles left
+  };
+  auto rounds_of = [&](int size, long long at_once) {
+    const long long across = ceil_div(a.n, size), all = tiles(size, size), rounds = all / at_once;
+    const long long down = rounds * at_once / across;
+    return Rounds{rounds, down * size, all - down * across};
+  };
+  auto split = [&](const Rounds& r, double most_left, auto&& run) {
+    if (r.rows == 0 || r.left == 0 || r.left > most_left) return run(a);
+    run(rows_of(a, 0, r.rows, Elem<kOut>::kSize));
+    run_product<kOut>(rows_of(a, r.rows, a.m - r.rows, Elem<kOut>::kSize), stream);
+  };
+  const double steps = (double)(a.k / kBlock);
   // Half the CUs or more with a 256 x 256 tile: 1024 x 10240 x 2560 (160 tiles) 35.7,
   // in 64 x 128 tiles 44.2; 4096 x 1536 x 2560 (96) 35.7 and 27.8.
+  // (Left over: a step of a round takes 1.6 us, one of `left` tiles as smaller ones 0.45 +
+  // 0.0125 left, and 4 us once.)
   if constexpr (kOut == 0) {
-    if (a.m > 128 && a.k >= 3 * kBlock && tiles(kWide, kWide) >= kCUs / 2) return run_wide(a, stream);
+    if (a.m > 128 && a.k >= 3 * kBlock && tiles(kWide, kWide) >= kCUs / 2)
+      return split(rounds_of(kWide, kCUs), (1.1 - 4.0 / steps) / 0.0125, [&](const ProductArgs& p) { run_wide(p, stream); });
   }
   // Tiles of 64 x 64 while they run at once, four per CU: 1024 x 2560 x 2560 (640) 16.8,
   // in 64 x 128 tiles 17.9; 2048 x 2560 x 2560 (1280) 28.9 and 26.6.
@@ -626,9 +656,22 @@ void run_product(const ProductArgs& a, hipStream_t stream) {
   // Many columns for few rows are a matter of B's bytes: 64 x 61440 x 7168 85.5 in tiles
   // of 128 columns, 97.1 of 64; 128 x 61440 x 7168 102 (128 x 128 tiles), 137 (64 x 128).
   if (a.m <= 64) return run_tiles<kOut, 128, 64, 2, 2, 3>(a, stream);
-  // fp32 results (no larger tiles): 2048 x 10240 x 7168 (1280 tiles) 286, in 64 x 128 tiles
-  // 329; 1024 x 10240 x 7168 (640) 177 and 171.
-  if (a.m <= 128 || tiles(128, 128) >= 4 * kCUs) return run_tiles<kOut, 128, 128, 2, 2, 2>(a, stream);
+  if (a.m <= 128) return run_tiles<kOut, 128, 128, 2, 2, 2>(a, stream);
+  // fp32 results: 128 x 128 tiles, two per CU, where there are 1024 (2048 x 10240 x 7168,
+  // 1280 tiles, 286, in 64 x 128 tiles 329; 1024 x 10240 x 7168, 640 tiles, 177 and 171),
+  // or 256 x 256 ones if their rounds end sooner. A step of a round takes 3.1 us with
+  // those, 1.76 with two of the others per CU, 1.05 with one and 0.5 + 0.0025 left where the
+  // tiles left over are smaller ones: 8960 x 1536 x 16384 398 and 465, 2048 x 10240 x 7168
+  // 366 and 277.
+  if constexpr (kOut == 1) {
+    const Rounds r = rounds_of(128, 2 * kCUs);
+    const double most_left = (0.5 - 4.0 / steps) / 0.0025;
+    const double rest = r.left == 0 ? 0.0 : r.left <= most_left ? 0.5 + 0.0025 * r.left : r.left <= kCUs ? 1.05 : 1.76;
+    if (tiles(kWide, kWide) >= kCUs / 2 && ceil_div(tiles(kWide, kWide), kCUs) * 3.1 < r.rounds * 1.76 + rest)
+      return run_tiles<kOut, 256, 256, 2, 4, 2>(a, stream);
+    if (tiles(128, 128) >= 4 * kCUs)
+      return split(r, most_left, [&](const ProductArgs& p) { run_tiles<kOut, 128, 128, 2, 2, 2>(p, stream); });
+  }
   run_tiles<kOut, 64, 128, 2, 2, 2>(a, stream);
 }
 
@@ -636,7 +679,7 @@ void run_product(const ProductArgs& a, hipStream_t stream) {
 
 hipError_t launch_matmul_fp8_blocks(const MatmulFp8& c, hipStream_t stream) {
   const uintptr_t four = c.out_dtype == 0 ? 7 : 15;
-  const ProductArgs a{c.A, c.B, c.a_scale, c.b_scale, c.C, c.m, c.n, (int)c.k, 0, 0,
+  const ProductArgs a{c.A, c.B, c.a_scale, c.b_scale, c.C, c.m, c.n, c.m, (int)c.k, 0, 0,
                       c.n % 4 == 0 && (reinterpret_cast<uintptr_t>(c.C) & four) == 0,
                       c.n % (c.out_dtype == 0 ? 8 : 4) == 0 && (reinterpret_cast<uintptr_t>(c.C) & 15) == 0};
   if (c.out_dtype == 0) run_product<0>(a, stream);
