@@ -659,16 +659,20 @@ void run_product(const ProductArgs& a, hipStream_t stream) {
   if (a.m <= 128) return run_tiles<kOut, 128, 128, 2, 2, 2>(a, stream);
   // fp32 results: 128 x 128 tiles, two per CU, where there are 1024 (2048 x 10240 x 7168,
   // 1280 tiles, 286, in 64 x 128 tiles 329; 1024 x 10240 x 7168, 640 tiles, 177 and 171),
-  // or 256 x 256 ones if their rounds end sooner. A step of a round takes 3.1 us with
-  // those, 1.76 with two of the others per CU, 1.05 with one and 0.5 + 0.0025 left where the
-  // tiles left over are smaller ones: 8960 x 1536 x 16384 398 and 465, 2048 x 10240 x 7168
-  // 366 and 277.
+  // or 256 x 256 ones, their whole rounds at least, if those end sooner. A step of a round
+  // takes 3.2 us with 256 x 256, 2.0 with two of 128 x 128 per CU, 1.2 with one and 0.5 +
+  // 0.0025 left where the 128 x 128 tiles left over become smaller ones; another launch 4.
+  // 8960 x 1536 x 16384 (210 tiles of 256 x 256) 407, in 128 x 128 tiles 505; 4096 x 4200 x
+  // 4096 (256 and 16) 158, all in one size 225 or 175; 2560 x 10240 x 16384 (256 and 144)
+  // 804, 815 or 890; 2048 x 10240 x 7168 (256 and 64) 382, in 128 x 128 tiles 296.
   if constexpr (kOut == 1) {
-    const Rounds r = rounds_of(128, 2 * kCUs);
     const double most_left = (0.5 - 4.0 / steps) / 0.0025;
-    const double rest = r.left == 0 ? 0.0 : r.left <= most_left ? 0.5 + 0.0025 * r.left : r.left <= kCUs ? 1.05 : 1.76;
-    if (tiles(kWide, kWide) >= kCUs / 2 && ceil_div(tiles(kWide, kWide), kCUs) * 3.1 < r.rounds * 1.76 + rest)
-      return run_tiles<kOut, 256, 256, 2, 4, 2>(a, stream);
+    auto left_over = [&](long long n) { return n == 0 ? 0.0 : n <= most_left ? 0.5 + 0.0025 * n : n <= kCUs ? 1.2 : 2.0; };
+    const Rounds r = rounds_of(128, 2 * kCUs), w = rounds_of(kWide, kCUs);
+    const double small = r.rounds * 2.0 + left_over(r.left);
+    const double rest = 4 * w.left / (2 * kCUs) * 2.0 + left_over(4 * w.left % (2 * kCUs)) + 4.0 / steps;  // of w.left
+    if (tiles(kWide, kWide) >= kCUs / 2 && w.rounds * 3.2 + (w.left == 0 ? 0.0 : std::min(3.2, rest)) < small)
+      return split(w, rest < 3.2 ? w.left : 0, [&](const ProductArgs& p) { run_tiles<kOut, 256, 256, 2, 4, 2>(p, stream); });
     if (tiles(128, 128) >= 4 * kCUs)
       return split(r, most_left, [&](const ProductArgs& p) { run_tiles<kOut, 128, 128, 2, 2, 2>(p, stream); });
   }
