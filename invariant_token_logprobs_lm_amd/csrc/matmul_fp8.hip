@@ -139,8 +139,18 @@ __device__ __forceinline__ void store8(const ProductArgs& a, uint16_t* to, uint4
     if (col + e < a.n) to[e] = (uint16_t)(w[e >> 1] >> (16 * (e & 1)));
 }
 
-// kBR columns of C (rows of B) by kAR rows, a grid of kWB x kWA wavefronts, both
-// operands through kSlots LDS slots loaded kSlots - 1 steps ahead.
+// Medium products, and all larger ones with fp32 results: kBR columns of C (rows of B) by
+// kAR rows, a grid of kWB x kWA wavefronts, both operands through kSlots LDS slots loaded
+// kSlots - 1 steps ahead.
+//
+// Few rows are bound by B's bytes: 16 x 129280 x 7168, fp32, 166 us (5.6 TB/s). Few
+// steps are bound by latency: 777 x 1001 x 1536 9.5 us, 12 steps of 0.4 and the launch.
+// Large fp32 results: 2560 x 10240 x 16384 770 to 820 us (1.05 to 1.1 PFLOP/s; the
+// library's bf16 product reaches 1.31 at 8192 x 8192 x 8192). In 256 x 256 tiles the matrix
+// cores are busy 49 % of the cycles, at 2.24 GHz, and a step issues 5 cycles of vector
+// instructions per 4 of theirs, 3 of them conversions (two codes in 8 cycles). Widening each
+// code once per workgroup and passing it on through LDS as bf16 (twice the LDS bytes, a
+// second barrier a step) took 1071 us, where this took 857.
 template <int kOut, int kBR, int kAR, int kWB, int kWA, int kSlots>
 __global__ __launch_bounds__(64 * kWB * kWA) void product_tile_kernel(ProductArgs a) {
   constexpr int kWaves = kWB * kWA;
@@ -248,7 +258,7 @@ __global__ __launch_bounds__(64 * kWB * kWA) void product_tile_kernel(ProductArg
       store4<kOut>(a, i0 + wa * (kAR / kWA) + an * 16 + c16, j0 + wb * (kBR / kWB) + bm * 16 + 4 * quad, acc[bm][an]);
 }
 
-// 256 x 256 tiles for large products: eight wavefronts, each 128 columns of C by
+// 256 x 256 tiles for large products (bf16 results): eight wavefronts, each 128 columns of C by
 // 64 rows, one workgroup per CU that walks its tiles without letting the loads
 // run dry between them.
 //
@@ -262,6 +272,11 @@ __global__ __launch_bounds__(64 * kWB * kWA) void product_tile_kernel(ProductArg
 // whose loads for the step after next are spread over the second half. An
 // instruction's sums are scaled into the accumulators three instructions later,
 // when they are there.
+//
+// 16384 x 10240 x 2560 takes 390 to 410 us (2.1 to 2.2 PFLOP/s; the library's product of
+// E4M3 matrices with one scale each reaches 2.77 at 8192 x 8192 x 8192). In calls right
+// after idling (450 us) the matrix cores are busy 53 % of the cycles, vector instructions
+// issue in 47 %, and the clock is 1.73 GHz: power, not a stall, sets the pace there.
 constexpr int kWide = 256;
 constexpr int kWideRows = kWide * kRowChunks;          // chunks of an operand's rows of a step
 constexpr int kWideSlot = 2 * kWideRows + 64 + 16;     // and A's 256 scales, B's two (of 64 lanes)
@@ -662,17 +677,21 @@ void run_product(const ProductArgs& a, hipStream_t stream) {
   // or 256 x 256 ones, their whole rounds at least, if those end sooner. A step of a round
   // takes 3.2 us with 256 x 256, 2.0 with two of 128 x 128 per CU, 1.2 with one and 0.5 +
   // 0.0025 left where the 128 x 128 tiles left over become smaller ones; another launch 4.
-  // 8960 x 1536 x 16384 (210 tiles of 256 x 256) 407, in 128 x 128 tiles 505; 4096 x 4200 x
-  // 4096 (256 and 16) 158, all in one size 225 or 175; 2560 x 10240 x 16384 (256 and 144)
-  // 804, 815 or 890; 2048 x 10240 x 7168 (256 and 64) 382, in 128 x 128 tiles 296.
+  // 8960 x 1536 x 16384 (210 tiles of 256 x 256) 401, in 128 x 128 tiles 471; 4096 x 4200 x
+  // 4096 (256 and 33) 147, all in one size 216 or 167; 2560 x 10240 x 16384 (240 and 160)
+  // 770, 791 or 807; 2048 x 10240 x 7168 (320) 369, in 128 x 128 tiles 286.
   if constexpr (kOut == 1) {
     const double most_left = (0.5 - 4.0 / steps) / 0.0025;
-    auto left_over = [&](long long n) { return n == 0 ? 0.0 : n <= most_left ? 0.5 + 0.0025 * n : n <= kCUs ? 1.2 : 2.0; };
+    auto in128 = [&](long long n, bool smaller) {  // n tiles of 128 x 128, those left over smaller or not
+      const long long over = n % (2 * kCUs);
+      return n / (2 * kCUs) * 2.0 + (over == 0 ? 0.0 : smaller && over <= most_left ? 0.5 + 0.0025 * over : over <= kCUs ? 1.2 : 2.0);
+    };
     const Rounds r = rounds_of(128, 2 * kCUs), w = rounds_of(kWide, kCUs);
-    const double small = r.rounds * 2.0 + left_over(r.left);
-    const double rest = 4 * w.left / (2 * kCUs) * 2.0 + left_over(4 * w.left % (2 * kCUs)) + 4.0 / steps;  // of w.left
-    if (tiles(kWide, kWide) >= kCUs / 2 && w.rounds * 3.2 + (w.left == 0 ? 0.0 : std::min(3.2, rest)) < small)
-      return split(w, rest < 3.2 ? w.left : 0, [&](const ProductArgs& p) { run_tiles<kOut, 256, 256, 2, 4, 2>(p, stream); });
+    const double all128 = std::min(in128(tiles(128, 128), false), r.rounds * 2.0 + in128(r.left, r.rows > 0));
+    const double all256 = ceil_div(tiles(kWide, kWide), kCUs) * 3.2;
+    const double parts = w.rows > 0 ? w.rounds * 3.2 + in128(4 * w.left, true) + 4.0 / steps : all256;
+    if (tiles(kWide, kWide) >= kCUs / 2 && std::min(all256, parts) < all128)
+      return split(w, parts < all256 ? w.left : 0, [&](const ProductArgs& p) { run_tiles<kOut, 256, 256, 2, 4, 2>(p, stream); });
     if (tiles(128, 128) >= 4 * kCUs)
       return split(r, most_left, [&](const ProductArgs& p) { run_tiles<kOut, 128, 128, 2, 2, 2>(p, stream); });
   }

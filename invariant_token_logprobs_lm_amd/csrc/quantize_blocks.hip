@@ -14,7 +14,9 @@
 // written: a workgroup holds a 128 x 128 tile in registers (thread: 8 rows by 8
 // columns), takes the rows' maxima over 16 lanes and the columns' through LDS,
 // and turns the codes through 16 KB of LDS so that both are written in whole
-// lines.
+// lines. 16384 x 2560 bf16 rows alone 31 us (4.0 TB/s), both ways
+// 41 (4.1 TB/s; 68 % of the cycles issue vector instructions); 8960 x 1536 fp32 by
+// tiles, both ways, 16 (5.2 TB/s). One decode token 3, launch and latency.
 
 #include <algorithm>
 
