@@ -42,7 +42,9 @@
  *  - each resp_loss[i] is a bitwise function of response i's own
  *    (logprob, rollout_logprob, advantage, T_i) only;
  *  - loss, coef, advantages, dH and dW are run-to-run deterministic (no
- *    atomics, no split-K, fixed reduction orders).
+ *    atomics, no split-K, fixed reduction orders);
+ *  - a row of a norm, of dropout, of codes by blocks and of a block-scaled product
+ *    is the same whatever the other rows (with dropout: at the same row number).
  *
  * Conventions shared by every entry point.
  *  - All array pointers are DEVICE memory owned by the caller. The library
@@ -453,9 +455,12 @@ itl_status itl_quantize_tiles_fp8(const void* X, itl_dtype dtype, int64_t n_rows
  * C [m, n] of out_dtype, rounded once. A linear layer Y = X W^T takes it three times:
  *   Y = matmul(blocks(X), tiles(W)),  dX = matmul(blocks(dY), transposed tiles(W)),
  *   dW = matmul(transposed blocks(dY), transposed tiles(X)).
- * Each block's product and the sum over blocks are fp32, blocks in ascending
- * order: C's row i depends on row i of Aq and a_scale, Bq and b_scale alone, whatever
- * m [BC]. k a multiple of 128 (ITL_ERR_UNSUPPORTED otherwise), up to 2^23; 0: C is
+ * The sum over blocks is fp32, blocks in ascending order, as is a block's sum with
+ * fp32 results, of exact products. With bf16 results the products of eight consecutive
+ * columns are added with 13 bits below the largest of them (the matrix cores' own sum for
+ * E4M3), the sixteen sums of a block in fp32: off by 7 2^-13 of the products' absolute sum
+ * at worst, measured 1e-6 to 4e-5, before C's rounding of 2^-9. C's row i depends on row i of Aq and a_scale, Bq and
+ * b_scale alone, whatever m, and any call of it has the same bits [BC]. k a multiple of 128 (ITL_ERR_UNSUPPORTED otherwise), up to 2^23; 0: C is
  * zeros. Aq, Bq 16-byte aligned, C by element; C that shares memory with an operand
  * is refused. */
 itl_status itl_matmul_fp8_blocks(const uint8_t* Aq, const float* a_scale,
