@@ -101,16 +101,19 @@ struct ProductArgs {
   bool lines;  // C's rows are whole 16-byte pieces, aligned as such
 };
 
-// Four consecutive columns of a row of C, aligned as such.
-template <int kOut>
+// Four consecutive columns of a row of C, aligned as such or not (1321 x 72281 x 128, fp32
+// 116 us by 16-byte stores at any element, 218 element by element).
+template <int kOut, bool kAligned = true>
 __device__ __forceinline__ void put4(typename Elem<kOut>::T* out, const floatx4& v) {
   using E = Elem<kOut>;
-  if constexpr (kOut == 0) {
-    *reinterpret_cast<uint2*>(out) = make_uint2((uint32_t)E::from_f(v[0]) | ((uint32_t)E::from_f(v[1]) << 16),
-                                                (uint32_t)E::from_f(v[2]) | ((uint32_t)E::from_f(v[3]) << 16));
-  } else {
-    *reinterpret_cast<float4*>(out) = make_float4(v[0], v[1], v[2], v[3]);
-  }
+  std::conditional_t<kOut == 0, uint2, floatx4> w;
+  if constexpr (kOut == 0)
+    w = make_uint2((uint32_t)E::from_f(v[0]) | ((uint32_t)E::from_f(v[1]) << 16),
+                   (uint32_t)E::from_f(v[2]) | ((uint32_t)E::from_f(v[3]) << 16));
+  else
+    w = v;
+  if constexpr (kAligned) *reinterpret_cast<decltype(w)*>(out) = w;
+  else __builtin_memcpy(out, &w, sizeof w);
 }
 
 // The same within C, of any alignment.
@@ -121,8 +124,9 @@ __device__ __forceinline__ void store4(const ProductArgs& a, long long row, long
   if (row >= a.m || col >= a.n) return;
   T* out = static_cast<T*>(a.C) + row * a.n + col;
   if (a.quads) return put4<kOut>(out, v);
+  if (col + 4 <= a.n) return put4<kOut, false>(out, v);
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
+  for (int i = 0; i < 3; ++i)
     if (col + i < a.n) out[i] = E::from_f(v[i]);
 }
 
@@ -133,25 +137,29 @@ __device__ __forceinline__ void store8(const ProductArgs& a, uint16_t* to, uint4
     *reinterpret_cast<uint4*>(to) = v;
     return;
   }
+  if (col + 8 <= a.n) {
+    __builtin_memcpy(to, &v, sizeof v);
+    return;
+  }
   uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-  for (int e = 0; e < 8; ++e)
+  for (int e = 0; e < 7; ++e)
     if (col + e < a.n) to[e] = (uint16_t)(w[e >> 1] >> (16 * (e & 1)));
 }
 
 // Medium products, and all larger ones with fp32 results: kBR columns of C (rows of B) by
 // kAR rows, a grid of kWB x kWA wavefronts, both operands through kSlots LDS slots loaded
-// kSlots - 1 steps ahead.
+// kSlots - kPer steps ahead, kPer steps per barrier.
 //
 // Few rows are bound by B's bytes: 16 x 129280 x 7168, fp32, 166 us (5.6 TB/s). Few
-// steps are bound by latency: 777 x 1001 x 1536 9.5 us, 12 steps of 0.4 and the launch.
+// steps are bound by latency: 777 x 1001 x 1536 7.5 us, 12 steps of 0.3 and the launch.
 // Large fp32 results: 2560 x 10240 x 16384 770 to 820 us (1.05 to 1.1 PFLOP/s; the
 // library's bf16 product reaches 1.31 at 8192 x 8192 x 8192). In 256 x 256 tiles the matrix
 // cores are busy 49 % of the cycles, at 2.24 GHz, and a step issues 5 cycles of vector
 // instructions per 4 of theirs, 3 of them conversions (two codes in 8 cycles). Widening each
 // code once per workgroup and passing it on through LDS as bf16 (twice the LDS bytes, a
 // second barrier a step) took 1071 us, where this took 857.
-template <int kOut, int kBR, int kAR, int kWB, int kWA, int kSlots>
+template <int kOut, int kBR, int kAR, int kWB, int kWA, int kSlots, int kPer = 1>
 __global__ __launch_bounds__(64 * kWB * kWA) void product_tile_kernel(ProductArgs a) {
   constexpr int kWaves = kWB * kWA;
   constexpr int kBM = kBR / kWB / 16, kAN = kAR / kWA / 16;  // 16-row blocks per wavefront
@@ -217,14 +225,7 @@ __global__ __launch_bounds__(64 * kWB * kWA) void product_tile_kernel(ProductArg
 #pragma unroll
     for (int an = 0; an < kAN; ++an) acc[bm][an] = floatx4{};
 
-#pragma unroll
-  for (int p = 0; p < kSlots - 1; ++p)
-    if (p < steps) load(p);
-  for (int s = 0; s < steps; ++s) {
-    // (past the end nothing is loaded, and fewer loads are in flight)
-    if (s + kSlots - 2 < steps) wait_and_barrier<(kSlots - 2) * kLoads>();
-    else wait_and_barrier<0>();
-    if (s + kSlots - 1 < steps) load(s + kSlots - 1);
+  auto multiply = [&](int s) {
     if (s > 0 && (s & 63) == 0) {
       sb64 = s + lane < steps ? b_scale[s + lane] : 0.0f;
       asm volatile("" ::"v"(sb64));
@@ -250,6 +251,26 @@ __global__ __launch_bounds__(64 * kWB * kWA) void product_tile_kernel(ProductArg
 #pragma unroll
         for (int i = 0; i < 4; ++i) acc[bm][an][i] = __builtin_fmaf(p[an][i], sc_ab[an], acc[bm][an][i]);
     }
+  };
+  // kPer steps per barrier, loaded kSlots - kPer steps ahead.
+  constexpr int kAhead = kSlots - kPer;
+#pragma unroll
+  for (int p = 0; p < kAhead; ++p)
+    if (p < steps) load(p);
+  int s = 0;
+  for (; s + kPer <= steps; s += kPer) {
+    // (past the end nothing is loaded, and fewer loads are in flight)
+    if (s + kAhead <= steps) wait_and_barrier<(kAhead - kPer) * kLoads>();
+    else wait_and_barrier<0>();
+#pragma unroll
+    for (int p = 0; p < kPer; ++p)
+      if (s + kAhead + p < steps) load(s + kAhead + p);
+#pragma unroll
+    for (int p = 0; p < kPer; ++p) multiply(s + p);
+  }
+  if constexpr (kPer > 1) {
+    wait_and_barrier<0>();
+    for (; s < steps; ++s) multiply(s);
   }
 #pragma unroll
   for (int an = 0; an < kAN; ++an)
@@ -505,11 +526,11 @@ void run_wide(ProductArgs a, hipStream_t stream) {
   hipLaunchKernelGGL((product_wide_kernel), dim3((unsigned)std::min<long long>(ceil_div(a.tiles, 8) * 8, kCUs)), dim3(kThreads8), 0, stream, a);
 }
 
-template <int kOut, int kBR, int kAR, int kWB, int kWA, int kSlots>
+template <int kOut, int kBR, int kAR, int kWB, int kWA, int kSlots, int kPer = 1>
 void run_tiles(ProductArgs a, hipStream_t stream) {
   a.tiles_n = (int)ceil_div(a.n, kBR);
   a.tiles = ceil_div(a.m, kAR) * a.tiles_n;
-  hipLaunchKernelGGL((product_tile_kernel<kOut, kBR, kAR, kWB, kWA, kSlots>), flat_grid(a.tiles), dim3(64 * kWB * kWA), 0, stream, a);
+  hipLaunchKernelGGL((product_tile_kernel<kOut, kBR, kAR, kWB, kWA, kSlots, kPer>), flat_grid(a.tiles), dim3(64 * kWB * kWA), 0, stream, a);
 }
 
 // Small products, however long the contraction: tiles of 16 kBM columns by 16 kAN
@@ -665,9 +686,12 @@ void run_product(const ProductArgs& a, hipStream_t stream) {
     if (a.m > 128 && a.k >= 3 * kBlock && tiles(kWide, kWide) >= kCUs / 2)
       return split(rounds_of(kWide, kCUs), (1.1 - 4.0 / steps) / 0.0125, [&](const ProductArgs& p) { run_wide(p, stream); });
   }
-  // Tiles of 64 x 64 while they run at once, four per CU: 1024 x 2560 x 2560 (640) 16.8,
-  // in 64 x 128 tiles 17.9; 2048 x 2560 x 2560 (1280) 28.9 and 26.6.
-  if (tiles(64, 64) <= 4 * kCUs) return run_tiles<kOut, 64, 64, 2, 2, 2>(a, stream);
+  // Tiles of 64 x 64, two steps per barrier while they run at once, two per CU: 512 x 2048 x
+  // 7168 (256) 21.7, with one step 28.8; 196 x 1996 x 9472 (128) 27.1 and 34.9; 1024 x 2560 x
+  // 2560 (640) 18.8 and 16.1, in 64 x 128 tiles 17.3; 1280 x 2560 x 7936 (800) 50.6, in 64 x
+  // 128 tiles 43.1; 1024 x 4000 x 4096 (1008) 38.8 and 27.5.
+  if (tiles(64, 64) <= 2 * kCUs) return run_tiles<kOut, 64, 64, 2, 2, 4, 2>(a, stream);
+  if (tiles(64, 64) <= 3 * kCUs) return run_tiles<kOut, 64, 64, 2, 2, 2>(a, stream);
   // Many columns for few rows are a matter of B's bytes: 64 x 61440 x 7168 85.5 in tiles
   // of 128 columns, 97.1 of 64; 128 x 61440 x 7168 102 (128 x 128 tiles), 137 (64 x 128).
   if (a.m <= 64) return run_tiles<kOut, 128, 64, 2, 2, 3>(a, stream);

@@ -28,7 +28,7 @@ SIZES = [(1, 1, 128), (1, 16, 256), (1, 1536, 1536), (2, 100, 384), (5, 127, 128
          (128, 256, 512), (129, 257, 384), (200, 1001, 1536), (256, 256, 128), (257, 513, 256), (300, 200, 8448),
          (777, 1001, 1536), (1024, 1536, 640), (8, 40, 16640), (3, 5000, 256), (16, 9000, 384), (30, 8000, 128),
          (33, 70000, 128), (90, 70000, 256), (4000, 1100, 128), (2100, 4100, 384), (4353, 4097, 640), (16900, 600, 512), (2900, 6100, 2560),
-         (5400, 2600, 2560), (4200, 4100, 2560)]
+         (5400, 2600, 2560), (4200, 4100, 2560), (300, 3001, 8576), (700, 999, 384)]
 
 
 @pytest.fixture(scope="module")
