@@ -655,8 +655,8 @@ void run_product(const ProductArgs& a, hipStream_t stream) {
   auto tiles = [&](int cols, int rows) { return ceil_div(a.n, cols) * ceil_div(a.m, rows); };
   // No more tiles of 16 to 64 columns by 16 or 32 rows than CUs (the smallest that are
   // so few: larger ones read less): the wavefronts share the blocks. 16 x 2560 x 7168
-  // 9.5, in 64 x 64 tiles 21.8; 16 x 10240 x 7168 19.0 and 28.2; 16 x 20480 x 7168
-  // 35.5 and 29.6; 128 x 2048 x 16384 36.4 and 58.4; 256 x 2048 x 16384 64.2 and 58.9.
+  // 9.5, in 64 x 64 tiles 20.1; 16 x 10240 x 7168 19.2 and 20.7; 16 x 20480 x 7168
+  // 35.6 and 26.6; 128 x 2048 x 16384 35.2 and 44.3; 256 x 2048 x 16384 63.0 and 44.9.
   if (tiles(16, 16) <= kCUs) return run_few<kOut, 1, 1>(a, stream);
   if (tiles(32, 16) <= kCUs) return run_few<kOut, 2, 1>(a, stream);
   if (a.m <= 16 && tiles(64, 16) <= kCUs) return run_few<kOut, 4, 1>(a, stream);
@@ -678,12 +678,12 @@ void run_product(const ProductArgs& a, hipStream_t stream) {
     run_product<kOut>(rows_of(a, r.rows, a.m - r.rows, Elem<kOut>::kSize), stream);
   };
   const double steps = (double)(a.k / kBlock);
-  // Half the CUs or more with a 256 x 256 tile: 1024 x 10240 x 2560 (160 tiles) 35.7,
-  // in 64 x 128 tiles 44.2; 4096 x 1536 x 2560 (96) 35.7 and 27.8.
+  // More than half the CUs with a 256 x 256 tile: 2048 x 5120 x 4096 (160 tiles) 49, in
+  // 128 x 128 tiles 58; 2048 x 4096 x 4096 (128) 54 and 42.
   // (Left over: a step of a round takes 1.6 us, one of `left` tiles as smaller ones 0.45 +
   // 0.0125 left, and 4 us once.)
   if constexpr (kOut == 0) {
-    if (a.m > 128 && a.k >= 3 * kBlock && tiles(kWide, kWide) >= kCUs / 2)
+    if (a.m > 128 && a.k >= 3 * kBlock && tiles(kWide, kWide) > kCUs / 2)
       return split(rounds_of(kWide, kCUs), (1.1 - 4.0 / steps) / 0.0125, [&](const ProductArgs& p) { run_wide(p, stream); });
   }
   // Tiles of 64 x 64, two steps per barrier while they run at once, two per CU: 512 x 2048 x
@@ -693,16 +693,21 @@ void run_product(const ProductArgs& a, hipStream_t stream) {
   if (tiles(64, 64) <= 2 * kCUs) return run_tiles<kOut, 64, 64, 2, 2, 4, 2>(a, stream);
   if (tiles(64, 64) <= 3 * kCUs) return run_tiles<kOut, 64, 64, 2, 2, 2>(a, stream);
   // Many columns for few rows are a matter of B's bytes: 64 x 61440 x 7168 85.5 in tiles
-  // of 128 columns, 97.1 of 64; 128 x 61440 x 7168 102 (128 x 128 tiles), 137 (64 x 128).
+  // of 128 columns, 97.1 of 64.
   if (a.m <= 64) return run_tiles<kOut, 128, 64, 2, 2, 3>(a, stream);
-  if (a.m <= 128) return run_tiles<kOut, 128, 128, 2, 2, 2>(a, stream);
-  // fp32 results: 128 x 128 tiles, two per CU, where there are 1024 (2048 x 10240 x 7168,
-  // 1280 tiles, 286, in 64 x 128 tiles 329; 1024 x 10240 x 7168, 640 tiles, 177 and 171),
-  // or 256 x 256 ones, their whole rounds at least, if those end sooner. A step of a round
-  // takes 3.2 us with 256 x 256, 2.0 with two of 128 x 128 per CU, 1.2 with one and 0.5 +
-  // 0.0025 left where the 128 x 128 tiles left over become smaller ones; another launch 4.
-  // 8960 x 1536 x 16384 (210 tiles of 256 x 256) 401, in 128 x 128 tiles 471; 4096 x 4200 x
-  // 4096 (256 and 33) 147, all in one size 216 or 167; 2560 x 10240 x 16384 (240 and 160)
+  // bf16 results: 128 x 128 tiles (of eight wavefronts, two workgroups per CU; of four
+  // 2 to 15 % slower) where there are more than CUs: 1024 x 5000 x 4096 (320) 33.8, in 64 x
+  // 128 tiles 38.1; 128 x 61440 x 7168 (480) 103 and 137; 1500 x 2600 x 4096 (252) 27.8 and 26.3.
+  if constexpr (kOut == 0) {
+    if (tiles(128, 128) > kCUs) return run_tiles<kOut, 128, 128, 2, 4, 2>(a, stream);
+  }
+  // fp32 results: 128 x 128, 64 x 128 or 256 x 256 tiles, of the last the whole rounds at
+  // least, whichever end sooner. A step of a round takes 3.2 us with 256 x 256, 2.0 with two
+  // of 128 x 128 per CU, 1.2 with one, 0.62 a 64 x 128 tile per CU, and 0.5 + 0.0025 left
+  // where 128 x 128 tiles left over become smaller ones; another launch 4.
+  // 2048 x 4096 x 4096 in 128 x 128 (512 tiles) 67, in 64 x 128 79; 900 x 5000 x 2560 (320) 39.7
+  // and 36.4; 8960 x 1536 x 16384 (210 tiles of 256 x 256) 401, in 128 x 128 tiles 471; 4096 x
+  // 4200 x 4096 (256 and 33) 147, all in one size 216 or 167; 2560 x 10240 x 16384 (240 and 160)
   // 770, 791 or 807; 2048 x 10240 x 7168 (320) 369, in 128 x 128 tiles 286.
   if constexpr (kOut == 1) {
     const double most_left = (0.5 - 4.0 / steps) / 0.0025;
@@ -712,12 +717,13 @@ void run_product(const ProductArgs& a, hipStream_t stream) {
     };
     const Rounds r = rounds_of(128, 2 * kCUs), w = rounds_of(kWide, kCUs);
     const double all128 = std::min(in128(tiles(128, 128), false), r.rounds * 2.0 + in128(r.left, r.rows > 0));
+    const double all64 = ceil_div(tiles(64, 128), kCUs) * 0.62;
     const double all256 = ceil_div(tiles(kWide, kWide), kCUs) * 3.2;
     const double parts = w.rows > 0 ? w.rounds * 3.2 + in128(4 * w.left, true) + 4.0 / steps : all256;
-    if (tiles(kWide, kWide) >= kCUs / 2 && std::min(all256, parts) < all128)
+    if (std::min(all256, parts) < std::min(all128, all64))
       return split(w, parts < all256 ? w.left : 0, [&](const ProductArgs& p) { run_tiles<kOut, 256, 256, 2, 4, 2>(p, stream); });
-    if (tiles(128, 128) >= 4 * kCUs)
-      return split(r, most_left, [&](const ProductArgs& p) { run_tiles<kOut, 128, 128, 2, 2, 2>(p, stream); });
+    if (all128 < all64)
+      return split(r, most_left, [&](const ProductArgs& p) { run_tiles<kOut, 128, 128, 2, 4, 2>(p, stream); });
   }
   run_tiles<kOut, 64, 128, 2, 2, 2>(a, stream);
 }
