@@ -153,12 +153,12 @@ __device__ __forceinline__ void store8(const ProductArgs& a, uint16_t* to, uint4
 //
 // Few rows are bound by B's bytes: 16 x 129280 x 7168, fp32, 166 us (5.6 TB/s). Few
 // steps are bound by latency: 777 x 1001 x 1536 7.5 us, 12 steps of 0.3 and the launch.
-// Large fp32 results: 2560 x 10240 x 16384 770 to 820 us (1.05 to 1.1 PFLOP/s; the
-// library's bf16 product reaches 1.31 at 8192 x 8192 x 8192). In 256 x 256 tiles the matrix
-// cores are busy 49 % of the cycles, at 2.24 GHz, and a step issues 5 cycles of vector
-// instructions per 4 of theirs, 3 of them conversions (two codes in 8 cycles). Widening each
-// code once per workgroup and passing it on through LDS as bf16 (twice the LDS bytes, a
-// second barrier a step) took 1071 us, where this took 857.
+// Large fp32 results: 2048 x 8192 x 8192 (256 tiles of 256 x 256) 207 us, 1.32 PFLOP/s (the
+// library's bf16 product reaches 1.31 at 8192 x 8192 x 8192); 2560 x 10240 x 16384 770 to
+// 820 us (1.05 to 1.1). A step issues 5 cycles of vector instructions per 4 of the matrix
+// cores, 3 of them conversions (two codes in 8 cycles). Widening each code once per
+// workgroup and passing it on through LDS as bf16 (twice the LDS bytes, a second barrier a
+// step) took 1071 us, where this took 857.
 template <int kOut, int kBR, int kAR, int kWB, int kWA, int kSlots, int kPer = 1>
 __global__ __launch_bounds__(64 * kWB * kWA) void product_tile_kernel(ProductArgs a) {
   constexpr int kWaves = kWB * kWA;
@@ -294,10 +294,11 @@ __global__ __launch_bounds__(64 * kWB * kWA) void product_tile_kernel(ProductArg
 // instruction's sums are scaled into the accumulators three instructions later,
 // when they are there.
 //
-// 16384 x 10240 x 2560 takes 390 to 410 us (2.1 to 2.2 PFLOP/s; the library's product of
-// E4M3 matrices with one scale each reaches 2.77 at 8192 x 8192 x 8192). In calls right
-// after idling (450 us) the matrix cores are busy 53 % of the cycles, vector instructions
-// issue in 47 %, and the clock is 1.73 GHz: power, not a stall, sets the pace there.
+// 16384 x 10240 x 2560 takes 360 to 410 us (2.1 to 2.4 PFLOP/s; the library's product of
+// E4M3 matrices with one scale each reaches 2.77 at 8192 x 8192 x 8192). The matrix cores
+// are busy 55 % of the cycles, vector instructions issue in 49 %, at 2.0 to 2.1 GHz: the
+// busier they are, the lower the clock (8192 x 8192 x 8192: 60 % at 2.0). A tile's stores
+// cost 3.6 us, which the next tile's second step waits for.
 constexpr int kWide = 256;
 constexpr int kWideRows = kWide * kRowChunks;          // chunks of an operand's rows of a step
 constexpr int kWideSlot = 2 * kWideRows + 64 + 16;     // and A's 256 scales, B's two (of 64 lanes)
