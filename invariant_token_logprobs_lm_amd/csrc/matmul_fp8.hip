@@ -99,10 +99,11 @@ struct ProductArgs {
   long long tiles;
   bool quads;  // C's rows are whole fours of columns, aligned as such
   bool lines;  // C's rows are whole 16-byte pieces, aligned as such
+  bool runs;   // a die's workgroups take consecutive tiles (see tiles_in_runs)
 };
 
 // Four consecutive columns of a row of C, aligned as such or not (1321 x 72281 x 128, fp32
-// 116 us by 16-byte stores at any element, 218 element by element).
+// 104 us by 16-byte stores at any element; element by element twice the time).
 template <int kOut, bool kAligned = true>
 __device__ __forceinline__ void put4(typename Elem<kOut>::T* out, const floatx4& v) {
   using E = Elem<kOut>;
@@ -173,8 +174,10 @@ __global__ __launch_bounds__(64 * kWB * kWA) void product_tile_kernel(ProductArg
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wb = wave % kWB, wa = wave / kWB;
   const int quad = lane >> 4, c16 = lane & 15;
-  const long long tile = flat_group();
-  if (tile >= a.tiles) return;
+  const long long group = flat_group();
+  if (group >= a.tiles) return;
+  const int die = (int)(group & 7);  // consecutive workgroups go to the eight dies in turn
+  const long long tile = a.runs ? die * (a.tiles >> 3) + min((long long)die, a.tiles & 7) + (group >> 3) : group;
   const long long i0 = tile / a.tiles_n * kAR;
   const long long j0 = tile % a.tiles_n * kBR;
   const int steps = a.k / kBlock;
@@ -272,11 +275,39 @@ __global__ __launch_bounds__(64 * kWB * kWA) void product_tile_kernel(ProductArg
     wait_and_barrier<0>();
     for (; s < steps; ++s) multiply(s);
   }
+  if constexpr (kOut == 1) {
 #pragma unroll
-  for (int an = 0; an < kAN; ++an)
+    for (int an = 0; an < kAN; ++an)
 #pragma unroll
-    for (int bm = 0; bm < kBM; ++bm)
-      store4<kOut>(a, i0 + wa * (kAR / kWA) + an * 16 + c16, j0 + wb * (kBR / kWB) + bm * 16 + 4 * quad, acc[bm][an]);
+      for (int bm = 0; bm < kBM; ++bm)
+        store4<kOut>(a, i0 + wa * (kAR / kWA) + an * 16 + c16, j0 + wb * (kBR / kWB) + bm * 16 + 4 * quad, acc[bm][an]);
+  } else {
+    // 16 rows of a wavefront at a time through LDS, so that a lane stores eight columns and
+    // a row's are one stretch (264 x 94720 x 512 in 128 x 128 tiles 35 us, straight from the
+    // registers 40; 389 x 12864 x 256 7.1 and 9). fp32 results, four columns a lane either
+    // way, took longer through LDS (8192 x 8192 x 640: 117 us, 104 straight).
+    constexpr int kRowBytes = kBM * 32, kPitch = kRowBytes + 16;   // (16 rows take kPitch chunks)
+    constexpr int kPieces = kRowBytes / 16, kAtOnce = 64 / kPieces;  // 8 columns each; rows per store
+    static_assert(16 % kAtOnce == 0 && kWaves * kPitch <= kSlots * kChunks, "within the slots");
+    __syncthreads();  // (the last step's slot has been read)
+    int ln = lane;
+    asm volatile("" : "+v"(ln));  // (per-lane addresses formed here, not kept across the steps)
+    char* turn = reinterpret_cast<char*>(smem + wave * kPitch);
+    char* put = turn + (ln & 15) * kPitch + (ln >> 4) * 8;
+    const char* get = turn + ln / kPieces * kPitch + ln % kPieces * 16;
+    const long long row0 = i0 + wa * (kAR / kWA) + ln / kPieces, col = j0 + wb * (kBR / kWB) + ln % kPieces * 8;
+#pragma unroll
+    for (int an = 0; an < kAN; ++an) {
+#pragma unroll
+      for (int bm = 0; bm < kBM; ++bm) put4<0>(reinterpret_cast<uint16_t*>(put + bm * 32), acc[bm][an]);
+#pragma unroll
+      for (int r = 0; r < 16 / kAtOnce; ++r) {
+        const uint4 v = *reinterpret_cast<const uint4*>(get + r * kAtOnce * kPitch);
+        const long long row = row0 + an * 16 + r * kAtOnce;
+        store8(a, static_cast<uint16_t*>(a.C) + row * a.n + col, v, row, col);
+      }
+    }
+  }
 }
 
 // 256 x 256 tiles for large products (bf16 results): eight wavefronts, each 128 columns of C by
@@ -527,10 +558,22 @@ void run_wide(ProductArgs a, hipStream_t stream) {
   hipLaunchKernelGGL((product_wide_kernel), dim3((unsigned)std::min<long long>(ceil_div(a.tiles, 8) * 8, kCUs)), dim3(kThreads8), 0, stream, a);
 }
 
+// Whether a die's workgroups take consecutive tiles: where C's rows do not start at whole
+// 128-byte lines, tiles side by side share lines, and a line written by two dies goes to
+// memory in two pieces. fp32 results: 882 x 72178 x 640 111 us, tiles in turn 129; 1321 x 72281 x
+// 128 104 and 126; 2000 x 10001 x 4096 171 and 172; rows of whole lines 8192 x 8192 x 640 113 and
+// 107. bf16 results: 4000 x 20001 x 256 57 and 70; 1000 x 5001 x 512 9.2 and 9.5, x 1024, more
+// bound by its steps, 13.4 and 12.9.
+template <int kOut>
+bool tiles_in_runs(const ProductArgs& a) {
+  return a.n * Elem<kOut>::kSize % 128 != 0 && (kOut == 1 || a.k <= 4 * kBlock);
+}
+
 template <int kOut, int kBR, int kAR, int kWB, int kWA, int kSlots, int kPer = 1>
 void run_tiles(ProductArgs a, hipStream_t stream) {
   a.tiles_n = (int)ceil_div(a.n, kBR);
   a.tiles = ceil_div(a.m, kAR) * a.tiles_n;
+  a.runs = tiles_in_runs<kOut>(a);
   hipLaunchKernelGGL((product_tile_kernel<kOut, kBR, kAR, kWB, kWA, kSlots, kPer>), flat_grid(a.tiles), dim3(64 * kWB * kWA), 0, stream, a);
 }
 
@@ -735,7 +778,7 @@ hipError_t launch_matmul_fp8_blocks(const MatmulFp8& c, hipStream_t stream) {
   const uintptr_t four = c.out_dtype == 0 ? 7 : 15;
   const ProductArgs a{c.A, c.B, c.a_scale, c.b_scale, c.C, c.m, c.n, c.m, (int)c.k, 0, 0,
                       c.n % 4 == 0 && (reinterpret_cast<uintptr_t>(c.C) & four) == 0,
-                      c.n % (c.out_dtype == 0 ? 8 : 4) == 0 && (reinterpret_cast<uintptr_t>(c.C) & 15) == 0};
+                      c.n % (c.out_dtype == 0 ? 8 : 4) == 0 && (reinterpret_cast<uintptr_t>(c.C) & 15) == 0, false};
   if (c.out_dtype == 0) run_product<0>(a, stream);
   else run_product<1>(a, stream);
   return hipGetLastError();
