@@ -35,8 +35,8 @@ struct Quotient {
   __device__ __forceinline__ bool plain() const { return s >= 0x1p-80f; }
   __device__ __forceinline__ float of(float x) const {
     float q = x * r;
-    q = __builtin_fmaf(__builtin_fmaf(-s, q, x), r, q);
-    return __builtin_fmaf(__builtin_fmaf(-s, q, x), r, q);
+    q = __builtin_fmaf(-__builtin_fmaf(s, q, -x), r, q);  // (a remainder of -0: -0 stays -0)
+    return __builtin_fmaf(-__builtin_fmaf(s, q, -x), r, q);
   }
 };
 

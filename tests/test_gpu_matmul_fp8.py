@@ -84,6 +84,20 @@ def test_codes_of_odd_alignment_and_small_values(cuda, itl):
     assert bool((s == 2.0 ** -126).all()) and bool(torch.isfinite(B.values(q)).all())
 
 
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("n,d", [(2, 128), (3, 100), (130, 264)])
+def test_zeros_keep_their_sign(cuda, itl, n, d, dtype):
+    """A code's bits are the quotient's, negative zeros among them."""
+    x = _matrix(n, d, 5).to(dtype)
+    x[:, ::2] = torch.where(torch.arange(d)[::2] % 4 == 0, 0.0, -0.0).to(dtype)
+    x[0] = -0.0
+    for make, ref in ((itl.quantize_blocks_fp8, B.blocks), (itl.quantize_tiles_fp8, B.tiles)):
+        say("zeros", n, d, dtype, make.__name__)
+        q, _, qt, _ = make(x.to(cuda), columns=True)
+        assert torch.equal(q.cpu(), ref(x)[0]) and torch.equal(qt.cpu(), ref(x.t().contiguous())[0])
+        assert torch.equal(make(x.to(cuda))[0], q)
+
+
 def test_nothing_beyond_the_codes_is_written(cuda, itl):
     n, d = 130, 200
     x = torch.randn(n, d, device=cuda)
