@@ -566,7 +566,7 @@ def lmhead_logprob_mxfp4(Hq, h_scale, Wq4, w_scale_codes, tokens, *, logprob=Non
 def _new(shape, dtype, like, name, given):
     """`given`, checked, or a new tensor of that shape and dtype on like's device."""
     if given is None:
-        return like.new_empty(shape, dtype=dtype)
+        return like.new_empty(*shape, dtype=dtype)  # (single sizes are read faster than a tuple)
     _need(given, name, (dtype,), device=like.device, ndim=len(shape))
     if tuple(given.shape) != tuple(shape):
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(given.shape)}")
@@ -676,8 +676,8 @@ def residual_norm(x, y, w_pre, *, w_post=None, gate=None, scale=1.0, eps=1e-6, h
     n, d, stride = _norm_operands(x, y, w_pre, w_post, gate, "x")
     h = _stream_rows(x, y, h, n, d)
     u = _new((n, d), x.dtype, x, "u", u)
-    rstd_pre = torch.empty(n, dtype=torch.float32, device=x.device)
-    rstd_post = None if w_post is None else torch.empty(n, dtype=torch.float32, device=x.device)
+    rstd_pre = x.new_empty(n, dtype=torch.float32)
+    rstd_post = None if w_post is None else x.new_empty(n, dtype=torch.float32)
     operands = (_ptr(x), _ptr(y), _ptr(gate), stride, _ptr(w_post), _ptr(w_pre), _HEAD_DTYPES[x.dtype], n, d, scale, eps)
     outputs = (_ptr(h), _ptr(u), _ptr(rstd_pre), _ptr(rstd_post))
     if dropout is None:
@@ -695,8 +695,8 @@ def residual_norm_fp8(x, y, w_pre, *, w_post=None, gate=None, scale=1.0, eps=1e-
     h = _stream_rows(x, y, h, n, d)
     Uq = _new((n, d), torch.uint8, x, "Uq", Uq)
     u_scale = _new((n,), torch.float32, x, "u_scale", u_scale)
-    rstd_pre = torch.empty(n, dtype=torch.float32, device=x.device)
-    rstd_post = None if w_post is None else torch.empty(n, dtype=torch.float32, device=x.device)
+    rstd_pre = x.new_empty(n, dtype=torch.float32)
+    rstd_post = None if w_post is None else x.new_empty(n, dtype=torch.float32)
     _launch(x.device, lib.itl_residual_norm_fp8, _ptr(x), _ptr(y), _ptr(gate), stride, _ptr(w_post), _ptr(w_pre),
             _HEAD_DTYPES[x.dtype], n, d, scale, eps, _ptr(h), _ptr(Uq), _ptr(u_scale), _ptr(rstd_pre),
             _ptr(rstd_post))
@@ -712,8 +712,8 @@ def residual_norm_blocks_fp8(x, y, w_pre, *, w_post=None, gate=None, scale=1.0, 
     h = _stream_rows(x, y, h, n, d)
     Uq = _new((n, d), torch.uint8, x, "Uq", Uq)
     u_scale = _new((d // 128, n), torch.float32, x, "u_scale", u_scale)
-    rstd_pre = torch.empty(n, dtype=torch.float32, device=x.device)
-    rstd_post = None if w_post is None else torch.empty(n, dtype=torch.float32, device=x.device)
+    rstd_pre = x.new_empty(n, dtype=torch.float32)
+    rstd_post = None if w_post is None else x.new_empty(n, dtype=torch.float32)
     _launch(x.device, lib.itl_residual_norm_blocks_fp8, _ptr(x), _ptr(y), _ptr(gate), stride, _ptr(w_post), _ptr(w_pre),
             _HEAD_DTYPES[x.dtype], n, d, scale, eps, None if dropout is None else _dropout_spec(dropout, x.device),
             _ptr(h), _ptr(Uq), _ptr(u_scale), _ptr(rstd_pre), _ptr(rstd_post))
