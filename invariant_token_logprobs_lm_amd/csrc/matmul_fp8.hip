@@ -94,7 +94,7 @@ struct ProductArgs {
   const float *a_scale, *b_scale;
   void* C;
   long long m, n;
-  long long scale_rows;  // of a_scale: m, or more where these are some of its rows
+  long long scale_rows, c_cols;  // of a_scale and C: m and n, or more where these are some of them
   int k, tiles_n;
   long long tiles;
   bool quads;  // C's rows are whole fours of columns, aligned as such
@@ -123,7 +123,7 @@ __device__ __forceinline__ void store4(const ProductArgs& a, long long row, long
   using E = Elem<kOut>;
   using T = typename E::T;
   if (row >= a.m || col >= a.n) return;
-  T* out = static_cast<T*>(a.C) + row * a.n + col;
+  T* out = static_cast<T*>(a.C) + row * a.c_cols + col;
   if (a.quads) return put4<kOut>(out, v);
   if (col + 4 <= a.n) return put4<kOut, false>(out, v);
 #pragma unroll
@@ -304,7 +304,7 @@ __global__ __launch_bounds__(64 * kWB * kWA) void product_tile_kernel(ProductArg
       for (int r = 0; r < 16 / kAtOnce; ++r) {
         const uint4 v = *reinterpret_cast<const uint4*>(get + r * kAtOnce * kPitch);
         const long long row = row0 + an * 16 + r * kAtOnce;
-        store8(a, static_cast<uint16_t*>(a.C) + row * a.n + col, v, row, col);
+        store8(a, static_cast<uint16_t*>(a.C) + row * a.c_cols + col, v, row, col);
       }
     }
   }
@@ -527,7 +527,7 @@ __global__ __launch_bounds__(kThreads8, 2) void product_wide_kernel(ProductArgs 
     char* put = turn + (ln & 15) * kTurnPitch + (ln >> 4) * 8;
     const char* get = turn + (ln >> 3) * kTurnPitch + (ln & 7) * 16;
     const long long row0 = (long long)at.x * kWide + L.tq * 64 + (ln >> 3), col0 = (long long)at.y * kWide + L.wv * 128 + (ln & 7) * 8;
-    uint16_t* out = static_cast<uint16_t*>(a.C) + row0 * a.n + col0;
+    uint16_t* out = static_cast<uint16_t*>(a.C) + row0 * a.c_cols + col0;
     const bool whole = a.lines && (long long)(at.x + 1) * kWide <= a.m && (long long)(at.y + 1) * kWide <= a.n;
 #pragma unroll
     for (int an = 0; an < 4; ++an) {
@@ -538,7 +538,7 @@ __global__ __launch_bounds__(kThreads8, 2) void product_wide_kernel(ProductArgs 
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
           const uint4 v = *reinterpret_cast<const uint4*>(get + r * 8 * kTurnPitch);
-          uint16_t* to = out + (an * 16 + r * 8) * a.n + half * 64;
+          uint16_t* to = out + (an * 16 + r * 8) * a.c_cols + half * 64;
           if (whole) *reinterpret_cast<uint4*>(to) = v;
           else store8(a, to, v, row0 + an * 16 + r * 8, col0 + half * 64);
         }
@@ -566,7 +566,7 @@ void run_wide(ProductArgs a, hipStream_t stream) {
 // bound by its steps, 13.4 and 12.9.
 template <int kOut>
 bool tiles_in_runs(const ProductArgs& a) {
-  return a.n * Elem<kOut>::kSize % 128 != 0 && (kOut == 1 || a.k <= 4 * kBlock);
+  return a.c_cols * Elem<kOut>::kSize % 128 != 0 && (kOut == 1 || a.k <= 4 * kBlock);
 }
 
 template <int kOut, int kBR, int kAR, int kWB, int kWA, int kSlots, int kPer = 1>
@@ -672,7 +672,7 @@ __global__ __launch_bounds__(64 * kFewWaves) void product_few_kernel(ProductArgs
     const int f = 64 * kFewWaves * e + threadIdx.x, which = f >> 8;
     const long long row = i0 + 16 * (which % kAN) + ((f >> 2) & 15), col = j0 + 16 * (which / kAN) + 4 * ((f >> 6) & 3) + (f & 3);
     if (f < kBM * kAN * 256 && row < a.m && col < a.n)
-      static_cast<typename Elem<kOut>::T*>(a.C)[row * a.n + col] = Elem<kOut>::from_f(acc[e]);
+      static_cast<typename Elem<kOut>::T*>(a.C)[row * a.c_cols + col] = Elem<kOut>::from_f(acc[e]);
   }
 }
 
@@ -687,8 +687,17 @@ void run_few(ProductArgs a, hipStream_t stream) {
 ProductArgs rows_of(ProductArgs a, long long first, long long count, size_t elem) {
   a.A += first * a.k;
   a.a_scale += first;
-  a.C = static_cast<char*>(a.C) + (size_t)first * a.n * elem;
+  a.C = static_cast<char*>(a.C) + (size_t)first * a.c_cols * elem;
   a.m = count;
+  return a;
+}
+
+// Columns first .. first + count, first a multiple of 128.
+ProductArgs columns_of(ProductArgs a, long long first, long long count, size_t elem) {
+  a.B += first * a.k;
+  a.b_scale += first / kBlock * (a.k / kBlock);
+  a.C = static_cast<char*>(a.C) + (size_t)first * elem;
+  a.n = count;
   return a;
 }
 
@@ -705,21 +714,34 @@ void run_product(const ProductArgs& a, hipStream_t stream) {
   if (tiles(32, 16) <= kCUs) return run_few<kOut, 2, 1>(a, stream);
   if (a.m <= 16 && tiles(64, 16) <= kCUs) return run_few<kOut, 4, 1>(a, stream);
   if (a.m > 16 && tiles(32, 32) <= kCUs) return run_few<kOut, 2, 2>(a, stream);
-  // Rows whose tiles fill the CUs a whole number of times, and what is left: a few tiles
-  // more than whole rounds take as long as another round, or a third of it in smaller
+  // Rows or columns whose tiles fill the CUs a whole number of times, and what is left: a few
+  // tiles more than whole rounds take as long as another round, or a third of it in smaller
   // tiles of their own. 6000 x 3000 x 7168 (288 tiles of 256 x 256) 130, all in those 169.
+  // Columns where they leave a tenth less, in tiles of 128 x 128: 300 x 70000 x 4096 (by columns
+  // 36 of 548 tiles, by rows none whole) 138 and 165, 4096 x 4200 x 4096, fp32 (32 of those and
+  // 66) 131 and 141; 2560 x 10240 x 16384, fp32 (600 and 640) 797 and 785.
   struct Rounds {
-    long long rounds, rows, left;  // whole rounds, their rows, the tiles left
+    long long rounds, rows, columns, left;  // whole rounds, their rows and columns, the tiles left
   };
   auto rounds_of = [&](int size, long long at_once) {
-    const long long across = ceil_div(a.n, size), all = tiles(size, size), rounds = all / at_once;
-    const long long down = rounds * at_once / across;
-    return Rounds{rounds, down * size, all - down * across};
+    const long long across = ceil_div(a.n, size), down = ceil_div(a.m, size), all = tiles(size, size);
+    const long long rounds = all / at_once, fit = rounds * at_once;
+    const long long rows = fit / across * size, columns = fit / down * size;
+    const long long rows_left = ceil_div(std::max(a.m - rows, 0LL), 128) * ceil_div(a.n, 128);
+    const long long columns_left = ceil_div(std::max(a.n - columns, 0LL), 128) * ceil_div(a.m, 128);
+    if (10 * columns_left > 9 * rows_left) return Rounds{rounds, rows, a.n, all - fit / across * across};
+    return Rounds{rounds, a.m, columns, all - fit / down * down};
   };
   auto split = [&](const Rounds& r, double most_left, auto&& run) {
-    if (r.rows == 0 || r.left == 0 || r.left > most_left) return run(a);
-    run(rows_of(a, 0, r.rows, Elem<kOut>::kSize));
-    run_product<kOut>(rows_of(a, r.rows, a.m - r.rows, Elem<kOut>::kSize), stream);
+    constexpr size_t elem = Elem<kOut>::kSize;
+    if (r.rows == 0 || r.columns == 0 || r.left == 0 || r.left > most_left) return run(a);
+    if (r.rows < a.m) {
+      run(rows_of(a, 0, r.rows, elem));
+      run_product<kOut>(rows_of(a, r.rows, a.m - r.rows, elem), stream);
+    } else {
+      run(columns_of(a, 0, r.columns, elem));
+      run_product<kOut>(columns_of(a, r.columns, a.n - r.columns, elem), stream);
+    }
   };
   const double steps = (double)(a.k / kBlock);
   // More than half the CUs with a 256 x 256 tile: 2048 x 5120 x 4096 (160 tiles) 49, in
@@ -760,10 +782,10 @@ void run_product(const ProductArgs& a, hipStream_t stream) {
       return n / (2 * kCUs) * 2.0 + (over == 0 ? 0.0 : smaller && over <= most_left ? 0.5 + 0.0025 * over : over <= kCUs ? 1.2 : 2.0);
     };
     const Rounds r = rounds_of(128, 2 * kCUs), w = rounds_of(kWide, kCUs);
-    const double all128 = std::min(in128(tiles(128, 128), false), r.rounds * 2.0 + in128(r.left, r.rows > 0));
+    const double all128 = std::min(in128(tiles(128, 128), false), r.rounds * 2.0 + in128(r.left, r.rounds > 0));
     const double all64 = ceil_div(tiles(64, 128), kCUs) * 0.62;
     const double all256 = ceil_div(tiles(kWide, kWide), kCUs) * 3.2;
-    const double parts = w.rows > 0 ? w.rounds * 3.2 + in128(4 * w.left, true) + 4.0 / steps : all256;
+    const double parts = w.rounds > 0 ? w.rounds * 3.2 + in128(4 * w.left, true) + 4.0 / steps : all256;
     if (std::min(all256, parts) < std::min(all128, all64))
       return split(w, parts < all256 ? w.left : 0, [&](const ProductArgs& p) { run_tiles<kOut, 256, 256, 2, 4, 2>(p, stream); });
     if (all128 < all64)
@@ -776,7 +798,7 @@ void run_product(const ProductArgs& a, hipStream_t stream) {
 
 hipError_t launch_matmul_fp8_blocks(const MatmulFp8& c, hipStream_t stream) {
   const uintptr_t four = c.out_dtype == 0 ? 7 : 15;
-  const ProductArgs a{c.A, c.B, c.a_scale, c.b_scale, c.C, c.m, c.n, c.m, (int)c.k, 0, 0,
+  const ProductArgs a{c.A, c.B, c.a_scale, c.b_scale, c.C, c.m, c.n, c.m, c.n, (int)c.k, 0, 0,
                       c.n % 4 == 0 && (reinterpret_cast<uintptr_t>(c.C) & four) == 0,
                       c.n % (c.out_dtype == 0 ? 8 : 4) == 0 && (reinterpret_cast<uintptr_t>(c.C) & 15) == 0, false};
   if (c.out_dtype == 0) run_product<0>(a, stream);

@@ -197,6 +197,26 @@ def test_rows_of_a_large_product(cuda, itl, k):
     assert torch.equal(_bits(other), _bits(whole)) and torch.equal(_bits(again), _bits(whole))
 
 
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("m,n,k", [(2560, 6656, 1024), (2550, 6601, 1024), (1500, 5601, 2560), (2049, 8200, 2560), (120, 70000, 2560)])
+def test_products_of_more_than_whole_rounds(cuda, itl, m, n, k, dtype):
+    """Tiles just past a whole number of rounds, by rows or by columns: some of the rows and
+    columns against 64 bits, all of them against smaller calls' bits, nothing beyond written."""
+    say("rounds", m, n, k, dtype)
+    a, sa, b, sb = _operands(itl, m, n, k, cuda)
+    flat = torch.full((m * n + 32,), 7.0, dtype=dtype, device=cuda)
+    out = itl.matmul_fp8_blocks(a, sa, b, sb, out_dtype=dtype, out=flat[16:16 + m * n].view(m, n))
+    assert bool((flat[:16] == 7).all()) and bool((flat[16 + m * n:] == 7).all())
+    rows = torch.unique(torch.tensor([0, 1, m // 3, m // 2, m - 200, m - 130, m - 2, m - 1]).clamp(min=0))
+    _check(out[rows.to(cuda)], (a[rows.to(cuda)], sa[:, rows.to(cuda)], b, sb))
+    for i in range(0, m, 700):
+        some = itl.matmul_fp8_blocks(a[i:i + 700], sa[:, i:i + 700].contiguous(), b, sb, out_dtype=dtype)
+        assert torch.equal(_bits(some), _bits(out[i:i + 700])), i
+    for j in range(0, n, 1280):
+        some = itl.matmul_fp8_blocks(a, sa, b[j:j + 1280], sb[j // 128:j // 128 + 10], out_dtype=dtype)
+        assert torch.equal(_bits(some), _bits(out[:, j:j + 1280])), j
+
+
 def test_columns_do_not_depend_on_the_width(cuda, itl):
     """The first columns of a wider B, down to a few: the same bits."""
     for m in (3, 40, 300):
