@@ -507,9 +507,10 @@ __global__ __launch_bounds__(64 * kBwdMaxWaves, kGroups == 1 && !kDrop ? 3 : 2) 
       if (a.w_post) {
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-          const float s = (kDrop ? kept[c].at[j] ? scale : 0.0f : scale) * (a.gate ? gate[c][j] : 1.0f) * w_post[c][j] * q[c][j];
-          B += s * g[c][j];
-          C += s * (r_pre * n[c][j]);
+          const float s = scale * (a.gate ? gate[c][j] : 1.0f) * w_post[c][j] * q[c][j];
+          const float b = s * g[c][j], e = s * (r_pre * n[c][j]);
+          B += kDrop && !kept[c].at[j] ? 0.0f : b;  // (whole products: 0 whatever meets a dropped value)
+          C += kDrop && !kept[c].at[j] ? 0.0f : e;
         }
       }
     }
@@ -535,9 +536,9 @@ __global__ __launch_bounds__(64 * kBwdMaxWaves, kGroups == 1 && !kDrop ? 3 : 2) 
         float dy[8], dg[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-          float sdx = scale * g[c][j];
-          if constexpr (kDrop) sdx = kept[c].at[j] ? sdx : 0.0f;
-          const float dp = a.gate ? sdx * gate[c][j] : sdx;
+          const float sdx = scale * g[c][j];
+          float dp = a.gate ? sdx * gate[c][j] : sdx;
+          if constexpr (kDrop) dp = kept[c].at[j] ? dp : 0.0f;
           if (a.gate) {
             dg[j] = sdx * (a.w_post ? q[c][j] * w_post[c][j] : q[c][j]);
             if constexpr (kDrop) dg[j] = kept[c].at[j] ? dg[j] : 0.0f;
@@ -545,7 +546,9 @@ __global__ __launch_bounds__(64 * kBwdMaxWaves, kGroups == 1 && !kDrop ? 3 : 2) 
           }
           if (a.w_post) {
             s_post[c][j] += dp * q[c][j];
-            dy[j] = r_post * (dp * w_post[c][j] - q[c][j] * c2);
+            float dq = dp * w_post[c][j];
+            if constexpr (kDrop) dq = kept[c].at[j] ? dq : 0.0f;
+            dy[j] = r_post * (dq - q[c][j] * c2);
           } else {
             dy[j] = dp;
           }
@@ -603,27 +606,42 @@ __global__ __launch_bounds__(kNormThreads) void norm_backward_rows_kernel(BwdArg
   };
   DropoutKey key;
   if constexpr (kDrop) key = dropout_key(a.drop);
-  auto kept = [&](int k, float v) {  // v with dropout
-    if constexpr (kDrop) return dropped(v, dropout_keeps_one(a.drop, key, k, a.drop.first_row + row), a.drop.scale);
+  auto keeps = [&](int k) {
+    if constexpr (kDrop) return dropout_keeps_one(a.drop, key, k, a.drop.first_row + row);
+    else return true;
+  };
+  auto kept = [&](float v, bool keep) {  // v with dropout
+    if constexpr (kDrop) return dropped(v, keep, a.drop.scale);
     else return v;
   };
-  auto grad_p = [&](int k, float dxv) { return gate ? kept(k, a.scale * dxv) * E::to_f(gate[k]) : kept(k, a.scale * dxv); };
+  // (chosen after the gate's and the weight's products: 0 whatever meets a dropped value)
+  auto grad_p = [&](int k, float dxv, bool keep) {
+    float p = kept(a.scale * dxv, keep);
+    if (gate) p *= E::to_f(gate[k]);
+    return keep ? p : 0.0f;
+  };
+  auto grad_q = [&](int k, float dp, bool keep) {
+    const float q = dp * E::to_f(w_post[k]);
+    return keep ? q : 0.0f;
+  };
   s = 0.0f;
   for (int k = threadIdx.x; k < d; k += kNormThreads) {
     const float v = grad_h(k);
-    if (w_post) s += (grad_p(k, v) * E::to_f(w_post[k])) * (E::to_f(y[k]) * r_post);
+    const bool keep = keeps(k);
+    if (w_post) s += grad_q(k, grad_p(k, v, keep), keep) * (E::to_f(y[k]) * r_post);
     if (dgate) {
       const float p = w_post ? E::to_f(y[k]) * r_post * E::to_f(w_post[k]) : E::to_f(y[k]);
-      dgate[k] = E::from_f(kept(k, a.scale * p * v));
+      dgate[k] = E::from_f(kept(a.scale * p * v, keep));
     }
-    if (!w_post && y) dy[k] = E::from_f(grad_p(k, v));
+    if (!w_post && y) dy[k] = E::from_f(grad_p(k, v, keep));
     if (!w_post) dx[k] = E::from_f(v);
   }
   if (!w_post) return;
   const float c2 = block_sum<kW>(s, lds) / (float)d;
   for (int k = threadIdx.x; k < d; k += kNormThreads) {
     const float v = grad_h(k);
-    const float dq = grad_p(k, v) * E::to_f(w_post[k]);
+    const bool keep = keeps(k);
+    const float dq = grad_q(k, grad_p(k, v, keep), keep);
     dy[k] = E::from_f(r_post * (dq - E::to_f(y[k]) * r_post * c2));
     dx[k] = E::from_f(v);
   }
@@ -671,6 +689,7 @@ __global__ __launch_bounds__(kNormThreads) void norm_backward_columns_kernel(Bwd
         if constexpr (kDrop) dg = dropped(dg, keep, a.drop.scale);
         s_gate += dg;
         dp *= E::to_f(gate[(size_t)row * a.gate_stride + k]);
+        if constexpr (kDrop) dp = keep ? dp : 0.0f;  // (whatever meets a dropped value)
       }
       if (a.w_post) s_post += dp * q;
     }

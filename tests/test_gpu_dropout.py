@@ -251,6 +251,38 @@ def test_norm_gradient_against_differences(cuda, itl):
         assert abs(along - slope) <= 1e-5 * bound, name
 
 
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("d", [64, 65, 5000, 5001, 8200])
+def test_dropped_gradients_are_zero_whatever_they_meet(cuda, itl, d, dtype):
+    """Gates, post norm weights and a gradient of h that are not finite where the value is
+    dropped: the bits of a call with ordinary numbers there (dx holds dh itself)."""
+    for n, post, gate in ((6, False, 2), (6, True, 2), (1, False, 1), (1, True, 1)):
+        say("dropped gradients", n, d, dtype, post, gate)
+        t, drop = _operands(n, d, dtype, post, gate, d, cuda), _drop(itl, cuda, 0.5)
+        out = (_factors(n, d, drop) == 0).to(cuda)
+        g = torch.Generator().manual_seed(d)
+        du, dh = torch.randn(n, d, generator=g).to(cuda), torch.randn(n, d, generator=g).to(dtype).to(cuda)
+        forward = itl.residual_norm(t["x"], t["y"], t["w_pre"], dropout=drop, **_kw(t))
+        h, _, r_pre, r_post = forward
+
+        def grads(t, dh=dh):
+            return itl.residual_norm_backward(du, dh, h, t["y"], t["w_pre"], r_pre, rstd_post=r_post, dropout=drop, **_kw(t))
+
+        def same(a, b):
+            return all(torch.equal(_bits(p), _bits(q)) for p, q in zip(a, b) if p is not None)
+
+        want = grads(t)
+        for bad in (float("nan"), float("inf"), -float("inf")):
+            spoilt = lambda v: torch.where(out if v.dim() == 2 else out[0], torch.full_like(v, bad), v)
+            with_gate = {**t, "gate": spoilt(t["gate"])}
+            assert same(itl.residual_norm(t["x"], t["y"], t["w_pre"], dropout=drop, **_kw(with_gate)), forward), bad
+            assert same(grads(with_gate), want), ("gate", bad)
+            if post and n == 1:
+                assert same(grads({**t, "w_post": spoilt(t["w_post"])}), want), ("w_post", bad)
+            got = grads(t, spoilt(dh))
+            assert same(got[1:], want[1:]) and torch.equal(got[0][~out], want[0][~out]), ("dh", bad)
+
+
 def test_norm_rows_do_not_depend_on_their_batch(cuda, itl):
     for d in (2560, 1001):
         t, drop = _operands(50, d, torch.bfloat16, True, 2, 3, cuda), _drop(itl, cuda, 0.2)
