@@ -1,0 +1,81 @@
+"""Each kernel of the block-scaled product over more steps than its slots, rounds and
+registers hold at once: some rows and columns against 64 bits, others against smaller
+calls' bits.
+
+Tolerances as in test_gpu_matmul_fp8.py.
+"""
+
+import pytest
+import torch
+
+import block_refs as B
+import learner_refs as R
+from helpers import say
+
+pytestmark = pytest.mark.gpu
+
+DTYPES = [torch.bfloat16, torch.float32]
+
+LONG = [
+    (16, 70000, 1024), (33, 60001, 640), (64, 50000, 8448),  # 128 x 64 tiles through three slots: 8, 5 and 66 steps
+    (16, 4096, 16640), (16, 8000, 8448), (30, 8000, 8448),   # blocks shared by wavefronts: 3, 3 and 5 rounds
+    (16, 9000, 4224), (5, 16384, 16640),                     # the same, 64 columns: 3 and 9 rounds
+    (512, 2048, 8448), (1024, 2560, 8448),                   # 64 x 64 tiles, two steps per barrier and one
+    (1024, 4000, 8448),                                      # 64 x 128 tiles (bf16)
+    (128, 40000, 8448), (2048, 4096, 8448),                  # 128 x 128 tiles (bf16; fp32)
+    (4096, 4096, 8448),                                      # 256 x 256 tiles
+]
+
+
+@pytest.fixture(scope="module")
+def itl():
+    import invariant_token_logprobs_lm_amd as itl
+
+    return itl
+
+
+def _bits(t):
+    return t.contiguous().view(torch.uint8)
+
+
+def _codes(n, k, seed, device):
+    """Codes of either sign, none of them NaN (the lowest bit of the exponent is 0)."""
+    g = torch.Generator(device=device).manual_seed(seed)
+    return torch.randint(0, 256, (n, k), generator=g, device=device, dtype=torch.uint8).bitwise_and_(0xF7)
+
+
+def _operands(m, n, k, device):
+    g = torch.Generator(device=device).manual_seed(m + n + k)
+    scale = lambda *s: torch.rand(*s, generator=g, device=device) + 0.5
+    return _codes(m, k, m, device), scale(k // 128, m), _codes(n, k, n + 1, device), scale(-(-n // 128), k // 128)
+
+
+def _check_some(out, ops, rows):
+    """Those rows at the columns of the first, the middle and the last of B's tiles, against 64 bits."""
+    a, sa, b, sb = ops
+    n, tiles = b.shape[0], sb.shape[0]
+    some = sorted({0, tiles // 2, tiles - 1})
+    cols = torch.cat([torch.arange(t * 128, min(n, t * 128 + 128)) for t in some]).to(b.device)
+    rows = torch.tensor(rows, device=b.device)
+    want, mag = B.product(a[rows], sa[:, rows].contiguous(), b[cols], sb[torch.tensor(some, device=b.device)])
+    off = (R.f64(out[rows][:, cols]) - want).abs()
+    bound = (256 + sa.shape[0] + 3) * R.EPS24 * mag
+    if out.dtype == torch.bfloat16:
+        bound += R.half_step(torch.bfloat16) * want.abs() + 7 * 2.0 ** -13 * mag
+        assert float(off.norm()) <= 2.0 ** -8 * float(want.norm())
+    assert bool((off <= bound).all())
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("m,n,k", LONG)
+def test_long_contractions(cuda, itl, m, n, k, dtype):
+    say("long", m, n, k, dtype)
+    a, sa, b, sb = ops = _operands(m, n, k, cuda)
+    out = itl.matmul_fp8_blocks(*ops, out_dtype=dtype)
+    _check_some(out, ops, sorted({0, m // 3, m // 2, m - 1}))
+    for i, some in ((0, 1), (m // 2, min(20, m - m // 2)), (m - 1, 1)):
+        got = itl.matmul_fp8_blocks(a[i:i + some], sa[:, i:i + some].contiguous(), b, sb, out_dtype=dtype)
+        assert torch.equal(_bits(got), _bits(out[i:i + some])), i
+    for t, some in ((0, 1), (n // 256, 5), ((n - 1) // 128, 1)):
+        got = itl.matmul_fp8_blocks(a, sa, b[128 * t:128 * (t + some)], sb[t:t + some], out_dtype=dtype)
+        assert torch.equal(_bits(got), _bits(out[:, 128 * t:128 * (t + some)])), t
