@@ -1,6 +1,6 @@
 """Each kernel of the block-scaled product over more steps than its slots, rounds and
 registers hold at once: some rows and columns against 64 bits, others against smaller
-calls' bits.
+calls' bits; codes of NaN.
 
 Tolerances as in test_gpu_matmul_fp8.py.
 """
@@ -79,3 +79,23 @@ def test_long_contractions(cuda, itl, m, n, k, dtype):
     for t, some in ((0, 1), (n // 256, 5), ((n - 1) // 128, 1)):
         got = itl.matmul_fp8_blocks(a, sa, b[128 * t:128 * (t + some)], sb[t:t + some], out_dtype=dtype)
         assert torch.equal(_bits(got), _bits(out[:, 128 * t:128 * (t + some)])), t
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("m,n,k", [(20, 130, 256), (16, 9000, 384), (300, 1001, 256), (33, 60001, 384), (128, 40000, 256),
+                                   (900, 5000, 256), (2100, 4100, 384), (4096, 4096, 384)])
+def test_codes_of_nan_stay_in_their_row_and_column(cuda, itl, m, n, k, dtype):
+    say("nan", m, n, k, dtype)
+    a, sa, b, sb = _operands(m, n, k, cuda)
+    want = itl.matmul_fp8_blocks(a, sa, b, sb, out_dtype=dtype)
+    rows, cols = sorted({0, m // 2 + 1, m - 1}), sorted({1, n // 2, n - 1})
+    hit = torch.zeros(m, n, dtype=torch.bool, device=cuda)
+    for at, i in enumerate(rows):
+        a[i, (at * 131) % k] = 0x7F if at % 2 else 0xFF
+        hit[i] = True
+    for at, j in enumerate(cols):
+        b[j, (at * 77 + 5) % k] = 0xFF if at % 2 else 0x7F
+        hit[:, j] = True
+    got = itl.matmul_fp8_blocks(a, sa, b, sb, out_dtype=dtype)
+    assert torch.equal(torch.isnan(got), hit)
+    assert torch.equal(got[~hit], want[~hit])
