@@ -1,6 +1,6 @@
 """Each kernel of the block-scaled product over more steps than its slots, rounds and
 registers hold at once: some rows and columns against 64 bits, others against smaller
-calls' bits; codes of NaN.
+calls' bits; codes of NaN; operands and results past 2^31 elements.
 
 Tolerances as in test_gpu_matmul_fp8.py.
 """
@@ -99,3 +99,27 @@ def test_codes_of_nan_stay_in_their_row_and_column(cuda, itl, m, n, k, dtype):
     got = itl.matmul_fp8_blocks(a, sa, b, sb, out_dtype=dtype)
     assert torch.equal(torch.isnan(got), hit)
     assert torch.equal(got[~hit], want[~hit])
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("k", [128, 384])
+@pytest.mark.parametrize("long_rows", [True, False])
+def test_more_than_2_to_the_31_elements(cuda, itl, k, long_rows, dtype):
+    """An operand and C both past 2^31 elements (and 2^32 bytes), along either of C's sides."""
+    far = (1 << 24) + 1000
+    m, n = (far, 130) if long_rows else (130, far)
+    say("large", m, n, k, dtype)
+    a, sa, b, sb = ops = _operands(m, n, k, cuda)
+    out = itl.matmul_fp8_blocks(*ops, out_dtype=dtype)
+    _check_some(out, ops, [0, 1, m // 2, m - 2, m - 1])
+    # (along C's rows: where the operand's and C's offsets pass 31 and 32 bits)
+    ends = [(1 << 31) // k, (1 << 32) // k, (1 << 31) // 130, (1 << 32) // (130 * out.element_size()), far]
+    for end in (e for e in ends if e <= far):
+        i = max(0, end - 400) // 128 * 128
+        some = min(600, far - i)
+        if long_rows:
+            got = itl.matmul_fp8_blocks(a[i:i + some], sa[:, i:i + some].contiguous(), b, sb, out_dtype=dtype)
+            assert torch.equal(_bits(got), _bits(out[i:i + some])), i
+        else:
+            got = itl.matmul_fp8_blocks(a, sa, b[i:i + some], sb[i // 128:i // 128 - (-some // 128)], out_dtype=dtype)
+            assert torch.equal(_bits(got), _bits(out[:, i:i + some])), i
