@@ -133,6 +133,13 @@ def test_kernels_have_no_scratch(tmp_path, src, kernels):
 
 
 @needs_hipcc
+@pytest.mark.parametrize("src", ["norm_dropout.hip", "norm_codes.hip"])
+def test_norms_with_dropout_and_codes_have_no_scratch(tmp_path, src):
+    """The norms' other instances: those of two groups with dropout are at the registers' end."""
+    test_kernels_have_no_scratch(tmp_path, src, ["norm_"])
+
+
+@needs_hipcc
 def test_inline_asm_loads_write_lds_only(tmp_path):
     out = str(tmp_path / "k.s")
     _compile(os.path.join(build.CSRC, "matmul_fp8.hip"), str(tmp_path), ("-S", "-o", out))
