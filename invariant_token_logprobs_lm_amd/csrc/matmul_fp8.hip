@@ -17,8 +17,11 @@
 // bf16 results: v_mfma_scale_f32_16x16x128_f8f6f4 (its own scales 1) takes a whole
 // block of 16 rows of each operand. It adds the eight products of a lane's eight
 // consecutive bytes with 13 bits below the largest (measured: a product 2^-14 of
-// it is lost; the sixteen sums of eight are added in fp32), so p_b is off by 1e-6 to
-// 4e-5 of itself, far inside a bf16 result's 2^-9.
+// it is lost; the sixteen sums of eight are added in fp32), so p_b is off by 7 2^-13 of
+// its products' absolute sum at worst, by 1e-6 to 4e-5 of itself on random operands, beside
+// a bf16 result's 2^-9. Where the products cancel it is the products that count: with
+// results 1 / 1800 of their products' sum, 300 x 500 x 2560 is off by 1.73e-3 of its norm,
+// bf16's rounding alone by 1.66e-3.
 // fp32 results: the codes become bf16, which holds every one of them, and
 // v_mfma_f32_16x16x32_bf16 sums their products in fp32 (off by 1e-8 of p_b; twice
 // the instructions' time). A lane's 32 bytes are four instructions' fragments.
