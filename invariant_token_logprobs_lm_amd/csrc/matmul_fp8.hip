@@ -109,7 +109,7 @@ struct ProductArgs {
 };
 
 // Four consecutive columns of a row of C, aligned as such or not (1321 x 72281 x 128, fp32
-// 104 us by 16-byte stores at any element; element by element twice the time).
+// 99 to 104 us by 16-byte stores at any element; element by element twice the time).
 template <int kOut, bool kAligned = true>
 __device__ __forceinline__ void put4(typename Elem<kOut>::T* out, const floatx4& v) {
   using E = Elem<kOut>;
@@ -158,11 +158,11 @@ __device__ __forceinline__ void store8(const ProductArgs& a, uint16_t* to, uint4
 // kAR rows, a grid of kWB x kWA wavefronts, both operands through kSlots LDS slots loaded
 // kSlots - kPer steps ahead, kPer steps per barrier.
 //
-// Few rows are bound by B's bytes: 16 x 129280 x 7168, fp32, 166 us (5.6 TB/s). Few
-// steps are bound by latency: 777 x 1001 x 1536 7.5 us, 12 steps of 0.3 and the launch.
-// Large fp32 results: 2048 x 8192 x 8192 (256 tiles of 256 x 256) 207 us, 1.32 PFLOP/s (the
-// library's bf16 product reaches 1.31 at 8192 x 8192 x 8192); 2560 x 10240 x 16384 770 to
-// 820 us (1.05 to 1.1). A step issues 5 cycles of vector instructions per 4 of the matrix
+// Few rows are bound by B's bytes: 16 x 129280 x 7168, fp32, 161 to 190 us (4.9 to 5.8 TB/s).
+// Few steps are bound by latency: 777 x 1001 x 1536 7 to 8 us, 12 steps of 0.3 and the launch.
+// Large fp32 results: 2048 x 8192 x 8192 (256 tiles of 256 x 256) 234 to 240 us, 1.15 PFLOP/s
+// (the library's bf16 product reaches 1.31 to 1.46 at 8192 x 8192 x 8192); 2560 x 10240 x 16384
+// 785 to 835 us (1.03 to 1.1). A step issues 5 cycles of vector instructions per 4 of the matrix
 // cores, 3 of them conversions (two codes in 8 cycles). Widening each code once per
 // workgroup and passing it on through LDS as bf16 (twice the LDS bytes, a second barrier a
 // step) took 1071 us, where this took 857.
@@ -331,10 +331,10 @@ __global__ __launch_bounds__(64 * kWB * kWA) void product_tile_kernel(ProductArg
 // instruction's sums are scaled into the accumulators three instructions later,
 // when they are there.
 //
-// 16384 x 10240 x 2560 takes 360 to 410 us (2.1 to 2.4 PFLOP/s; the library's product of
+// 16384 x 10240 x 2560 takes 390 to 420 us (2.05 to 2.2 PFLOP/s; the library's product of
 // E4M3 matrices with one scale each reaches 2.77 at 8192 x 8192 x 8192). The matrix cores
-// are busy 55 % of the cycles, vector instructions issue in 49 %, at 2.0 to 2.1 GHz: the
-// busier they are, the lower the clock (8192 x 8192 x 8192: 60 % at 2.0). A tile's stores
+// are busy 55 % of the cycles, vector instructions issue in 50 %, at 1.9 to 2.1 GHz: the
+// busier they are, the lower the clock (8192 x 8192 x 8192: 61 % at 1.85). A tile's stores
 // cost 3.6 us, which the next tile's second step waits for.
 constexpr int kWide = 256;
 constexpr int kWideRows = kWide * kRowChunks;          // chunks of an operand's rows of a step
@@ -566,10 +566,10 @@ void run_wide(ProductArgs a, hipStream_t stream) {
 
 // Whether a die's workgroups take consecutive tiles: where C's rows do not start at whole
 // 128-byte lines, tiles side by side share lines, and a line written by two dies goes to
-// memory in two pieces. fp32 results: 882 x 72178 x 640 111 us, tiles in turn 129; 1321 x 72281 x
-// 128 104 and 126; 2000 x 10001 x 4096 171 and 172; rows of whole lines 8192 x 8192 x 640 113 and
-// 107. bf16 results: 4000 x 20001 x 256 57 and 70; 1000 x 5001 x 512 9.2 and 9.5, x 1024, more
-// bound by its steps, 13.4 and 12.9.
+// memory in two pieces. fp32 results: 1321 x 72281 x 128 99 us, tiles in turn 112; 882 x 72178 x
+// 640, bound by more steps, 126 and 124; 2000 x 10001 x 4096 166 and 166; rows of whole lines
+// 8192 x 8192 x 640 113 and 104. bf16 results: 4000 x 20001 x 256 58 and 62; 1000 x 5001 x 512
+// 9.5 and 10.0, x 1024, more bound by its steps, 13.7 and 13.0.
 template <int kOut>
 bool tiles_in_runs(const ProductArgs& a) {
   return a.c_cols * Elem<kOut>::kSize % 128 != 0 && (kOut == 1 || a.k <= 4 * kBlock);
@@ -708,24 +708,24 @@ ProductArgs columns_of(ProductArgs a, long long first, long long count, size_t e
 }
 
 // Which kernel: all give the same bits. us measured on both sides of each border
-// (bf16 results where not said otherwise; m x n x k).
+// (bf16 results where not said otherwise; m x n x k; operands of normally distributed values).
 template <int kOut>
 void run_product(const ProductArgs& a, hipStream_t stream) {
   auto tiles = [&](int cols, int rows) { return ceil_div(a.n, cols) * ceil_div(a.m, rows); };
   // No more tiles of 16 to 64 columns by 16 or 32 rows than CUs (the smallest that are
   // so few: larger ones read less): the wavefronts share the blocks. 16 x 2560 x 7168
-  // 9.5, in 64 x 64 tiles 20.1; 16 x 10240 x 7168 19.2 and 20.7; 16 x 20480 x 7168
-  // 35.6 and 26.6; 128 x 2048 x 16384 35.2 and 44.3; 256 x 2048 x 16384 63.0 and 44.9.
+  // 10.0, in 64 x 64 tiles 20.3; 16 x 10240 x 7168 19.5 and 21.1; 16 x 20480 x 7168
+  // 35.6 and 26.7; 128 x 2048 x 16384 35.5 and 43.8; 256 x 2048 x 16384 63.2 and 44.2.
   if (tiles(16, 16) <= kCUs) return run_few<kOut, 1, 1>(a, stream);
   if (tiles(32, 16) <= kCUs) return run_few<kOut, 2, 1>(a, stream);
   if (a.m <= 16 && tiles(64, 16) <= kCUs) return run_few<kOut, 4, 1>(a, stream);
   if (a.m > 16 && tiles(32, 32) <= kCUs) return run_few<kOut, 2, 2>(a, stream);
   // Rows or columns whose tiles fill the CUs a whole number of times, and what is left: a few
   // tiles more than whole rounds take as long as another round, or a third of it in smaller
-  // tiles of their own. 6000 x 3000 x 7168 (288 tiles of 256 x 256) 130, all in those 169.
+  // tiles of their own. 6000 x 3000 x 7168 (288 tiles of 256 x 256) 145, all in those 186.
   // Columns where they leave a tenth less, in tiles of 128 x 128: 300 x 70000 x 4096 (by columns
-  // 36 of 548 tiles, by rows none whole) 138 and 165, 4096 x 4200 x 4096, fp32 (32 of those and
-  // 66) 131 and 141; 2560 x 10240 x 16384, fp32 (600 and 640) 797 and 785.
+  // 36 of 548 tiles, by rows none whole) 145 and 170, 4096 x 4200 x 4096, fp32 (32 of those and
+  // 66) 142 and 150; 2560 x 10240 x 16384, fp32 (600 and 640) 797 and 785.
   struct Rounds {
     long long rounds, rows, columns, left;  // whole rounds, their rows and columns, the tiles left
   };
@@ -750,8 +750,8 @@ void run_product(const ProductArgs& a, hipStream_t stream) {
     }
   };
   const double steps = (double)(a.k / kBlock);
-  // More than half the CUs with a 256 x 256 tile: 2048 x 5120 x 4096 (160 tiles) 49, in
-  // 128 x 128 tiles 58; 2048 x 4096 x 4096 (128) 54 and 42.
+  // More than half the CUs with a 256 x 256 tile: 2048 x 5120 x 4096 (160 tiles) 52, in
+  // 128 x 128 tiles 60; 2048 x 4096 x 4096 (128) 50 and 42.
   // (Left over: a step of a round takes 1.6 us, one of `left` tiles as smaller ones 0.45 +
   // 0.0125 left, and 4 us once.)
   if constexpr (kOut == 0) {
@@ -759,17 +759,17 @@ void run_product(const ProductArgs& a, hipStream_t stream) {
       return split(rounds_of(kWide, kCUs), (1.1 - 4.0 / steps) / 0.0125, [&](const ProductArgs& p) { run_wide(p, stream); });
   }
   // Tiles of 64 x 64, two steps per barrier while they run at once, two per CU: 512 x 2048 x
-  // 7168 (256) 21.7, with one step 28.8; 196 x 1996 x 9472 (128) 27.1 and 34.9; 1024 x 2560 x
-  // 2560 (640) 18.8 and 16.1, in 64 x 128 tiles 17.3; 1280 x 2560 x 7936 (800) 50.6, in 64 x
-  // 128 tiles 43.1; 1024 x 4000 x 4096 (1008) 38.8 and 27.5.
+  // 7168 (256) 22.1, with one step 28.8; 196 x 1996 x 9472 (128) 26.7 and 34.9; 1024 x 2560 x
+  // 2560 (640) 18.8 and 15.9, in 64 x 128 tiles 17.0; 1280 x 2560 x 7936 (800) 52.0, in 64 x
+  // 128 tiles 45.1; 1024 x 4000 x 4096 (1008) 36.6 and 28.2.
   if (tiles(64, 64) <= 2 * kCUs) return run_tiles<kOut, 64, 64, 2, 2, 4, 2>(a, stream);
   if (tiles(64, 64) <= 3 * kCUs) return run_tiles<kOut, 64, 64, 2, 2, 2>(a, stream);
-  // Many columns for few rows are a matter of B's bytes: 64 x 61440 x 7168 85.5 in tiles
-  // of 128 columns, 97.1 of 64.
+  // Many columns for few rows are a matter of B's bytes: 64 x 61440 x 7168 82.9 in tiles
+  // of 128 columns, 95.5 of 64.
   if (a.m <= 64) return run_tiles<kOut, 128, 64, 2, 2, 3>(a, stream);
   // bf16 results: 128 x 128 tiles (of eight wavefronts, two workgroups per CU; of four
-  // 2 to 15 % slower) where there are more than CUs: 1024 x 5000 x 4096 (320) 33.8, in 64 x
-  // 128 tiles 38.1; 128 x 61440 x 7168 (480) 103 and 137; 1500 x 2600 x 4096 (252) 27.8 and 26.3.
+  // 2 to 15 % slower) where there are more than CUs: 1024 x 5000 x 4096 (320) 34.2, in 64 x
+  // 128 tiles 39.2; 128 x 61440 x 7168 (480) 101 and 141; 1500 x 2600 x 4096 (252) 28.0 and 28.0.
   if constexpr (kOut == 0) {
     if (tiles(128, 128) > kCUs) return run_tiles<kOut, 128, 128, 2, 4, 2>(a, stream);
   }
@@ -777,10 +777,10 @@ void run_product(const ProductArgs& a, hipStream_t stream) {
   // least, whichever end sooner. A step of a round takes 3.2 us with 256 x 256, 2.0 with two
   // of 128 x 128 per CU, 1.2 with one, 0.62 a 64 x 128 tile per CU, and 0.5 + 0.0025 left
   // where 128 x 128 tiles left over become smaller ones; another launch 4.
-  // 2048 x 4096 x 4096 in 128 x 128 (512 tiles) 67, in 64 x 128 79; 900 x 5000 x 2560 (320) 39.7
-  // and 36.4; 8960 x 1536 x 16384 (210 tiles of 256 x 256) 401, in 128 x 128 tiles 471; 4096 x
-  // 4200 x 4096 (256 and 33) 147, all in one size 216 or 167; 2560 x 10240 x 16384 (240 and 160)
-  // 770, 791 or 807; 2048 x 10240 x 7168 (320) 369, in 128 x 128 tiles 286.
+  // 2048 x 4096 x 4096 in 128 x 128 (512 tiles) 75, in 64 x 128 86; 900 x 5000 x 2560 (320) 42.9
+  // and 39.3; 8960 x 1536 x 16384 (210 tiles of 256 x 256) 418, in 128 x 128 tiles 519; 4096 x
+  // 4200 x 4096 (256 and 16) 142, all in one size 222 or 172; 2560 x 10240 x 16384 (240 and 160)
+  // 835, 852 or 919; 2048 x 10240 x 7168 (256 and 64) 285, 385 or 307.
   if constexpr (kOut == 1) {
     const double most_left = (0.5 - 4.0 / steps) / 0.0025;
     auto in128 = [&](long long n, bool smaller) {  // n tiles of 128 x 128, those left over smaller or not

@@ -36,16 +36,20 @@
 // Bound by memory: 16384 x 2560 bf16 with a post norm and a gate 64 to 71 us
 // forward (336 MB, 4.7 to 5.2 TB/s), 137 to 150 us backward (fp32 du; 590 MB,
 // 3.9 to 4.3 TB/s); 4096 x 7168 to E4M3 rows 39 to 44 us. One decode token
-// takes 4.2 us, launch and latency. Rows of odd width: 10000 x 2999 bf16 53 us
-// forward (4.5 TB/s), 125 backward (3.4 TB/s).
+// takes 4.2 us, launch and latency. Rows of odd width load and store single
+// values: 10000 x 2999 bf16 64 us forward (3.8 TB/s), 124 backward (3.4 TB/s). Odd ones
+// above 4096 leave the held backward for three launches, or four with dx over dh: 4096 x
+// 5001 270 us, 5000 76.
 //
 // Dropout of the block's output (kDrop) multiplies gate p by the keep factors of
 // dropout.h in the forward, and the gradients of gate and p in the backward. Its
 // instances are files of their own, with arguments of their own: calls without it
-// keep the registers that they had. With it: 8192 x 2560 bf16 35 us forward (4.8
-// TB/s; without 34), to block-scaled E4M3 rows 37 (4.0 TB/s: a value costs about 50
-// instructions there, 30 us of all SIMDs beside 29 of memory); backward 16384 x
-// 2560, fp32 du, 147 to 156 us (3.8 to 4.0 TB/s; without 140 to 148).
+// keep the registers that they had. With it: 8192 x 2560 bf16 34 us forward (4.9
+// TB/s; without 34), to block-scaled E4M3 rows 33 to 37 (4.0 to 4.5 TB/s: a value costs
+// about 50 instructions there, 30 us of all SIMDs beside 29 of memory); backward 16384 x
+// 2560, fp32 du, 148 to 162 us (3.6 to 4.0 TB/s; without 139 to 148). Odd widths: 10000 x
+// 2999 81 us forward, 153 backward; 4096 x 5001 backward 364 (one call of the generator per
+// value instead of per eight; 5000: 88).
 #pragma once
 
 #include <algorithm>
@@ -135,7 +139,7 @@ struct Group {
   uint32_t w[kVec ? 2 * E::kSize : 8];
 
   // kNow: used at once, single values past the row are loaded from its end and replaced,
-  // without a branch each (forward, 10000 x 2999 bf16: 53 us, with branches 80). Not for
+  // without a branch each (forward, 10000 x 2999 bf16 from the caches: 53 us, with branches 80). Not for
   // loads ahead of their use, which would wait for them (backward: 125, so 224).
   template <bool kNow = false>
   __device__ __forceinline__ void load(const void* row, const Columns<kVec>& k, int c) {
@@ -428,7 +432,7 @@ using BwdArgs = std::conditional_t<kDrop, NormBwdDropArgs, NormBwdArgs>;
 constexpr int kBwdMaxWaves = 8;
 
 // (Dropout's bits leave the registers of three wavefronts per SIMD short: with two,
-// 16384 x 2560 fp32 takes 218 us, spilling with three 259; bf16 the same either way.)
+// 16384 x 2560 fp32 takes 195 to 218 us, spilling with three 259; bf16 the same either way.)
 template <int kDtype, int kGrad, bool kDrop, bool kVec, int kGroups>
 __global__ __launch_bounds__(64 * kBwdMaxWaves, kGroups == 1 && !kDrop ? 3 : 2) void norm_backward_held_kernel(BwdArgs<kDrop> a) {
   using T = typename Elem<kDtype>::T;

@@ -14,9 +14,11 @@
 // written: a workgroup holds a 128 x 128 tile in registers (thread: 8 rows by 8
 // columns), takes the rows' maxima over 16 lanes and the columns' through LDS,
 // and turns the codes through 16 KB of LDS so that both are written in whole
-// lines. 16384 x 2560 bf16 rows alone 31 us (4.0 TB/s), both ways
-// 41 (4.1 TB/s; 68 % of the cycles issue vector instructions); 8960 x 1536 fp32 by
-// tiles, both ways, 16 (5.2 TB/s). One decode token 3, launch and latency.
+// lines. 16384 x 2560 bf16 rows alone 31 to 33 us (3.8 to 4.0 TB/s), the
+// transpose alone 28 (4.6), both ways 39 to 42 (4.0 to 4.3; 68 % of the cycles issue vector
+// instructions); by tiles 23, 24 and 33 (5.0 to 5.4); 8960 x 1536 fp32 by tiles, both ways,
+// 16 to 19 (4.3 to 5.2). Odd widths: 10000 x 2999 bf16 26, 35 and 45 (2.6 to 3.4), by tiles
+// 30, 30 and 36. One decode token 3, launch and latency.
 
 #include <algorithm>
 
