@@ -401,7 +401,8 @@ itl_status itl_dropout(const void* x, itl_dtype dtype, int64_t n_rows, int64_t d
  *   h = x + scale gate D p
  *   dp = scale gate D dx, dgate = scale D p dx, the rest as there;
  * where a value is dropped both are 0, and so is dp w_post in dy, whatever gate, p,
- * w_post and dx are there. y must be given. */
+ * w_post and dx are there. y must be given. (itl_residual_norm_fp8 has no such form:
+ * itl_quantize_rows_fp8 of u.) */
 itl_status itl_residual_norm_dropout(const void* x, const void* y, const void* gate, int64_t gate_stride,
                                      const void* w_post, const void* w_pre, itl_dtype dtype,
                                      int64_t n_rows, int64_t d, float scale, float eps,

@@ -23,8 +23,8 @@ Entry points (same names as the C ABI without the ``itl_`` prefix):
   ``residual_norm_backward(du, dh, h, y, w_pre, rstd_pre) -> (dx, dy, dw_pre, dw_post, dgate)``
 * ``cross_entropy(H, W, targets) -> (loss, token_loss, lse)``,
   ``cross_entropy_grad(H, W, targets) -> (loss, token_loss, lse, dH, dW)``
-* ``dropout(x, Dropout(p, seed)) -> y``; ``dropout=`` of the norms above, and
-  ``residual_norm_blocks_fp8(x, y, w_pre) -> (h, Uq, u_scale, rstd_pre, rstd_post)``
+* ``dropout(x, Dropout(p, seed)) -> y``; ``dropout=`` of ``residual_norm``, of
+  ``residual_norm_backward`` and of ``residual_norm_blocks_fp8(x, y, w_pre) -> (h, Uq, u_scale, rstd_pre, rstd_post)``
 * ``quantize_blocks_fp8(X)``, ``quantize_tiles_fp8(X) -> (Xq, scale, Xtq, t_scale)``,
   ``matmul_fp8_blocks(Aq, a_scale, Bq, b_scale) -> C``
 * ``adamw_plan(params, grads, lr=...) -> plan``, ``adamw_step(plan) -> grad_norm``
@@ -689,8 +689,9 @@ def residual_norm(x, y, w_pre, *, w_post=None, gate=None, scale=1.0, eps=1e-6, h
 
 def residual_norm_fp8(x, y, w_pre, *, w_post=None, gate=None, scale=1.0, eps=1e-6, h=None, Uq=None, u_scale=None):
     """residual_norm with u as E4M3 codes (uint8 [n, d]) and a scale per row
-    (fp32 [n]), as lmhead_logprob_fp8 takes them; d a multiple of 128. Returns
-    (h, Uq, u_scale, rstd_pre, rstd_post)."""
+    (fp32 [n]), as lmhead_logprob_fp8 takes them; d a multiple of 128. It has no
+    dropout (take quantize_rows_fp8 of residual_norm's u). Returns (h, Uq, u_scale,
+    rstd_pre, rstd_post)."""
     n, d, stride = _norm_operands(x, y, w_pre, w_post, gate, "x")
     h = _stream_rows(x, y, h, n, d)
     Uq = _new((n, d), torch.uint8, x, "Uq", Uq)

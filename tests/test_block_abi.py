@@ -3,6 +3,7 @@ launched): argument checks before any device work, and what the compiled
 kernels hold."""
 
 import ctypes
+import inspect
 import os
 import re
 
@@ -110,6 +111,15 @@ def test_bindings_refuse(itl):
         itl.matmul_fp8_blocks(codes, torch.zeros(1, 4), codes, torch.zeros(1, 1))
     with pytest.raises(TypeError):
         itl.dropout([1.0], None)
+
+
+def test_which_norms_take_dropout(itl):
+    """Those that the package's documentation names, and no other."""
+    norms = ("residual_norm", "residual_norm_fp8", "residual_norm_blocks_fp8", "residual_norm_backward")
+    takes = {name for name in norms if "dropout" in inspect.signature(getattr(itl, name)).parameters}
+    entry = next(e for e in itl.__doc__.split("\n* ") if "``dropout=``" in e)
+    named = set(re.findall(r"``(residual_\w+)", entry.split("``dropout=``")[1]))
+    assert named == takes and "norms above" not in entry
 
 
 @needs_hipcc
