@@ -162,7 +162,7 @@ __device__ __forceinline__ void store8(const ProductArgs& a, uint16_t* to, uint4
 // Few steps are bound by latency: 777 x 1001 x 1536 7 to 8 us, 12 steps of 0.3 and the launch.
 // Large fp32 results: 2048 x 8192 x 8192 (256 tiles of 256 x 256) 234 to 240 us, 1.15 PFLOP/s
 // (the library's bf16 product reaches 1.31 to 1.46 at 8192 x 8192 x 8192); 2560 x 10240 x 16384
-// 785 to 835 us (1.03 to 1.1). A step issues 5 cycles of vector instructions per 4 of the matrix
+// 763 to 835 us (1.03 to 1.13). A step issues 5 cycles of vector instructions per 4 of the matrix
 // cores, 3 of them conversions (two codes in 8 cycles). Widening each code once per
 // workgroup and passing it on through LDS as bf16 (twice the LDS bytes, a second barrier a
 // step) took 1071 us, where this took 857.
